@@ -12,9 +12,11 @@ Entry points (same names as the C ABI):
   attn_bwd_fixed_scratch, attn_status_string, attn_version   (include/attn.h)
   dsa_indexer_fwd, dsa_topk, dsa_indexer_bwd_workspace_size, dsa_indexer_bwd, dsa_sparse_kl,
   csa_compressor_fwd, csa_compressor_bwd_workspace_size, csa_compressor_bwd  (include/dsa.h)
+  attn_cache_append, attn_cache_fwd_workspace_size, attn_cache_fwd  (include/cache.h)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -31,6 +33,7 @@ __all__ = [
     "FIXED_SCRATCH_BYTES", "csa_compressor_fwd", "csa_compressor_bwd_workspace_size",
     "csa_compressor_bwd", "dsa_indexer_fwd", "dsa_topk", "dsa_indexer_bwd_workspace_size",
     "dsa_indexer_bwd", "dsa_sparse_kl", "INDEXER_HEAD_DIM", "attn_wait_selftest",
+    "attn_cache_append", "attn_cache_fwd_workspace_size", "attn_cache_fwd", "attn_cache_empty",
 ]
 
 ATTN_DQ_ATOMIC = 0
@@ -47,6 +50,7 @@ EXPORTED_SYMBOLS = (
     "csa_compressor_fwd", "csa_compressor_bwd_workspace_size", "csa_compressor_bwd",
     "dsa_indexer_fwd", "dsa_topk", "dsa_indexer_bwd_workspace_size", "dsa_indexer_bwd",
     "dsa_sparse_kl", "attn_wait_selftest",
+    "attn_cache_append", "attn_cache_fwd_workspace_size", "attn_cache_fwd",
 )
 INDEXER_HEAD_DIM = 128
 FIXED_SCRATCH_BYTES = 16 << 20
@@ -93,6 +97,20 @@ class _IndexerProblem(ctypes.Structure):
     ]
 
 
+class _CacheProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("tokens", ctypes.c_int), ("heads_q", ctypes.c_int),
+        ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("cache_type", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("max_new", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float),
+        ("rot_dim", ctypes.c_int), ("rot_interleaved", ctypes.c_int),
+        ("max_position", ctypes.c_int), ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("seqlens_kv", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("error_word", ctypes.c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -133,6 +151,11 @@ def lib() -> ctypes.CDLL:
         L.dsa_indexer_bwd_workspace_size.restype = sz
         L.dsa_indexer_bwd.argtypes = [IP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.dsa_sparse_kl.argtypes = [SP, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        KP = ctypes.POINTER(_CacheProblem)
+        L.attn_cache_append.argtypes = [KP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.attn_cache_fwd_workspace_size.argtypes = [KP]
+        L.attn_cache_fwd_workspace_size.restype = sz
+        L.attn_cache_fwd.argtypes = [KP, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.attn_wait_selftest.argtypes = [vp, ctypes.c_uint, vp, vp]
         L.attn_wait_selftest.restype = i32
         L.attn_status_string.argtypes = [i32]
@@ -141,7 +164,7 @@ def lib() -> ctypes.CDLL:
         for name in ("attn_fwd", "attn_bwd_preprocess", "attn_bwd", "attn_bwd_postprocess",
                      "sparse_attn_fwd", "sparse_attn_bwd", "attn_bwd_fixed_scratch",
                      "csa_compressor_fwd", "csa_compressor_bwd", "dsa_indexer_fwd", "dsa_topk",
-                     "dsa_indexer_bwd", "dsa_sparse_kl"):
+                     "dsa_indexer_bwd", "dsa_sparse_kl", "attn_cache_append", "attn_cache_fwd"):
             getattr(L, name).restype = i32
         _LIB = L
     return _LIB
@@ -635,3 +658,183 @@ def dsa_sparse_kl(q, kv, lse, idx, scores, *, scale=None, loss=None, grad=None, 
            lib().dsa_sparse_kl(ctypes.byref(p), _ptr(q), _ptr(kv), _ptr(lse), _ptr(idx),
                                _ptr(scores), _ptr(loss), _ptr(grad), _ptr(target), _stream(stream)))
     return loss, grad, target
+
+
+# ----------------------------------------------------------------------------
+# paged key/value cache (include/cache.h)
+# ----------------------------------------------------------------------------
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+def attn_cache_empty(num_pages, heads_kv, page_size, head_dim, *, dtype=torch.bfloat16, device=None):
+    """An empty cache: (k_cache, v_cache, k_scale, v_scale), the pools
+    [num_pages, heads_kv, page_size, head_dim] of `dtype` (bfloat16 or
+    float8_e4m3fn) uninitialized, the scales fp32 [num_pages, heads_kv] (None for
+    bfloat16)."""
+    if dtype not in _CACHE_TYPES:
+        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {dtype}")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    k, v = (torch.empty(num_pages, heads_kv, page_size, head_dim, dtype=dtype, device=dev)
+            for _ in range(2))
+    if dtype == torch.bfloat16:
+        return k, v, None, None
+    ks, vs = (torch.ones(num_pages, heads_kv, dtype=torch.float32, device=dev) for _ in range(2))
+    return k, v, ks, vs
+
+
+def _need_rows(t, name, heads, dim, device):
+    """bf16 [tokens, heads, dim] whose tokens may lie apart (a slice of a fused
+    projection); returns the elements between two tokens."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0] if t.shape[0] > 1 else 0
+
+
+def _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                   max_new, error_word, tokens, heads_q):
+    dev = k_cache.device
+    if k_cache.dtype not in _CACHE_TYPES:
+        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, heads_kv, page_size, head_dim]")
+    _need(k_cache, "k_cache", k_cache.dtype)
+    _need(v_cache, "v_cache", k_cache.dtype, dev)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    p = _CacheProblem()
+    p.num_pages, p.heads_kv, p.page_size, p.head_dim = k_cache.shape
+    p.cache_type = _CACHE_TYPES[k_cache.dtype]
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if p.cache_type == 0:
+            if t is not None:
+                raise ValueError(f"{name}: a bfloat16 cache has no scales")
+        elif _need(t, name, torch.float32, dev).shape != k_cache.shape[:2]:
+            raise ValueError(f"{name} must be [num_pages, heads_kv]")
+    for t, name in ((page_table, "page_table"), (seqlens_kv, "seqlens_kv"),
+                    (cu_seqlens, "cu_seqlens")):
+        _need(t, name, torch.int32, dev)
+    n = seqlens_kv.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n or cu_seqlens.numel() != n + 1:
+        raise ValueError("seqlens_kv [n], cu_seqlens [n + 1] and page_table [n, max_pages] disagree")
+    if error_word is not None:
+        _need(error_word, "error_word", torch.int32, dev)
+    p.num_seqs, p.max_pages = page_table.shape
+    p.tokens, p.heads_q, p.max_new = tokens, heads_q, int(max_new)
+    p.cu_seqlens, p.seqlens_kv = cu_seqlens.data_ptr(), seqlens_kv.data_ptr()
+    p.page_table = page_table.data_ptr()
+    p.error_word = None if error_word is None else error_word.data_ptr()
+    return p
+
+
+def _on(device, stream):
+    """The context in which a call on `device` runs and allocates (so that what it
+    allocates belongs to the stream that writes it), and that stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream), stream
+    stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), stream
+    return torch.cuda.device(device), stream
+
+
+def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, max_new,
+                      k_scale=None, v_scale=None, cos_sin=None, interleaved=False, q_out=None,
+                      error_word=None, stream=None):
+    """Writes the new tokens' keys and values (k, v bf16 [T, Hkv, D]) into the
+    paged cache and returns the rotated queries (q bf16 [T, Hq, D], or None for
+    both).  k_cache, v_cache [pages, Hkv, page_size, D] bfloat16, or
+    float8_e4m3fn with k_scale, v_scale fp32 [pages, Hkv]; page_table int32
+    [n, max_pages]; seqlens_kv int32 [n], the lengths including the new tokens;
+    cu_seqlens int32 [n + 1]; max_new bounds the new tokens of a sequence.
+    cos_sin fp32 [positions, rot_dim] (cosines, then sines) rotates q and k, None
+    leaves them; `interleaved` pairs neighbouring dims.  The tokens of q, k and v
+    may lie apart, as in a fused projection."""
+    dev = k_cache.device
+    if q is None and q_out is not None:
+        raise ValueError("q_out is given without q")
+    heads_q = k_cache.shape[1] if q is None else q.shape[1]
+    p = _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                       max_new, error_word, k.shape[0], heads_q)
+    p.k_stride = _need_rows(k, "k", p.heads_kv, p.head_dim, dev)
+    p.v_stride = _need_rows(v, "v", p.heads_kv, p.head_dim, dev)
+    if v.shape[0] != p.tokens or (q is not None and q.shape[0] != p.tokens):
+        raise ValueError("q, k and v must have the same tokens")
+    if cos_sin is not None:
+        if _need(cos_sin, "cos_sin", torch.float32, dev).dim() != 2:
+            raise ValueError("cos_sin must be [positions, rot_dim]")
+        p.max_position, p.rot_dim = cos_sin.shape
+        p.rot_interleaved = 1 if interleaved else 0
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if q is not None:
+            p.q_stride = _need_rows(q, "q", heads_q, p.head_dim, dev)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            elif _need(q_out, "q_out", torch.bfloat16, dev).shape != q.shape:
+                raise ValueError("q_out must have the shape of q")
+        _check("attn_cache_append",
+               lib().attn_cache_append(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cos_sin),
+                                       _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                       _ptr(v_scale), ctypes.c_void_p(s.cuda_stream)))
+    return q_out
+
+
+def _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                       max_new, causal, scale, error_word):
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    p = _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                       max_new, error_word, q.shape[0], q.shape[1])
+    p.q_stride = _need_rows(q, "q", p.heads_q, p.head_dim, k_cache.device)
+    p.causal = 1 if causal else 0
+    p.scale = float(scale if scale is not None else 1.0 / math.sqrt(p.head_dim))
+    return p
+
+
+def attn_cache_fwd_workspace_size(q, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens,
+                                  max_new, k_scale=None, v_scale=None) -> int:
+    p = _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv,
+                           cu_seqlens, max_new, True, None, None)
+    return int(lib().attn_cache_fwd_workspace_size(ctypes.byref(p)))
+
+
+def attn_cache_fwd(q, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, max_new,
+                   k_scale=None, v_scale=None, causal=True, scale=None, out=None, lse=None,
+                   workspace=None, error_word=None, stream=None):
+    """Attention of the new tokens' queries (q bf16 [T, Hq, D], rotated) over the
+    paged cache, which holds their own keys already; arguments as for
+    attn_cache_append.  Returns (o bf16 [T, Hq, D], lse fp32 [Hq, T]).  A
+    workspace is allocated here when none is given."""
+    dev = k_cache.device
+    p = _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv,
+                           cu_seqlens, max_new, causal, scale, error_word)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        elif _need(out, "out", torch.bfloat16, dev).shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        if lse is None:
+            lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=dev)
+        elif _need(lse, "lse", torch.float32, dev).shape != (q.shape[1], q.shape[0]):
+            raise ValueError("lse must be [heads, tokens]")
+        if workspace is None:
+            n = lib().attn_cache_fwd_workspace_size(ctypes.byref(p))
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, "workspace", torch.uint8, dev)
+        _check("attn_cache_fwd",
+               lib().attn_cache_fwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
+                                    _ptr(workspace), workspace.numel(),
+                                    ctypes.c_void_p(s.cuda_stream)))
+    return out, lse

@@ -1,0 +1,96 @@
+// Kernel-side view of a paged-cache step and the launch wrappers shared by the
+// cache kernels and their C ABI layer.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "cache.h"
+#include "common.cuh"
+
+namespace attn {
+
+struct CacheStep {
+  int num_seqs, tokens;
+  int heads_q, heads_kv, group;
+  int ps_shift;              // log2 of page_size
+  int num_pages, max_pages;
+  int max_new;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int32_t* err;
+};
+
+// Sequence n of a step: its new tokens are rows t0 .. t0 + m - 1 at positions
+// pos0 .. (negative where there are more of them than the length), its keys
+// are 0 .. len - 1.  Rows outside [0, tokens) and keys past the page table are
+// cut off, so that arrays breaking their contract move no access out of its
+// buffer.
+struct StepSeq {
+  int t0, m, pos0, len;
+};
+
+__device__ __forceinline__ StepSeq step_seq(const CacheStep& s, int n, int* bad = nullptr) {
+  const int a = __ldg(s.cu + n), b = __ldg(s.cu + n + 1), l = __ldg(s.kv_len + n);
+  StepSeq q;
+  q.t0 = min(max(a, 0), s.tokens);
+  q.m = min(max(b, q.t0), s.tokens) - q.t0;
+  const int cap = static_cast<int>(
+      min(static_cast<long long>(s.max_pages) << s.ps_shift, static_cast<long long>(0x7fffffff)));
+  q.len = min(max(l, 0), cap);
+  q.pos0 = max(l, 0) - q.m;
+  if (bad && (l > cap || l < 0 || q.m > s.max_new || q.m > l)) *bad |= ATTN_DEVERR_SEQLEN;
+  return q;
+}
+
+struct AppendArgs {
+  CacheStep s;
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float* cos_sin;
+  int rot_dim, interleaved, max_position;
+  __nv_bfloat16* q_out;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int unit_blocks;   // leading blocks of the grid that append; the others rotate q
+  int slots;         // page slots per sequence, 0: found by a scan over the sequences
+  int units;         // (page item, KV head, K or V) units
+  FastDiv fd_slots, fd_hq;
+};
+
+cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, bool small,
+                                int q_blocks, cudaStream_t st);
+
+// Calls with at most this many new tokens per sequence give each (page, KV
+// head, K or V) unit to one warp, the others to a block.
+constexpr int kAppendSmall = 8;
+
+// Chunks of 16 keys are the unit in which attn_cache_fwd deals work.
+constexpr int kChunk = 16;
+// CTAs of attn_cache_fwd (fewer for small steps): a fixed count, not the
+// device's SM count, so that the result does not depend on the device.
+constexpr int kCacheCtas = 152;
+
+struct CacheFwdArgs {
+  CacheStep s;
+  int causal;
+  float scale_log2;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;     // [grid][2][rows][head_dim] partial outputs
+  float2* part_ml;   // [grid][2][rows] running maximum (log2) and sum
+  int4* part_meta;   // [grid][2] {kind bits, sequence, KV head, row block}
+};
+
+// Rows per work item of the variant that serves `rows` query rows per KV head.
+int cache_fwd_rows(int rows, bool e4m3);
+cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int rows, int grid,
+                             cudaStream_t st);
+
+}  // namespace attn

@@ -1,0 +1,205 @@
+// C ABI of the paged cache (declared and documented in cache.h): argument
+// validation, the choice of a variant and the launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "cache.cuh"
+#include "launch.h"
+
+namespace attn {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status_t check_step(const attn_cache_problem_t* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->num_seqs <= 0 || p->tokens < 0 || p->heads_q <= 0 || p->heads_kv <= 0 ||
+      p->head_dim <= 0 || p->num_pages <= 0 || p->max_pages <= 0 || p->max_new < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->tokens > 0 && p->max_new == 0) return ATTN_ERR_INVALID_ARG;
+  if (p->heads_q % p->heads_kv) return ATTN_ERR_INVALID_ARG;
+  if (p->cache_type != ATTN_CACHE_BF16 && p->cache_type != ATTN_CACHE_E4M3)
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if (!p->cu_seqlens || !p->seqlens_kv || !p->page_table) return ATTN_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+    return ATTN_ERR_UNSUPPORTED;
+  const int64_t lim = int64_t(1) << 31;
+  if (p->heads_q > 65535 || static_cast<int64_t>(p->tokens) * p->heads_q >= lim ||
+      static_cast<int64_t>(p->num_pages) * p->heads_kv >= lim / p->page_size)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned(p->cu_seqlens, 4) || !aligned(p->seqlens_kv, 4) || !aligned(p->page_table, 4) ||
+      !aligned(p->error_word, 4))
+    return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
+// A token stride: 0 stands for dense rows.
+bool good_stride(int64_t stride, int heads, int dim, int64_t* out) {
+  const int64_t dense = static_cast<int64_t>(heads) * dim;
+  *out = stride == 0 ? dense : stride;
+  return *out >= dense && *out % 8 == 0;
+}
+
+CacheStep to_step(const attn_cache_problem_t* p) {
+  CacheStep s;
+  s.num_seqs = p->num_seqs;
+  s.tokens = p->tokens;
+  s.heads_q = p->heads_q;
+  s.heads_kv = p->heads_kv;
+  s.group = p->heads_q / p->heads_kv;
+  s.ps_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
+  s.num_pages = p->num_pages;
+  s.max_pages = p->max_pages;
+  s.max_new = p->max_new;
+  s.cu = p->cu_seqlens;
+  s.kv_len = p->seqlens_kv;
+  s.table = p->page_table;
+  s.err = p->error_word;
+  return s;
+}
+
+// Query rows that one KV head has in the longest sequence of the step.
+int step_rows(const attn_cache_problem_t* p) {
+  const int64_t r = static_cast<int64_t>(p->max_new) * (p->heads_q / p->heads_kv);
+  return static_cast<int>(r < 1 << 30 ? r : 1 << 30);
+}
+
+struct Workspace {
+  size_t o, ml, meta, bytes;
+};
+Workspace fwd_workspace(const attn_cache_problem_t* p) {
+  const size_t rows = 2 * static_cast<size_t>(kCacheCtas) *
+                      cache_fwd_rows(step_rows(p), p->cache_type == ATTN_CACHE_E4M3);
+  Workspace w;
+  w.o = 0;
+  w.ml = rows * p->head_dim * sizeof(float);
+  w.meta = w.ml + rows * sizeof(float2);
+  w.bytes = w.meta + 2 * kCacheCtas * sizeof(int4);
+  return w;
+}
+
+attn_status_t status_of(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, const void* k,
+                                const void* v, const float* cos_sin, void* q_out, void* k_cache,
+                                void* v_cache, float* k_scale, float* v_scale,
+                                attn_stream_t stream) {
+  const attn_status_t st = check_step(p);
+  if (st != ATTN_OK) return st;
+  const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
+  if (!k || !v || !k_cache || !v_cache || (q == nullptr) != (q_out == nullptr) ||
+      (e4m3 && (!k_scale || !v_scale)))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rot_dim < 0 || p->rot_dim > p->head_dim || p->rot_dim % 16 ||
+      (p->rot_dim > 0 && (!cos_sin || p->max_position <= 0)))
+    return ATTN_ERR_INVALID_ARG;
+  AppendArgs a;
+  if (!good_stride(p->q_stride, p->heads_q, p->head_dim, &a.q_stride) ||
+      !good_stride(p->k_stride, p->heads_kv, p->head_dim, &a.k_stride) ||
+      !good_stride(p->v_stride, p->heads_kv, p->head_dim, &a.v_stride))
+    return ATTN_ERR_INVALID_ARG;
+  if (q && q == q_out && a.q_stride != static_cast<int64_t>(p->heads_q) * p->head_dim)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cos_sin, 16) ||
+      !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->tokens == 0) return ATTN_OK;
+
+  a.s = to_step(p);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.cos_sin = cos_sin;
+  a.rot_dim = p->rot_dim;
+  a.interleaved = p->rot_interleaved ? 1 : 0;
+  a.max_position = p->max_position;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  // Pages that a sequence's new tokens can touch, and over all sequences
+  const int64_t slots = (static_cast<int64_t>(p->max_new) - 1 + p->page_size - 1) / p->page_size + 1;
+  const bool small = p->max_new <= kAppendSmall;
+  int64_t items = slots * p->num_seqs;
+  if (!small) {
+    const int64_t packed = p->tokens / p->page_size + 2 * static_cast<int64_t>(p->num_seqs);
+    if (packed < items) items = packed;
+  }
+  const int64_t units = items * 2 * p->heads_kv;
+  const int per_block = small ? 8 : 1;
+  const int64_t rows = q ? static_cast<int64_t>(p->tokens) * p->heads_q : 0;
+  const int rows_block = 256 / (p->head_dim / 16);
+  const int64_t unit_blocks = (units + per_block - 1) / per_block;
+  const int64_t q_blocks = (rows + rows_block - 1) / rows_block;
+  if (units >= (int64_t(1) << 30) || unit_blocks + q_blocks >= (int64_t(1) << 31))
+    return ATTN_ERR_UNSUPPORTED;
+  a.units = static_cast<int>(units);
+  a.unit_blocks = static_cast<int>(unit_blocks);
+  a.slots = small ? static_cast<int>(slots) : 0;
+  a.fd_slots = make_fastdiv(static_cast<uint32_t>(a.slots > 0 ? a.slots : 1));
+  a.fd_hq = make_fastdiv(static_cast<uint32_t>(p->heads_q));
+  return status_of(launch_cache_append(a, p->head_dim, e4m3, small, static_cast<int>(q_blocks),
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p) {
+  if (check_step(p) != ATTN_OK) return 0;
+  return fwd_workspace(p).bytes;
+}
+
+attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream) {
+  const attn_status_t st = check_step(p);
+  if (st != ATTN_OK) return st;
+  const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
+  if (!q || !k_cache || !v_cache || !o || !lse || (e4m3 && (!k_scale || !v_scale)))
+    return ATTN_ERR_INVALID_ARG;
+  CacheFwdArgs a;
+  if (!good_stride(p->q_stride, p->heads_q, p->head_dim, &a.q_stride)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(lse, 16) || !aligned(workspace, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->tokens == 0) return ATTN_OK;
+  const Workspace w = fwd_workspace(p);
+  if (!workspace || workspace_bytes < w.bytes) return ATTN_ERR_WORKSPACE;
+
+  a.s = to_step(p);
+  a.causal = p->causal ? 1 : 0;
+  a.scale_log2 = p->scale * kLog2e;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
+  const int rows = step_rows(p);
+  const int item_rows = cache_fwd_rows(rows, e4m3);
+  // the most chunks that the step can have; a CTA takes at least one per warp
+  const double items = (static_cast<double>(p->tokens) * a.s.group / item_rows + p->num_seqs) * p->heads_kv;
+  const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size + kChunk - 1) / kChunk);
+  const int grid = chunks / 6 + 1 < kCacheCtas ? static_cast<int>(chunks / 6) + 1 : kCacheCtas;
+  return status_of(launch_cache_fwd(a, p->head_dim, e4m3, rows, grid,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
