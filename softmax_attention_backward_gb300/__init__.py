@@ -687,63 +687,71 @@ def _need_rows(t, name, heads, dim, device):
     projection); returns the elements between two tokens."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st[0] if t.shape[0] > 1 else 0
 
 
-def _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
-                   max_new, error_word, tokens, heads_q):
-    dev = k_cache.device
-    if k_cache.dtype not in _CACHE_TYPES:
-        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    if k_cache.dim() != 4:
+def _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                   max_new, error_word, tokens, heads_q, causal=1, scale=1.0):
+    # (a step of one token takes the GPU a few microseconds, so this stays short:
+    # each tensor is looked at once, and the fields are set in one go)
+    dtype, dev, shape = k_cache.dtype, k_cache.device, k_cache.shape
+    kind = _CACHE_TYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {dtype}")
+    if len(shape) != 4:
         raise ValueError("k_cache must be [num_pages, heads_kv, page_size, head_dim]")
-    _need(k_cache, "k_cache", k_cache.dtype)
-    _need(v_cache, "v_cache", k_cache.dtype, dev)
-    if v_cache.shape != k_cache.shape:
+    _need(k_cache, "k_cache", dtype)
+    _need(v_cache, "v_cache", dtype, dev)
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    p = _CacheProblem()
-    p.num_pages, p.heads_kv, p.page_size, p.head_dim = k_cache.shape
-    p.cache_type = _CACHE_TYPES[k_cache.dtype]
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if p.cache_type == 0:
-            if t is not None:
-                raise ValueError(f"{name}: a bfloat16 cache has no scales")
-        elif _need(t, name, torch.float32, dev).shape != k_cache.shape[:2]:
-            raise ValueError(f"{name} must be [num_pages, heads_kv]")
-    for t, name in ((page_table, "page_table"), (seqlens_kv, "seqlens_kv"),
-                    (cu_seqlens, "cu_seqlens")):
-        _need(t, name, torch.int32, dev)
+    if kind:
+        if (_need(k_scale, "k_scale", torch.float32, dev).shape != shape[:2]
+                or _need(v_scale, "v_scale", torch.float32, dev).shape != shape[:2]):
+            raise ValueError("k_scale and v_scale must be [num_pages, heads_kv]")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
+    _need(page_table, "page_table", torch.int32, dev)
+    _need(seqlens_kv, "seqlens_kv", torch.int32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if error_word is not None:
+        _need(error_word, "error_word", torch.int32, dev)
+        error_word = error_word.data_ptr()
     n = seqlens_kv.numel()
     if page_table.dim() != 2 or page_table.shape[0] != n or cu_seqlens.numel() != n + 1:
         raise ValueError("seqlens_kv [n], cu_seqlens [n + 1] and page_table [n, max_pages] disagree")
-    if error_word is not None:
-        _need(error_word, "error_word", torch.int32, dev)
-    p.num_seqs, p.max_pages = page_table.shape
-    p.tokens, p.heads_q, p.max_new = tokens, heads_q, int(max_new)
-    p.cu_seqlens, p.seqlens_kv = cu_seqlens.data_ptr(), seqlens_kv.data_ptr()
-    p.page_table = page_table.data_ptr()
-    p.error_word = None if error_word is None else error_word.data_ptr()
-    return p
+    return _CacheProblem(n, tokens, heads_q, shape[1], shape[3], kind, shape[2], shape[0],
+                         page_table.shape[1], max_new, causal, scale, 0, 0, 0, 0, 0, 0,
+                         cu_seqlens.data_ptr(), seqlens_kv.data_ptr(), page_table.data_ptr(),
+                         error_word)
 
 
 def _on(device, stream):
     """The context in which a call on `device` runs and allocates (so that what it
-    allocates belongs to the stream that writes it), and that stream."""
+    allocates belongs to the stream that writes it), and that stream's handle."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream), stream
-    stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), stream
-    return torch.cuda.device(device), stream
+        return torch.cuda.stream(stream), stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
+        return _HERE, handle
+    return torch.cuda.device(device), handle
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, max_new,
@@ -759,15 +767,20 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
     leaves them; `interleaved` pairs neighbouring dims.  The tokens of q, k and v
     may lie apart, as in a fused projection."""
     dev = k_cache.device
-    if q is None and q_out is not None:
-        raise ValueError("q_out is given without q")
-    heads_q = k_cache.shape[1] if q is None else q.shape[1]
-    p = _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
-                       max_new, error_word, k.shape[0], heads_q)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out is given without q")
+        heads_q = k_cache.shape[1]
+    else:
+        if q.dim() != 3 or q.shape[0] != k.shape[0]:
+            raise ValueError("q must be [tokens, heads, head_dim], with the tokens of k and v")
+        heads_q = q.shape[1]
+    p = _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                       int(max_new), error_word, k.shape[0], heads_q)
     p.k_stride = _need_rows(k, "k", p.heads_kv, p.head_dim, dev)
     p.v_stride = _need_rows(v, "v", p.heads_kv, p.head_dim, dev)
-    if v.shape[0] != p.tokens or (q is not None and q.shape[0] != p.tokens):
-        raise ValueError("q, k and v must have the same tokens")
+    if v.shape[0] != p.tokens:
+        raise ValueError("k and v must have the same tokens")
     if cos_sin is not None:
         if _need(cos_sin, "cos_sin", torch.float32, dev).dim() != 2:
             raise ValueError("cos_sin must be [positions, rot_dim]")
@@ -778,13 +791,14 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
         if q is not None:
             p.q_stride = _need_rows(q, "q", heads_q, p.head_dim, dev)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+                q_out = q.new_empty(q.shape)
             elif _need(q_out, "q_out", torch.bfloat16, dev).shape != q.shape:
                 raise ValueError("q_out must have the shape of q")
-        _check("attn_cache_append",
-               lib().attn_cache_append(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cos_sin),
-                                       _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                       _ptr(v_scale), ctypes.c_void_p(s.cuda_stream)))
+        code = lib().attn_cache_append(ctypes.byref(p), _at(q), k.data_ptr(), v.data_ptr(),
+                                       _at(cos_sin), _at(q_out), k_cache.data_ptr(),
+                                       v_cache.data_ptr(), _at(k_scale), _at(v_scale), s)
+    if code:
+        raise AttnError("attn_cache_append", code)
     return q_out
 
 
@@ -792,11 +806,10 @@ def _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlen
                        max_new, causal, scale, error_word):
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    p = _cache_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
-                       max_new, error_word, q.shape[0], q.shape[1])
+    p = _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
+                       int(max_new), error_word, q.shape[0], q.shape[1], 1 if causal else 0,
+                       float(scale) if scale is not None else 1.0 / math.sqrt(q.shape[2]))
     p.q_stride = _need_rows(q, "q", p.heads_q, p.head_dim, k_cache.device)
-    p.causal = 1 if causal else 0
-    p.scale = float(scale if scale is not None else 1.0 / math.sqrt(p.head_dim))
     return p
 
 
@@ -817,24 +830,25 @@ def attn_cache_fwd(q, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, m
     dev = k_cache.device
     p = _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv,
                            cu_seqlens, max_new, causal, scale, error_word)
+    shape, ref = q.shape, ctypes.byref(p)
     ctx, s = _on(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        elif _need(out, "out", torch.bfloat16, dev).shape != q.shape:
+            out = q.new_empty(shape)
+        elif _need(out, "out", torch.bfloat16, dev).shape != shape:
             raise ValueError("out must have the shape of q")
         if lse is None:
-            lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=dev)
-        elif _need(lse, "lse", torch.float32, dev).shape != (q.shape[1], q.shape[0]):
+            lse = q.new_empty((shape[1], shape[0]), dtype=torch.float32)
+        elif _need(lse, "lse", torch.float32, dev).shape != (shape[1], shape[0]):
             raise ValueError("lse must be [heads, tokens]")
         if workspace is None:
-            n = lib().attn_cache_fwd_workspace_size(ctypes.byref(p))
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+            n = max(lib().attn_cache_fwd_workspace_size(ref), 16)
+            workspace = q.new_empty(n, dtype=torch.uint8)
         else:
-            _need(workspace, "workspace", torch.uint8, dev)
-        _check("attn_cache_fwd",
-               lib().attn_cache_fwd(ctypes.byref(p), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                    _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
-                                    _ptr(workspace), workspace.numel(),
-                                    ctypes.c_void_p(s.cuda_stream)))
+            n = _need(workspace, "workspace", torch.uint8, dev).numel()
+        code = lib().attn_cache_fwd(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                    _at(k_scale), _at(v_scale), out.data_ptr(), lse.data_ptr(),
+                                    workspace.data_ptr(), n, s)
+    if code:
+        raise AttnError("attn_cache_fwd", code)
     return out, lse

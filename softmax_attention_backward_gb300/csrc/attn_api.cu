@@ -71,6 +71,23 @@ bool make_dq_map(CUtensorMap* m, float* acc, int batch, int rows, int heads, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map over a pool of cache rows [rows, dim] of bf16 or 8-bit codes: box of
+// min(128 bytes, a row) x box_rows rows, swizzled over that width.
+bool make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool bytes,
+                   int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int el = bytes ? 1 : 2, width = dim * el < 128 ? dim * el : 128;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim) * el};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(width / el), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Validates a dense/THD problem.  Sets *empty when there is nothing to compute.
@@ -148,6 +165,11 @@ attn_status_t validate_dense_problem(const attn_problem_t* p, bool* empty) {
 bool make_bf16_tile_map(CUtensorMap* m, const void* ptr, int batch, int rows, int heads, int dim,
                         int box_rows) {
   return make_map(m, ptr, batch, rows, heads, dim, box_rows);
+}
+
+bool make_cache_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool bytes,
+                         int box_rows) {
+  return make_rows_map(m, ptr, rows, dim, bytes, box_rows);
 }
 
 // Streaming multiprocessors of the current device (persistent grid size).

@@ -67,8 +67,9 @@ cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, bo
 // head, K or V) unit to one warp, the others to a block.
 constexpr int kAppendSmall = 8;
 
-// Chunks of 16 keys are the unit in which attn_cache_fwd deals work.
-constexpr int kChunk = 16;
+// Chunks of 32 keys are the unit in which attn_cache_fwd deals work.
+constexpr int kChunk = 32;
+constexpr int kCacheWarps = 8;
 // CTAs of attn_cache_fwd (fewer for small steps): a fixed count, not the
 // device's SM count, so that the result does not depend on the device.
 constexpr int kCacheCtas = 152;
@@ -84,12 +85,14 @@ struct CacheFwdArgs {
   __nv_bfloat16* o;
   float* lse;
   float* part_o;     // [grid][2][rows][head_dim] partial outputs
+  float* stash;      // [grid][warps][rows][head_dim] parts that a warp finished early
   float2* part_ml;   // [grid][2][rows] running maximum (log2) and sum
   int4* part_meta;   // [grid][2] {kind bits, sequence, KV head, row block}
+  CUtensorMap tm_k, tm_v;   // the pools' rows in boxes of min(page_size, kChunk)
 };
 
 // Rows per work item of the variant that serves `rows` query rows per KV head.
-int cache_fwd_rows(int rows, bool e4m3);
+int cache_fwd_rows(int rows);
 cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int rows, int grid,
                              cudaStream_t st);
 

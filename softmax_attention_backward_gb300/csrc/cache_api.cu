@@ -69,14 +69,15 @@ int step_rows(const attn_cache_problem_t* p) {
 }
 
 struct Workspace {
-  size_t o, ml, meta, bytes;
+  size_t o, stash, ml, meta, bytes;
 };
 Workspace fwd_workspace(const attn_cache_problem_t* p) {
-  const size_t rows = 2 * static_cast<size_t>(kCacheCtas) *
-                      cache_fwd_rows(step_rows(p), p->cache_type == ATTN_CACHE_E4M3);
+  const size_t item = cache_fwd_rows(step_rows(p));
+  const size_t rows = 2 * static_cast<size_t>(kCacheCtas) * item;
   Workspace w;
   w.o = 0;
-  w.ml = rows * p->head_dim * sizeof(float);
+  w.stash = rows * p->head_dim * sizeof(float);
+  w.ml = w.stash + kCacheCtas * kCacheWarps * item * p->head_dim * sizeof(float);
   w.meta = w.ml + rows * sizeof(float2);
   w.bytes = w.meta + 2 * kCacheCtas * sizeof(int4);
   return w;
@@ -190,14 +191,21 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   a.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.stash = reinterpret_cast<float*>(ws + w.stash);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
   const int rows = step_rows(p);
-  const int item_rows = cache_fwd_rows(rows, e4m3);
+  const int item_rows = cache_fwd_rows(rows);
+  const int64_t pool_rows = static_cast<int64_t>(p->num_pages) * p->heads_kv * p->page_size;
+  const int box = p->page_size < kChunk ? p->page_size : kChunk;
+  if (!make_cache_rows_map(&a.tm_k, k_cache, pool_rows, p->head_dim, e4m3, box) ||
+      !make_cache_rows_map(&a.tm_v, v_cache, pool_rows, p->head_dim, e4m3, box))
+    return ATTN_ERR_CUDA;
   // the most chunks that the step can have; a CTA takes at least one per warp
   const double items = (static_cast<double>(p->tokens) * a.s.group / item_rows + p->num_seqs) * p->heads_kv;
   const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size + kChunk - 1) / kChunk);
-  const int grid = chunks / 6 + 1 < kCacheCtas ? static_cast<int>(chunks / 6) + 1 : kCacheCtas;
+  const double ctas = chunks / kCacheWarps + 1;
+  const int grid = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
   return status_of(launch_cache_fwd(a, p->head_dim, e4m3, rows, grid,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -5,43 +5,55 @@
 // Work.  An item is (sequence, KV head, block of up to ROWS query rows); the
 // rows of a KV head are its (new token, query head of the group) pairs, token
 // major, so the heads that share a key read it once.  An item's keys are cut
-// into chunks of 16.  All items' chunks, in one line, are dealt to the CTAs in
+// into chunks of 32.  All items' chunks, in one line, are dealt to the CTAs in
 // equal contiguous ranges, and a CTA's range to its warps, so every SM streams
 // the same number of bytes whatever the sequences' lengths are.  An item that
 // ends up in several warps is joined in shared memory, one that ends up in
 // several CTAs by a second kernel, in a fixed order.
 //
-// A warp runs on its own, without barriers: each thread copies with cp.async
-// exactly the 16-byte vectors that it will feed to the tensor cores
-// (mma.sync.m16n8k16) itself, into a ring of its own, in which neither bank
-// conflicts nor other threads' copies matter.  That works because the order of
-// the contracted index is free as long as both operands agree on it, and the
-// order of the output columns as long as the epilogue undoes it:
-//   S = Q K^T: the thread of column g (key g of 8) and quad index t takes the
-//     vector of dims [V t, V t + V) of its key (V = 8 bf16 or 16 codes) in each
-//     4 V dims, and Q is loaded in the same order;
-//   O = P V: it takes vector g of keys 2t, 2t+1, 2t+8, 2t+9; output column g of
-//     the j-th MMA is then dim V g + j, and a byte permutation pairs the keys.
-// Tensor-core work is a small part of what mma.sync can do (one 16-row tile
-// meets each key), so tcgen05, whose operands have to lie in shared memory
-// in a swizzled order, would add data movement and gain nothing here.
+// A warp runs on its own, without block barriers: its lane 0 has TMA copy the
+// keys and the values of a chunk, in turn, into the warp's ring, running ahead
+// across items, and its lanes feed them to the tensor cores straight from
+// 16-byte vectors.  The few query rows are the N side of mma.sync.m16n8k16, the
+// keys and then the output dims its M side, so that 8 rows fill an MMA:
+//   S^T = K Q^T: a thread of row g (of 8) and quad index t takes vector 4 j + t of
+//     its keys (V = 8 bf16 or 16 codes); Q is loaded in the same order, in
+//     which the contracted index is free;
+//   O^T = V^T P^T: movmatrix turns P over, and the thread takes vector g of the
+//     four keys that it holds probabilities of; rows g and g + 8 of the i-th MMA
+//     are dims V g + 2 i and V g + 2 i + 1, and a byte permutation pairs keys.
+// Row 2t of an 8-key tile is its key 2t, row 2t + 1 its key (2t) ^ 5: with the
+// 128-byte swizzle, in which the copies arrive, both reads are then free of
+// bank conflicts.  mma.sync has several times the rate that the HBM bound asks
+// for here, and tcgen05, whose smallest tile has 64 rows and whose operands
+// would have to be converted in shared memory, has nothing to gain.
 //
 // Softmax statistics, sums and O are fp32.  bf16 caches: S is exact products in
-// fp32, and with ROWS = 8 the unused half of the 16-row tile carries the
-// rounding residue of P (P = hi + lo in bf16), at no cost; with more rows P is
-// rounded to bf16 once, as in attn_fwd.  e4m3 caches: codes convert to fp16
-// exactly; q, scaled by a power of two per row, is exact in fp16 too, and P is
-// rounded to fp16 (2^-11).  The page scales multiply the logits of a chunk and
-// its P; O is kept relative to the largest value scale seen so far, so that P
-// times scale stays within fp16.
+// fp32; P goes in as hi + lo, two bf16 (2^-17).  e4m3 caches: codes convert to
+// fp16 exactly; q, scaled by a power of two per row, is exact in fp16 too, and
+// P is rounded to fp16 (2^-11).  The page scales multiply the logits of a page
+// and its P; O is kept relative to the largest value scale seen so far, so that
+// P times scale stays within fp16.
 #include "cache.cuh"
 
 namespace attn {
 namespace {
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-               : "memory");
+__device__ __forceinline__ void tma_load_2d(const CUtensorMap* m, uint64_t* bar, uint32_t dst,
+                                            int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+// One fp32 into shared memory.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// An arrival on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -79,44 +91,83 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   return h;
 }
+// 8 x 8 matrix of 16-bit elements over a warp (row = lane / 4, columns 2 (lane % 4)
+// and the next), transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// MT: 16-row tiles of an item.  HALF: only rows 0..7 of the one tile are used
-// (bf16), the others carry the residue of P.
-template <int D, bool E4M3, int MT, bool HALF>
+// NQ: tiles of 8 query rows of an item.
+template <int D, bool E4M3, int NQ>
 struct Cfg {
-  static constexpr int ROWS = HALF ? 8 : 16 * MT;
-  static constexpr int WARPS = (D == 128 && !(E4M3 && MT == 1)) ? (HALF ? 7 : 6) : 8;
+  static constexpr int ROWS = 8 * NQ;
+  static constexpr int WARPS = kCacheWarps;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int EL = E4M3 ? 1 : 2;
-  // 16-byte vectors a thread copies for the keys of a chunk; the values' are
-  // as many, of 8 bytes for e4m3 at D = 64
-  static constexpr int NK = kChunk * D * EL / 512;
-  static constexpr int NV = (E4M3 && D == 64) ? 4 : NK;
-  static constexpr int VB = (E4M3 && D == 64) ? 8 : 16;
-  static constexpr int STAGE = NK * 512 + NV * VB * 32;
-  static constexpr int SLOT_LD = D + 4;   // fp32 row stride of a partial result
-  static constexpr int SLOT = ROWS * SLOT_LD * 4;
-  static constexpr int BUDGET = 216 * 1024;
-  static constexpr int RING_MAX = (BUDGET / WARPS - SLOT) / STAGE;
-  static constexpr int STAGES = RING_MAX < 8 ? RING_MAX : 8;
-  // (a warp's last partial goes into its drained ring)
-  static constexpr int RING = STAGES * STAGE > SLOT ? STAGES * STAGE : SLOT;
-  static_assert(STAGES >= 2 && WARPS * (RING + SLOT) <= BUDGET, "shared memory");
-  static constexpr int SMEM = WARPS * (RING + SLOT);
+  static constexpr int RB = D * EL < 128 ? D * EL : 128;   // bytes of a row in a panel
+  static constexpr int PANELS = D * EL / RB;
+  static constexpr int SLOT = kChunk * D * EL;             // keys or values of a chunk
+  // 16 KB a warp, 128 KB an SM: 24 KB measured 3-7% slower, the copies queueing
+  // longer at HBM in front of what an item's start waits for
+  static constexpr int RING_MAX = 16384;
+  static constexpr int SLOTS = RING_MAX / SLOT < 8 ? RING_MAX / SLOT : 8;
+  static constexpr int PART_LD = D + 4;   // fp32 row stride of a partial result
+  static constexpr int PART = ROWS * PART_LD * 4;
+  // the ring; a warp's last partial goes into it once it is drained
+  static constexpr int RING = SLOTS * SLOT;
+  static_assert(RING >= PART && RING % 1024 == 0 && SLOTS >= 2, "ring");
+  static constexpr int SMEM = WARPS * RING + 1024;
 };
 
-// Chunks of an item of sequence q (all items of a sequence count the same, the
-// causal ones with fewer visible keys too), and its items per KV head.
-__device__ __forceinline__ int seq_chunks(const StepSeq& q) {
-  return q.len > 0 ? (q.len + kChunk - 1) / kChunk : 1;   // 1: an item always writes its rows
-}
+// Chunks that an item of sequence q counts for in the dealing (all items of a
+// sequence the same, the causal ones with fewer visible keys too), and its
+// items per KV head.  The two chunks more than it has stand for an item's own
+// cost, its query rows and outputs, and give items without keys a place: 64
+// decoding sequences of 15 to 8192 e4m3 keys took 58 us with one, 49 with two,
+// 51 with three (the slowest warps hold ten items of one chunk each).
+__device__ __forceinline__ int seq_chunks(const StepSeq& q) { return (q.len + kChunk - 1) / kChunk + 2; }
 template <int ROWS>
 __device__ __forceinline__ int seq_blocks(const CacheFwdArgs& a, const StepSeq& q) {
   return static_cast<int>((static_cast<int64_t>(q.m) * a.s.group + ROWS - 1) / ROWS);
+}
+
+// An item and the walk over the items in the order in which they are dealt:
+// sequence, KV head, row block.
+struct Item {
+  int n, h, rb;
+  int nb, nc;   // row blocks per KV head, chunks per item
+  StepSeq q;
+};
+template <int ROWS>
+__device__ __forceinline__ void item_load(const CacheFwdArgs& a, Item& it) {
+  it.q = step_seq(a.s, it.n);
+  it.nc = seq_chunks(it.q);
+  it.nb = seq_blocks<ROWS>(a, it.q);
+}
+// The next item; the caller knows that there is one.
+template <int ROWS>
+__device__ __forceinline__ void item_next(const CacheFwdArgs& a, Item& it) {
+  if (++it.rb < it.nb) return;
+  it.rb = 0;
+  if (++it.h < a.s.heads_kv) return;
+  it.h = 0;
+  do {
+    ++it.n;
+    item_load<ROWS>(a, it);
+  } while (it.nb == 0);
+}
+// Chunks of the item that some row of it sees.
+template <int ROWS>
+__device__ __forceinline__ int item_seen(const CacheFwdArgs& a, const Item& it) {
+  const int r_hi = min(it.q.m * a.s.group, (it.rb + 1) * ROWS) - 1;
+  const int vis = min(it.q.len, a.causal ? it.q.pos0 + r_hi / a.s.group + 1 : it.q.len);
+  return vis > 0 ? (vis + kChunk - 1) / kChunk : 0;
 }
 
 // A partial result: which item, and whether it holds the item's first / last
@@ -141,23 +192,40 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.f || l != l ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool E4M3, int MT, bool HALF>
-__global__ void __launch_bounds__(Cfg<D, E4M3, MT, HALF>::THREADS, 1)
-    cache_fwd_kernel(const CacheFwdArgs a) {
-  using C = Cfg<D, E4M3, MT, HALF>;
+template <int D, bool E4M3, int NQ>
+__global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
+    cache_fwd_kernel(const __grid_constant__ CacheFwdArgs a) {
+  using C = Cfg<D, E4M3, NQ>;
   constexpr int ROWS = C::ROWS;
-  constexpr int NT = D / 8;                 // 8-column output tiles
+  constexpr int MT = D / 16;                // 16-dim output tiles
   constexpr int VN = E4M3 ? (D == 64 ? 8 : 16) : 8;   // dims of a value vector
-  constexpr int NH = D / (8 * VN);          // value vectors per key and thread
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
   __shared__ int64_t sh_pre[C::THREADS + 1];
   __shared__ int64_t sh_warp[C::WARPS];
-  __shared__ float4 sh_scale[C::WARPS][C::STAGES];    // {k scale, v scale, valid keys, -}
+  __shared__ uint64_t bar_full[C::WARPS][C::SLOTS];
+  __shared__ float4 sh_scale[C::WARPS][8];   // {k, v scale} of both halves of a chunk
+  __shared__ int sh_bad[C::WARPS][8];        // halves (bits) without a page
   __shared__ PartMeta sh_meta[C::WARPS][2];
   __shared__ float2 sh_ml[C::WARPS][2][ROWS];
+  __shared__ const float* sh_part[C::WARPS][2];
+  __shared__ int sh_ld[C::WARPS][2];
+  __shared__ int abort_flag;
 
   const CacheStep& s = a.s;
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
+  AbortCtx ac{&abort_flag, s.err};
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    // two arrivals: the bytes of TMA, and the scales (or a plain one)
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&bar_full[warp][i], 2);
+    fence_mbar_init();
+    if (warp == 0) {
+      tma_prefetch_desc(&a.tm_k);
+      tma_prefetch_desc(&a.tm_v);
+    }
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- every thread sums a slice of the sequences, a block scan joins them ----
@@ -194,10 +262,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, MT, HALF>::THREADS, 1)
   const int64_t f0 = cta0 + (cta1 - cta0) * warp / C::WARPS;
   const int64_t f1 = cta0 + (cta1 - cta0) * (warp + 1) / C::WARPS;
 
-  uint8_t* ring = smem + warp * (C::RING + C::SLOT);
-  float* slot_a = reinterpret_cast<float*>(ring + C::RING);   // a part that began before f0
-  float* slot_b = reinterpret_cast<float*>(ring);             // one that goes on past f1
+  uint8_t* ring = smem + warp * C::RING;
   const uint32_t ring_u = smem_u32(ring);
+  bool ok = true;
 
   if (f0 < f1) {
     // ---- the item of chunk f0 ----
@@ -210,407 +277,486 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, MT, HALF>::THREADS, 1)
       }
       sl = lo;
     }
-    int n = sl * per;
+    Item it;
+    it.n = sl * per;
+    it.rb = 0;
     int64_t base = sh_pre[sl];
-    StepSeq q = step_seq(s, n);
-    int nc = seq_chunks(q), nb = seq_blocks<ROWS>(a, q);
+    item_load<ROWS>(a, it);
     while (true) {
-      const int64_t w = static_cast<int64_t>(s.heads_kv) * nb * nc;
+      const int64_t w = static_cast<int64_t>(s.heads_kv) * it.nb * it.nc;
       if (base + w > f0) break;
       base += w;
-      ++n;
-      q = step_seq(s, n);
-      nc = seq_chunks(q);
-      nb = seq_blocks<ROWS>(a, q);
+      ++it.n;
+      item_load<ROWS>(a, it);
     }
-    int64_t off = f0 - base;
-    int h = static_cast<int>(off / (static_cast<int64_t>(nb) * nc));
-    off -= static_cast<int64_t>(h) * nb * nc;
-    int rb = static_cast<int>(off / nc);
-    int c0 = static_cast<int>(off - static_cast<int64_t>(rb) * nc);
-    int64_t left = f1 - f0;
+    const int64_t off = f0 - base;
+    int c0;
+    if (off >> 32) {
+      const int64_t item = off / it.nc;
+      c0 = static_cast<int>(off - item * it.nc);
+      it.h = static_cast<int>(item / it.nb);
+      it.rb = static_cast<int>(item - static_cast<int64_t>(it.h) * it.nb);
+    } else {   // short divisions
+      const uint32_t item = static_cast<uint32_t>(off) / it.nc;
+      c0 = static_cast<int>(static_cast<uint32_t>(off) - item * it.nc);
+      it.h = static_cast<int>(item / it.nb);
+      it.rb = static_cast<int>(item) - it.h * it.nb;
+    }
+    int left = static_cast<int>(min(f1 - f0, static_cast<int64_t>(0x7fffffff)));
+
+    // ---- the copies, which run ahead of the computation, across items ----
+    // lane l holds the page of column pg0 + l of item `cp`, and that of column l of
+    // the next sequence
+    Item cp = it;
+    int cp_c = c0, cp_left = left;                 // next chunk; the warp's chunks from the item on
+    int cp_span = min(cp.nc - c0, left);           // those of the item
+    int cp_end = min(c0 + cp_span, item_seen<ROWS>(a, cp));   // end of its chunks to copy
+    int pg0 = -1, pid = -1, npid = -1, cp_half = 0;       // cp_half: halves issued so far
+    auto fetch_pages = [&](int col, bool ahead) {
+      const int cc = col + lane;
+      pg0 = col;
+      if (!ahead) pid = cc < s.max_pages ? __ldg(s.table + static_cast<int64_t>(cp.n) * s.max_pages + cc) : -1;
+      else pid = npid;
+      if (col == 0)
+        npid = cp.n + 1 < s.num_seqs && lane < s.max_pages
+                   ? __ldg(s.table + static_cast<int64_t>(cp.n + 1) * s.max_pages + lane)
+                   : -1;
+      if (cc > (cp.q.len - 1) >> s.ps_shift) {
+        pid = -1;
+      } else if (pid < 0 || pid >= s.num_pages) {
+        pid = -1;
+        if (s.err) atomicOr(s.err, ATTN_DEVERR_INDEX_RANGE);
+      }
+    };
+    // A sequence's query rows towards L2 (the first 32 KB), well before their loads
+    auto prefetch_q = [&]() {
+      const int words = min(cp.q.m * s.heads_q * (D / 64), 256);   // of 128 bytes
+      for (int i = lane; i < words; i += 32) {
+        const int tok = i / (s.heads_q * (D / 64));
+        const __nv_bfloat16* p = a.q + (cp.q.t0 + tok) * a.q_stride + (i - tok * s.heads_q * (D / 64)) * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+      }
+    };
+    // Half u: the keys (even) or values (odd) of a chunk.  False when all are issued.
+    bool ahead = false;   // npid is of the sequence that begins
+    int pg_seq = -2;      // the sequence before that of npid
+    auto issue = [&]() -> bool {
+      if (!(cp_half & 1)) {
+        while (cp_c >= cp_end) {   // on to the next item
+          const int n_old = cp.n;
+          cp_left -= cp_span;
+          if (cp_left <= 0) return false;
+          item_next<ROWS>(a, cp);
+          cp_c = 0;
+          cp_span = min(cp.nc, cp_left);
+          cp_end = min(cp_span, item_seen<ROWS>(a, cp));
+          if (cp.n != n_old) {
+            prefetch_q();
+            ahead = cp.n == n_old + 1 && pg_seq == n_old;
+            pg0 = -1;
+          } else if (pg0 != 0) {
+            pg0 = -1;
+          }
+        }
+      }
+      const int col0 = (cp_c * kChunk) >> s.ps_shift, col1 = (cp_c * kChunk + 16) >> s.ps_shift;
+      if (pg0 < 0 || col1 >= pg0 + 32) {
+        fetch_pages(col0, ahead && col0 == 0);
+        ahead = false;
+        if (col0 == 0) pg_seq = cp.n;
+      }
+      const int p0 = __shfl_sync(0xffffffffu, pid, col0 - pg0);
+      const int p1 = __shfl_sync(0xffffffffu, pid, col1 - pg0);
+      const bool values = cp_half & 1;
+      if (lane == 0) {
+        const uint32_t at = static_cast<uint32_t>(cp_half) % C::SLOTS;
+        uint64_t* bar = &bar_full[warp][at];
+        const int ix = (cp_half >> 1) & 7;
+        if (!values) sh_bad[warp][ix] = (p0 < 0 ? 1 : 0) | (p1 < 0 ? 2 : 0);
+        if (E4M3 && !values) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int page = b ? p1 : p0;
+            float2* sc = reinterpret_cast<float2*>(&sh_scale[warp][ix]) + b;
+            if (page >= 0) {
+              const int64_t i = static_cast<int64_t>(page) * s.heads_kv + cp.h;
+              cp_async4(smem_u32(sc), a.k_scale + i);
+              cp_async4(smem_u32(sc) + 4, a.v_scale + i);
+            } else {
+              *sc = make_float2(0.f, 0.f);
+            }
+          }
+          cp_async_arrive(bar);
+        } else {
+          mbar_arrive(bar);
+        }
+        const uint32_t dst = ring_u + at * C::SLOT;
+        const CUtensorMap* m = values ? &a.tm_v : &a.tm_k;
+        const int in_page = (cp_c * kChunk) & ((1 << s.ps_shift) - 1);
+        const int y0 = ((p0 * s.heads_kv + cp.h) << s.ps_shift) + in_page;
+        if (s.ps_shift > 4) {   // one box of 32 rows
+          mbar_arrive_expect_tx(bar, p0 < 0 ? 0 : C::SLOT);
+          if (p0 >= 0)
+            for (int pn = 0; pn < C::PANELS; ++pn)
+              tma_load_2d(m, bar, dst + pn * kChunk * 128, pn * 64, y0);
+        } else {
+          const int y1 = (p1 * s.heads_kv + cp.h) << 4;
+          mbar_arrive_expect_tx(bar, (p0 < 0 ? 0 : C::SLOT / 2) + (p1 < 0 ? 0 : C::SLOT / 2));
+          for (int pn = 0; pn < C::PANELS; ++pn) {
+            if (p0 >= 0) tma_load_2d(m, bar, dst + pn * kChunk * 128, pn * 64, y0);
+            if (p1 >= 0) tma_load_2d(m, bar, dst + pn * kChunk * 128 + 16 * C::RB, pn * 64, y1);
+          }
+        }
+      }
+      if (values) ++cp_c;
+      ++cp_half;
+      return true;
+    };
+    for (int u = 0; u < C::SLOTS; ++u)
+      if (!issue()) break;
+    __syncwarp();
+
+    // The raw words of row g of the item's tiles: vector 4 j + t of 8 dims; e4m3: half of
+    // vector 4 (j / 2) + t of 16 dims.
+    uint32_t qw[NQ][D / 8];
+    auto load_q = [&](const Item& x) {
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        const int r = x.rb * ROWS + nq * 8 + g, i = r / s.group;
+        const bool in = r < x.q.m * s.group;
+        const __nv_bfloat16* src = a.q + (x.q.t0 + (in ? i : 0)) * a.q_stride +
+                                   (x.h * s.group + (in ? r - i * s.group : 0)) * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (in)
+            v = *reinterpret_cast<const uint4*>(src + (E4M3 ? (j >> 1) * 64 + t * 16 + (j & 1) * 8
+                                                            : j * 32 + t * 8));
+          qw[nq][4 * j] = v.x, qw[nq][4 * j + 1] = v.y, qw[nq][4 * j + 2] = v.z, qw[nq][4 * j + 3] = v.w;
+        }
+      }
+    };
+    load_q(it);
+    int half = 0;   // halves computed so far
 
     while (true) {
-      const int c1 = static_cast<int>(min(static_cast<int64_t>(nc), c0 + left));   // chunks [c0, c1)
-      // last chunk that any of the block's rows sees
+      const StepSeq q = it.q;
+      const int nc = it.nc, n = it.n, h = it.h, rb = it.rb;
+      const int c1 = min(nc, c0 + left);   // chunks [c0, c1), of which those below ce are seen
+      const int ce = min(c1, item_seen<ROWS>(a, it));
       const int rows_all = q.m * s.group;
-      const int r_hi = min(rows_all, (rb + 1) * ROWS) - 1;
-      const int vis_hi = min(q.len, a.causal ? q.pos0 + r_hi / s.group + 1 : q.len);
-      const int ce = min(c1, vis_hi > 0 ? (vis_hi + kChunk - 1) / kChunk : 0);   // exclusive
 
-      // ---- page look-ahead: lane l holds the page of column pg0 + l ----
-      int pg0 = -1, pid = -1;
-      float pks = 1.f, pvs = 1.f;
-      const int32_t* trow = s.table + static_cast<int64_t>(n) * s.max_pages;
-      auto fetch_pages = [&](int col) {
-        pg0 = col;
-        const int cc = col + lane;
-        const int last = (q.len - 1) >> s.ps_shift;
-        pid = cc <= last ? __ldg(trow + cc) : 0;
-        if (pid < 0 || pid >= s.num_pages) {
-          pid = -1;
-          if (s.err) atomicOr(s.err, ATTN_DEVERR_INDEX_RANGE);
+      // ---- the block's query rows: B fragments of row g, statistics of rows 2t and 2t + 1 ----
+      uint32_t qf[NQ][D / 8];        // [2 step], [2 step + 1]: k low, k high
+      float qs[NQ][2];               // logit factors
+      int vis[NQ][2];                // keys that they see
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = rb * ROWS + nq * 8 + 2 * t + e;
+          vis[nq][e] = r >= rows_all ? 0 : min(q.len, a.causal ? q.pos0 + r / s.group + 1 : q.len);
+          qs[nq][e] = a.scale_log2;
         }
+        uint32_t(&w)[D / 8] = qw[nq];
         if constexpr (E4M3) {
-          if (cc <= last && pid >= 0) {
-            pks = __ldg(a.k_scale + static_cast<int64_t>(pid) * s.heads_kv + h);
-            pvs = __ldg(a.v_scale + static_cast<int64_t>(pid) * s.heads_kv + h);
-          }
+          float amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
+                                     fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // q 2^(8 - k), k the exponent of the row's largest element: below
+          // 512, exact in fp16 down to 2^-32 of it and then within 2^-33 of it
+          const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+          const float f = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
+          const float back = __uint_as_float(static_cast<uint32_t>(k - 8 + 127) << 23);
+          qs[nq][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
+          qs[nq][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            w[j] = pack_f16(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
         }
-      };
-      auto issue = [&](int c, int st) {
-        const int col = (c * kChunk) >> s.ps_shift;
-        if (pg0 < 0 || col >= pg0 + 32) fetch_pages(col);
-        const int page = __shfl_sync(0xffffffffu, pid, col - pg0);
-        int valid = min(q.len - c * kChunk, kChunk);
-        if (page < 0) valid = 0;
-        const float kf = E4M3 ? __shfl_sync(0xffffffffu, pks, col - pg0) : 1.f;
-        const float vf = E4M3 ? __shfl_sync(0xffffffffu, pvs, col - pg0) : 1.f;
-        if (lane == 0) sh_scale[warp][st] = make_float4(kf, vf, __int_as_float(valid), 0.f);
-        const int64_t row = ((static_cast<int64_t>(max(page, 0)) * s.heads_kv + h) << s.ps_shift) +
-                            ((c * kChunk) & ((1 << s.ps_shift) - 1));
-        const uint8_t* kp = static_cast<const uint8_t*>(a.k_cache) + row * (D * C::EL);
-        const uint8_t* vp = static_cast<const uint8_t*>(a.v_cache) + row * (D * C::EL);
-        const uint32_t dst = ring_u + st * C::STAGE;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int j = 0; j < C::NK / 2; ++j) {
-            const int key = x * 8 + g;
-            cp_async16(dst + ((x * (C::NK / 2) + j) * 32 + lane) * 16,
-                       kp + key * (D * C::EL) + j * 64 + t * 16, key < valid ? 16u : 0u);
-          }
-        const uint32_t dv = dst + C::NK * 512;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int j = 0; j < C::NV / 4; ++j) {
-            const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-            const uint8_t* src = vp + key * (D * C::EL) + j * 128 + g * C::VB;
-            if constexpr (C::VB == 16)
-              cp_async16(dv + ((x * (C::NV / 4) + j) * 32 + lane) * 16, src, key < valid ? 16u : 0u);
-            else
-              cp_async8(dv + (x * 32 + lane) * 8, src, key < valid ? 8u : 0u);
-          }
-      };
-#pragma unroll
-      for (int i = 0; i < C::STAGES - 1; ++i) {
-        if (c0 + i < ce) issue(c0 + i, i);
-        cp_async_commit();
+        for (int j = 0; j < D / 8; ++j) qf[nq][j] = w[j];
+      }
+      left -= c1 - c0;
+      const bool last_part = left <= 0;
+      Item nx = it;
+      if (!last_part) {   // the next item's rows arrive while this one is computed
+        item_next<ROWS>(a, nx);
+        load_q(nx);
       }
 
-      // ---- the block's query rows ----
-      uint32_t qf[MT][D / 16][4];
-      float qs[MT][2];          // logit factor of the thread's rows
-      int vis[MT][2];           // keys its rows see
+      float acc[NQ][MT][4];
+      float mrun[NQ][2], lrun[NQ][2], vref = 0.f, vinv = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int r = rb * ROWS + mt * 16 + hh * 8 + g;
-          const bool ok = r < rows_all && !(HALF && hh == 1);
-          const int i = r / s.group;
-          const __nv_bfloat16* src =
-              a.q + (q.t0 + (ok ? i : 0)) * a.q_stride + (h * s.group + (ok ? r - i * s.group : 0)) * D;
-          vis[mt][hh] = !ok ? 0 : min(q.len, a.causal ? q.pos0 + i + 1 : q.len);
-          qs[mt][hh] = a.scale_log2;
-          if constexpr (!E4M3) {
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              if (ok) w = *reinterpret_cast<const uint4*>(src + j * 32 + t * 8);
-              qf[mt][2 * j][hh] = w.x;
-              qf[mt][2 * j][2 + hh] = w.y;
-              qf[mt][2 * j + 1][hh] = w.z;
-              qf[mt][2 * j + 1][2 + hh] = w.w;
-            }
-          } else {
-            uint32_t w[D / 8];
-            float amax = 0.f;
+          for (int e = 0; e < 4; ++e) acc[nq][i][e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {   // 16 dims: two vectors per 64 dims
-              uint4 x = make_uint4(0u, 0u, 0u, 0u);
-              if (ok) x = *reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
-              w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
-                                       fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // q 2^(8 - k), k the exponent of the row's largest element: below
-            // 512, exact in fp16 down to 2^-32 of it and then within 2^-33 of it
-            const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-            const float f = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
-            qs[mt][hh] *= __uint_as_float(static_cast<uint32_t>(k - 8 + 127) << 23);
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              w[j] = pack_f16(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              qf[mt][j][hh] = w[2 * j];
-              qf[mt][j][2 + hh] = w[2 * j + 1];
-            }
-          }
+        for (int e = 0; e < 2; ++e) {
+          mrun[nq][e] = -INFINITY;
+          lrun[nq][e] = 0.f;
         }
-
-      float acc[MT][NT][4];
-      float mrun[MT][2], lrun[MT][2], vref = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][i][e] = 0.f;
-        mrun[mt][0] = mrun[mt][1] = -INFINITY;
-        lrun[mt][0] = lrun[mt][1] = 0.f;
       }
 
       // ---- the chunks ----
-      int st = 0;
       for (int c = c0; c < ce; ++c) {
-        {
-          const int nx = c + C::STAGES - 1;
-          int sx = st + C::STAGES - 1;
-          if (sx >= C::STAGES) sx -= C::STAGES;
-          if (nx < ce) issue(nx, sx);
-          cp_async_commit();
+        uint32_t at = static_cast<uint32_t>(half) % C::SLOTS;
+        if (!mbar_wait_w(&bar_full[warp][at], (static_cast<uint32_t>(half) / C::SLOTS) & 1, ac)) {
+          ok = false;
+          break;
         }
-        cp_async_wait<C::STAGES - 1>();
-        __syncwarp();
-        const float4 sc = sh_scale[warp][st];
-        const int kend = c * kChunk + __float_as_int(sc.z);   // keys of the chunk end here
-        const uint32_t src = ring_u + st * C::STAGE;
+        uint32_t src = ring_u + at * C::SLOT;
+        const float4 sc = sh_scale[warp][(half >> 1) & 7];
+        const int bad = sh_bad[warp][(half >> 1) & 7];
+        const int key0 = c * kChunk;
 
-        float x[MT][2][4];
+        // S^T, tiles of 16 keys; row 2t of 8 is key 2t, row 2t + 1 key (2t) ^ 5
+        float x[2][NQ][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) x[mt][nq][e] = 0.f;
+        const int krow = (g & 1) ? (g - 1) ^ 5 : g;
 #pragma unroll
-        for (int j = 0; j < C::NK / 2; ++j)
+        for (int j = 0; j < D * C::EL / 64; ++j)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint4 w = lds128(src + ((nt * (C::NK / 2) + j) * 32 + lane) * 16);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t ww[2][4];
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+              const int row = mt * 16 + hi * 8 + krow;
+              uint32_t off;
+              if constexpr (C::RB == 128)
+                off = (j >> 1) * (kChunk * 128) + row * 128 + ((((j & 1) * 4 + t) ^ krow) << 4);
+              else
+                off = row * 64 + ((t ^ ((krow >> 1) & 3)) << 4);
+              const uint4 w = lds128(src + off);
+              ww[hi][0] = w.x, ww[hi][1] = w.y, ww[hi][2] = w.z, ww[hi][3] = w.w;
+            }
             if constexpr (E4M3) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t b0 = e4m3x2_f16x2(ww[i]), b1 = e4m3x2_f16x2(ww[i] >> 16);
+                const uint32_t a0 = e4m3x2_f16x2(ww[0][i]), a2 = e4m3x2_f16x2(ww[0][i] >> 16);
+                const uint32_t a1 = e4m3x2_f16x2(ww[1][i]), a3 = e4m3x2_f16x2(ww[1][i] >> 16);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  const uint32_t(&q4)[4] = qf[mt][4 * j + i];
-                  mma16816<true>(x[mt][nt], q4[0], q4[1], q4[2], q4[3], b0, b1);
-                }
+                for (int nq = 0; nq < NQ; ++nq)
+                  mma16816<true>(x[mt][nq], a0, a1, a2, a3, qf[nq][8 * j + 2 * i], qf[nq][8 * j + 2 * i + 1]);
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  const uint32_t(&q4)[4] = qf[mt][2 * j + i];
-                  mma16816<false>(x[mt][nt], q4[0], q4[1], q4[2], q4[3], ww[2 * i], ww[2 * i + 1]);
-                }
+                for (int nq = 0; nq < NQ; ++nq)
+                  mma16816<false>(x[mt][nq], ww[0][2 * i], ww[1][2 * i], ww[0][2 * i + 1], ww[1][2 * i + 1],
+                                  qf[nq][4 * j + 2 * i], qf[nq][4 * j + 2 * i + 1]);
             }
           }
+        __syncwarp();
+        issue();
 
-        // values' factor relative to the largest value scale so far
-        float vratio = 1.f, vfac = 1.f;
+        // values' factors relative to the largest value scale so far
+        float vratio = 1.f, vf0 = 1.f, vf1 = 1.f;
         if constexpr (E4M3) {
-          const bool any = __float_as_int(sc.z) > 0;
-          const float vs = any ? sc.y : 0.f;
-          if (vs > vref) {
-            vratio = vref / vs;
-            vref = vs;
-          } else {
-            vfac = vref > 0.f ? vs / vref : 0.f;
+          const float top = fmaxf(sc.y, sc.w);
+          if (top > vref) {
+            vratio = vref / top;
+            vref = top;
+            vinv = 1.f / top;
           }
+          vf0 = sc.y * vinv;
+          vf1 = sc.w * vinv;
         }
-        uint32_t pa[MT][4];
+        constexpr int LO = E4M3 ? 1 : 2;   // P itself, or its hi and lo parts
+        uint32_t pb[2][NQ][LO][2];         // B fragments of P^T: 16 keys each
         bool grow = vratio != 1.f;
-        float alpha[MT][2];
+        float alpha[NQ][2];
+        const bool dirty = bad != 0 || key0 + kChunk > q.len;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nq = 0; nq < NQ; ++nq) {
+          float p[2][2][2];   // [row][16-key tile][lower or upper 8 keys]
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            alpha[mt][hh] = 1.f;
-            if (HALF && hh == 1) continue;
-            const float f = E4M3 ? qs[mt][hh] * sc.x : qs[mt][hh];
-            const int lim = min(vis[mt][hh], kend) - c * kChunk - 2 * t;
-            float y[4];
+          for (int e = 0; e < 2; ++e) {
+            const float f0 = E4M3 ? qs[nq][e] * sc.x : qs[nq][e], f1 = E4M3 ? qs[nq][e] * sc.z : qs[nq][e];
+            float(&y)[2][2] = p[e];
+            y[0][0] = x[0][nq][e] * f0;
+            y[0][1] = x[0][nq][2 + e] * f0;
+            y[1][0] = x[1][nq][e] * f1;
+            y[1][1] = x[1][nq][2 + e] * f1;
+            if (dirty || key0 + kChunk > vis[nq][e]) {
+              const int lim = vis[nq][e] - key0;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float v = x[mt][nt][2 * hh + e] * f;
-                y[2 * nt + e] = nt * 8 + e < lim ? v : -INFINITY;
-              }
-            float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(mrun[mt][hh], mx);
+              for (int k = 0; k < 4; ++k)
+                if (k * 8 + krow >= lim || (bad >> (k >> 1) & 1)) y[k >> 1][k & 1] = -INFINITY;
+            }
+            float mx = fmaxf(fmax3(y[0][0], y[0][1], y[1][0]), y[1][1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(mrun[nq][e], mx);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            alpha[mt][hh] = ex2(mrun[mt][hh] - ms);   // 0 while nothing has been seen
-            grow |= mn > mrun[mt][hh];
-            mrun[mt][hh] = mn;
-            float p[4], sum;
+            alpha[nq][e] = ex2(mrun[nq][e] - ms);   // 0 while nothing has been seen
+            grow |= mn > mrun[nq][e];
+            mrun[nq][e] = mn;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ex2(y[e] - ms);
-            sum = (p[0] + p[1]) + (p[2] + p[3]);
-            lrun[mt][hh] = lrun[mt][hh] * alpha[mt][hh] + sum;
-            if constexpr (E4M3) {
-              pa[mt][hh] = pack_f16(p[0] * vfac, p[1] * vfac);
-              pa[mt][2 + hh] = pack_f16(p[2] * vfac, p[3] * vfac);
-            } else {
-              pa[mt][hh] = pack_bf16(p[0], p[1]);
-              pa[mt][2 + hh] = pack_bf16(p[2], p[3]);
-              if constexpr (HALF) {   // the residues, as rows 8..15
-                pa[mt][1] = pack_bf16(p[0] - __uint_as_float(pa[mt][0] << 16),
-                                      p[1] - __uint_as_float(pa[mt][0] & 0xffff0000u));
-                pa[mt][3] = pack_bf16(p[2] - __uint_as_float(pa[mt][2] << 16),
-                                      p[3] - __uint_as_float(pa[mt][2] & 0xffff0000u));
-              }
-            }
+            for (int k = 0; k < 4; ++k) y[k >> 1][k & 1] = ex2(y[k >> 1][k & 1] - ms);
+            lrun[nq][e] = lrun[nq][e] * alpha[nq][e] + ((y[0][0] + y[0][1]) + (y[1][0] + y[1][1]));
           }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const float a0 = alpha[mt][0] * vratio, a1 = (HALF ? alpha[mt][0] : alpha[mt][1]) * vratio;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              acc[mt][i][0] *= a0;
-              acc[mt][i][1] *= a0;
-              acc[mt][i][2] *= a1;
-              acc[mt][i][3] *= a1;
-            }
-          }
-        }
-
-        // O += P V: keys (2t, 2t+1) are the low and high half of b0, (2t+8, 2t+9) of b1
-        const uint32_t sv = src + C::NK * 512;
-#pragma unroll
-        for (int j = 0; j < NH; ++j) {
-          uint32_t vw[4][VN * C::EL / 4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if constexpr (C::VB == 16) {
-              const uint4 w = lds128(sv + ((k * NH + j) * 32 + lane) * 16);
-              vw[k][0] = w.x, vw[k][1] = w.y, vw[k][2] = w.z, vw[k][3] = w.w;
+            const float p0 = p[0][k >> 1][k & 1], p1 = p[1][k >> 1][k & 1];
+            if constexpr (E4M3) {
+              const float vf = k < 2 ? vf0 : vf1;
+              pb[k >> 1][nq][0][k & 1] = transpose8x8(pack_f16(p0 * vf, p1 * vf));
             } else {
-              const uint2 w = lds64(sv + (k * 32 + lane) * 8);
-              vw[k][0] = w.x, vw[k][1] = w.y;
+              const uint32_t hi = pack_bf16(p0, p1);
+              const uint32_t lo = pack_bf16(p0 - __uint_as_float(hi << 16),
+                                            p1 - __uint_as_float(hi & 0xffff0000u));
+              pb[k >> 1][nq][0][k & 1] = transpose8x8(hi);
+              pb[k >> 1][nq][LO - 1][k & 1] = transpose8x8(lo);
             }
           }
-          if constexpr (E4M3) {
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) {
+            const float a0 = alpha[nq][0] * vratio, a1 = alpha[nq][1] * vratio;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              acc[nq][i][0] *= a0;
+              acc[nq][i][1] *= a1;
+              acc[nq][i][2] *= a0;
+              acc[nq][i][3] *= a1;
+            }
+          }
+        }
+
+        // O^T += V^T P^T: keys (2t, (2t)^5) are the low and high half of a0 and a1, + 8 of a2 and a3
+        ++half;
+        at = static_cast<uint32_t>(half) % C::SLOTS;
+        if (!mbar_wait_w(&bar_full[warp][at], (static_cast<uint32_t>(half) / C::SLOTS) & 1, ac)) {
+          ok = false;
+          break;
+        }
+        src = ring_u + at * C::SLOT;
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+          for (int j = 0; j < C::PANELS; ++j) {
+            uint32_t vw[4][VN * C::EL / 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = 8 * (k >> 1) + ((k & 1) ? (2 * t) ^ 5 : 2 * t);
+              if constexpr (C::RB == 128) {
+                const uint4 w = lds128(src + j * (kChunk * 128) + (i2 * 16 + row) * 128 + ((g ^ (row & 7)) << 4));
+                vw[k][0] = w.x, vw[k][1] = w.y, vw[k][2] = w.z, vw[k][3] = w.w;
+              } else {
+                const uint2 w = lds64(src + (i2 * 16 + row) * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                vw[k][0] = w.x, vw[k][1] = w.y;
+              }
+              // values that no key has must not meet P = 0: they may be NaN
+              if (dirty && (key0 + i2 * 16 + row >= q.len || (bad >> i2 & 1)))
+#pragma unroll
+                for (int i = 0; i < VN * C::EL / 4; ++i) vw[k][i] = 0u;
+            }
 #pragma unroll
             for (int i = 0; i < VN / 2; ++i) {   // dims 2i, 2i+1
-              const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-              const uint32_t b0 = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel);
-              const uint32_t b1 = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
-              const uint32_t e0 = e4m3x2_f16x2(b0), o0 = e4m3x2_f16x2(b0 >> 16);
-              const uint32_t e1 = e4m3x2_f16x2(b1), o1 = e4m3x2_f16x2(b1 >> 16);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<true>(acc[mt][j * VN + 2 * i], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
-                mma16816<true>(acc[mt][j * VN + 2 * i + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], o0, o1);
+              uint32_t a0, a1, a2, a3;
+              if constexpr (E4M3) {
+                const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                const uint32_t b0 = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel);
+                const uint32_t b1 = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
+                a0 = e4m3x2_f16x2(b0), a1 = e4m3x2_f16x2(b0 >> 16);
+                a2 = e4m3x2_f16x2(b1), a3 = e4m3x2_f16x2(b1 >> 16);
+              } else {
+                a0 = __byte_perm(vw[0][i], vw[1][i], 0x5410u);
+                a1 = __byte_perm(vw[0][i], vw[1][i], 0x7632u);
+                a2 = __byte_perm(vw[2][i], vw[3][i], 0x5410u);
+                a3 = __byte_perm(vw[2][i], vw[3][i], 0x7632u);
               }
-            }
-          } else {
 #pragma unroll
-            for (int i = 0; i < VN / 2; ++i) {
-              const uint32_t e0 = __byte_perm(vw[0][i], vw[1][i], 0x5410u);
-              const uint32_t o0 = __byte_perm(vw[0][i], vw[1][i], 0x7632u);
-              const uint32_t e1 = __byte_perm(vw[2][i], vw[3][i], 0x5410u);
-              const uint32_t o1 = __byte_perm(vw[2][i], vw[3][i], 0x7632u);
+              for (int lo = 0; lo < LO; ++lo)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<false>(acc[mt][j * VN + 2 * i], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
-                mma16816<false>(acc[mt][j * VN + 2 * i + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], o0, o1);
-              }
+                for (int nq = 0; nq < NQ; ++nq)
+                  mma16816<E4M3>(acc[nq][j * (VN / 2) + i], a0, a1, a2, a3, pb[i2][nq][lo][0],
+                                 pb[i2][nq][lo][1]);
             }
           }
-        }
-        if (++st == C::STAGES) st = 0;
+        ++half;
+        __syncwarp();
+        issue();
       }
-      cp_async_wait<0>();
-      __syncwarp();
+      if (!ok) {   // a wait ran out: the copies in flight get a moment to land, then the warp leaves
+        for (int u = half; u < cp_half; ++u) {
+          const uint32_t bar = smem_u32(&bar_full[warp][static_cast<uint32_t>(u) % C::SLOTS]);
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try_wait(bar, (static_cast<uint32_t>(u) / C::SLOTS) & 1) &&
+                 globaltimer() - t0 < 10000000ull) {
+          }
+        }
+        break;
+      }
 
       // ---- the end of the item's part ----
-      const bool begins = c0 == 0, ends = c1 == nc;
-      const bool part_b = begins && !ends;     // goes on past f1: the warp's last part
-      float* slot = part_b ? slot_b : slot_a;
+      const bool begins = c0 == 0, ends = c1 == nc, whole = begins && ends;
+      const int which = begins ? 1 : 0;   // 1: goes on past f1, 0: began before f0
+      // the warp's last part may lie in its drained ring
+      float* part = last_part ? reinterpret_cast<float*>(ring)
+                              : a.stash + (static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * ROWS * D;
+      const int ld = last_part ? C::PART_LD : D;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-        for (int hh = 0; hh < (HALF ? 1 : 2); ++hh) {
-          float l = lrun[mt][hh];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          const int rl = mt * 16 + hh * 8 + g, r = rb * ROWS + rl;
-          const float vf = E4M3 ? vref : 1.f;
-          // columns 2t and 2t+1 of the VN MMAs of vector j: dims (8 j + 2t + col) VN + i
+        for (int e = 0; e < 2; ++e) {
+          float l = lrun[nq][e];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const int rl = nq * 8 + 2 * t + e, r = rb * ROWS + rl, tok = r / s.group;
+          const int hd = h * s.group + (r - tok * s.group);
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          // dims VN (8 j + g) + 2 i (c0, c1 of MMA i of panel j) and + 2 i + 1 (c2, c3)
 #pragma unroll
-          for (int j = 0; j < NH; ++j)
+          for (int j = 0; j < C::PANELS; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int i = 0; i < VN; i += 8) {
+              float o[8];
 #pragma unroll
-              for (int i = 0; i < VN; i += 8) {
-                float o[8];
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                  const float(&ac)[4] = acc[mt][j * VN + i + z];
-                  o[z] = (HALF ? ac[e] + ac[2 + e] : ac[2 * hh + e]) * vf;
-                }
-                const int d = (8 * j + 2 * t + e) * VN + i;
-                const float4 lo = make_float4(o[0], o[1], o[2], o[3]);
-                const float4 hi = make_float4(o[4], o[5], o[6], o[7]);
-                if (begins && ends) {
-                  if (r < rows_all) {
-                    const int tok = r / s.group;
-                    store_row8<D>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + h * s.group +
-                                         (r - tok * s.group)) * D + d,
-                                  lo, hi, l > 0.f || l != l ? 1.f / l : 0.f);
-                  }
-                } else {
-                  float4* dst = reinterpret_cast<float4*>(slot + rl * C::SLOT_LD + d);
-                  dst[0] = lo;
-                  dst[1] = hi;
-                }
+              for (int z = 0; z < 8; ++z)
+                o[z] = acc[nq][j * (VN / 2) + (i + z) / 2][(z & 1) * 2 + e] * (E4M3 ? vref : 1.f);
+              const int d = (8 * j + g) * VN + i;
+              const float4 lo = make_float4(o[0], o[1], o[2], o[3]);
+              const float4 hi = make_float4(o[4], o[5], o[6], o[7]);
+              if (!whole) {
+                float4* dst = reinterpret_cast<float4*>(part + rl * ld + d);
+                dst[0] = lo;
+                dst[1] = hi;
+              } else if (r < rows_all) {
+                store_row8<D>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + hd) * D + d, lo, hi, inv);
               }
-          if (t == 0) {
-            if (begins && ends) {
-              if (r < rows_all) {
-                const int tok = r / s.group;
-                a.lse[static_cast<int64_t>(h * s.group + (r - tok * s.group)) * s.tokens + q.t0 + tok] =
-                    lse_of(mrun[mt][hh], l);
-              }
-            } else {
-              sh_ml[warp][part_b][rl] = make_float2(mrun[mt][hh], l);
             }
+          if (g == 0) {
+            if (!whole) sh_ml[warp][which][rl] = make_float2(mrun[nq][e], l);
+            else if (r < rows_all)
+              a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(mrun[nq][e], l);
           }
         }
-      if (!(begins && ends) && lane == 0)
-        sh_meta[warp][part_b] = PartMeta{1 | (begins ? 2 : 0) | (ends ? 4 : 0), n, h, rb};
-
-      // ---- the next item ----
-      left -= c1 - c0;
-      if (left <= 0) break;
-      c0 = 0;
-      if (++rb == nb) {
-        rb = 0;
-        if (++h == s.heads_kv) {
-          h = 0;
-          do {
-            ++n;
-            q = step_seq(s, n);
-            nb = seq_blocks<ROWS>(a, q);
-          } while (nb == 0);
-          nc = seq_chunks(q);
-        }
+      if (!whole && lane == 0) {
+        sh_meta[warp][which] = PartMeta{1 | (begins ? 2 : 0) | (ends ? 4 : 0), n, h, rb};
+        sh_part[warp][which] = part;
+        sh_ld[warp][which] = ld;
       }
+
+      if (last_part) break;
+      it = nx;
+      c0 = 0;
     }
   }
   __syncthreads();
@@ -650,9 +796,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, MT, HALF>::THREADS, 1)
         if (!(sh_meta[k >> 1][k & 1].kind & 1)) continue;
         const float2 ml = sh_ml[k >> 1][k & 1][rl];
         const float w = ex2(ml.x - ms);
-        const float* sp = reinterpret_cast<const float*>(smem + (k >> 1) * (C::RING + C::SLOT) +
-                                                         ((k & 1) ? 0 : C::RING)) +
-                          rl * C::SLOT_LD + d;
+        const float* sp = sh_part[k >> 1][k & 1] + rl * sh_ld[k >> 1][k & 1] + d;
         const float4 x = *reinterpret_cast<const float4*>(sp);
         const float4 y = *reinterpret_cast<const float4*>(sp + 4);
         l += w * ml.y;
@@ -695,10 +839,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, MT, HALF>::THREADS, 1)
 // item that begins in CTA b and goes on in CTA b + 1 (there is at most one):
 // its parts are CTA b's second, then the first of each following CTA until one
 // ends the item.
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;   // few enough to wait beside the main kernel's CTA on an SM
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheFwdArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int POS = ROWS * (D / 4);                    // float4 positions of a partial
   constexpr int SPLIT = POS >= kJoinThreads ? 1 : kJoinThreads / POS;
@@ -780,10 +924,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheFwd
   }
 }
 
-template <int D, bool E4M3, int MT, bool HALF>
+template <int D, bool E4M3, int NQ>
 cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
-  using C = Cfg<D, E4M3, MT, HALF>;
-  auto kern = cache_fwd_kernel<D, E4M3, MT, HALF>;
+  using C = Cfg<D, E4M3, NQ>;
+  auto kern = cache_fwd_kernel<D, E4M3, NQ>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
@@ -801,28 +945,21 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, C::ROWS>, a, grid);
 }
 
-template <int D, bool E4M3>
-cudaError_t launch_rows(const CacheFwdArgs& a, int rows, int grid, cudaStream_t st) {
-  switch (cache_fwd_rows(rows, E4M3)) {
-    case 8:
-      if constexpr (!E4M3) return launch<D, false, 1, true>(a, grid, st);
-    case 16: return launch<D, E4M3, 1, false>(a, grid, st);
-    default: return launch<D, E4M3, 2, false>(a, grid, st);
-  }
+template <int D>
+cudaError_t launch_dim(const CacheFwdArgs& a, bool e4m3, int rows, int grid, cudaStream_t st) {
+  if (cache_fwd_rows(rows) == 8)
+    return e4m3 ? launch<D, true, 1>(a, grid, st) : launch<D, false, 1>(a, grid, st);
+  return e4m3 ? launch<D, true, 2>(a, grid, st) : launch<D, false, 2>(a, grid, st);
 }
 
 }  // namespace
 
-int cache_fwd_rows(int rows, bool e4m3) {
-  if (rows <= 8 && !e4m3) return 8;
-  return rows <= 16 ? 16 : 32;
-}
+int cache_fwd_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int rows, int grid,
                              cudaStream_t st) {
-  if (head_dim == 64)
-    return e4m3 ? launch_rows<64, true>(a, rows, grid, st) : launch_rows<64, false>(a, rows, grid, st);
-  return e4m3 ? launch_rows<128, true>(a, rows, grid, st) : launch_rows<128, false>(a, rows, grid, st);
+  return head_dim == 64 ? launch_dim<64>(a, e4m3, rows, grid, st)
+                        : launch_dim<128>(a, e4m3, rows, grid, st);
 }
 
 }  // namespace attn

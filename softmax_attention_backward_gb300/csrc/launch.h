@@ -19,6 +19,12 @@ attn_status_t validate_dense_problem(const attn_problem_t* p, bool* empty);
 bool make_bf16_tile_map(CUtensorMap* m, const void* ptr, int batch, int rows, int heads, int dim,
                         int box_rows);
 
+// 2-D TMA map over a pool of cache rows [rows, dim] of bf16 or (`bytes`) 8-bit
+// codes: box of min(128 bytes, one row) x box_rows rows, with a swizzle as wide
+// as the box.
+bool make_cache_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool bytes,
+                         int box_rows);
+
 // Streaming multiprocessors of the current device (0 if it cannot be read).
 int sm_count();
 

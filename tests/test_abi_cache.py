@@ -90,8 +90,11 @@ def test_fwd_refusals_and_workspace(L):
         assert _fwd(L, _p(), **{f"i{i}": FAKE + 8}) == 3
     assert _fwd(L, _p(cache_type=1), i3=0) == 1 and _fwd(L, _p(cache_type=1), i4=0) == 1
     n = L.attn_cache_fwd_workspace_size(ctypes.byref(_p()))
-    # 2 parts per CTA of 8 rows x 128 fp32, (maximum, sum) and 16 bytes of meta data
-    assert n == 2 * 152 * (8 * 128 * 4 + 8 * 8 + 16)
+    # per CTA: a part of 8 rows x 128 fp32 for each of 8 warps, and two parts with (maximum,
+    # sum) of their rows and 16 bytes of meta data
+    assert n == 152 * (8 * 8 * 128 * 4 + 2 * (8 * 128 * 4 + 8 * 8 + 16))
+    assert L.attn_cache_fwd_workspace_size(ctypes.byref(_p(max_new=3))) == 152 * (
+        8 * 16 * 128 * 4 + 2 * (16 * 128 * 4 + 16 * 8 + 16))
     assert _fwd(L, _p(), ws=n - 1) == 5 and _fwd(L, _p(), i7=0) == 5
     assert _fwd(L, _p(), i7=FAKE + 4) == 3
     assert _fwd(L, _p(tokens=0), ws=0) == 0
