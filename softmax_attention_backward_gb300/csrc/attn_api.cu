@@ -88,6 +88,22 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map over bf16 rows [tokens, heads, dim], `stride` elements from token to
+// token: box of 64 dims x box_heads x box_tokens, 128-byte swizzle, zero fill.
+bool make_heads_map(CUtensorMap* m, const void* ptr, int tokens, int heads, int dim, int64_t stride,
+                    int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Validates a dense/THD problem.  Sets *empty when there is nothing to compute.
@@ -170,6 +186,11 @@ bool make_bf16_tile_map(CUtensorMap* m, const void* ptr, int batch, int rows, in
 bool make_cache_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool bytes,
                          int box_rows) {
   return make_rows_map(m, ptr, rows, dim, bytes, box_rows);
+}
+
+bool make_bf16_heads_map(CUtensorMap* m, const void* ptr, int tokens, int heads, int dim,
+                         int64_t stride, int box_heads, int box_tokens) {
+  return make_heads_map(m, ptr, tokens, heads, dim, stride, box_heads, box_tokens);
 }
 
 // Streaming multiprocessors of the current device (persistent grid size).

@@ -88,8 +88,20 @@ struct CacheFwdArgs {
   float* stash;      // [grid][warps][rows][head_dim] parts that a warp finished early
   float2* part_ml;   // [grid][2][rows] running maximum (log2) and sum
   int4* part_meta;   // [grid][2] {kind bits, sequence, KV head, row block}
-  CUtensorMap tm_k, tm_v;   // the pools' rows in boxes of min(page_size, kChunk)
+  int tiles, tile_rows;     // an item's row tiles, and the query rows in each
+  int tile_tokens;          // cache_fwd_tc: tile_rows / group
+  CUtensorMap tm_k, tm_v;   // the pools' rows in boxes of min(page_size, chunk)
+  CUtensorMap tm_q;         // cache_fwd_tc: q in boxes of tile_tokens x group heads x 64 dims
 };
+
+// Rows of an item of the tcgen05 kernel, and of each of its two tiles.
+constexpr int kCacheTcRows = 256, kCacheTcTile = 128;
+// The number of keys of its chunks.
+int cache_tc_box(int head_dim);
+cudaError_t launch_cache_fwd_tc(const CacheFwdArgs& a, int head_dim, int grid, cudaStream_t st);
+// Joins the items that several CTAs hold parts of (parts of item_rows rows).
+cudaError_t launch_cache_join(const CacheFwdArgs& a, int head_dim, int item_rows, int grid,
+                              cudaStream_t st);
 
 // Rows per work item of the variant that serves `rows` query rows per KV head.
 int cache_fwd_rows(int rows);

@@ -71,13 +71,22 @@ int step_rows(const attn_cache_problem_t* p) {
 struct Workspace {
   size_t o, stash, ml, meta, bytes;
 };
+// The tcgen05 kernel takes steps with more than 16 query rows per KV head in their
+// longest sequence (its tiles hold 128; the other kernel would read the keys
+// again for every 16), where a whole group fits a tile.
+bool use_tc(const attn_cache_problem_t* p) {
+  return p->cache_type == ATTN_CACHE_BF16 && step_rows(p) > 16 &&
+         p->heads_q / p->heads_kv <= kCacheTcTile;
+}
+
 Workspace fwd_workspace(const attn_cache_problem_t* p) {
-  const size_t item = cache_fwd_rows(step_rows(p));
+  const bool tc = use_tc(p);
+  const size_t item = tc ? kCacheTcRows : cache_fwd_rows(step_rows(p));
   const size_t rows = 2 * static_cast<size_t>(kCacheCtas) * item;
   Workspace w;
   w.o = 0;
   w.stash = rows * p->head_dim * sizeof(float);
-  w.ml = w.stash + kCacheCtas * kCacheWarps * item * p->head_dim * sizeof(float);
+  w.ml = w.stash + (tc ? 0 : kCacheCtas * kCacheWarps * item * p->head_dim * sizeof(float));
   w.meta = w.ml + rows * sizeof(float2);
   w.bytes = w.meta + 2 * kCacheCtas * sizeof(int4);
   return w;
@@ -195,19 +204,35 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
   const int rows = step_rows(p);
-  const int item_rows = cache_fwd_rows(rows);
+  const bool tc = use_tc(p);
+  const int chunk = tc ? cache_tc_box(p->head_dim) : kChunk;
   const int64_t pool_rows = static_cast<int64_t>(p->num_pages) * p->heads_kv * p->page_size;
-  const int box = p->page_size < kChunk ? p->page_size : kChunk;
+  const int box = p->page_size < chunk ? p->page_size : chunk;
   if (!make_cache_rows_map(&a.tm_k, k_cache, pool_rows, p->head_dim, e4m3, box) ||
       !make_cache_rows_map(&a.tm_v, v_cache, pool_rows, p->head_dim, e4m3, box))
     return ATTN_ERR_CUDA;
-  // the most chunks that the step can have; a CTA takes at least one per warp
-  const double items = (static_cast<double>(p->tokens) * a.s.group / item_rows + p->num_seqs) * p->heads_kv;
-  const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size + kChunk - 1) / kChunk);
-  const double ctas = chunks / kCacheWarps + 1;
+  if (tc) {
+    a.tiles = kCacheTcRows / kCacheTcTile;
+    a.tile_tokens = kCacheTcTile / a.s.group;
+    a.tile_rows = a.tile_tokens * a.s.group;
+    if (!make_bf16_heads_map(&a.tm_q, q, p->tokens, p->heads_q, p->head_dim, a.q_stride, a.s.group,
+                             a.tile_tokens))
+      return ATTN_ERR_CUDA;
+  } else {
+    a.tiles = 1;
+    a.tile_rows = cache_fwd_rows(rows);
+    a.tile_tokens = 0;
+  }
+  // The most chunks that the step can have.  A CTA takes at least one per warp, of
+  // the tcgen05 kernel one.
+  const double items =
+      (static_cast<double>(p->tokens) * a.s.group / (a.tiles * a.tile_rows) + p->num_seqs) * p->heads_kv;
+  const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size) / chunk + 3);
+  const double ctas = chunks / (tc ? 1 : kCacheWarps) + 1;
   const int grid = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
-  return status_of(launch_cache_fwd(a, p->head_dim, e4m3, rows, grid,
-                                    reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return status_of(tc ? launch_cache_fwd_tc(a, p->head_dim, grid, cs)
+                      : launch_cache_fwd(a, p->head_dim, e4m3, rows, grid, cs));
 }
 
 }  // extern "C"

@@ -835,37 +835,48 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
     a.lse[w / pad * s.tokens + end + w % pad] = -INFINITY;
 }
 
-// Joins the items that several CTAs hold parts of.  Block b looks after the
-// item that begins in CTA b and goes on in CTA b + 1 (there is at most one):
-// its parts are CTA b's second, then the first of each following CTA until one
-// ends the item.
+// Joins the items that several CTAs hold parts of.  Block (b, y) looks after rows
+// [y ROWS, (y + 1) ROWS) of the item that begins in CTA b and goes on in CTA b + 1
+// (there is at most one): its parts are CTA b's second, then the first of each
+// following CTA until one ends the item.
 constexpr int kJoinThreads = 256;   // few enough to wait beside the main kernel's CTA on an SM
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads)
+    cache_join_kernel(const __grid_constant__ CacheFwdArgs a, int grid, int item_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int POS = ROWS * (D / 4);                    // float4 positions of a partial
   constexpr int SPLIT = POS >= kJoinThreads ? 1 : kJoinThreads / POS;
   __shared__ float sh_w[kCacheCtas][ROWS];
   __shared__ float sh_l[ROWS], sh_m[ROWS];
   __shared__ float4 sh_o[SPLIT > 1 ? kJoinThreads : 1];
+  __shared__ int sh_end;
+  const CacheStep& s = a.s;
   const int b = blockIdx.x;
   const int4 meta = a.part_meta[2 * b + 1];
   if (!(meta.x & 1)) return;   // (kind bit 1, "begins", is set in every second part)
-  int parts = 1;
-  {
-    // the following CTAs' first parts, until one ends the item
-    __shared__ int sh_end;
-    if (threadIdx.x == 0) sh_end = grid;
-    __syncthreads();
-    for (int c = b + 1 + threadIdx.x; c < grid; c += kJoinThreads)
-      if (a.part_meta[2 * c].x & 4) atomicMin(&sh_end, c);
-    __syncthreads();
-    parts = min(sh_end, grid - 1) - b + 1;
-  }
+  const StepSeq q = step_seq(s, meta.y);
+  const int rows_all = q.m * s.group;
+  // row rl of the item: row tr of its tile, query row r of the sequence and KV head
+  const int tile_size = item_rows / a.tiles;
+  auto row_of = [&](int rl) {
+    const int tile = rl / tile_size, tr = rl - tile * tile_size;
+    return tr < a.tile_rows ? (meta.w * a.tiles + tile) * a.tile_rows + tr : rows_all;
+  };
+  const int base = blockIdx.y * ROWS;
+  if (threadIdx.x == 0) sh_end = grid;
+  if (!__syncthreads_or(threadIdx.x < ROWS && row_of(base + threadIdx.x) < rows_all)) return;
+  // the following CTAs' first parts, until one ends the item
+  for (int c = b + 1 + threadIdx.x; c < grid; c += kJoinThreads)
+    if (a.part_meta[2 * c].x & 4) atomicMin(&sh_end, c);
+  __syncthreads();
+  const int parts = min(sh_end, grid - 1) - b + 1;
   const int warp = warp_id(), lane = lane_id();
-  auto part_at = [&](int p) { return static_cast<int64_t>(p == 0 ? 2 * b + 1 : 2 * (b + p)) * ROWS; };
+  auto part_at = [&](int p) {
+    return static_cast<int64_t>(p == 0 ? 2 * b + 1 : 2 * (b + p)) * item_rows + base;
+  };
   for (int r = warp; r < ROWS; r += kJoinThreads / 32) {
+    if (row_of(base + r) >= rows_all) continue;
     float m = -INFINITY;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[part_at(p) + r].x);
 #pragma unroll
@@ -886,13 +897,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
   }
   __syncthreads();
-  const CacheStep& s = a.s;
-  const StepSeq q = step_seq(s, meta.y);
-  const int rows_all = q.m * s.group;
   for (int e0 = 0; e0 < POS; e0 += kJoinThreads) {
     const int e = SPLIT > 1 ? threadIdx.x % POS : e0 + threadIdx.x;
     const int sp = SPLIT > 1 ? threadIdx.x / POS : 0;
-    const int rl = e / (D / 4), d = (e - rl * (D / 4)) * 4, r = meta.w * ROWS + rl;
+    const int rl = e / (D / 4), d = (e - rl * (D / 4)) * 4, r = row_of(base + rl);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows_all) {
 #pragma unroll 4
@@ -924,6 +932,20 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
 }
 
+template <int D, int ROWS>
+cudaError_t launch_join(const CacheFwdArgs& a, int item_rows, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, item_rows / ROWS);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, ROWS>, a, grid, item_rows);
+}
+
 template <int D, bool E4M3, int NQ>
 cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   using C = Cfg<D, E4M3, NQ>;
@@ -933,16 +955,7 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid < 2) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, C::ROWS>, a, grid);
+  return launch_cache_join(a, D, C::ROWS, grid, st);
 }
 
 template <int D>
@@ -953,6 +966,14 @@ cudaError_t launch_dim(const CacheFwdArgs& a, bool e4m3, int rows, int grid, cud
 }
 
 }  // namespace
+
+cudaError_t launch_cache_join(const CacheFwdArgs& a, int head_dim, int item_rows, int grid,
+                              cudaStream_t st) {
+  if (item_rows == 8)
+    return head_dim == 64 ? launch_join<64, 8>(a, 8, grid, st) : launch_join<128, 8>(a, 8, grid, st);
+  return head_dim == 64 ? launch_join<64, 16>(a, item_rows, grid, st)
+                        : launch_join<128, 16>(a, item_rows, grid, st);
+}
 
 int cache_fwd_rows(int rows) { return rows <= 8 ? 8 : 16; }
 

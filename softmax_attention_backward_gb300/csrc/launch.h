@@ -25,6 +25,11 @@ bool make_bf16_tile_map(CUtensorMap* m, const void* ptr, int batch, int rows, in
 bool make_cache_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int dim, bool bytes,
                          int box_rows);
 
+// 3-D TMA map over bf16 [tokens, heads, dim], `stride` elements from token to
+// token: box of 64 dims x box_heads x box_tokens, 128-byte swizzle.
+bool make_bf16_heads_map(CUtensorMap* m, const void* ptr, int tokens, int heads, int dim,
+                         int64_t stride, int box_heads, int box_tokens);
+
 // Streaming multiprocessors of the current device (0 if it cannot be read).
 int sm_count();
 

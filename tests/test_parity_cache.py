@@ -80,6 +80,47 @@ def test_long_axis_is_split_and_joined(cache, D):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("D,hq,hkv,ps", [(64, 2, 1, 16), (128, 3, 1, 32), (64, 8, 8, 64), (128, 8, 2, 128), (128, 4, 1, 16)])
+def test_chunks_of_prompts(cache, D, hq, hkv, ps):
+    # several row tiles and blocks; tiles of an odd number of rows (groups of 3); prefixes of every kind;
+    # decoding sequences, empty ones and short drafts among them
+    seqs = [(700, 300), (129, 129), (2, 1), (513, 1), (0, 0), (400, 90), (130, 7), (64, 64), (33, 20)]
+    s = Step(cache, D, hq, hkv, ps, seqs, seed=ps + D)
+    check(s.answer(), *run_fwd(s))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_over_a_long_prefix_is_split_and_joined(cache, D):
+    s = Step(cache, D, 4, 1, 64, [(9000, 40)], seed=41)
+    check(s.answer(), *run_fwd(s))
+    s = Step(cache, D, 4, 2, 16, [(3000, 70), (20, 20), (1500, 1), (800, 5)], seed=42)
+    check(s.answer(False), *run_fwd(s, False))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_chunk_with_bad_pages(cache):
+    # pages missing at the start, in the middle and at the end of a chunk's keys
+    for ps, cols in ((16, (0, 2, 7)), (64, (1,)), (128, (0,))):
+        s = Step(cache, 64, 4, 2, ps, [(230, 40), (90, 60)], seed=43)
+        keep = torch.ones(230, dtype=torch.bool)
+        for c in cols:
+            s.table[0, c] = -3 if c else 10 ** 6
+            keep[c * ps:(c + 1) * ps] = False
+        o, lse = run_fwd(s, causal=False, expect=1)
+        t = s.table.clone()
+        s.table[0].clamp_(0, s.pools[0].shape[0] - 1)
+        k, v = s.keys(0)
+        r = slice(0, 40)
+        ro, rl, wabs, smax = OC.attention(s.q[r], k[keep], v[keep], 64 ** -0.5, causal=False)
+        b = bounds(ro, rl, wabs, v[keep].abs().sum(0).repeat_interleave(2, 0)[None], smax, 64, cache)
+        check(dict(o=ro, lse=rl, **b), o[r], lse[:, r])
+        ref = s.answer(False)
+        r = slice(40, 100)
+        check({n: x[r] if n.startswith("o") else x[:, r] for n, x in ref.items()}, o[r], lse[:, r])
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_many_short_sequences(cache):
     # more sequences than threads of a CTA, empty ones among them, all within few chunks
     seqs = [((7 * n) % 41, 1 if (7 * n) % 41 else 0) for n in range(700)]
