@@ -97,8 +97,9 @@ struct CacheFwdArgs {
 // Rows of an item of the tcgen05 kernel, and of each of its two tiles.
 constexpr int kCacheTcRows = 256, kCacheTcTile = 128;
 // The number of keys of its chunks.
-int cache_tc_box(int head_dim);
-cudaError_t launch_cache_fwd_tc(const CacheFwdArgs& a, int head_dim, int grid, cudaStream_t st);
+int cache_tc_chunk(int head_dim, bool e4m3);
+cudaError_t launch_cache_fwd_tc(const CacheFwdArgs& a, int head_dim, bool e4m3, int grid,
+                                cudaStream_t st);
 // Joins the items that several CTAs hold parts of (parts of item_rows rows).
 cudaError_t launch_cache_join(const CacheFwdArgs& a, int head_dim, int item_rows, int grid,
                               cudaStream_t st);

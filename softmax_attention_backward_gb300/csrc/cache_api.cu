@@ -75,8 +75,7 @@ struct Workspace {
 // longest sequence (its tiles hold 128; the other kernel would read the keys
 // again for every 16), where a whole group fits a tile.
 bool use_tc(const attn_cache_problem_t* p) {
-  return p->cache_type == ATTN_CACHE_BF16 && step_rows(p) > 16 &&
-         p->heads_q / p->heads_kv <= kCacheTcTile;
+  return step_rows(p) > 16 && p->heads_q / p->heads_kv <= kCacheTcTile;
 }
 
 Workspace fwd_workspace(const attn_cache_problem_t* p) {
@@ -205,7 +204,7 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
   const int rows = step_rows(p);
   const bool tc = use_tc(p);
-  const int chunk = tc ? cache_tc_box(p->head_dim) : kChunk;
+  const int chunk = tc ? cache_tc_chunk(p->head_dim, e4m3) : kChunk;
   const int64_t pool_rows = static_cast<int64_t>(p->num_pages) * p->heads_kv * p->page_size;
   const int box = p->page_size < chunk ? p->page_size : chunk;
   if (!make_cache_rows_map(&a.tm_k, k_cache, pool_rows, p->head_dim, e4m3, box) ||
@@ -231,7 +230,7 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   const double ctas = chunks / (tc ? 1 : kCacheWarps) + 1;
   const int grid = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return status_of(tc ? launch_cache_fwd_tc(a, p->head_dim, grid, cs)
+  return status_of(tc ? launch_cache_fwd_tc(a, p->head_dim, e4m3, grid, cs)
                       : launch_cache_fwd(a, p->head_dim, e4m3, rows, grid, cs));
 }
 

@@ -26,22 +26,26 @@
 namespace attn {
 namespace {
 
-template <int D>
+template <int D, bool E4M3>
 struct TcCfg {
   static constexpr int BM = 128;
-  static constexpr int BN = D == 128 ? 64 : 128;   // as in attn_fwd
+  static constexpr int BN = D == 128 || E4M3 ? 64 : 128;   // bf16: as in attn_fwd
   static constexpr int PANELS = D / 64;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int NSLOT = 6;
+  static constexpr int NSLOT = D == 128 && E4M3 ? 4 : 6;
   static constexpr int QBUFS = 2;
-  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + 1024;
-  static constexpr int THREADS = 352;
+  // e4m3: warps 11..14 bring the codes into a ring of RAW chunks of their own and
+  // convert them into the slots
+  static constexpr int RAW = 4, RAW_BYTES = E4M3 ? BN * D : 0;
+  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + RAW * RAW_BYTES + 1024;
+  static constexpr int THREADS = E4M3 ? 480 : 352;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S0 = 0, COL_S1 = BN, COL_O0 = 256, COL_O1 = 256 + D;
   static constexpr uint32_t COL_P0 = D == 128 ? 2 * BN : 256 + 2 * D, COL_P1 = COL_P0 + BN / 2;
   static_assert(D != 128 || 3 * BN <= 256, "S and P of both tiles below O");
   static_assert(D == 128 || 256 + 2 * D + BN <= 512, "TMEM budget");
+  static_assert(SMEM <= 226 * 1024, "shared memory");
 };
 
 // Chunks by which an item counts more in the dealing than it has: its query
@@ -123,10 +127,10 @@ __device__ __forceinline__ Part part_of(const TcItem& it, int c0, int64_t left) 
   return p;
 }
 
-template <int D>
-__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     cache_fwd_tc_kernel(const __grid_constant__ CacheFwdArgs a) {
-  using C = TcCfg<D>;
+  using C = TcCfg<D, E4M3>;
   constexpr int BN = C::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -139,7 +143,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   __shared__ uint64_t bar_s[2], bar_p[2], bar_o[2], bar_sfree[2], bar_stagger;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  __shared__ int sh_bad[16];   // by chunk: 16-key groups (bits) without a page
+  // by chunk, which 16-key groups have no page: a bit each; e4m3: a byte each
+  constexpr int BAD_SHIFT = E4M3 ? 8 : 1;
+  __shared__ int sh_bad[16];
+  __shared__ float sh_scale[4][C::RAW];   // e4m3: of each converting warp's 16 keys
   __shared__ int64_t sh_warp[C::THREADS / 32 + 1];
   __shared__ TcItem sh_item;
   __shared__ int sh_c0;
@@ -159,7 +166,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       mbar_init(&bar_qempty[b], 2);      // released by both issuers
     }
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(&bar_full[i], 1);
+      mbar_init(&bar_full[i], E4M3 ? 128 : 1);
       mbar_init(&bar_empty[i], 2);       // released by both issuers
     }
     mbar_init(&bar_tail, 1);
@@ -172,8 +179,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     mbar_init(&bar_stagger, 1);
     fence_mbar_init();
     tma_prefetch_desc(&a.tm_q);
-    tma_prefetch_desc(&a.tm_k);
-    tma_prefetch_desc(&a.tm_v);
+    if constexpr (!E4M3) {
+      tma_prefetch_desc(&a.tm_k);
+      tma_prefetch_desc(&a.tm_v);
+    }
   }
   if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
   if (warp == 9) tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         bool q_pending = have_next;
         const int nqb = (ic + 1) % C::QBUFS;
         const uint32_t nq_par = (((ic + 1) / C::QBUFS) & 1) ^ 1;
-        for (int c = 0; ok && c < pt.n_kv; ++c, ++gchunk) {
+        for (int c = 0; ok && c < (E4M3 ? 0 : pt.n_kv); ++c, ++gchunk) {
           const int kv0 = (pt.c0 + c) * BN;
           // pages of the chunk: one, or `boxes` of them
           const int col0 = kv0 >> s.ps_shift;
@@ -433,6 +442,125 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         if (!ok || !advance(it, pt, left)) break;
       }
     }
+  } else if (E4M3 && warp > 10) {
+    // ---------------- e4m3: codes to bf16 values ----------------
+    // Warp w has keys 16 w .. 16 w + 15 of every chunk, which lie in one page under one
+    // scale; a thread copies, four chunks of keys or values ahead, the vectors of 16 codes
+    // that it converts: vector 4 j + lane % 4 of rows lane / 4 and lane / 4 + 8.  Codes go
+    // through fp16 and fp32 (exactly, NaN included); code * scale is rounded to bf16,
+    // which is exact for scales that are powers of two.
+    if constexpr (E4M3) {
+      if (range > 0) {
+        constexpr int NV = 2 * C::PANELS;   // vectors of a thread
+        const int w = warp - 11;
+        uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + w * (C::RAW_BYTES / 4);   // + stage * RAW_BYTES
+        TcItem cp = first;                  // the copies' place
+        int64_t cp_left = range;
+        Part cp_pt = part_of(cp, first_c0, cp_left);
+        int cp_c = 0, cp_half = 0, cp_chunk = 0;
+        int pg0 = -1, pg_n = -1, pid = -1;  // lane l holds the page of column pg0 + l of sequence pg_n
+        bool cp_more = true;
+        auto copy = [&]() {
+          if (cp_more && !(cp_half & 1))
+            while (cp_c >= cp_pt.n_kv) {
+              cp_more = advance(cp, cp_pt, cp_left);
+              cp_c = 0;
+              if (!cp_more) break;
+            }
+          if (cp_more) {
+            const int key0 = (cp_pt.c0 + cp_c) * BN + 16 * w;
+            const int col = key0 >> s.ps_shift;
+            if (pg_n != cp.n || col < pg0 || col >= pg0 + 32) {
+              pg_n = cp.n;
+              pg0 = col;
+              const int cc = col + lane;
+              pid = -1;
+              if (cc <= (cp.q.len - 1) >> s.ps_shift) {
+                pid = __ldg(s.table + static_cast<int64_t>(cp.n) * s.max_pages + cc);
+                if (pid < 0 || pid >= s.num_pages) {
+                  pid = -1;
+                  if (s.err) atomicOr(s.err, ATTN_DEVERR_INDEX_RANGE);
+                }
+              }
+            }
+            const int page = __shfl_sync(0xffffffffu, pid, col - pg0);
+            const bool values = cp_half & 1;
+            const int64_t ph = static_cast<int64_t>(max(page, 0)) * s.heads_kv + cp.h;
+            const uint8_t* src = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache) +
+                                 ((ph << s.ps_shift) + (key0 & ((1 << s.ps_shift) - 1))) * D;
+            uint8_t* dst = raw + (cp_half % C::RAW) * C::RAW_BYTES;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const int row = (v & 1) * 8 + (lane >> 2);
+              const uint32_t n = page >= 0 && key0 + row < cp.q.len ? 16u : 0u;   // else zeros
+              cp_async16(smem_u32(dst + (v * 32 + lane) * 16), src + row * D + (v >> 1) * 64 + (lane & 3) * 16, n);
+            }
+            if (lane == 0) {
+              float* sc = &sh_scale[w][cp_half % C::RAW];
+              if (page >= 0)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sc)),
+                             "l"((values ? a.v_scale : a.k_scale) + ph)
+                             : "memory");
+              else
+                *sc = 0.f;
+              // (missing pages; keys past the length are masked by it)
+              if (!values)
+                reinterpret_cast<volatile uint8_t*>(&sh_bad[cp_chunk & 15])[w] = page < 0 && key0 < cp.q.len;
+            }
+            if (values) {
+              ++cp_c;
+              ++cp_chunk;
+            }
+            ++cp_half;
+          }
+          cp_async_commit();
+        };
+        TcItem it = first;
+        int64_t left = range;
+        Part pt = part_of(it, first_c0, left);
+        for (int i = 0; i < C::RAW; ++i) copy();
+        int half = 0;
+        bool ok = true;
+        while (ok) {
+          for (int i = 0; ok && i < 2 * pt.n_kv; ++i, ++half) {
+            cp_async_wait<C::RAW - 1>();
+            __syncwarp();
+            const int slot = half % C::NSLOT;
+            if (!mbar_wait_w(&bar_empty[slot], ((half / C::NSLOT) & 1) ^ 1, ac)) { ok = false; break; }
+            const uint8_t* src = raw + (half % C::RAW) * C::RAW_BYTES;
+            const float sc = sh_scale[w][half % C::RAW];
+            const uint64_t sc2 = f2_pack(sc, sc);
+            uint8_t* dst = sRing + slot * C::KV_BYTES;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const int row = 16 * w + (v & 1) * 8 + (lane >> 2);
+              const uint4 x = *reinterpret_cast<const uint4*>(src + (v * 32 + lane) * 16);
+              const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                uint32_t h;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                    : "=r"(h)
+                    : "h"(static_cast<uint16_t>(xx[e >> 1] >> (16 * (e & 1)))));
+                const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+                y[e] = f2_to_bf16x2(f2_mul(f2_pack(f.x, f.y), sc2));
+              }
+              uint8_t* line = dst + (v >> 1) * (BN * 128) + row * 128;
+              const int ch = 2 * (lane & 3);
+              *reinterpret_cast<uint4*>(line + ((ch ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar_full[slot]);
+            __syncwarp();
+            copy();
+          }
+          if (!ok || !advance(it, pt, left)) break;
+        }
+        cp_async_wait<0>();
+      }
+    }
   } else if (range > 0) {
     // ---------------- softmax warpgroups ----------------
     const int t = warp >> 2;                 // query tile of this warpgroup
@@ -486,7 +614,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         if (bad) {
 #pragma unroll
           for (int cc = 0; cc < BN; ++cc)
-            if (bad >> (cc / 16) & 1) x[cc] = -INFINITY;
+            if (bad >> (BAD_SHIFT * (cc / 16)) & 1) x[cc] = -INFINITY;
         }
         float mx[8];
 #pragma unroll
@@ -622,10 +750,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, bool E4M3>
 cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
-  using C = TcCfg<D>;
-  auto kern = cache_fwd_tc_kernel<D>;
+  using C = TcCfg<D, E4M3>;
+  auto kern = cache_fwd_tc_kernel<D, E4M3>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
@@ -635,10 +763,14 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int cache_tc_box(int head_dim) { return head_dim == 128 ? TcCfg<128>::BN : TcCfg<64>::BN; }
+int cache_tc_chunk(int head_dim, bool e4m3) {
+  return head_dim == 128 ? TcCfg<128, false>::BN : e4m3 ? TcCfg<64, true>::BN : TcCfg<64, false>::BN;
+}
 
-cudaError_t launch_cache_fwd_tc(const CacheFwdArgs& a, int head_dim, int grid, cudaStream_t st) {
-  return head_dim == 64 ? launch<64>(a, grid, st) : launch<128>(a, grid, st);
+cudaError_t launch_cache_fwd_tc(const CacheFwdArgs& a, int head_dim, bool e4m3, int grid,
+                                cudaStream_t st) {
+  if (head_dim == 64) return e4m3 ? launch<64, true>(a, grid, st) : launch<64, false>(a, grid, st);
+  return e4m3 ? launch<128, true>(a, grid, st) : launch<128, false>(a, grid, st);
 }
 
 }  // namespace attn

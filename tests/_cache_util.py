@@ -91,10 +91,11 @@ class Step:
             r = slice(int(self.cu[n]), int(self.cu[n + 1]))
             o[r], lse[:, r], wabs[r], smax[:, r] = OC.attention(self.q[r], k, v, scale, causal)
             vsum[r] = v.abs().sum(0).repeat_interleave(self.hq // self.hkv, 0)
-        return dict(o=o, lse=lse, **bounds(o, lse, wabs, vsum, smax, self.D, self.cache))
+        rows = self.max_new * (self.hq // self.hkv)
+        return dict(o=o, lse=lse, **bounds(o, lse, wabs, vsum, smax, self.D, self.cache, rows))
 
 
-def bounds(o, lse, wabs, vsum, smax, D, cache):
+def bounds(o, lse, wabs, vsum, smax, D, cache, rows):
     """Error bounds of attn_cache_fwd.
 
     A logit is D exact products summed in fp32 (in any order within (D + 2) half steps
@@ -103,12 +104,14 @@ def bounds(o, lse, wabs, vsum, smax, D, cache):
     its error is at most (D + 8) 2^-24 smax, in natural units; smax >= 1 covers the
     exponential's own 2^-22 and the fp32 sums and joins (a few dozen of them: 2^-19).
     The error of a probability relative to itself is twice that (numerator and sum).
-    P is rounded to bf16 (2^-8; with 8 rows the residue is carried along, which the same
-    bound covers) or to fp16 (2^-11, and 2^-25 absolute below its normal range, over
-    a sum of at least 1); each of these scales |v|.  Then one rounding to bf16, 2^-8."""
+    P is rounded, by the kernel for at most 16 query rows per KV head to two bf16 (2^-16) or,
+    e4m3, to fp16 (2^-11, and 2^-25 absolute below its normal range, over a sum of at
+    least 1), by the tcgen05 kernel for more rows to bf16 (2^-8, whatever the cache's
+    type); each of these scales |v|.  Then one rounding to bf16, 2^-8."""
+    few = rows <= 16
     es = (D + 8) * 2.0 ** -24 * smax.clamp(min=1) + 2.0 ** -19
-    e = 2 * es.t()[..., None] + (2.0 ** -8 if cache == "bf16" else 2.0 ** -11)
-    err = e * wabs + (0 if cache == "bf16" else 2.0 ** -25 * vsum)
+    e = 2 * es.t()[..., None] + (2.0 ** -8 if not few else 2.0 ** -16 if cache == "bf16" else 2.0 ** -11)
+    err = e * wabs + (2.0 ** -25 * vsum if few and cache != "bf16" else 0)
     return dict(o_tol=err * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs() + 1e-37,
                 lse_tol=es + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0))
 

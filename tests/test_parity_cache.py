@@ -113,7 +113,7 @@ def test_chunk_with_bad_pages(cache):
         k, v = s.keys(0)
         r = slice(0, 40)
         ro, rl, wabs, smax = OC.attention(s.q[r], k[keep], v[keep], 64 ** -0.5, causal=False)
-        b = bounds(ro, rl, wabs, v[keep].abs().sum(0).repeat_interleave(2, 0)[None], smax, 64, cache)
+        b = bounds(ro, rl, wabs, v[keep].abs().sum(0).repeat_interleave(2, 0)[None], smax, 64, cache, 120)
         check(dict(o=ro, lse=rl, **b), o[r], lse[:, r])
         ref = s.answer(False)
         r = slice(40, 100)
@@ -192,7 +192,7 @@ def test_bad_page_is_flagged_and_its_keys_left_out():
         rows = [t[s.table[0, keep].long()].permute(0, 2, 1, 3).reshape(-1, 1, 64) for t in s.true]
         rows = [torch.cat([r[:32], r[32:]])[:84] for r in rows]   # 100 keys less 16
         ro, rl, wabs, smax = OC.attention(s.q[:1], *rows, 64 ** -0.5)
-        b = bounds(ro, rl, wabs, rows[1].abs().sum(0).expand(2, 64)[None], smax, 64, cache)
+        b = bounds(ro, rl, wabs, rows[1].abs().sum(0).expand(2, 64)[None], smax, 64, cache, 2)
         check(dict(o=ro, lse=rl, **b), o[:1], lse[:, :1])
 
 
@@ -473,7 +473,7 @@ def test_generation_matches_the_forward_over_the_whole_text(D, hq, hkv):
     kr = kc[tab[0].long()].transpose(1, 2).reshape(-1, hkv, D)[:S]
     wo, wl = A.attn_fwd(qr[None], kr[None].contiguous(), v[None], causal=True)
     ro, rl, wabs, smax = OC.attention(qr.cpu(), kr.cpu(), v.cpu(), D ** -0.5)
-    b = bounds(ro, rl, wabs, torch.zeros_like(ro), smax, D, "bf16")
+    b = bounds(ro, rl, wabs, torch.zeros_like(ro), smax, D, "bf16", 1000)   # its prompt and chunk: many rows
     check(dict(o=ro, lse=rl, **b), o, lse)
     # both within their bounds of the same rows: at most twice the bound apart
     assert ((o.double() - wo[0].double()).abs().cpu() <= 2 * b["o_tol"]).all()
