@@ -35,22 +35,36 @@ struct TcCfg {
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int NSLOT = D == 128 && E4M3 ? 4 : 6;
   static constexpr int QBUFS = 2;
-  // e4m3: warps 11..14 bring the codes into a ring of RAW chunks of their own and
-  // convert them into the slots
-  static constexpr int RAW = 4, RAW_BYTES = E4M3 ? BN * D : 0;
-  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + RAW * RAW_BYTES + 1024;
-  static constexpr int THREADS = E4M3 ? 480 : 352;
+  // e4m3: warps 12..15 bring the keys' codes, warps 16..19 the values', into a ring of
+  // RAW chunks each and convert them into the slots, after a list that warp 8 writes
+  static constexpr int RAW = 2, RAW_BYTES = E4M3 ? BN * D : 0;
+  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + 2 * RAW * RAW_BYTES + 1024;
+  static constexpr int THREADS = E4M3 ? 640 : 352;
+  static constexpr int LIST = 8;   // chunks of the list
+  // e4m3: registers of a thread, at launch and then by warpgroup (softmax, issue and
+  // copy, conversion); the shares add up to what the block was launched with
+  static constexpr int REGS = 96, REGS_SOFTMAX = 120, REGS_ISSUE = 80, REGS_CONVERT = 80;
+  static_assert(2 * REGS_SOFTMAX + REGS_ISSUE + 2 * REGS_CONVERT <= 5 * REGS, "register shares");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S0 = 0, COL_S1 = BN, COL_O0 = 256, COL_O1 = 256 + D;
   static constexpr uint32_t COL_P0 = D == 128 ? 2 * BN : 256 + 2 * D, COL_P1 = COL_P0 + BN / 2;
   static_assert(D != 128 || 3 * BN <= 256, "S and P of both tiles below O");
   static_assert(D == 128 || 256 + 2 * D + BN <= 512, "TMEM budget");
-  static_assert(SMEM <= 226 * 1024, "shared memory");
+  static_assert(SMEM <= 227 * 1024 - 700, "shared memory");
 };
 
 // Chunks by which an item counts more in the dealing than it has: its query
 // tiles, its first and last chunk and its outputs.
 constexpr int kItemCost = 3;
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* m, uint64_t* bar, void* dst, int c0,
                                             int c1) {
@@ -127,6 +141,15 @@ __device__ __forceinline__ Part part_of(const TcItem& it, int c0, int64_t left) 
   return p;
 }
 
+// What warp 8 tells the other roles about a part, in shared memory beside its query
+// tiles: they read it when those have arrived.
+struct PartInfo {
+  int n_w[2], n_kv, c0;
+  StepSeq q;
+  int n, h, rb;
+  int kind;   // bit 0: a part, bit 1: begins its item, bit 2: ends it; 0: no more parts
+};
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     cache_fwd_tc_kernel(const __grid_constant__ CacheFwdArgs a) {
@@ -143,12 +166,15 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   __shared__ uint64_t bar_s[2], bar_p[2], bar_o[2], bar_sfree[2], bar_stagger;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  // by chunk, which 16-key groups have no page: a bit each; e4m3: a byte each
-  constexpr int BAD_SHIFT = E4M3 ? 8 : 1;
-  __shared__ int sh_bad[16];
-  __shared__ float sh_scale[4][C::RAW];   // e4m3: of each converting warp's 16 keys
+  __shared__ int sh_bad[32];   // by chunk: 16-key groups (bits) without a page
+  // e4m3, by chunk: the pool row of each 16-key group and how many of its rows exist
+  // (first group -1: the end); the scales of the groups in the raw rings
+  __shared__ int2 sh_list[C::LIST][4];
+  __shared__ uint64_t bar_lfull[C::LIST], bar_lempty[C::LIST];
+  __shared__ float sh_scale[2][4][C::RAW];
   __shared__ int64_t sh_warp[C::THREADS / 32 + 1];
   __shared__ TcItem sh_item;
+  __shared__ PartInfo sh_info[C::QBUFS];
   __shared__ int sh_c0;
   __shared__ int64_t sh_left;
 
@@ -163,13 +189,18 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     sh_left = 0;
     for (int b = 0; b < C::QBUFS; ++b) {
       mbar_init(&bar_q[b], 1);
-      mbar_init(&bar_qempty[b], 2);      // released by both issuers
+      mbar_init(&bar_qempty[b], 10);     // released by both issuers and 8 softmax warps
     }
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(&bar_full[i], E4M3 ? 128 : 1);
       mbar_init(&bar_empty[i], 2);       // released by both issuers
     }
     mbar_init(&bar_tail, 1);
+    if constexpr (E4M3)
+      for (int i = 0; i < C::LIST; ++i) {
+        mbar_init(&bar_lfull[i], 1);
+        mbar_init(&bar_lempty[i], 8);    // released by the converting warps
+      }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar_s[w], 1);
       mbar_init(&bar_p[w], 128);
@@ -242,39 +273,47 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     __syncthreads();
   }
   const uint32_t tmem = tmem_base_sh;
-  const TcItem first = sh_item;   // (not read when sh_left is 0)
-  const int first_c0 = sh_c0;
-  const int64_t range = sh_left;
-  // the walk of every role: item, part, next
-  auto advance = [&](TcItem& it, Part& pt, int64_t& left) -> bool {
-    left -= pt.span;
-    if (left <= 0) return false;
-    item_next<BN>(a, it);
-    pt = part_of(it, 0, left);
-    return true;
-  };
+  const int64_t range = sh_left;   // chunks of the CTA
 
+  if constexpr (E4M3) {
+    if (warp < 8) setmaxnreg_inc<C::REGS_SOFTMAX>();
+    else if (warp < 12) setmaxnreg_dec<C::REGS_ISSUE>();
+    else setmaxnreg_dec<C::REGS_CONVERT>();
+  }
   if (warp == 8) {
     // ---------------- copies (warp-uniform, lane 0 issues) ----------------
     if (range > 0) {
       const int box = min(BN, 1 << s.ps_shift), boxes = BN / box;
       const int tile_bytes = a.tile_tokens * s.group * 128 * C::PANELS;
-      auto issue_q = [&](const TcItem& it, int icq) {
+      auto issue_q = [&](const TcItem& it, const Part& pt, int icq) {
         if (lane != 0) return;
         const int qb = icq % C::QBUFS;
+        PartInfo f;
+        f.n_w[0] = pt.n_w[0], f.n_w[1] = pt.n_w[1], f.n_kv = pt.n_kv, f.c0 = pt.c0;
+        f.q = it.q, f.n = it.n, f.h = it.h, f.rb = it.rb;
+        f.kind = 1 | (pt.c0 == 0 ? 2 : 0) | (pt.c0 + pt.span == it.nc ? 4 : 0);
+        sh_info[qb] = f;
         mbar_arrive_expect_tx(&bar_q[qb], 2 * tile_bytes);
         for (int t = 0; t < 2; ++t)
           for (int pn = 0; pn < C::PANELS; ++pn)
             tma_load_3d(&a.tm_q, &bar_q[qb], sQ + (qb * 2 + t) * C::Q_BYTES + pn * C::BM * 128, pn * 64,
                         it.h * s.group, it.q.t0 + (2 * it.rb + t) * a.tile_tokens);
       };
-      TcItem it = first, nx;
+      // the walk: item, part, next
+      auto advance = [&](TcItem& it, Part& pt, int64_t& left) -> bool {
+        left -= pt.span;
+        if (left <= 0) return false;
+        item_next<BN>(a, it);
+        pt = part_of(it, 0, left);
+        return true;
+      };
+      TcItem it = sh_item, nx;
       int64_t left = range;
-      Part pt = part_of(it, first_c0, left), pn_;
+      Part pt = part_of(it, sh_c0, left), pn_;
       int ic = 0, gring = 0, gchunk = 0, tails = 0;
       int pg0 = -1, pg_n = -1, pid = -1;   // lane l holds the page of column pg0 + l of sequence pg_n
       bool ok = mbar_wait_w(&bar_qempty[0], 1, ac);
-      if (ok) issue_q(it, 0);
+      if (ok) issue_q(it, pt, 0);
       while (ok) {
         nx = it;
         pn_ = pt;
@@ -283,10 +322,14 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         bool q_pending = have_next;
         const int nqb = (ic + 1) % C::QBUFS;
         const uint32_t nq_par = (((ic + 1) / C::QBUFS) & 1) ^ 1;
-        for (int c = 0; ok && c < (E4M3 ? 0 : pt.n_kv); ++c, ++gchunk) {
+        for (int c = 0; ok && c < pt.n_kv; ++c, ++gchunk) {
           const int kv0 = (pt.c0 + c) * BN;
           // pages of the chunk: one, or `boxes` of them
           const int col0 = kv0 >> s.ps_shift;
+          if (q_pending && mbar_test_wait_w(smem_u32(&bar_qempty[nqb]), nq_par)) {
+            issue_q(nx, pn_, ic + 1);
+            q_pending = false;
+          }
           if (pg_n != it.n || col0 < pg0 || col0 + boxes > pg0 + 32) {
             pg_n = it.n;
             pg0 = col0;
@@ -300,6 +343,22 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
               }
             }
           }
+          if constexpr (E4M3) {
+            // lanes 0..3 list the chunk's groups of 16 keys
+            const int key0 = kv0 + 16 * (lane & 3), col = key0 >> s.ps_shift;
+            const int page = __shfl_sync(0xffffffffu, pid, col - pg0);
+            const int rows = page < 0 ? 0 : max(0, min(16, it.q.len - key0));
+            const int bad = __ballot_sync(0xffffffffu, lane < 4 && page < 0 && key0 < it.q.len);
+            const int at = gchunk % C::LIST;
+            if (!mbar_wait_w(&bar_lempty[at], ((gchunk / C::LIST) & 1) ^ 1, ac)) { ok = false; break; }
+            if (lane < 4)
+              sh_list[at][lane] = make_int2(((max(page, 0) * s.heads_kv + it.h) << s.ps_shift) +
+                                                (key0 & ((1 << s.ps_shift) - 1)), rows);
+            if (lane == 0) sh_bad[gchunk & 31] = bad;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_lfull[at]);
+            continue;
+          }
           // bits of the boxes that have a page; the y coordinate of lane l's box
           const uint32_t have = (__ballot_sync(0xffffffffu, pid >= 0) >> (col0 - pg0)) & ((1u << boxes) - 1);
           const int mine = __shfl_sync(0xffffffffu, pid, (col0 - pg0 + lane) & 31);
@@ -310,15 +369,11 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           if (!full)
             for (int b = 0; b < boxes; ++b)
               if (!(have >> b & 1)) bad |= ((1 << (box / 16)) - 1) << (b * (box / 16));
-          if (lane == 0) sh_bad[gchunk & 15] = bad;
+          if (lane == 0) sh_bad[gchunk & 31] = bad;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int gi = gring + 2 * c + kv;
             const int slot = gi % C::NSLOT, use = gi / C::NSLOT;
-            if (q_pending && mbar_test_wait_w(smem_u32(&bar_qempty[nqb]), nq_par)) {
-              issue_q(nx, ic + 1);
-              q_pending = false;
-            }
             if (!mbar_wait_w(&bar_empty[slot], (use & 1) ^ 1, ac)) { ok = false; break; }
             uint8_t* dst = sRing + slot * C::KV_BYTES;
             const CUtensorMap* m = kv ? &a.tm_v : &a.tm_k;
@@ -346,14 +401,30 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         }
         if (ok && q_pending) {
           ok = mbar_wait_w(&bar_qempty[nqb], nq_par, ac);
-          if (ok) issue_q(nx, ic + 1);
+          if (ok) issue_q(nx, pn_, ic + 1);
         }
         gring += 2 * pt.n_kv;
         ++ic;
-        if (!have_next) break;
+        if (!have_next) {   // no more parts
+          const int qb = ic % C::QBUFS;
+          if (ok && mbar_wait_w(&bar_qempty[qb], ((ic / C::QBUFS) & 1) ^ 1, ac) && lane == 0) {
+            sh_info[qb].kind = 0;
+            mbar_arrive(&bar_q[qb]);
+          }
+          break;
+        }
         it = nx;
         pt = pn_;
         left = left_nx;
+      }
+      if constexpr (E4M3) {   // the list's end
+        const int at = gchunk % C::LIST;
+        if (ok && mbar_wait_w(&bar_lempty[at], ((gchunk / C::LIST) & 1) ^ 1, ac)) {
+          if (lane == 0) {
+            sh_list[at][0].x = sh_list[at][1].x = sh_list[at][2].x = sh_list[at][3].x = -1;
+            mbar_arrive(&bar_lfull[at]);
+          }
+        }
       }
     }
   } else if (warp == 9 || warp == 10) {
@@ -367,18 +438,16 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       const uint32_t tS = tmem + (t ? C::COL_S1 : C::COL_S0);
       const uint32_t tO = tmem + (t ? C::COL_O1 : C::COL_O0);
       const uint32_t tP = tmem + (t ? C::COL_P1 : C::COL_P0);
-      TcItem it = first;
-      int64_t left = range;
-      Part pt = part_of(it, first_c0, left);
       int ic = 0, gring = 0, cs = 0;   // cs: S tiles of this query tile so far
-      bool ok = true, stagger = t == 1;
+      bool ok = true;
       while (ok) {
         const int qb = ic % C::QBUFS, qu = ic / C::QBUFS;
-        const int nt = pt.n_w[t];
         if (!mbar_wait_w(&bar_q[qb], qu & 1, ac)) break;
+        if (sh_info[qb].kind == 0) break;
+        const int nt = sh_info[qb].n_w[t], n_kv = sh_info[qb].n_kv;
         // tile 1 starts one softmax phase after tile 0, as in attn_fwd (only where
         // tile 0 of the first item computes something)
-        if (stagger && ic == 0 && pt.n_w[0] > 0 && !mbar_wait_w(&bar_stagger, 0, ac)) break;
+        if (t == 1 && ic == 0 && sh_info[qb].n_w[0] > 0 && !mbar_wait_w(&bar_stagger, 0, ac)) break;
         const uint64_t dQt = desc_kmajor_base(smem_u32(sQ + (qb * 2 + t) * C::Q_BYTES));
         auto issue_s = [&](int j) -> bool {
           const int gi = gring + 2 * j, sk = gi % C::NSLOT;
@@ -424,7 +493,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         }
         // chunks that this tile does not reach: it still waits for each load and
         // releases the slot itself, so that it stays within one phase of it
-        for (int j = nt; ok && j < pt.n_kv; ++j) {
+        for (int j = nt; ok && j < n_kv; ++j) {
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int gi = gring + 2 * j + kv, sl = gi % C::NSLOT;
@@ -436,127 +505,97 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           if (nt > 0) umma_commit_w(&bar_qempty[qb]);
           else if (lane == 0) mbar_arrive(&bar_qempty[qb]);
         }
-        gring += 2 * pt.n_kv;
+        gring += 2 * n_kv;
         cs += nt;
         ++ic;
-        if (!ok || !advance(it, pt, left)) break;
       }
     }
   } else if (E4M3 && warp > 10) {
     // ---------------- e4m3: codes to bf16 values ----------------
-    // Warp w has keys 16 w .. 16 w + 15 of every chunk, which lie in one page under one
-    // scale; a thread copies, four chunks of keys or values ahead, the vectors of 16 codes
-    // that it converts: vector 4 j + lane % 4 of rows lane / 4 and lane / 4 + 8.  Codes go
-    // through fp16 and fp32 (exactly, NaN included); code * scale is rounded to bf16,
-    // which is exact for scales that are powers of two.
+    // Four warps for the keys, four for the values; warp w of them has keys 16 w ..
+    // 16 w + 15 of every chunk, which lie in one page under one scale.  A thread copies, RAW
+    // chunks ahead, the vectors of 16 codes that it converts: vector 4 j + lane % 4 of rows
+    // lane / 4 and lane / 4 + 8.  Codes go through fp16 and fp32 (exactly, NaN included);
+    // code * scale is rounded to bf16, which is exact for scales that are powers of two.
+    // (Moving bits and one bf16 multiply, for such scales, measured 9% slower.)
     if constexpr (E4M3) {
-      if (range > 0) {
+      if (range > 0 && warp >= 12) {
         constexpr int NV = 2 * C::PANELS;   // vectors of a thread
-        const int w = warp - 11;
-        uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + w * (C::RAW_BYTES / 4);   // + stage * RAW_BYTES
-        TcItem cp = first;                  // the copies' place
-        int64_t cp_left = range;
-        Part cp_pt = part_of(cp, first_c0, cp_left);
-        int cp_c = 0, cp_half = 0, cp_chunk = 0;
-        int pg0 = -1, pg_n = -1, pid = -1;  // lane l holds the page of column pg0 + l of sequence pg_n
-        bool cp_more = true;
+        const int w = warp & 3, values = warp >= 16;
+        const uint8_t* pool = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache);
+        const float* scales = values ? a.v_scale : a.k_scale;
+        uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + (values * C::RAW * 4 + w) * (C::RAW_BYTES / 4);
+        float* sc_at = sh_scale[values][w];
+        const int lane_row = lane >> 2;
+        const int lane_off = lane_row * D + (lane & 3) * 16;
+        int copied = 0;   // chunks taken from the list
+        bool more = true;
         auto copy = [&]() {
-          if (cp_more && !(cp_half & 1))
-            while (cp_c >= cp_pt.n_kv) {
-              cp_more = advance(cp, cp_pt, cp_left);
-              cp_c = 0;
-              if (!cp_more) break;
-            }
-          if (cp_more) {
-            const int key0 = (cp_pt.c0 + cp_c) * BN + 16 * w;
-            const int col = key0 >> s.ps_shift;
-            if (pg_n != cp.n || col < pg0 || col >= pg0 + 32) {
-              pg_n = cp.n;
-              pg0 = col;
-              const int cc = col + lane;
-              pid = -1;
-              if (cc <= (cp.q.len - 1) >> s.ps_shift) {
-                pid = __ldg(s.table + static_cast<int64_t>(cp.n) * s.max_pages + cc);
-                if (pid < 0 || pid >= s.num_pages) {
-                  pid = -1;
-                  if (s.err) atomicOr(s.err, ATTN_DEVERR_INDEX_RANGE);
-                }
-              }
-            }
-            const int page = __shfl_sync(0xffffffffu, pid, col - pg0);
-            const bool values = cp_half & 1;
-            const int64_t ph = static_cast<int64_t>(max(page, 0)) * s.heads_kv + cp.h;
-            const uint8_t* src = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache) +
-                                 ((ph << s.ps_shift) + (key0 & ((1 << s.ps_shift) - 1))) * D;
-            uint8_t* dst = raw + (cp_half % C::RAW) * C::RAW_BYTES;
+          const int at = copied % C::LIST;
+          more = mbar_wait_w(&bar_lfull[at], (copied / C::LIST) & 1, ac);
+          if (!more) return;
+          const int2 e = sh_list[at][w];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_lempty[at]);
+          more = e.x >= 0;
+          if (!more) return;
+          const uint8_t* src = pool + static_cast<int64_t>(e.x) * D + lane_off;
+          const int st = copied % C::RAW;
+          const uint32_t dst = smem_u32(raw) + st * C::RAW_BYTES + lane * 16;
+          const uint32_t n0 = lane_row < e.y ? 16u : 0u, n1 = lane_row + 8 < e.y ? 16u : 0u;   // else zeros
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const int row = (v & 1) * 8 + (lane >> 2);
-              const uint32_t n = page >= 0 && key0 + row < cp.q.len ? 16u : 0u;   // else zeros
-              cp_async16(smem_u32(dst + (v * 32 + lane) * 16), src + row * D + (v >> 1) * 64 + (lane & 3) * 16, n);
-            }
-            if (lane == 0) {
-              float* sc = &sh_scale[w][cp_half % C::RAW];
-              if (page >= 0)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sc)),
-                             "l"((values ? a.v_scale : a.k_scale) + ph)
-                             : "memory");
-              else
-                *sc = 0.f;
-              // (missing pages; keys past the length are masked by it)
-              if (!values)
-                reinterpret_cast<volatile uint8_t*>(&sh_bad[cp_chunk & 15])[w] = page < 0 && key0 < cp.q.len;
-            }
-            if (values) {
-              ++cp_c;
-              ++cp_chunk;
-            }
-            ++cp_half;
+          for (int v = 0; v < NV; ++v)
+            cp_async16(dst + v * 512, src + (v & 1) * 8 * D + (v >> 1) * 64, (v & 1) ? n1 : n0);
+          if (lane == 0) {
+            if (e.y > 0)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sc_at + st)),
+                           "l"(scales + (e.x >> s.ps_shift))
+                           : "memory");
+            else
+              sc_at[st] = 0.f;
           }
           cp_async_commit();
+          ++copied;
         };
-        TcItem it = first;
-        int64_t left = range;
-        Part pt = part_of(it, first_c0, left);
-        for (int i = 0; i < C::RAW; ++i) copy();
-        int half = 0;
-        bool ok = true;
-        while (ok) {
-          for (int i = 0; ok && i < 2 * pt.n_kv; ++i, ++half) {
-            cp_async_wait<C::RAW - 1>();
-            __syncwarp();
-            const int slot = half % C::NSLOT;
-            if (!mbar_wait_w(&bar_empty[slot], ((half / C::NSLOT) & 1) ^ 1, ac)) { ok = false; break; }
-            const uint8_t* src = raw + (half % C::RAW) * C::RAW_BYTES;
-            const float sc = sh_scale[w][half % C::RAW];
-            const uint64_t sc2 = f2_pack(sc, sc);
-            uint8_t* dst = sRing + slot * C::KV_BYTES;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const int row = 16 * w + (v & 1) * 8 + (lane >> 2);
-              const uint4 x = *reinterpret_cast<const uint4*>(src + (v * 32 + lane) * 16);
-              const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                uint32_t h;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-                    : "=r"(h)
-                    : "h"(static_cast<uint16_t>(xx[e >> 1] >> (16 * (e & 1)))));
-                const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-                y[e] = f2_to_bf16x2(f2_mul(f2_pack(f.x, f.y), sc2));
-              }
-              uint8_t* line = dst + (v >> 1) * (BN * 128) + row * 128;
-              const int ch = 2 * (lane & 3);
-              *reinterpret_cast<uint4*>(line + ((ch ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar_full[slot]);
-            __syncwarp();
+        for (int i = 0;; ++i) {
+          // RAW chunks ahead, but a chunk in hand never waits for the list: what comes
+          // next may depend on it (a part's query tiles on an earlier part's end)
+          while (more && copied < i + C::RAW &&
+                 (copied == i || mbar_test_wait_w(smem_u32(&bar_lfull[copied % C::LIST]), (copied / C::LIST) & 1)))
             copy();
+          if (copied == i) break;
+          static_assert(C::RAW == 2, "the waits below");
+          if (copied > i + 1) cp_async_wait<1>();
+          else cp_async_wait<0>();
+          __syncwarp();
+          const int gi = 2 * i + values, slot = gi % C::NSLOT;
+          if (!mbar_wait_w(&bar_empty[slot], ((gi / C::NSLOT) & 1) ^ 1, ac)) break;
+          const uint8_t* src = raw + (i % C::RAW) * C::RAW_BYTES + lane * 16;
+          const float sc = sc_at[i % C::RAW];
+          const uint64_t sc2 = f2_pack(sc, sc);
+          uint8_t* dst = sRing + slot * C::KV_BYTES + (16 * w + lane_row) * 128;
+          const int sw = lane_row & 7, ch = 2 * (lane & 3);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + v * 512);
+            const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint32_t h;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                  : "=r"(h)
+                  : "h"(static_cast<uint16_t>(xx[e >> 1] >> (16 * (e & 1)))));
+              const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+              y[e] = f2_to_bf16x2(f2_mul(f2_pack(f.x, f.y), sc2));
+            }
+            uint8_t* line = dst + (v >> 1) * (BN * 128) + (v & 1) * 8 * 128;
+            *reinterpret_cast<uint4*>(line + ((ch ^ sw) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(line + (((ch + 1) ^ sw) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
-          if (!ok || !advance(it, pt, left)) break;
+          fence_proxy_async_smem();
+          mbar_arrive(&bar_full[slot]);
+          __syncwarp();
         }
         cp_async_wait<0>();
       }
@@ -575,15 +614,24 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const int row_tok = tr / s.group, row_head = tr - row_tok * s.group;
     const bool row_in = row_tok < a.tile_tokens;
-    TcItem it = first;
-    int64_t left = range;
-    Part pt = part_of(it, first_c0, left);
-    int cs = 0, gchunk = 0;
+    int ic = 0, cs = 0, gchunk = 0;
     bool ok = true;
     while (ok) {
-      const int nt = pt.n_w[t];
-      const int tok0 = (2 * it.rb + t) * a.tile_tokens, tok = tok0 + row_tok;
-      const int lim = a.causal ? min(it.q.len - 1, it.q.pos0 + tok) : it.q.len - 1;   // last key seen
+      const int qb = ic % C::QBUFS;
+      if (!mbar_wait(&bar_q[qb], (ic / C::QBUFS) & 1, ac)) break;
+      const PartInfo& f = sh_info[qb];
+      const int kind = f.kind;
+      if (kind == 0) break;
+      const int nt = f.n_w[t], n_kv = f.n_kv, c0 = f.c0;
+      const int tok0 = (2 * f.rb + t) * a.tile_tokens, tok = tok0 + row_tok;
+      const int len = f.q.len, diag = f.q.pos0 + tok0;   // diag: the first row's position
+      const int lim = a.causal ? min(len - 1, f.q.pos0 + tok) : len - 1;   // last key seen
+      const int row_out = row_in && tok < f.q.m ? f.q.t0 + tok : -1;      // q's and o's row
+      const int hd = f.h * s.group + row_head;
+      if (kind != 7 && threadIdx.x == 0)
+        a.part_meta[2 * blockIdx.x + (kind >> 1 & 1)] = make_int4(kind, f.n, f.h, f.rb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_qempty[qb]);   // (the warp has read what it needs of f)
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nt; ++j) {
         const int c = cs + j;
@@ -604,9 +652,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
           for (int cc = 0; cc < BN; ++cc) x[cc] = -x[cc];
         }
-        const int kv0 = (pt.c0 + j) * BN;
-        const int bad = sh_bad[(gchunk + j) & 15];
-        if (kv0 + BN > it.q.len || (a.causal && kv0 + BN - 1 > it.q.pos0 + tok0)) {
+        const int kv0 = (c0 + j) * BN;
+        const int bad = sh_bad[(gchunk + j) & 31];
+        if (kv0 + BN > len || (a.causal && kv0 + BN - 1 > diag)) {
 #pragma unroll
           for (int cc = 0; cc < BN; ++cc)
             if (kv0 + cc > lim) x[cc] = -INFINITY;
@@ -614,7 +662,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         if (bad) {
 #pragma unroll
           for (int cc = 0; cc < BN; ++cc)
-            if (bad >> (BAD_SHIFT * (cc / 16)) & 1) x[cc] = -INFINITY;
+            if (bad >> (cc / 16) & 1) x[cc] = -INFINITY;
         }
         float mx[8];
 #pragma unroll
@@ -672,18 +720,15 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         mbar_arrive(&bar_p[t]);
       }
       // ---- the part's end: normalized rows, or a partial result ----
-      const bool begins = pt.c0 == 0, ends = pt.c0 + pt.span == it.nc, whole = begins && ends;
-      const int which = begins ? 1 : 0;
       if (ok && nt > 0) {
         ok = mbar_wait(&bar_o[t], (cs + nt - 1) & 1, ac);
         tc_fence_after();
       }
       if (ok) {
-        const bool valid = row_in && tok < it.q.m;
+        const bool valid = row_out >= 0, whole = kind == 7;
         const float inv = l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f;
-        const int hd = it.h * s.group + row_head;
-        __nv_bfloat16* orow = a.o + (static_cast<int64_t>(it.q.t0 + tok) * s.heads_q + hd) * D;
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + which) * 2 * C::BM + t * C::BM + tr;
+        __nv_bfloat16* orow = a.o + (static_cast<int64_t>(row_out) * s.heads_q + hd) * D;
+        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1)) * 2 * C::BM + t * C::BM + tr;
 #pragma unroll
         for (int cc = 0; cc < D; cc += 32) {
           uint32_t r[32];
@@ -715,18 +760,16 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         tc_fence_before();
         if (valid) {
           if (whole) {
-            a.lse[static_cast<int64_t>(hd) * s.tokens + it.q.t0 + tok] =
+            a.lse[static_cast<int64_t>(hd) * s.tokens + row_out] =
                 l_run > 0.f || l_run != l_run ? (m_run + __log2f(l_run)) * kLn2 : -INFINITY;
           } else {
             a.part_ml[at] = make_float2(m_run, l_run);
           }
         }
-        if (!whole && threadIdx.x == 0)
-          a.part_meta[2 * blockIdx.x + which] = make_int4(1 | (begins ? 2 : 0) | (ends ? 4 : 0), it.n, it.h, it.rb);
       }
       cs += nt;
-      gchunk += pt.n_kv;
-      if (!ok || !advance(it, pt, left)) break;
+      gchunk += n_kv;
+      ++ic;
     }
   }
 
@@ -756,6 +799,14 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   auto kern = cache_fwd_tc_kernel<D, E4M3>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  if constexpr (E4M3) {
+    // the warpgroups' register shares draw on what the block is launched with: a build
+    // with fewer registers than they count on must not run (it would wait forever)
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < C::REGS) return cudaErrorInvalidConfiguration;
+  }
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   return e != cudaSuccess || grid < 2 ? e : launch_cache_join(a, D, kCacheTcRows, grid, st);

@@ -92,7 +92,7 @@ class Step:
             o[r], lse[:, r], wabs[r], smax[:, r] = OC.attention(self.q[r], k, v, scale, causal)
             vsum[r] = v.abs().sum(0).repeat_interleave(self.hq // self.hkv, 0)
         rows = self.max_new * (self.hq // self.hkv)
-        return dict(o=o, lse=lse, **bounds(o, lse, wabs, vsum, smax, self.D, self.cache, rows))
+        return dict(o=o, lse=lse, wabs=wabs, **bounds(o, lse, wabs, vsum, smax, self.D, self.cache, rows))
 
 
 def bounds(o, lse, wabs, vsum, smax, D, cache, rows):

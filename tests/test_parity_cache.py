@@ -69,6 +69,16 @@ def test_rows_that_see_nothing(cache, causal):
 
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("D", [64, 128])
+def test_items_without_keys_between_others(cache, D):
+    # many rows: items that have no chunk at all before, between and after items of one chunk and more
+    for seqs in ([(0, 20), (100, 40), (0, 20), (0, 33), (64, 30), (0, 40)], [(0, 40)], [(30, 30), (0, 25)],
+                 [(20, 20)] * 3 + [(0, 30)] * 3 + [(20, 20)] * 2, [(0, 30)] * 40 + [(10, 10)] * 40 + [(0, 18)] * 3):
+        s = Step(cache, D, 4, 2, 16, seqs, seed=61)
+        check(s.answer(), *run_fwd(s, expect=4))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("D", [64, 128])
 def test_long_axis_is_split_and_joined(cache, D):
     # one sequence over every CTA, and lengths that put range borders inside items
     s = Step(cache, D, 4, 1, 64, [(12345, 1)], seed=7)
@@ -117,7 +127,7 @@ def test_chunk_with_bad_pages(cache):
         check(dict(o=ro, lse=rl, **b), o[r], lse[:, r])
         ref = s.answer(False)
         r = slice(40, 100)
-        check({n: x[r] if n.startswith("o") else x[:, r] for n, x in ref.items()}, o[r], lse[:, r])
+        check({n: x[:, r] if n.startswith("lse") else x[r] for n, x in ref.items()}, o[r], lse[:, r])
 
 
 @pytest.mark.parametrize("cache", CACHES)
@@ -157,6 +167,41 @@ def test_page_scales_far_apart():
         s.scales[i][live] = torch.exp2(e[live].float())
         s.true[i] = s.pools[i].float().double() * s.scales[i].double()[..., None, None]
     check(s.answer(), *run_fwd(s))
+
+
+@pytest.mark.parametrize("D,m", [(64, 1), (128, 1), (64, 40), (128, 40)])
+def test_subnormal_codes_and_odd_scales(D, m):
+    # codes below the normal range (tiny values under large scales), scales past the range of
+    # the fast conversion and, for values, scales that are no powers of two
+    s = Step("e4m3", D, 4, 2, 16, [(120, m), (77, m)], seed=51)
+    g = torch.Generator().manual_seed(3)
+    for i in range(2):
+        live = ~s.scales[i].isnan()
+        x = 0.02 * torch.randn(s.pools[i].shape, generator=g)
+        ok = ~s.pools[i].float().isnan()
+        s.pools[i].view(torch.uint8)[ok] = x.to(F8).view(torch.uint8)[ok]
+        e = torch.randint(0, 12, s.scales[i].shape, generator=g).float()
+        s.scales[i][live] = (torch.exp2(e) * (1.0 if i == 0 else 1.37))[live]
+        s.true[i] = s.pools[i].float().double() * s.scales[i].double()[..., None, None]
+    ref = s.answer(scale=2.0 ** -8)
+    if m > 16:   # the product with such a scale is rounded to bf16
+        ref["o_tol"] += 2.0 ** -8 * ref["wabs"]
+    check(ref, *run_fwd(s, scale=2.0 ** -8))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("m", [1, 40])
+def test_nan_of_a_seen_key_stays_nan(cache, m):
+    s = Step(cache, 64, 4, 2, 16, [(100, m), (100, m)], seed=52)
+    (q, k, v), kw = s.to(DEV)
+    page = int(s.table[0, 1])
+    v.view(torch.uint8 if cache == "e4m3" else torch.int16)[page, 0, 3, 5] = 0x7f if cache == "e4m3" else 0x7fc0
+    o, lse = A.attn_cache_fwd(q, k, v, causal=False, **kw)
+    bad = o[:m, :2, 5].isnan()
+    assert bad.all() and int(o.isnan().sum()) == bad.numel() and torch.isfinite(lse[:, :2 * m]).all()
+    k.view(torch.uint8 if cache == "e4m3" else torch.int16)[page, 1, 3, 5] = 0x7f if cache == "e4m3" else 0x7fc0
+    o, lse = A.attn_cache_fwd(q, k, v, causal=False, **kw)
+    assert o[:m, 2:].isnan().all() and lse[2:, :m].isnan().all() and torch.isfinite(o[m:2 * m].float()).all()
 
 
 def test_lowest_and_infinite_keys():
