@@ -33,18 +33,15 @@ struct TcCfg {
   static constexpr int PANELS = D / 64;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int NSLOT = D == 128 && E4M3 ? 4 : 6;
-  static constexpr int QBUFS = 2;
-  // e4m3: warps 12..15 bring the keys' codes, warps 16..19 the values', into a ring of
-  // RAW chunks each and convert them into the slots, after a list that warp 8 writes
-  static constexpr int RAW = 2, RAW_BYTES = E4M3 ? BN * D : 0;
-  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + 2 * RAW * RAW_BYTES + 1024;
-  static constexpr int THREADS = E4M3 ? 640 : 352;
-  static constexpr int LIST = 8;   // chunks of the list
-  // e4m3: registers of a thread, at launch and then by warpgroup (softmax, issue and
-  // copy, conversion); the shares add up to what the block was launched with
-  static constexpr int REGS = 96, REGS_SOFTMAX = 120, REGS_ISSUE = 80, REGS_CONVERT = 80;
-  static_assert(2 * REGS_SOFTMAX + REGS_ISSUE + 2 * REGS_CONVERT <= 5 * REGS, "register shares");
+  static constexpr int NSLOT = 6;
+  static constexpr int QBUFS = E4M3 ? 1 : 2;   // query tile pairs
+  // e4m3: warp 8 brings the codes into a ring of RAW chunks of keys or values, which
+  // warps 11..14 convert into the slots
+  static constexpr int RAW = 4, RAW_BYTES = E4M3 ? BN * D : 0;
+  static constexpr int SMEM = QBUFS * 2 * Q_BYTES + NSLOT * KV_BYTES + RAW * RAW_BYTES + 1024;
+  static constexpr int THREADS = E4M3 ? 480 : 352;
+  static constexpr int INFOS = 2;   // parts announced at a time
+  static_assert(E4M3 || QBUFS == INFOS, "a bf16 part's queries come with its announcement");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S0 = 0, COL_S1 = BN, COL_O0 = 256, COL_O1 = 256 + D;
   static constexpr uint32_t COL_P0 = D == 128 ? 2 * BN : 256 + 2 * D, COL_P1 = COL_P0 + BN / 2;
@@ -57,13 +54,13 @@ struct TcCfg {
 // tiles, its first and last chunk and its outputs.
 constexpr int kItemCost = 3;
 
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// A contiguous copy, 16-byte aligned on both sides and a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* m, uint64_t* bar, void* dst, int c0,
@@ -161,20 +158,20 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   uint8_t* sQ = smem;                                // QBUFS x 2 tiles
   uint8_t* sRing = sQ + C::QBUFS * 2 * C::Q_BYTES;   // NSLOT chunks of keys or values
 
-  __shared__ uint64_t bar_q[C::QBUFS], bar_qempty[C::QBUFS];
+  __shared__ uint64_t bar_q[C::INFOS], bar_qempty[C::INFOS], bar_qready[2];
   __shared__ uint64_t bar_full[C::NSLOT], bar_empty[C::NSLOT], bar_tail;
   __shared__ uint64_t bar_s[2], bar_p[2], bar_o[2], bar_sfree[2], bar_stagger;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ int sh_bad[32];   // by chunk: 16-key groups (bits) without a page
-  // e4m3, by chunk: the pool row of each 16-key group and how many of its rows exist
-  // (first group -1: the end); the scales of the groups in the raw rings
-  __shared__ int2 sh_list[C::LIST][4];
-  __shared__ uint64_t bar_lfull[C::LIST], bar_lempty[C::LIST];
-  __shared__ float sh_scale[2][4][C::RAW];
+  // e4m3, by chunk: the key scale and log2 of the value scale of its 16-key groups; by raw
+  // chunk: its barriers, which rows exist (a bit each), and whether it is one at all
+  __shared__ float2 sh_scale[E4M3 ? 32 : 1][4];
+  __shared__ uint64_t bar_rfull[C::RAW], bar_rempty[C::RAW], sh_rows[C::RAW];
+  __shared__ int sh_more[C::RAW];
   __shared__ int64_t sh_warp[C::THREADS / 32 + 1];
   __shared__ TcItem sh_item;
-  __shared__ PartInfo sh_info[C::QBUFS];
+  __shared__ PartInfo sh_info[C::INFOS];
   __shared__ int sh_c0;
   __shared__ int64_t sh_left;
 
@@ -187,7 +184,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     sh_left = 0;
-    for (int b = 0; b < C::QBUFS; ++b) {
+    for (int b = 0; b < C::INFOS; ++b) {
       mbar_init(&bar_q[b], 1);
       mbar_init(&bar_qempty[b], 10);     // released by both issuers and 8 softmax warps
     }
@@ -197,20 +194,21 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     }
     mbar_init(&bar_tail, 1);
     if constexpr (E4M3)
-      for (int i = 0; i < C::LIST; ++i) {
-        mbar_init(&bar_lfull[i], 1);
-        mbar_init(&bar_lempty[i], 8);    // released by the converting warps
+      for (int i = 0; i < C::RAW; ++i) {
+        mbar_init(&bar_rfull[i], 1);
+        mbar_init(&bar_rempty[i], 4);    // released by the converting warps
       }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar_s[w], 1);
       mbar_init(&bar_p[w], 128);
       mbar_init(&bar_o[w], 1);
       mbar_init(&bar_sfree[w], 128);
+      mbar_init(&bar_qready[w], 128);
     }
     mbar_init(&bar_stagger, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&a.tm_q);
     if constexpr (!E4M3) {
+      tma_prefetch_desc(&a.tm_q);
       tma_prefetch_desc(&a.tm_k);
       tma_prefetch_desc(&a.tm_v);
     }
@@ -275,11 +273,6 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   const uint32_t tmem = tmem_base_sh;
   const int64_t range = sh_left;   // chunks of the CTA
 
-  if constexpr (E4M3) {
-    if (warp < 8) setmaxnreg_inc<C::REGS_SOFTMAX>();
-    else if (warp < 12) setmaxnreg_dec<C::REGS_ISSUE>();
-    else setmaxnreg_dec<C::REGS_CONVERT>();
-  }
   if (warp == 8) {
     // ---------------- copies (warp-uniform, lane 0 issues) ----------------
     if (range > 0) {
@@ -287,12 +280,16 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       const int tile_bytes = a.tile_tokens * s.group * 128 * C::PANELS;
       auto issue_q = [&](const TcItem& it, const Part& pt, int icq) {
         if (lane != 0) return;
-        const int qb = icq % C::QBUFS;
+        const int qb = icq % C::INFOS;
         PartInfo f;
         f.n_w[0] = pt.n_w[0], f.n_w[1] = pt.n_w[1], f.n_kv = pt.n_kv, f.c0 = pt.c0;
         f.q = it.q, f.n = it.n, f.h = it.h, f.rb = it.rb;
         f.kind = 1 | (pt.c0 == 0 ? 2 : 0) | (pt.c0 + pt.span == it.nc ? 4 : 0);
         sh_info[qb] = f;
+        if constexpr (E4M3) {   // (the softmax warps bring the rows)
+          mbar_arrive(&bar_q[qb]);
+          return;
+        }
         mbar_arrive_expect_tx(&bar_q[qb], 2 * tile_bytes);
         for (int t = 0; t < 2; ++t)
           for (int pn = 0; pn < C::PANELS; ++pn)
@@ -311,7 +308,10 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       int64_t left = range;
       Part pt = part_of(it, sh_c0, left), pn_;
       int ic = 0, gring = 0, gchunk = 0, tails = 0;
-      int pg0 = -1, pg_n = -1, pid = -1;   // lane l holds the page of column pg0 + l of sequence pg_n
+      // lane l holds the page of column pg0 + l of sequence pg_n, e4m3: and its scales for
+      // KV head pg_h
+      int pg0 = -1, pg_n = -1, pg_h = -1, pid = -1;
+      float pks = 1.f, pvs = 0.f;
       bool ok = mbar_wait_w(&bar_qempty[0], 1, ac);
       if (ok) issue_q(it, pt, 0);
       while (ok) {
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         int64_t left_nx = left;
         const bool have_next = advance(nx, pn_, left_nx);
         bool q_pending = have_next;
-        const int nqb = (ic + 1) % C::QBUFS;
-        const uint32_t nq_par = (((ic + 1) / C::QBUFS) & 1) ^ 1;
+        const int nqb = (ic + 1) % C::INFOS;
+        const uint32_t nq_par = (((ic + 1) / C::INFOS) & 1) ^ 1;
         for (int c = 0; ok && c < pt.n_kv; ++c, ++gchunk) {
           const int kv0 = (pt.c0 + c) * BN;
           // pages of the chunk: one, or `boxes` of them
@@ -342,22 +342,22 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
                 if (s.err) atomicOr(s.err, ATTN_DEVERR_INDEX_RANGE);
               }
             }
+            pg_h = -1;
           }
           if constexpr (E4M3) {
-            // lanes 0..3 list the chunk's groups of 16 keys
+            if (pg_h != it.h) {
+              pg_h = it.h;
+              pks = 1.f, pvs = 0.f;
+              if (pid >= 0) {
+                pks = __ldg(a.k_scale + static_cast<int64_t>(pid) * s.heads_kv + it.h);
+                pvs = __log2f(__ldg(a.v_scale + static_cast<int64_t>(pid) * s.heads_kv + it.h));
+              }
+            }
+            // the scales of the chunk's groups of 16 keys (lanes 0..3)
             const int key0 = kv0 + 16 * (lane & 3), col = key0 >> s.ps_shift;
-            const int page = __shfl_sync(0xffffffffu, pid, col - pg0);
-            const int rows = page < 0 ? 0 : max(0, min(16, it.q.len - key0));
-            const int bad = __ballot_sync(0xffffffffu, lane < 4 && page < 0 && key0 < it.q.len);
-            const int at = gchunk % C::LIST;
-            if (!mbar_wait_w(&bar_lempty[at], ((gchunk / C::LIST) & 1) ^ 1, ac)) { ok = false; break; }
-            if (lane < 4)
-              sh_list[at][lane] = make_int2(((max(page, 0) * s.heads_kv + it.h) << s.ps_shift) +
-                                                (key0 & ((1 << s.ps_shift) - 1)), rows);
-            if (lane == 0) sh_bad[gchunk & 31] = bad;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_lfull[at]);
-            continue;
+            const float ks = __shfl_sync(0xffffffffu, pks, col - pg0);
+            const float vs = __shfl_sync(0xffffffffu, pvs, col - pg0);
+            if (lane < 4) sh_scale[gchunk & 31][lane] = make_float2(ks, vs);
           }
           // bits of the boxes that have a page; the y coordinate of lane l's box
           const uint32_t have = (__ballot_sync(0xffffffffu, pid >= 0) >> (col0 - pg0)) & ((1u << boxes) - 1);
@@ -370,6 +370,29 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             for (int b = 0; b < boxes; ++b)
               if (!(have >> b & 1)) bad |= ((1 << (box / 16)) - 1) << (b * (box / 16));
           if (lane == 0) sh_bad[gchunk & 31] = bad;
+          if constexpr (E4M3) {
+            // rows that exist: those below the length, less those of missing pages
+            uint64_t rows = kv0 + 64 > it.q.len ? (1ull << (it.q.len - kv0)) - 1 : ~0ull;
+            for (int g = 0; g < 4; ++g)
+              if (bad >> g & 1) rows &= ~(0xffffull << (16 * g));
+            const int64_t at = static_cast<int64_t>(y) * D;   // of lane b's box
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const int gi = gring + 2 * c + kv, slot = gi % C::RAW;
+              if (!mbar_wait_w(&bar_rempty[slot], ((gi / C::RAW) & 1) ^ 1, ac)) { ok = false; break; }
+              uint64_t* bar = &bar_rfull[slot];
+              if (lane == 0) {
+                sh_rows[slot] = rows;
+                sh_more[slot] = 1;
+                mbar_arrive_expect_tx(bar, __popc(have) * box * D);
+              }
+              __syncwarp();
+              if (lane < boxes && mine >= 0)
+                bulk_load(bar, sRing + C::NSLOT * C::KV_BYTES + slot * C::RAW_BYTES + lane * box * D,
+                          static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache) + at, box * D);
+            }
+            continue;
+          }
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int gi = gring + 2 * c + kv;
@@ -406,8 +429,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         gring += 2 * pt.n_kv;
         ++ic;
         if (!have_next) {   // no more parts
-          const int qb = ic % C::QBUFS;
-          if (ok && mbar_wait_w(&bar_qempty[qb], ((ic / C::QBUFS) & 1) ^ 1, ac) && lane == 0) {
+          const int qb = ic % C::INFOS;
+          if (ok && mbar_wait_w(&bar_qempty[qb], ((ic / C::INFOS) & 1) ^ 1, ac) && lane == 0) {
             sh_info[qb].kind = 0;
             mbar_arrive(&bar_q[qb]);
           }
@@ -417,13 +440,11 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         pt = pn_;
         left = left_nx;
       }
-      if constexpr (E4M3) {   // the list's end
-        const int at = gchunk % C::LIST;
-        if (ok && mbar_wait_w(&bar_lempty[at], ((gchunk / C::LIST) & 1) ^ 1, ac)) {
-          if (lane == 0) {
-            sh_list[at][0].x = sh_list[at][1].x = sh_list[at][2].x = sh_list[at][3].x = -1;
-            mbar_arrive(&bar_lfull[at]);
-          }
+      if constexpr (E4M3) {   // no more chunks
+        const int slot = gring % C::RAW;
+        if (ok && mbar_wait_w(&bar_rempty[slot], ((gring / C::RAW) & 1) ^ 1, ac) && lane == 0) {
+          sh_more[slot] = 0;
+          mbar_arrive(&bar_rfull[slot]);
         }
       }
     }
@@ -431,24 +452,27 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     // ---------------- MMA issuer of query tile t ----------------
     const int t = warp - 9;
     if (range > 0) {
-      const uint32_t idS = idesc_bf16(C::BM, BN, false, false);
-      const uint32_t idO = idesc_bf16(C::BM, D, false, true);
+      // bf16 operands, e4m3: fp16 (A and B formats, bits 7..12, 0)
+      constexpr uint32_t fmt = E4M3 ? ~(0x3fu << 7) : ~0u;
+      const uint32_t idS = idesc_bf16(C::BM, BN, false, false) & fmt;
+      const uint32_t idO = idesc_bf16(C::BM, D, false, true) & fmt;
       const uint64_t dR_k0 = desc_kmajor_base(smem_u32(sRing));
       const uint64_t dR_mn0 = desc_mnmajor_base(smem_u32(sRing), BN);
       const uint32_t tS = tmem + (t ? C::COL_S1 : C::COL_S0);
       const uint32_t tO = tmem + (t ? C::COL_O1 : C::COL_O0);
       const uint32_t tP = tmem + (t ? C::COL_P1 : C::COL_P0);
-      int ic = 0, gring = 0, cs = 0;   // cs: S tiles of this query tile so far
+      int ic = 0, gring = 0, cs = 0, qc = 0;   // cs, qc: S and query tiles of this tile so far
       bool ok = true;
       while (ok) {
-        const int qb = ic % C::QBUFS, qu = ic / C::QBUFS;
+        const int qb = ic % C::INFOS, qu = ic / C::INFOS;
         if (!mbar_wait_w(&bar_q[qb], qu & 1, ac)) break;
         if (sh_info[qb].kind == 0) break;
         const int nt = sh_info[qb].n_w[t], n_kv = sh_info[qb].n_kv;
         // tile 1 starts one softmax phase after tile 0, as in attn_fwd (only where
         // tile 0 of the first item computes something)
         if (t == 1 && ic == 0 && sh_info[qb].n_w[0] > 0 && !mbar_wait_w(&bar_stagger, 0, ac)) break;
-        const uint64_t dQt = desc_kmajor_base(smem_u32(sQ + (qb * 2 + t) * C::Q_BYTES));
+        const uint64_t dQt = desc_kmajor_base(smem_u32(sQ + ((E4M3 ? 0 : qb) * 2 + t) * C::Q_BYTES));
+        if (E4M3 && nt > 0 && !mbar_wait_w(&bar_qready[t], qc++ & 1, ac)) break;
         auto issue_s = [&](int j) -> bool {
           const int gi = gring + 2 * j, sk = gi % C::NSLOT;
           if (!mbar_wait_w(&bar_full[sk], (gi / C::NSLOT) & 1, ac)) return false;
@@ -511,93 +535,52 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       }
     }
   } else if (E4M3 && warp > 10) {
-    // ---------------- e4m3: codes to bf16 values ----------------
-    // Four warps for the keys, four for the values; warp w of them has keys 16 w ..
-    // 16 w + 15 of every chunk, which lie in one page under one scale.  A thread copies, RAW
-    // chunks ahead, the vectors of 16 codes that it converts: vector 4 j + lane % 4 of rows
-    // lane / 4 and lane / 4 + 8.  Codes go through fp16 and fp32 (exactly, NaN included);
-    // code * scale is rounded to bf16, which is exact for scales that are powers of two.
-    // (Moving bits and one bf16 multiply, for such scales, measured 9% slower.)
+    // ---------------- e4m3: codes to fp16, exactly ----------------
+    // Warp w of four has rows 16 w .. 16 w + 15 of every chunk of keys or values; a thread
+    // takes vectors of 16 codes.  The scales are left to the softmax.  (code * scale as
+    // bf16, four instructions more for two codes, and per-thread copies of the codes took
+    // eight warps and 712 us where this form takes F16US.)
     if constexpr (E4M3) {
-      if (range > 0 && warp >= 12) {
-        constexpr int NV = 2 * C::PANELS;   // vectors of a thread
-        const int w = warp & 3, values = warp >= 16;
-        const uint8_t* pool = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache);
-        const float* scales = values ? a.v_scale : a.k_scale;
-        uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + (values * C::RAW * 4 + w) * (C::RAW_BYTES / 4);
-        float* sc_at = sh_scale[values][w];
-        const int lane_row = lane >> 2;
-        const int lane_off = lane_row * D + (lane & 3) * 16;
-        int copied = 0;   // chunks taken from the list
-        bool more = true;
-        auto copy = [&]() {
-          const int at = copied % C::LIST;
-          more = mbar_wait_w(&bar_lfull[at], (copied / C::LIST) & 1, ac);
-          if (!more) return;
-          const int2 e = sh_list[at][w];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_lempty[at]);
-          more = e.x >= 0;
-          if (!more) return;
-          const uint8_t* src = pool + static_cast<int64_t>(e.x) * D + lane_off;
-          const int st = copied % C::RAW;
-          const uint32_t dst = smem_u32(raw) + st * C::RAW_BYTES + lane * 16;
-          const uint32_t n0 = lane_row < e.y ? 16u : 0u, n1 = lane_row + 8 < e.y ? 16u : 0u;   // else zeros
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-            cp_async16(dst + v * 512, src + (v & 1) * 8 * D + (v >> 1) * 64, (v & 1) ? n1 : n0);
-          if (lane == 0) {
-            if (e.y > 0)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sc_at + st)),
-                           "l"(scales + (e.x >> s.ps_shift))
-                           : "memory");
-            else
-              sc_at[st] = 0.f;
-          }
-          cp_async_commit();
-          ++copied;
-        };
+      if (range > 0) {
+        constexpr int VR = D / 16;          // vectors of a row
+        constexpr int NV = 16 * VR / 32;    // vectors of a thread
+        const int w = warp - 11, v = lane % VR;
+        // two 16-byte pieces of a vector: dims 16 v .. + 7 and + 8 .. + 15; the upper half of
+        // a 128-dim row stores the second first, so that eight lanes meet eight banks
+        const int ch = 2 * (v & 3), flip = v >> 2;
+        const uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + (16 * w) * D + lane * 16;
         for (int i = 0;; ++i) {
-          // RAW chunks ahead, but a chunk in hand never waits for the list: what comes
-          // next may depend on it (a part's query tiles on an earlier part's end)
-          while (more && copied < i + C::RAW &&
-                 (copied == i || mbar_test_wait_w(smem_u32(&bar_lfull[copied % C::LIST]), (copied / C::LIST) & 1)))
-            copy();
-          if (copied == i) break;
-          static_assert(C::RAW == 2, "the waits below");
-          if (copied > i + 1) cp_async_wait<1>();
-          else cp_async_wait<0>();
-          __syncwarp();
-          const int gi = 2 * i + values, slot = gi % C::NSLOT;
-          if (!mbar_wait_w(&bar_empty[slot], ((gi / C::NSLOT) & 1) ^ 1, ac)) break;
-          const uint8_t* src = raw + (i % C::RAW) * C::RAW_BYTES + lane * 16;
-          const float sc = sc_at[i % C::RAW];
-          const uint64_t sc2 = f2_pack(sc, sc);
-          uint8_t* dst = sRing + slot * C::KV_BYTES + (16 * w + lane_row) * 128;
-          const int sw = lane_row & 7, ch = 2 * (lane & 3);
+          const int rs = i % C::RAW, slot = i % C::NSLOT;
+          if (!mbar_wait_w(&bar_rfull[rs], (i / C::RAW) & 1, ac)) break;
+          if (!sh_more[rs]) break;
+          const uint32_t rows = static_cast<uint32_t>(sh_rows[rs] >> (16 * w)) & 0xffffu;
+          if (!mbar_wait_w(&bar_empty[slot], ((i / C::NSLOT) & 1) ^ 1, ac)) break;
+          uint4 x[NV];
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + v * 512);
-            const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+          for (int k = 0; k < NV; ++k) {
+            x[k] = *reinterpret_cast<const uint4*>(raw + rs * C::RAW_BYTES + k * 512);
+            if (rows != 0xffffu && !(rows >> (k * (32 / VR) + lane / VR) & 1)) x[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_rempty[rs]);
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            const int row = 16 * w + k * (32 / VR) + lane / VR;
+            const uint32_t xx[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint32_t h;
+            for (int e = 0; e < 8; ++e)
               asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-                  : "=r"(h)
+                  : "=r"(y[e])
                   : "h"(static_cast<uint16_t>(xx[e >> 1] >> (16 * (e & 1)))));
-              const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-              y[e] = f2_to_bf16x2(f2_mul(f2_pack(f.x, f.y), sc2));
-            }
-            uint8_t* line = dst + (v >> 1) * (BN * 128) + (v & 1) * 8 * 128;
-            *reinterpret_cast<uint4*>(line + ((ch ^ sw) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(line + (((ch + 1) ^ sw) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
+            uint8_t* line = sRing + slot * C::KV_BYTES + (v >> 2) * (BN * 128) + row * 128;
+            *reinterpret_cast<uint4*>(line + (((ch + flip) ^ (row & 7)) << 4)) = flip ? y1 : y0;
+            *reinterpret_cast<uint4*>(line + (((ch + 1 - flip) ^ (row & 7)) << 4)) = flip ? y0 : y1;
           }
           fence_proxy_async_smem();
           mbar_arrive(&bar_full[slot]);
-          __syncwarp();
         }
-        cp_async_wait<0>();
       }
     }
   } else if (range > 0) {
@@ -617,8 +600,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     int ic = 0, cs = 0, gchunk = 0;
     bool ok = true;
     while (ok) {
-      const int qb = ic % C::QBUFS;
-      if (!mbar_wait(&bar_q[qb], (ic / C::QBUFS) & 1, ac)) break;
+      const int qb = ic % C::INFOS;
+      if (!mbar_wait(&bar_q[qb], (ic / C::INFOS) & 1, ac)) break;
       const PartInfo& f = sh_info[qb];
       const int kind = f.kind;
       if (kind == 0) break;
@@ -633,6 +616,49 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_qempty[qb]);   // (the warp has read what it needs of f)
       float m_run = -INFINITY, l_run = 0.f;
+      float rowf = sl2;            // logit factor of the row
+      float lv_ref = -INFINITY;    // e4m3: O is kept in units of 2^lv_ref
+      if constexpr (E4M3) {
+        // The row as fp16 times a power of two, its largest element below 512: exact down
+        // to 2^-32 of it and then within 2^-33 of it.  (The tile is free: its last S of the
+        // part before has been read by this warpgroup.)
+        if (nt > 0) {
+          const __nv_bfloat16* src = a.q + static_cast<int64_t>(max(row_out, 0)) * a.q_stride + hd * D;
+          uint8_t* row = sQ + t * C::Q_BYTES + tr * 128;
+          uint4 v[D / 8];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row_out >= 0) v[i] = *reinterpret_cast<const uint4*>(src + i * 8);
+          }
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w4[e] << 16)),
+                                       fabsf(__uint_as_float(w4[e] & 0xffff0000u))));
+          }
+          const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+          const float up = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
+          rowf *= __uint_as_float(static_cast<uint32_t>(k - 8 + 127) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 hh = __floats2half2_rn(__uint_as_float(w4[e] << 16) * up,
+                                                   __uint_as_float(w4[e] & 0xffff0000u) * up);
+              w4[e] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            *reinterpret_cast<uint4*>(row + (i >> 3) * C::BM * 128 + (((i & 7) ^ (tr & 7)) << 4)) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bar_qready[t]);
+        }
+      }
       for (int j = 0; j < nt; ++j) {
         const int c = cs + j;
         if (!mbar_wait(&bar_s[t], c & 1, ac)) { ok = false; break; }
@@ -664,39 +690,92 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           for (int cc = 0; cc < BN; ++cc)
             if (bad >> (cc / 16) & 1) x[cc] = -INFINITY;
         }
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mx[i] = x[i];
-#pragma unroll
-          for (int b = 1; b + 1 < BN / 8; b += 2) mx[i] = fmax3(mx[i], x[8 * b + i], x[8 * b + 8 + i]);
-          if constexpr ((BN / 8) % 2 == 0) mx[i] = fmaxf(mx[i], x[BN - 8 + i]);
-        }
-        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7]))) * sl2;
-        const float m_new = fmaxf(m_run, mt);
-        const bool grow = m_new > m_run + 8.0f;          // also true on the first finite max
-        const float m_use = grow ? m_new : m_run;
-        const float alpha = grow ? ex2(m_run - m_use) : 1.0f;
-        const float msub = (m_use == -INFINITY) ? 0.f : m_use;
-        const bool warp_rescale = j > 0 && __any_sync(0xffffffffu, grow);
-        const uint64_t nm2 = f2_pack(-msub, -msub), sl2x2 = f2_pack(sl2, sl2);
-        uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
         uint32_t pk[BN / 2];
+        bool grow;
+        float alpha;
+        if constexpr (!E4M3) {
+          float mx[8];
 #pragma unroll
-        for (int cc = 0; cc < BN; cc += 2) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(x[cc], x[cc + 1]), sl2x2, nm2), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          rs2[(cc >> 1) & 3] = f2_add(rs2[(cc >> 1) & 3], f2_pack(p0, p1));
-          pk[cc / 2] = pack_bf16(p0, p1);
+          for (int i = 0; i < 8; ++i) {
+            mx[i] = x[i];
+#pragma unroll
+            for (int b = 1; b + 1 < BN / 8; b += 2) mx[i] = fmax3(mx[i], x[8 * b + i], x[8 * b + 8 + i]);
+            if constexpr ((BN / 8) % 2 == 0) mx[i] = fmaxf(mx[i], x[BN - 8 + i]);
+          }
+          const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7]))) * sl2;
+          const float m_new = fmaxf(m_run, mt);
+          grow = m_new > m_run + 8.0f;          // also true on the first finite max
+          const float m_use = grow ? m_new : m_run;
+          alpha = grow ? ex2(m_run - m_use) : 1.0f;
+          const float msub = (m_use == -INFINITY) ? 0.f : m_use;
+          const uint64_t nm2 = f2_pack(-msub, -msub), sl2x2 = f2_pack(sl2, sl2);
+          uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int cc = 0; cc < BN; cc += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(x[cc], x[cc + 1]), sl2x2, nm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            rs2[(cc >> 1) & 3] = f2_add(rs2[(cc >> 1) & 3], f2_pack(p0, p1));
+            pk[cc / 2] = pack_bf16(p0, p1);
+          }
+          float r0, r1, r2, r3, r4, r5, r6, r7;
+          f2_unpack(rs2[0], r0, r1);
+          f2_unpack(rs2[1], r2, r3);
+          f2_unpack(rs2[2], r4, r5);
+          f2_unpack(rs2[3], r6, r7);
+          l_run = l_run * alpha + (((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7)));
+          m_run = m_use;
+        } else {
+          // four groups of 16 keys with scales of their own: the logits' factor, and log2 of
+          // the values' factor relative to the largest so far, which P takes along and the
+          // row sum takes off again (below 2^-100 nothing of P times it is left in fp16)
+          const float2* sc = sh_scale[(gchunk + j) & 31];
+          float fg[4], lg[4], mt = -INFINITY, lv_new = lv_ref;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float2 kv = sc[g];
+            fg[g] = rowf * kv.x;
+            lg[g] = kv.y;
+            lv_new = fmaxf(lv_new, kv.y);
+            const float* xg = x + 16 * g;
+            float m0 = fmax3(xg[0], xg[1], xg[2]), m1 = fmax3(xg[3], xg[4], xg[5]);
+            m0 = fmax3(m0, xg[6], xg[7]);
+            m1 = fmax3(m1, xg[8], xg[9]);
+            m0 = fmax3(m0, xg[10], xg[11]);
+            m1 = fmax3(m1, xg[12], xg[13]);
+            mt = fmaxf(mt, fmax3(fmax3(m0, xg[14], xg[15]), m1, m1) * fg[g]);
+          }
+          const float m_new = fmaxf(m_run, mt);
+          const bool mgrow = m_new > m_run + 8.0f;
+          const float m_use = mgrow ? m_new : m_run;
+          alpha = mgrow ? ex2(m_run - m_use) : 1.0f;
+          const float msub = (m_use == -INFINITY) ? 0.f : m_use;
+          float sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float l = fmaxf(lg[g] - lv_new, -100.f);
+            const uint64_t nm2 = f2_pack(l - msub, l - msub), f2 = f2_pack(fg[g], fg[g]);
+            uint64_t rs2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int cc = 16 * g; cc < 16 * g + 16; cc += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(x[cc], x[cc + 1]), f2, nm2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              rs2[(cc >> 1) & 1] = f2_add(rs2[(cc >> 1) & 1], f2_pack(p0, p1));
+              const __half2 hh = __floats2half2_rn(p0, p1);
+              pk[cc / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            float r0, r1;
+            f2_unpack(f2_add(rs2[0], rs2[1]), r0, r1);
+            sum += (r0 + r1) * ex2(-l);
+          }
+          l_run = l_run * alpha + sum;
+          m_run = m_use;
+          grow = mgrow || lv_new > lv_ref;
+          if (lv_new > lv_ref) alpha *= ex2(lv_ref - lv_new);   // from here on O's factor
+          lv_ref = lv_new;
         }
-        float r0, r1, r2, r3, r4, r5, r6, r7;
-        f2_unpack(rs2[0], r0, r1);
-        f2_unpack(rs2[1], r2, r3);
-        f2_unpack(rs2[2], r4, r5);
-        f2_unpack(rs2[3], r6, r7);
-        l_run = l_run * alpha + (((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7)));
-        m_run = m_use;
+        const bool warp_rescale = j > 0 && __any_sync(0xffffffffu, grow);
         if (j > 0) {
           // PV(j-1) must be done before O is rescaled and P(j) overwrites P(j-1)
           if (!mbar_wait(&bar_o[t], (c - 1) & 1, ac)) { ok = false; break; }
@@ -726,7 +805,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       }
       if (ok) {
         const bool valid = row_out >= 0, whole = kind == 7;
-        const float inv = l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f;
+        const float unit = E4M3 && nt > 0 ? ex2(lv_ref) : 1.f;
+        const float inv = (l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f) * unit;
         __nv_bfloat16* orow = a.o + (static_cast<int64_t>(row_out) * s.heads_q + hd) * D;
         const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1)) * 2 * C::BM + t * C::BM + tr;
 #pragma unroll
@@ -753,7 +833,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(a.part_o + at * D + cc + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                *reinterpret_cast<float4*>(a.part_o + at * D + cc + i) =
+                    make_float4(__uint_as_float(r[i]) * unit, __uint_as_float(r[i + 1]) * unit,
+                                __uint_as_float(r[i + 2]) * unit, __uint_as_float(r[i + 3]) * unit);
             }
           }
         }
@@ -799,14 +881,6 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   auto kern = cache_fwd_tc_kernel<D, E4M3>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  if constexpr (E4M3) {
-    // the warpgroups' register shares draw on what the block is launched with: a build
-    // with fewer registers than they count on must not run (it would wait forever)
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs < C::REGS) return cudaErrorInvalidConfiguration;
-  }
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   return e != cudaSuccess || grid < 2 ? e : launch_cache_join(a, D, kCacheTcRows, grid, st);

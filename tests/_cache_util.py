@@ -90,7 +90,11 @@ class Step:
             k, v = self.keys(n)
             r = slice(int(self.cu[n]), int(self.cu[n + 1]))
             o[r], lse[:, r], wabs[r], smax[:, r] = OC.attention(self.q[r], k, v, scale, causal)
-            vsum[r] = v.abs().sum(0).repeat_interleave(self.hq // self.hkv, 0)
+            if self.cache != "bf16":
+                sc = self.scales[1][self.table[n, :-(-l // self.ps)].long()].double()      # [pages, Hkv]
+                codes = v.abs() / sc.repeat_interleave(self.ps, 0)[:l, :, None]
+                vs = codes.sum(0) * (sc.max(0).values[:, None] if l else 0)
+                vsum[r] = vs.repeat_interleave(self.hq // self.hkv, 0)
         rows = self.max_new * (self.hq // self.hkv)
         return dict(o=o, lse=lse, wabs=wabs, **bounds(o, lse, wabs, vsum, smax, self.D, self.cache, rows))
 
@@ -104,14 +108,14 @@ def bounds(o, lse, wabs, vsum, smax, D, cache, rows):
     its error is at most (D + 8) 2^-24 smax, in natural units; smax >= 1 covers the
     exponential's own 2^-22 and the fp32 sums and joins (a few dozen of them: 2^-19).
     The error of a probability relative to itself is twice that (numerator and sum).
-    P is rounded, by the kernel for at most 16 query rows per KV head to two bf16 (2^-16) or,
-    e4m3, to fp16 (2^-11, and 2^-25 absolute below its normal range, over a sum of at
-    least 1), by the tcgen05 kernel for more rows to bf16 (2^-8, whatever the cache's
-    type); each of these scales |v|.  Then one rounding to bf16, 2^-8."""
-    few = rows <= 16
+    P is rounded: bf16 caches, to two bf16 (2^-16) for at most 16 query rows per KV head and
+    to bf16 (2^-8) by the tcgen05 kernel for more rows; e4m3, by both to fp16: 2^-11, and
+    2^-25 absolute below its normal range, over a sum of at least 1.  Each of these scales
+    |v|, the last one |code| times the largest page scale (vsum).  Then one rounding to
+    bf16, 2^-8."""
     es = (D + 8) * 2.0 ** -24 * smax.clamp(min=1) + 2.0 ** -19
-    e = 2 * es.t()[..., None] + (2.0 ** -8 if not few else 2.0 ** -16 if cache == "bf16" else 2.0 ** -11)
-    err = e * wabs + (2.0 ** -25 * vsum if few and cache != "bf16" else 0)
+    pr = 2.0 ** -11 if cache != "bf16" else 2.0 ** -16 if rows <= 16 else 2.0 ** -8
+    err = (2 * es.t()[..., None] + pr) * wabs + (2.0 ** -25 * vsum if cache != "bf16" else 0)
     return dict(o_tol=err * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs() + 1e-37,
                 lse_tol=es + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0))
 
