@@ -684,7 +684,7 @@ def attn_cache_empty(num_pages, heads_kv, page_size, head_dim, *, dtype=torch.bf
 
 def _need_rows(t, name, heads, dim, device):
     """bf16 [tokens, heads, dim] whose tokens may lie apart (a slice of a fused
-    projection); returns the elements between two tokens."""
+    projection); returns the elements between two tokens, 0 for dense ones."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.device != device:
@@ -699,39 +699,54 @@ def _need_rows(t, name, heads, dim, device):
     return st[0] if t.shape[0] > 1 else 0
 
 
+# A step of one token takes the GPU a few microseconds, so the checks below look
+# at each tensor once, in one expression, and leave the wording to _need.
 def _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
                    max_new, error_word, tokens, heads_q, causal=1, scale=1.0):
-    # (a step of one token takes the GPU a few microseconds, so this stays short:
-    # each tensor is looked at once, and the fields are set in one go)
-    dtype, dev, shape = k_cache.dtype, k_cache.device, k_cache.shape
+    dtype, shape, gpu = k_cache.dtype, k_cache.shape, k_cache.get_device()
     kind = _CACHE_TYPES.get(dtype)
     if kind is None:
         raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {dtype}")
     if len(shape) != 4:
         raise ValueError("k_cache must be [num_pages, heads_kv, page_size, head_dim]")
-    _need(k_cache, "k_cache", dtype)
-    _need(v_cache, "v_cache", dtype, dev)
+    if (gpu < 0 or not k_cache.is_contiguous() or v_cache.dtype is not dtype
+            or v_cache.get_device() != gpu or not v_cache.is_contiguous()):
+        _need(k_cache, "k_cache", dtype)
+        _need(v_cache, "v_cache", dtype, k_cache.device)
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     if kind:
-        if (_need(k_scale, "k_scale", torch.float32, dev).shape != shape[:2]
-                or _need(v_scale, "v_scale", torch.float32, dev).shape != shape[:2]):
-            raise ValueError("k_scale and v_scale must be [num_pages, heads_kv]")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if _need(t, name, torch.float32, k_cache.device).shape != shape[:2]:
+                raise ValueError(f"{name} must be [num_pages, heads_kv]")
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
-    _need(page_table, "page_table", torch.int32, dev)
-    _need(seqlens_kv, "seqlens_kv", torch.int32, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    i32 = torch.int32
+    if (page_table.dtype is not i32 or seqlens_kv.dtype is not i32 or cu_seqlens.dtype is not i32
+            or page_table.get_device() != gpu or seqlens_kv.get_device() != gpu
+            or cu_seqlens.get_device() != gpu or not page_table.is_contiguous()
+            or not seqlens_kv.is_contiguous() or not cu_seqlens.is_contiguous()):
+        for t, name in ((page_table, "page_table"), (seqlens_kv, "seqlens_kv"),
+                        (cu_seqlens, "cu_seqlens")):
+            _need(t, name, i32, k_cache.device)
     if error_word is not None:
-        _need(error_word, "error_word", torch.int32, dev)
-        error_word = error_word.data_ptr()
-    n = seqlens_kv.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n or cu_seqlens.numel() != n + 1:
+        error_word = _need(error_word, "error_word", i32, k_cache.device).data_ptr()
+    n, table = seqlens_kv.numel(), page_table.shape
+    if len(table) != 2 or table[0] != n or cu_seqlens.numel() != n + 1:
         raise ValueError("seqlens_kv [n], cu_seqlens [n + 1] and page_table [n, max_pages] disagree")
-    return _CacheProblem(n, tokens, heads_q, shape[1], shape[3], kind, shape[2], shape[0],
-                         page_table.shape[1], max_new, causal, scale, 0, 0, 0, 0, 0, 0,
-                         cu_seqlens.data_ptr(), seqlens_kv.data_ptr(), page_table.data_ptr(),
-                         error_word)
+    return _CacheProblem(n, tokens, heads_q, shape[1], shape[3], kind, shape[2], shape[0], table[1],
+                         max_new, causal, scale, 0, 0, 0, 0, 0, 0, cu_seqlens.data_ptr(),
+                         seqlens_kv.data_ptr(), page_table.data_ptr(), error_word)
+
+
+def _rows_stride(t, name, tokens, heads, dim, gpu, device):
+    if (t.dtype is torch.bfloat16 and t.get_device() == gpu and t.shape == (tokens, heads, dim)
+            and t.is_contiguous()):
+        return 0
+    stride = _need_rows(t, name, heads, dim, device)
+    if t.shape[0] != tokens:
+        raise ValueError("q, k and v must have the same tokens")
+    return stride
 
 
 def _on(device, stream):
@@ -772,15 +787,15 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
             raise ValueError("q_out is given without q")
         heads_q = k_cache.shape[1]
     else:
-        if q.dim() != 3 or q.shape[0] != k.shape[0]:
-            raise ValueError("q must be [tokens, heads, head_dim], with the tokens of k and v")
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, head_dim]")
         heads_q = q.shape[1]
+    T = k.shape[0]
     p = _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
-                       int(max_new), error_word, k.shape[0], heads_q)
-    p.k_stride = _need_rows(k, "k", p.heads_kv, p.head_dim, dev)
-    p.v_stride = _need_rows(v, "v", p.heads_kv, p.head_dim, dev)
-    if v.shape[0] != p.tokens:
-        raise ValueError("k and v must have the same tokens")
+                       int(max_new), error_word, T, heads_q)
+    _, heads, _, dim = k_cache.shape
+    p.k_stride = _rows_stride(k, "k", T, heads, dim, dev.index, dev)
+    p.v_stride = _rows_stride(v, "v", T, heads, dim, dev.index, dev)
     if cos_sin is not None:
         if _need(cos_sin, "cos_sin", torch.float32, dev).dim() != 2:
             raise ValueError("cos_sin must be [positions, rot_dim]")
@@ -789,9 +804,9 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
     ctx, s = _on(dev, stream)
     with ctx:
         if q is not None:
-            p.q_stride = _need_rows(q, "q", heads_q, p.head_dim, dev)
+            p.q_stride = _rows_stride(q, "q", T, heads_q, dim, dev.index, dev)
             if q_out is None:
-                q_out = q.new_empty(q.shape)
+                q_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
             elif _need(q_out, "q_out", torch.bfloat16, dev).shape != q.shape:
                 raise ValueError("q_out must have the shape of q")
         code = lib().attn_cache_append(ctypes.byref(p), _at(q), k.data_ptr(), v.data_ptr(),
@@ -809,7 +824,8 @@ def _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlen
     p = _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, cu_seqlens,
                        int(max_new), error_word, q.shape[0], q.shape[1], 1 if causal else 0,
                        float(scale) if scale is not None else 1.0 / math.sqrt(q.shape[2]))
-    p.q_stride = _need_rows(q, "q", p.heads_q, p.head_dim, k_cache.device)
+    dev = k_cache.device
+    p.q_stride = _rows_stride(q, "q", q.shape[0], q.shape[1], k_cache.shape[3], dev.index, dev)
     return p
 
 
@@ -834,7 +850,7 @@ def attn_cache_fwd(q, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, m
     ctx, s = _on(dev, stream)
     with ctx:
         if out is None:
-            out = q.new_empty(shape)
+            out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
         elif _need(out, "out", torch.bfloat16, dev).shape != shape:
             raise ValueError("out must have the shape of q")
         if lse is None:

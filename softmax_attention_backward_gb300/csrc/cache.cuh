@@ -54,17 +54,26 @@ struct AppendArgs {
   __nv_bfloat16* q_out;
   void *k_cache, *v_cache;
   float *k_scale, *v_scale;
-  int unit_blocks;   // leading blocks of the grid that append; the others rotate q
+  // e4m3: leading blocks of the grid, and how they find their pages
+  int unit_blocks;
   int slots;         // page slots per sequence, 0: found by a scan over the sequences
-  int units;         // (page item, KV head, K or V) units
-  FastDiv fd_slots, fd_hq;
+  int units;         // slots > 0: (page item, KV head, K or V) units
+  int head_blocks;   // slots == 0: blocks of a page item
+  FastDiv fd_slots;
+  // the other blocks: row_blocks blocks of tokens for each group of hb heads of q and,
+  // bf16, of k and v
+  int row_blocks, hb, q_groups, kv_groups;
 };
 
-cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, bool small,
-                                int q_blocks, cudaStream_t st);
+cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, int page_size,
+                                cudaStream_t st);
+// Blocks that a page item of heads_kv heads takes (pages of page_size rows).
+int append_head_blocks(int head_dim, int page_size, int heads_kv);
+// Tokens of a block of the row path.
+int append_row_tokens(int head_dim);
 
-// Calls with at most this many new tokens per sequence give each (page, KV
-// head, K or V) unit to one warp, the others to a block.
+// e4m3 calls with at most this many new tokens per sequence give each (page, KV
+// head, K or V) unit to one warp, the others to as many threads as a page needs.
 constexpr int kAppendSmall = 8;
 
 // Chunks of 32 keys are the unit in which attn_cache_fwd deals work.
@@ -84,7 +93,7 @@ struct CacheFwdArgs {
   const float *k_scale, *v_scale;
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;     // [grid][2][rows][head_dim] partial outputs
+  float* part_o;     // [grid][2][head_dim / 4][rows][4] partial outputs
   float* stash;      // [grid][warps][rows][head_dim] parts that a warp finished early
   float2* part_ml;   // [grid][2][rows] running maximum (log2) and sum
   int4* part_meta;   // [grid][2] {kind bits, sequence, KV head, row block}

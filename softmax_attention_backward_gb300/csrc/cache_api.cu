@@ -139,7 +139,7 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
   a.v_cache = v_cache;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  // Pages that a sequence's new tokens can touch, and over all sequences
+  // e4m3: pages that a sequence's new tokens can touch, and over all sequences
   const int64_t slots = (static_cast<int64_t>(p->max_new) - 1 + p->page_size - 1) / p->page_size + 1;
   const bool small = p->max_new <= kAppendSmall;
   int64_t items = slots * p->num_seqs;
@@ -148,19 +148,25 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
     if (packed < items) items = packed;
   }
   const int64_t units = items * 2 * p->heads_kv;
-  const int per_block = small ? 8 : 1;
-  const int64_t rows = q ? static_cast<int64_t>(p->tokens) * p->heads_q : 0;
-  const int rows_block = 256 / (p->head_dim / 16);
-  const int64_t unit_blocks = (units + per_block - 1) / per_block;
-  const int64_t q_blocks = (rows + rows_block - 1) / rows_block;
-  if (units >= (int64_t(1) << 30) || unit_blocks + q_blocks >= (int64_t(1) << 31))
+  a.head_blocks = append_head_blocks(p->head_dim, p->page_size, p->heads_kv);
+  const int64_t unit_blocks = !e4m3 ? 0 : small ? (units + 7) / 8 : items * a.head_blocks;
+  // Rows: blocks of tokens for groups of heads, as large (up to 8) as leaves two
+  // blocks for every SM
+  const int per = append_row_tokens(p->head_dim);
+  a.row_blocks = (p->tokens + per - 1) / per;
+  const int64_t heads = (q ? p->heads_q : 0) + (e4m3 ? 0 : 2 * p->heads_kv);
+  a.hb = 8;
+  while (a.hb > 1 && a.row_blocks * heads / a.hb < 304) a.hb /= 2;
+  a.q_groups = q ? (p->heads_q + a.hb - 1) / a.hb : 0;
+  a.kv_groups = e4m3 ? 0 : (p->heads_kv + a.hb - 1) / a.hb;
+  const int64_t row_blocks = static_cast<int64_t>(a.row_blocks) * (a.q_groups + 2 * a.kv_groups);
+  if (units >= (int64_t(1) << 30) || unit_blocks + row_blocks >= (int64_t(1) << 31))
     return ATTN_ERR_UNSUPPORTED;
   a.units = static_cast<int>(units);
   a.unit_blocks = static_cast<int>(unit_blocks);
   a.slots = small ? static_cast<int>(slots) : 0;
   a.fd_slots = make_fastdiv(static_cast<uint32_t>(a.slots > 0 ? a.slots : 1));
-  a.fd_hq = make_fastdiv(static_cast<uint32_t>(p->heads_q));
-  return status_of(launch_cache_append(a, p->head_dim, e4m3, small, static_cast<int>(q_blocks),
+  return status_of(launch_cache_append(a, p->head_dim, e4m3, p->page_size,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -2,16 +2,22 @@
 // queries and keys applied on the way.
 //
 // Pair a = (x, y) of a row at position p becomes (x c - y s, y c + x s) with
-// c = cos_sin[p, a], s = cos_sin[p, rot/2 + a].  An e4m3 page and head share one
-// scale 2^e, e the least integer with amax <= 448 * 2^e, so a unit of work is
-// the part of a call that falls into one page for one KV head and K or V: its
-// threads read the rows once, keep the rotated values in registers, reduce
-// their largest magnitude and write the codes.  Everything is one pass over
-// the inputs, bound by HBM for prompts and by latency for single tokens.
+// c = cos_sin[p, a], s = cos_sin[p, rot/2 + a].  Sixteen elements of a row, two
+// 16-byte chunks, belong to one thread: with half-split pairs the chunks rot/2
+// apart, so that both members of a pair meet in it.
 //
-// A group of G threads takes a unit.  Sixteen elements of a row, two 16-byte
-// chunks, belong to one thread: with half-split pairs the chunks rot/2 apart,
-// so that both members of a pair meet in it.
+// Queries, and bf16 keys and values: a thread keeps the angles of its token's
+// chunks and goes over a group of heads (an fp32 table row is as large as two
+// bf16 rows, so reading it once per head would double the traffic).
+//
+// An e4m3 page and head share one scale 2^e, e the least integer with
+// amax <= 448 * 2^e, so a unit of work is the part of a call that falls into one
+// page for one KV head and K or V: its threads read the rows once, keep the
+// rotated values in registers, reduce their largest magnitude and write the
+// codes.
+//
+// Everything is one pass over the inputs, bound by HBM for prompts and by
+// latency for single tokens.
 #include "cache.cuh"
 
 namespace attn {
@@ -49,34 +55,36 @@ __device__ __forceinline__ Chunks chunk_pair(int p, int rot, int interleaved) {
   return c;
 }
 
-__device__ __forceinline__ void load_rotated(const __nv_bfloat16* row, const Chunks& c,
-                                             const float* cs, int half, int interleaved,
-                                             float (&v)[16]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(row + c.ca * 8);
-  const uint4 b = *reinterpret_cast<const uint4*>(row + c.cb * 8);
+// The cosines and sines of eight pairs.
+struct Angles {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float* at, int half) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(at) + i);
+      const float4 y = __ldg(reinterpret_cast<const float4*>(at + half) + i);
+      c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+      s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+    }
+  }
+  // v: the two chunks; pairs are neighbours, or the chunks' elements of one index
+  __device__ __forceinline__ void apply(float (&v)[16], int interleaved) const {
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rotate(v[2 * i], v[2 * i + 1], c[i], s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rotate(v[i], v[8 + i], c[i], s[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&v)[16]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  if (c.rot >= 0) {
-    float cv[8], sv[8];
-    const float4* c4 = reinterpret_cast<const float4*>(cs + c.rot);
-    const float4* s4 = reinterpret_cast<const float4*>(cs + half + c.rot);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 x = __ldg(c4 + i), y = __ldg(s4 + i);
-      cv[4 * i] = x.x, cv[4 * i + 1] = x.y, cv[4 * i + 2] = x.z, cv[4 * i + 3] = x.w;
-      sv[4 * i] = y.x, sv[4 * i + 1] = y.y, sv[4 * i + 2] = y.z, sv[4 * i + 3] = y.w;
-    }
-    if (interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) rotate(v[2 * i], v[2 * i + 1], cv[i], sv[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) rotate(v[i], v[8 + i], cv[i], sv[i]);
-    }
   }
 }
 
@@ -144,177 +152,227 @@ __device__ __forceinline__ void append_range(const AppendArgs& a, const StepSeq&
   if (a.rot_dim > 0) hi = min(hi, a.max_position);
 }
 
-// D: head dim.  G: threads of a unit.  PASSES * (G / (D / 16)) rows at most
-// fall into one unit.
-template <int D, bool E4M3, int G, int PASSES>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
+// The rows of a group of heads for a block of tokens.
+template <int D>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, int block) {
   constexpr int CPR = D / 16;              // threads of a row
-  constexpr int RP = G / CPR;              // rows of a pass
   const CacheStep& s = a.s;
-  const int half = a.rot_dim >> 1;
-
-  if (static_cast<int>(blockIdx.x) >= a.unit_blocks) {
-    // ---------------- queries: one row (token, head) per CPR threads ----------------
-    const int64_t rows = static_cast<int64_t>(s.tokens) * s.heads_q;
-    const int p = threadIdx.x % CPR;
-    const Chunks c = chunk_pair(p, a.rot_dim, a.interleaved);
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x - a.unit_blocks) * (kThreads / CPR);
-    const int64_t wrow = row0 + (threadIdx.x / 32) * (32 / CPR);   // first row of the warp
-    if (wrow >= rows) return;
-    int n = warp_seq_of(s, static_cast<int>(fdiv(static_cast<uint32_t>(wrow), a.fd_hq)));
-    const int64_t row = row0 + threadIdx.x / CPR;
-    if (row >= rows) return;
-    const int t = static_cast<int>(fdiv(static_cast<uint32_t>(row), a.fd_hq));
-    const int h = static_cast<int>(row) - t * s.heads_q;
-    while (n < s.num_seqs && __ldg(s.cu + n + 1) <= t) ++n;
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (n < s.num_seqs && t >= __ldg(s.cu)) {
-      const StepSeq q = step_seq(s, n);
-      const int pos = q.pos0 + (t - q.t0);
-      if (t >= q.t0 && pos >= 0 && (a.rot_dim == 0 || pos < a.max_position))
-        load_rotated(a.q + t * a.q_stride + h * D, c, a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim,
-                     half, a.interleaved, v);
-    }
-    store_bf16(a.q_out + row * D, c, v);
-    return;
-  }
-
-  // ---------------- keys and values: one unit per G threads ----------------
-  __shared__ int sh_scan[kThreads / 32 + 1];
-  __shared__ int sh_unit[2];
-  __shared__ float sh_amax[kThreads / 32];
-  const int unit = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  const int tid = threadIdx.x % G;
-  const int item = unit / (2 * s.heads_kv);   // page item
-  const int hw = unit - item * 2 * s.heads_kv;
-  const int h = hw >> 1;
-  const bool is_v = hw & 1;
-  int n = -1, j = 0;   // sequence and its page among those that the call touches
-  if (a.slots > 0) {
-    const int nn = static_cast<int>(fdiv(static_cast<uint32_t>(item), a.fd_slots));
-    if (unit < a.units && nn < s.num_seqs) {
-      n = nn;
-      j = item - n * a.slots;
-    }
-  } else {
-    // block-wide scan over the sequences' touched pages (one unit per block)
-    if (threadIdx.x == 0) sh_unit[0] = -1;
-    int base = 0;
-    for (int n0 = 0; n0 < s.num_seqs; n0 += kThreads) {
-      const int nn = n0 + threadIdx.x;
-      int cnt = 0;
-      if (nn < s.num_seqs) {
-        int lo, hi;
-        append_range(a, step_seq(s, nn), lo, hi);
-        if (hi > lo) cnt = ((hi - 1) >> s.ps_shift) - (lo >> s.ps_shift) + 1;
-      }
-      int inc = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (static_cast<int>(lane_id()) >= o) inc += x;
-      }
-      __syncthreads();
-      if (lane_id() == 31) sh_scan[warp_id()] = inc;
-      __syncthreads();
-      int before = base, all = base;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < static_cast<int>(warp_id())) before += sh_scan[w];
-        all += sh_scan[w];
-      }
-      const int end = before + inc;
-      if (item >= end - cnt && item < end) {
-        sh_unit[0] = nn;
-        sh_unit[1] = item - (end - cnt);
-      }
-      base = all;
-      if (base > item) break;
-    }
-    __syncthreads();
-    n = sh_unit[0];
-    j = sh_unit[1];
-  }
-
-  bool live = n >= 0;
-  int lo = 0, hi = 0, pos0 = 0, t0 = 0, bad = 0;
-  if (live) {
+  const int grp = block / a.row_blocks;
+  const int tok0 = (block - grp * a.row_blocks) * (kThreads / CPR);
+  // what the group is of: 0 q, 1 k, 2 v
+  const int kind = grp < a.q_groups ? 0 : grp < a.q_groups + a.kv_groups ? 1 : 2;
+  const int h0 = (kind == 0 ? grp : grp - a.q_groups - (kind - 1) * a.kv_groups) * a.hb;
+  const int h1 = min(h0 + a.hb, kind == 0 ? s.heads_q : s.heads_kv);
+  const int wtok = tok0 + threadIdx.x / 32 * (32 / CPR);   // first token of the warp
+  if (wtok >= s.tokens) return;
+  int n = warp_seq_of(s, wtok);
+  const int t = tok0 + threadIdx.x / CPR;
+  if (t >= s.tokens) return;
+  while (n < s.num_seqs && __ldg(s.cu + n + 1) <= t) ++n;
+  const Chunks c = chunk_pair(threadIdx.x % CPR, kind == 2 ? 0 : a.rot_dim, a.interleaved);
+  int pos = -1, bad = 0;
+  __nv_bfloat16* dst = nullptr;   // the token's row of head 0, and the elements to the next head's
+  int64_t step = D;
+  if (n < s.num_seqs && t >= __ldg(s.cu)) {
     const StepSeq q = step_seq(s, n, &bad);
-    t0 = q.t0;
-    pos0 = q.pos0;
-    append_range(a, q, lo, hi);
-    if (q.m > 0 && a.rot_dim > 0 && pos0 > a.max_position - q.m) bad |= ATTN_DEVERR_SEQLEN;
-    live = hi > lo;
-  }
-  int page = 0, first = 0, cnt = 0;   // first: row in the page of the first new key
-  if (live) {
-    const int col = (lo >> s.ps_shift) + j;
-    const int p0 = max(lo, col << s.ps_shift);
-    const int p1 = min(hi, (col + 1) << s.ps_shift);
-    cnt = p1 - p0;
-    live = cnt > 0;
-    if (live) {
-      page = __ldg(s.table + static_cast<int64_t>(n) * s.max_pages + col);
+    pos = q.pos0 + (t - q.t0);
+    if (a.rot_dim > 0 && pos >= a.max_position) {
+      bad |= ATTN_DEVERR_SEQLEN;
+      pos = -1;
+    }
+    if (kind != 0 && pos >= 0 && pos < q.len && t - q.t0 < s.max_new) {
+      const int page = __ldg(s.table + static_cast<int64_t>(n) * s.max_pages + (pos >> s.ps_shift));
       if (page < 0 || page >= s.num_pages) {
         bad |= ATTN_DEVERR_INDEX_RANGE;
-        live = false;
-      }
-      first = p0 - (col << s.ps_shift);
-      t0 += p0 - pos0;
-      pos0 = p0;
-    }
-  }
-  if (bad && s.err && tid == 0) atomicOr(s.err, bad);
-  if (!live) return;   // uniform over the unit's threads
-
-  const int p = tid % CPR;
-  const int rot = is_v ? 0 : a.rot_dim;
-  const Chunks c = chunk_pair(p, rot, a.interleaved);
-  const __nv_bfloat16* src = (is_v ? a.v + t0 * a.v_stride : a.k + t0 * a.k_stride) + h * D;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const int64_t ph = static_cast<int64_t>(page) * s.heads_kv + h;
-  const int64_t slab = (ph << s.ps_shift) * D;
-  float v[PASSES][16];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = i * RP + tid / CPR;
-    if (r < cnt) {
-      load_rotated(src + r * stride, c, a.cos_sin + static_cast<int64_t>(pos0 + r) * a.rot_dim, half,
-                   a.interleaved, v[i]);
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float m = fabsf(v[i][e]);
-          if (m < INFINITY) amax = fmaxf(amax, m);   // neither infinities nor NaN
-        }
       } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + slab;
-        store_bf16(dst + (first + r) * D, c, v[i]);
+        step = static_cast<int64_t>(D) << s.ps_shift;
+        dst = static_cast<__nv_bfloat16*>(kind == 1 ? a.k_cache : a.v_cache) +
+              static_cast<int64_t>(page) * s.heads_kv * step + (pos & ((1 << s.ps_shift) - 1)) * D;
       }
     }
+    if (bad && s.err && threadIdx.x % CPR == 0) atomicOr(s.err, bad);
+  }
+  if (kind == 0) dst = a.q_out + static_cast<int64_t>(t) * s.heads_q * D;
+  if (!dst) return;
+  const __nv_bfloat16* src = kind == 0   ? a.q + t * a.q_stride
+                             : kind == 1 ? a.k + t * a.k_stride
+                                         : a.v + t * a.v_stride;
+  const bool live = pos >= 0;   // a query without a position: zeros
+  Angles ang;
+  if (c.rot >= 0 && live)
+    ang.load(a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim + c.rot, a.rot_dim >> 1);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (live) {
+      x = *reinterpret_cast<const uint4*>(src + h * D + c.ca * 8);
+      y = *reinterpret_cast<const uint4*>(src + h * D + c.cb * 8);
+    }
+    float v[16];
+    unpack16(x, y, v);
+    if (c.rot >= 0 && live) ang.apply(v, a.interleaved);
+    store_bf16(dst + h * step, c, v);
+  }
+}
+
+// D: head dim.  G: threads of an e4m3 unit, into which PASSES * (G / (D / 16)) rows
+// fall at most; SCAN: blocks of units of one page item each, found by a scan over
+// the sequences (else slots of a sequence, a warp each).
+template <int D, bool E4M3, int G, int PASSES, bool SCAN>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
+  if (!E4M3 || static_cast<int>(blockIdx.x) >= a.unit_blocks) {
+    append_rows<D>(a, blockIdx.x - a.unit_blocks);
+    return;
   }
   if constexpr (E4M3) {
-    // (a unit that left above took all G threads of it along, so the masks and
-    // barriers below see whole groups)
-    const uint32_t mask = 0xffffffffu;
+    constexpr int CPR = D / 16;              // threads of a row
+    constexpr int RP = G / CPR;              // rows of a pass
+    constexpr int UNITS = kThreads / G;      // units of a block
+    const CacheStep& s = a.s;
+    const int group = threadIdx.x / G, tid = threadIdx.x % G;
+    __shared__ float sh_amax[kThreads / 32];
+    int n = -1, j = 0;   // sequence and its page among those that the call touches
+    int hw;              // 2 KV head + (0: K, 1: V)
+    if constexpr (!SCAN) {
+      const int unit = blockIdx.x * UNITS + group;
+      const int item = unit / (2 * s.heads_kv);
+      hw = unit - item * 2 * s.heads_kv;
+      const int nn = static_cast<int>(fdiv(static_cast<uint32_t>(item), a.fd_slots));
+      if (unit < a.units && nn < s.num_seqs) {
+        n = nn;
+        j = item - n * a.slots;
+      }
+    } else {
+      __shared__ int sh_scan[kThreads / 32];
+      __shared__ int sh_unit[2];
+      const int item = blockIdx.x / a.head_blocks;
+      hw = (blockIdx.x - item * a.head_blocks) * UNITS + group;
+      // block-wide scan over the sequences' touched pages
+      if (threadIdx.x == 0) sh_unit[0] = -1;
+      int base = 0;
+      for (int n0 = 0; n0 < s.num_seqs; n0 += kThreads) {
+        const int nn = n0 + threadIdx.x;
+        int cnt = 0;
+        if (nn < s.num_seqs) {
+          int lo, hi;
+          append_range(a, step_seq(s, nn), lo, hi);
+          if (hi > lo) cnt = ((hi - 1) >> s.ps_shift) - (lo >> s.ps_shift) + 1;
+        }
+        int inc = cnt;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-    if constexpr (G == kThreads) {
-      if (lane_id() == 0) sh_amax[warp_id()] = amax;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (static_cast<int>(lane_id()) >= o) inc += x;
+        }
+        __syncthreads();
+        if (lane_id() == 31) sh_scan[warp_id()] = inc;
+        __syncthreads();
+        int before = base, all = base;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < static_cast<int>(warp_id())) before += sh_scan[w];
+          all += sh_scan[w];
+        }
+        const int end = before + inc;
+        if (item >= end - cnt && item < end) {
+          sh_unit[0] = nn;
+          sh_unit[1] = item - (end - cnt);
+        }
+        base = all;
+        if (base > item) break;
+      }
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, sh_amax[w]);
+      n = hw < 2 * s.heads_kv ? sh_unit[0] : -1;
+      j = sh_unit[1];
     }
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + slab;
+
+    const int h = hw >> 1;
+    const bool is_v = hw & 1;
+    bool live = n >= 0;
+    int lo = 0, hi = 0, pos0 = 0, t0 = 0, bad = 0;
+    if (live) {
+      const StepSeq q = step_seq(s, n, &bad);
+      t0 = q.t0;
+      pos0 = q.pos0;
+      append_range(a, q, lo, hi);
+      if (q.m > 0 && a.rot_dim > 0 && pos0 > a.max_position - q.m) bad |= ATTN_DEVERR_SEQLEN;
+      live = hi > lo;
+    }
+    int page = 0, first = 0, cnt = 0;   // first: row in the page of the first new key
+    if (live) {
+      const int col = (lo >> s.ps_shift) + j;
+      const int p0 = max(lo, col << s.ps_shift);
+      const int p1 = min(hi, (col + 1) << s.ps_shift);
+      cnt = p1 - p0;
+      live = cnt > 0;
+      if (live) {
+        page = __ldg(s.table + static_cast<int64_t>(n) * s.max_pages + col);
+        if (page < 0 || page >= s.num_pages) {
+          bad |= ATTN_DEVERR_INDEX_RANGE;
+          live = false;
+        }
+        first = p0 - (col << s.ps_shift);
+        t0 += p0 - pos0;
+        pos0 = p0;
+      }
+    }
+    if (bad && s.err && tid == 0) atomicOr(s.err, bad);
+    if (!live) return;   // uniform over the unit's threads
+    auto sync = [&] {
+      if constexpr (G > 32) named_bar_sync(1 + group, G);
+      else __syncwarp();
+    };
+
+    const Chunks c = chunk_pair(tid % CPR, is_v ? 0 : a.rot_dim, a.interleaved);
+    const __nv_bfloat16* src = (is_v ? a.v + t0 * a.v_stride : a.k + t0 * a.k_stride) + h * D;
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    const int64_t ph = static_cast<int64_t>(page) * s.heads_kv + h;
+    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (ph << s.ps_shift) * D;
     float* scale = (is_v ? a.v_scale : a.k_scale) + ph;
+    float old = 0.f;
+    if (first > 0) old = *scale;
+    float v[PASSES][16];
+    {
+      uint4 x[PASSES], y[PASSES];
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = i * RP + tid / CPR;
+        x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < cnt) {
+          x[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.ca * 8);
+          y[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.cb * 8);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) unpack16(x[i], y[i], v[i]);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = i * RP + tid / CPR;
+      if (r < cnt && c.rot >= 0) {
+        Angles ang;
+        ang.load(a.cos_sin + static_cast<int64_t>(pos0 + r) * a.rot_dim + c.rot, a.rot_dim >> 1);
+        ang.apply(v[i], a.interleaved);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float m = fabsf(v[i][e]);
+        if (m < INFINITY) amax = fmaxf(amax, m);   // neither infinities nor NaN
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (G > 32) {
+      if (lane_id() == 0) sh_amax[warp_id()] = amax;
+      sync();
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) amax = fmaxf(amax, sh_amax[group * (G / 32) + w]);
+    }
     const int e = scale_exponent(amax);
     float sc = exp2_int(e);
     float inv = exp2_int(-e);
     if (first > 0) {
-      const float old = *scale;
       if (old >= sc) {
         sc = old;
         inv = 1.f / old;   // exact: a power of two
@@ -328,9 +386,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
           w[i] = pack_e4m3(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
         }
       }
-      // every thread has read the old scale before one replaces it
-      if constexpr (G == kThreads) __syncthreads();
-      else __syncwarp();
+      sync();   // every thread has read the old scale
     }
     if (tid == 0) *scale = sc;
 #pragma unroll
@@ -350,28 +406,44 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   }
 }
 
+// Threads of a unit that holds a page of `page_size` rows: four rows a thread, two
+// where that would leave less than a warp.
+constexpr int page_threads(int head_dim, int page_size) {
+  return page_size * (head_dim / 16) / 4 < 32 ? 32 : page_size * (head_dim / 16) / 4;
+}
+
 template <int D>
-cudaError_t launch(const AppendArgs& a, bool e4m3, bool small, int q_blocks, cudaStream_t st) {
-  const int grid = a.unit_blocks + q_blocks;
+cudaError_t launch(const AppendArgs& a, bool e4m3, int page_size, cudaStream_t st) {
+  const int grid = a.unit_blocks + a.row_blocks * (a.q_groups + 2 * a.kv_groups);
   if (grid == 0) return cudaSuccess;
-  // rows of a unit: up to 8 for the small form (a warp), a whole page (128) else
-  constexpr int PS = 8 * (D / 16) / 32, PB = 128 * (D / 16) / kThreads;
-  if (small) {
-    if (e4m3) cache_append_kernel<D, true, 32, PS><<<grid, kThreads, 0, st>>>(a);
-    else cache_append_kernel<D, false, 32, PS><<<grid, kThreads, 0, st>>>(a);
+  if (!e4m3) {
+    cache_append_kernel<D, false, 32, 1, false><<<grid, kThreads, 0, st>>>(a);
+  } else if (a.slots > 0) {   // units of up to kAppendSmall rows, a warp each
+    cache_append_kernel<D, true, 32, kAppendSmall * (D / 16) / 32, false><<<grid, kThreads, 0, st>>>(a);
   } else {
-    if (e4m3) cache_append_kernel<D, true, kThreads, PB><<<grid, kThreads, 0, st>>>(a);
-    else cache_append_kernel<D, false, kThreads, PB><<<grid, kThreads, 0, st>>>(a);
+    constexpr int T16 = page_threads(D, 16), T32 = page_threads(D, 32), T64 = page_threads(D, 64),
+                  T128 = page_threads(D, 128);
+    switch (page_size) {
+      case 16: cache_append_kernel<D, true, T16, D / T16, true><<<grid, kThreads, 0, st>>>(a); break;
+      case 32: cache_append_kernel<D, true, T32, 2 * D / T32, true><<<grid, kThreads, 0, st>>>(a); break;
+      case 64: cache_append_kernel<D, true, T64, 4 * D / T64, true><<<grid, kThreads, 0, st>>>(a); break;
+      default: cache_append_kernel<D, true, T128, 8 * D / T128, true><<<grid, kThreads, 0, st>>>(a);
+    }
   }
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, bool small,
-                                int q_blocks, cudaStream_t st) {
-  return head_dim == 64 ? launch<64>(a, e4m3, small, q_blocks, st)
-                        : launch<128>(a, e4m3, small, q_blocks, st);
+int append_head_blocks(int head_dim, int page_size, int heads_kv) {
+  const int units = kThreads / page_threads(head_dim, page_size);
+  return (2 * heads_kv + units - 1) / units;
+}
+int append_row_tokens(int head_dim) { return kThreads / (head_dim / 16); }
+
+cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, int page_size,
+                                cudaStream_t st) {
+  return head_dim == 64 ? launch<64>(a, e4m3, page_size, st) : launch<128>(a, e4m3, page_size, st);
 }
 
 }  // namespace attn

@@ -811,11 +811,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
           if (d == 0) a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(m, l);
         }
       } else {
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + which) * ROWS + rl;
-        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + d);
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + which;
+        float4* dst = reinterpret_cast<float4*>(a.part_o) + (at * (D / 4) + d / 4) * ROWS + rl;
         dst[0] = lo;
-        dst[1] = hi;
-        if (d == 0) a.part_ml[at] = make_float2(m, l);
+        dst[ROWS] = hi;
+        if (d == 0) a.part_ml[at * ROWS + rl] = make_float2(m, l);
       }
     }
     if (!whole && threadIdx.x == 0)
@@ -845,11 +845,13 @@ template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
     cache_join_kernel(const __grid_constant__ CacheFwdArgs a, int grid, int item_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int POS = ROWS * (D / 4);                    // float4 positions of a partial
+  constexpr int POS = ROWS * (D / 4);                    // float4 positions, rows first
   constexpr int SPLIT = POS >= kJoinThreads ? 1 : kJoinThreads / POS;
+  constexpr int LD = D + 8;                              // bf16 row stride of the result
   __shared__ float sh_w[kCacheCtas][ROWS];
   __shared__ float sh_l[ROWS], sh_m[ROWS];
   __shared__ float4 sh_o[SPLIT > 1 ? kJoinThreads : 1];
+  __shared__ __align__(16) __nv_bfloat16 sh_out[ROWS * LD];
   __shared__ int sh_end;
   const CacheStep& s = a.s;
   const int b = blockIdx.x;
@@ -872,19 +874,18 @@ __global__ void __launch_bounds__(kJoinThreads)
   __syncthreads();
   const int parts = min(sh_end, grid - 1) - b + 1;
   const int warp = warp_id(), lane = lane_id();
-  auto part_at = [&](int p) {
-    return static_cast<int64_t>(p == 0 ? 2 * b + 1 : 2 * (b + p)) * item_rows + base;
-  };
+  auto slot_of = [&](int p) { return static_cast<int64_t>(p == 0 ? 2 * b + 1 : 2 * (b + p)); };
   for (int r = warp; r < ROWS; r += kJoinThreads / 32) {
     if (row_of(base + r) >= rows_all) continue;
     float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[part_at(p) + r].x);
+    for (int p = lane; p < parts; p += 32)
+      m = fmaxf(m, a.part_ml[slot_of(p) * item_rows + base + r].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     for (int p = lane; p < parts; p += 32) {
-      const float2 ml = a.part_ml[part_at(p) + r];
+      const float2 ml = a.part_ml[slot_of(p) * item_rows + base + r];
       const float w = ex2(ml.x - ms);
       sh_w[p][r] = w;
       l += w * ml.y;
@@ -897,38 +898,47 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
   }
   __syncthreads();
+#pragma unroll 2
   for (int e0 = 0; e0 < POS; e0 += kJoinThreads) {
     const int e = SPLIT > 1 ? threadIdx.x % POS : e0 + threadIdx.x;
     const int sp = SPLIT > 1 ? threadIdx.x / POS : 0;
-    const int rl = e / (D / 4), d = (e - rl * (D / 4)) * 4, r = row_of(base + rl);
+    const int rl = e % ROWS, d4 = e / ROWS;
+    const bool in = row_of(base + rl) < rows_all;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows_all) {
+    if (in) {
 #pragma unroll 4
       for (int p = sp; p < parts; p += SPLIT) {
         const float w = sh_w[p][rl];
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (part_at(p) + rl) * D + d);
+        const float4 x = *(reinterpret_cast<const float4*>(a.part_o) +
+                           (slot_of(p) * (D / 4) + d4) * item_rows + base + rl);
         o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
       }
     }
     if constexpr (SPLIT > 1) {
       sh_o[threadIdx.x] = o;
       __syncthreads();
-      if (sp > 0) return;
+      if (sp == 0) {
 #pragma unroll
-      for (int k = 1; k < SPLIT; ++k) {
-        const float4 x = sh_o[k * POS + e];
-        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        for (int k = 1; k < SPLIT; ++k) {
+          const float4 x = sh_o[k * POS + e];
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
       }
     }
-    if (r < rows_all) {
-      const int tok = r / s.group, hd = meta.z * s.group + (r - tok * s.group);
+    if (in && sp == 0) {
       const float l = sh_l[rl], f = l > 0.f || l != l ? 1.f / l : 0.f;
-      uint2 w;
-      w.x = pack_bf16(o.x * f, o.y * f);
-      w.y = pack_bf16(o.z * f, o.w * f);
-      *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + hd) * D + d) = w;
-      if (d == 0) a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(sh_m[rl], l);
+      *reinterpret_cast<uint2*>(sh_out + rl * LD + d4 * 4) =
+          make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < ROWS * (D / 8); e += kJoinThreads) {
+    const int rl = e / (D / 8), d = (e - rl * (D / 8)) * 8, r = row_of(base + rl);
+    if (r >= rows_all) continue;
+    const int tok = r / s.group, hd = meta.z * s.group + (r - tok * s.group);
+    *reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + hd) * D + d) =
+        *reinterpret_cast<const uint4*>(sh_out + rl * LD + d);
+    if (d == 0) a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(sh_m[rl], sh_l[rl]);
   }
 }
 

@@ -50,9 +50,13 @@ struct TcCfg {
   static_assert(SMEM <= 227 * 1024 - 700, "shared memory");
 };
 
-// Chunks by which an item counts more in the dealing than it has: its query
-// tiles, its first and last chunk and its outputs.
-constexpr int kItemCost = 3;
+// Chunks by which an item counts more in the dealing than it has, for its query
+// tiles, its first and last chunk and its outputs: 12 sequences of up to 700 new
+// tokens over 4000 keys took 56, 57, 61 us with 3, 6, 10 (bf16) and 94, 86, 80 us
+// (e4m3, whose queries the softmax warps convert), 2 x 4096 fresh tokens 273, 261,
+// 270 us.
+template <bool E4M3>
+constexpr int kItemCost = E4M3 ? 10 : 5;
 
 // A contiguous copy, 16-byte aligned on both sides and a multiple of 16 bytes.
 __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
@@ -88,17 +92,17 @@ __device__ __forceinline__ int tile_seen(const CacheFwdArgs& a, const StepSeq& q
   const int vis = a.causal ? min(q.len, q.pos0 + hi) : q.len;
   return vis > 0 ? (vis + BN - 1) / BN : 0;
 }
-template <int BN>
+template <int BN, bool E4M3>
 __device__ __forceinline__ void item_block(const CacheFwdArgs& a, TcItem& it) {
   it.seen[0] = tile_seen<BN>(a, it.q, 2 * it.rb);
   it.seen[1] = tile_seen<BN>(a, it.q, 2 * it.rb + 1);
-  it.nc = max(it.seen[0], it.seen[1]) + kItemCost;
+  it.nc = max(it.seen[0], it.seen[1]) + kItemCost<E4M3>;
 }
 __device__ __forceinline__ int seq_blocks(const CacheFwdArgs& a, const StepSeq& q) {
   return (q.m + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
 }
 // The next item; the caller knows that there is one.
-template <int BN>
+template <int BN, bool E4M3>
 __device__ __forceinline__ void item_next(const CacheFwdArgs& a, TcItem& it) {
   if (++it.rb == it.nb) {
     it.rb = 0;
@@ -111,13 +115,13 @@ __device__ __forceinline__ void item_next(const CacheFwdArgs& a, TcItem& it) {
       } while (it.nb == 0);
     }
   }
-  item_block<BN>(a, it);
+  item_block<BN, E4M3>(a, it);
 }
 // Chunks of one KV head of a sequence in the dealing.
-template <int BN>
+template <int BN, bool E4M3>
 __device__ __forceinline__ int64_t head_chunks(const CacheFwdArgs& a, const StepSeq& q) {
   const int nb = seq_blocks(a, q);
-  int64_t w = static_cast<int64_t>(nb) * kItemCost;
+  int64_t w = static_cast<int64_t>(nb) * kItemCost<E4M3>;
   for (int rb = 0; rb < nb; ++rb)
     w += max(tile_seen<BN>(a, q, 2 * rb), tile_seen<BN>(a, q, 2 * rb + 1));
   return w;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     int64_t mine = 0;
     int bad = 0;
     for (int n = n0; n < n1; ++n)
-      mine += s.heads_kv * head_chunks<BN>(a, step_seq(s, n, &bad));
+      mine += s.heads_kv * head_chunks<BN, E4M3>(a, step_seq(s, n, &bad));
     if (bad && s.err && blockIdx.x == 0) atomicOr(s.err, bad);
     int64_t inc = mine;
 #pragma unroll
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       int64_t off = f0 - (end - mine);
       for (it.n = n0;; ++it.n) {
         it.q = step_seq(s, it.n);
-        const int64_t w = head_chunks<BN>(a, it.q);
+        const int64_t w = head_chunks<BN, E4M3>(a, it.q);
         if (off < s.heads_kv * w) {
           it.h = static_cast<int>(off / w);
           off -= it.h * w;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       }
       it.nb = seq_blocks(a, it.q);
       for (it.rb = 0;; ++it.rb) {
-        item_block<BN>(a, it);
+        item_block<BN, E4M3>(a, it);
         if (off < it.nc) break;
         off -= it.nc;
       }
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       auto advance = [&](TcItem& it, Part& pt, int64_t& left) -> bool {
         left -= pt.span;
         if (left <= 0) return false;
-        item_next<BN>(a, it);
+        item_next<BN, E4M3>(a, it);
         pt = part_of(it, 0, left);
         return true;
       };
@@ -391,10 +395,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
                 bulk_load(bar, sRing + C::NSLOT * C::KV_BYTES + slot * C::RAW_BYTES + lane * box * D,
                           static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache) + at, box * D);
             }
-            continue;
           }
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
+          for (int kv = 0; kv < (E4M3 ? 0 : 2); ++kv) {
             const int gi = gring + 2 * c + kv;
             const int slot = gi % C::NSLOT, use = gi / C::NSLOT;
             if (!mbar_wait_w(&bar_empty[slot], (use & 1) ^ 1, ac)) { ok = false; break; }
@@ -808,7 +811,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         const float unit = E4M3 && nt > 0 ? ex2(lv_ref) : 1.f;
         const float inv = (l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f) * unit;
         __nv_bfloat16* orow = a.o + (static_cast<int64_t>(row_out) * s.heads_q + hd) * D;
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1)) * 2 * C::BM + t * C::BM + tr;
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1);
+        float4* part = reinterpret_cast<float4*>(a.part_o) + at * (D / 4) * 2 * C::BM + t * C::BM + tr;
 #pragma unroll
         for (int cc = 0; cc < D; cc += 32) {
           uint32_t r[32];
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(a.part_o + at * D + cc + i) =
+                part[(cc + i) / 4 * 2 * C::BM] =
                     make_float4(__uint_as_float(r[i]) * unit, __uint_as_float(r[i + 1]) * unit,
                                 __uint_as_float(r[i + 2]) * unit, __uint_as_float(r[i + 3]) * unit);
             }
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             a.lse[static_cast<int64_t>(hd) * s.tokens + row_out] =
                 l_run > 0.f || l_run != l_run ? (m_run + __log2f(l_run)) * kLn2 : -INFINITY;
           } else {
-            a.part_ml[at] = make_float2(m_run, l_run);
+            a.part_ml[at * 2 * C::BM + t * C::BM + tr] = make_float2(m_run, l_run);
           }
         }
       }
