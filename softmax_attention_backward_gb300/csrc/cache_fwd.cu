@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
   __shared__ float2 sh_ml[C::WARPS][2][ROWS];
   __shared__ const float* sh_part[C::WARPS][2];
   __shared__ int sh_ld[C::WARPS][2];
+  __shared__ float sh_w[2 * C::WARPS][ROWS];
+  __shared__ float2 sh_sum[2 * C::WARPS][ROWS];
   __shared__ int abort_flag;
 
   const CacheStep& s = a.s;
@@ -303,6 +305,28 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
       it.rb = static_cast<int>(item) - it.h * it.nb;
     }
     int left = static_cast<int>(min(f1 - f0, static_cast<int64_t>(0x7fffffff)));
+
+    // The raw words of row g of the item's tiles: vector 4 j + t of 8 dims; e4m3: half of
+    // vector 4 (j / 2) + t of 16 dims.
+    uint32_t qw[NQ][D / 8];
+    auto load_q = [&](const Item& x) {
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+        const int r = x.rb * ROWS + nq * 8 + g, i = r / s.group;
+        const bool in = r < x.q.m * s.group;
+        const __nv_bfloat16* src = a.q + (x.q.t0 + (in ? i : 0)) * a.q_stride +
+                                   (x.h * s.group + (in ? r - i * s.group : 0)) * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (in)
+            v = *reinterpret_cast<const uint4*>(src + (E4M3 ? (j >> 1) * 64 + t * 16 + (j & 1) * 8
+                                                            : j * 32 + t * 8));
+          qw[nq][4 * j] = v.x, qw[nq][4 * j + 1] = v.y, qw[nq][4 * j + 2] = v.z, qw[nq][4 * j + 3] = v.w;
+        }
+      }
+    };
+    load_q(it);
 
     // ---- the copies, which run ahead of the computation, across items ----
     // lane l holds the page of column pg0 + l of item `cp`, and that of column l of
@@ -416,27 +440,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
       if (!issue()) break;
     __syncwarp();
 
-    // The raw words of row g of the item's tiles: vector 4 j + t of 8 dims; e4m3: half of
-    // vector 4 (j / 2) + t of 16 dims.
-    uint32_t qw[NQ][D / 8];
-    auto load_q = [&](const Item& x) {
-#pragma unroll
-      for (int nq = 0; nq < NQ; ++nq) {
-        const int r = x.rb * ROWS + nq * 8 + g, i = r / s.group;
-        const bool in = r < x.q.m * s.group;
-        const __nv_bfloat16* src = a.q + (x.q.t0 + (in ? i : 0)) * a.q_stride +
-                                   (x.h * s.group + (in ? r - i * s.group : 0)) * D;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (in)
-            v = *reinterpret_cast<const uint4*>(src + (E4M3 ? (j >> 1) * 64 + t * 16 + (j & 1) * 8
-                                                            : j * 32 + t * 8));
-          qw[nq][4 * j] = v.x, qw[nq][4 * j + 1] = v.y, qw[nq][4 * j + 2] = v.z, qw[nq][4 * j + 3] = v.w;
-        }
-      }
-    };
-    load_q(it);
     int half = 0;   // halves computed so far
 
     while (true) {
@@ -762,65 +765,82 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
   __syncthreads();
 
   // ---- join the warps' parts (in order: part a, then part b of each warp) ----
-  if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
-  __syncthreads();
-  int i = 0;
-  while (i < 2 * C::WARPS) {
-    const PartMeta first = sh_meta[i >> 1][i & 1];
-    if (!(first.kind & 1)) {
-      ++i;
-      continue;
-    }
-    // the chain of one item: parts until one ends it, or the last of the CTA
-    int last = i, kind = first.kind;
-    for (int k = i + 1; !(kind & 4) && k < 2 * C::WARPS; ++k) {
-      const int kk = sh_meta[k >> 1][k & 1].kind;
-      if (kk & 1) {
-        last = k;
-        kind |= kk & 4;
-      }
-    }
-    const StepSeq q = step_seq(s, first.n);
-    const bool whole = (kind & 6) == 6;
-    const int which = (kind & 2) ? 1 : 0;   // the CTA's part that goes on, or came from before
-    const int rows_all = q.m * s.group;
-    for (int e = threadIdx.x; e < ROWS * (D / 8); e += C::THREADS) {
-      const int rl = e / (D / 8), d = (e - rl * (D / 8)) * 8, r = first.rb * ROWS + rl;
-      float m = -INFINITY;
-      for (int k = i; k <= last; ++k)
-        if (sh_meta[k >> 1][k & 1].kind & 1) m = fmaxf(m, sh_ml[k >> 1][k & 1][rl].x);
+  // A chain is the parts of one item: from the first, or the one after an end, to the
+  // next end, or the last of the CTA.
+  {
+    const int kind = lane < 2 * C::WARPS ? sh_meta[lane >> 1][lane & 1].kind : 0;
+    const uint32_t valid = __ballot_sync(0xffffffffu, kind & 1), ends = __ballot_sync(0xffffffffu, kind & 4);
+    const uint32_t before = valid & ((1u << lane) - 1);
+    const bool starts = (kind & 1) && (before == 0 || (ends >> (31 - __clz(before)) & 1));
+    const uint32_t first = __ballot_sync(0xffffffffu, starts);
+    const int chains = __popc(first);
+    // parts [i0, i1) of chain c
+    auto chain = [&](int c, int& i0, int& i1) {
+      uint32_t f = first;
+      for (int k = 0; k < c; ++k) f &= f - 1;
+      i0 = __ffs(f) - 1;
+      f &= f - 1;
+      i1 = f ? __ffs(f) - 1 : 2 * C::WARPS;
+    };
+    for (int e = threadIdx.x; e < chains * ROWS; e += C::THREADS) {
+      const int c = e / ROWS, rl = e - c * ROWS;
+      int i0, i1;
+      chain(c, i0, i1);
+      float m = -INFINITY, l = 0.f;
+      for (int k = i0; k < i1; ++k)
+        if (valid >> k & 1) m = fmaxf(m, sh_ml[k >> 1][k & 1][rl].x);
       const float ms = m == -INFINITY ? 0.f : m;
+      for (int k = i0; k < i1; ++k)
+        if (valid >> k & 1) {
+          const float2 ml = sh_ml[k >> 1][k & 1][rl];
+          const float w = ex2(ml.x - ms);
+          l += w * ml.y;
+          sh_w[k][rl] = w;
+        }
+      sh_sum[c][rl] = make_float2(m, l);
+    }
+    if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int e = threadIdx.x; e < chains * ROWS * (D / 8); e += C::THREADS) {
+      const int c = e / (ROWS * (D / 8)), er = e - c * (ROWS * (D / 8));
+      const int rl = er / (D / 8), d = (er - rl * (D / 8)) * 8;
+      int i0, i1;
+      chain(c, i0, i1);
+      const PartMeta meta = sh_meta[i0 >> 1][i0 & 1];
       float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-      float l = 0.f;
-      for (int k = i; k <= last; ++k) {
-        if (!(sh_meta[k >> 1][k & 1].kind & 1)) continue;
-        const float2 ml = sh_ml[k >> 1][k & 1][rl];
-        const float w = ex2(ml.x - ms);
+#pragma unroll 4
+      for (int k = i0; k < i1; ++k) {
+        if (!(valid >> k & 1)) continue;
+        const float w = sh_w[k][rl];
         const float* sp = sh_part[k >> 1][k & 1] + rl * sh_ld[k >> 1][k & 1] + d;
         const float4 x = *reinterpret_cast<const float4*>(sp);
         const float4 y = *reinterpret_cast<const float4*>(sp + 4);
-        l += w * ml.y;
         lo.x += w * x.x, lo.y += w * x.y, lo.z += w * x.z, lo.w += w * x.w;
         hi.x += w * y.x, hi.y += w * y.y, hi.z += w * y.z, hi.w += w * y.w;
       }
-      if (whole) {
-        if (r < rows_all) {
-          const int tok = r / s.group, hd = first.h * s.group + (r - tok * s.group);
+      // of the chain: whether it begins the item, ends it
+      const int kinds = (meta.kind & 2) | ((ends & valid) >> i0 & ((1u << (i1 - i0)) - 1) ? 4 : 0);
+      const float2 ml = sh_sum[c][rl];
+      if (kinds == 6) {
+        const StepSeq q = step_seq(s, meta.n);
+        const int r = meta.rb * ROWS + rl;
+        if (r < q.m * s.group) {
+          const int tok = r / s.group, hd = meta.h * s.group + (r - tok * s.group);
           store_row8<D>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + hd) * D + d, lo, hi,
-                        l > 0.f || l != l ? 1.f / l : 0.f);
-          if (d == 0) a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(m, l);
+                        ml.y > 0.f || ml.y != ml.y ? 1.f / ml.y : 0.f);
+          if (d == 0) a.lse[static_cast<int64_t>(hd) * s.tokens + q.t0 + tok] = lse_of(ml.x, ml.y);
         }
       } else {
+        // the CTA's part that goes on in the next (1), or came from the one before (0)
+        const int which = kinds >> 1 & 1;
         const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + which;
         float4* dst = reinterpret_cast<float4*>(a.part_o) + (at * (D / 4) + d / 4) * ROWS + rl;
         dst[0] = lo;
         dst[ROWS] = hi;
-        if (d == 0) a.part_ml[at * ROWS + rl] = make_float2(m, l);
+        if (d == 0) a.part_ml[at * ROWS + rl] = ml;
+        if (er == 0) a.part_meta[at] = make_int4(1 | kinds, meta.n, meta.h, meta.rb);
       }
     }
-    if (!whole && threadIdx.x == 0)
-      a.part_meta[2 * blockIdx.x + which] = make_int4(kind, first.n, first.h, first.rb);
-    i = last + 1;
   }
 
   // ---- padding rows: at or past cu_seqlens[num_seqs] ----
@@ -960,7 +980,8 @@ template <int D, bool E4M3, int NQ>
 cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   using C = Cfg<D, E4M3, NQ>;
   auto kern = cache_fwd_kernel<D, E4M3, NQ>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, ready);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();

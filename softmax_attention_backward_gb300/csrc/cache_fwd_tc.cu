@@ -883,7 +883,8 @@ template <int D, bool E4M3>
 cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
   using C = TcCfg<D, E4M3>;
   auto kern = cache_fwd_tc_kernel<D, E4M3>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, ready);
   if (e != cudaSuccess) return e;
   kern<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
