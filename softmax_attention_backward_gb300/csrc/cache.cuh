@@ -102,6 +102,8 @@ constexpr int kCacheCtas = 152;
 struct CacheFwdArgs {
   CacheStep s;
   int causal;
+  int rows_lo, rows_hi;   // sequences with more than rows_lo, at most rows_hi query rows per KV head
+  int pad;                // whether this launch writes the padding rows
   float scale_log2;
   const __nv_bfloat16* q;
   int64_t q_stride;
@@ -131,7 +133,13 @@ cudaError_t launch_cache_join(const CacheFwdArgs& a, int head_dim, int item_rows
 
 // Rows per work item of the variant that serves `rows` query rows per KV head.
 int cache_fwd_rows(int rows);
-cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int rows, int grid,
-                             cudaStream_t st);
+cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int item_rows,
+                             int grid, cudaStream_t st);
+
+// Whether a launch serves sequence q, its new tokens' rows being m * group.
+__device__ __forceinline__ bool serves(const CacheFwdArgs& a, const StepSeq& q) {
+  const int rows = q.m * a.s.group;
+  return rows > a.rows_lo && rows <= a.rows_hi;
+}
 
 }  // namespace attn

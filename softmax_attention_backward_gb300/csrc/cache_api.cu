@@ -68,27 +68,55 @@ int step_rows(const attn_cache_problem_t* p) {
   return static_cast<int>(r < 1 << 30 ? r : 1 << 30);
 }
 
+// Which kernels serve a step.  The one for few rows goes over the keys once for
+// every 16 rows of a KV head (8 where no sequence has more), the tcgen05 kernel
+// once for 256, but pays more for an item, above all with e4m3 keys.  Measured, few
+// rows / tcgen05, in us:
+//  - 32 sequences of 4096 keys, 8 KV heads of 128, all with the same rows: bf16
+//    181 / 115 at 20 rows; e4m3 142 / 153 at 20, 138 / 155 at 32, 195 / 154 at 40;
+//  - 64 sequences of up to 8192 keys with 1 to 5 new tokens, 10 rows on average and 20
+//    at most: bf16 84 / 91, e4m3 71 / 155.
+// A batch of decoding sequences with a prompt's chunk among them: both kernels, each
+// for its own sequences, cost two launches more; 63 + one chunk of 128 tokens took
+// bf16 94 us either way, e4m3 84 us with both and 145 us in the tcgen05 kernel alone;
+// 15 + one, e4m3, 58 us either way.
+struct Kernels {
+  bool few, tc;
+  int split;       // rows above which a sequence is the tcgen05 kernel's
+  int few_rows;    // rows of an item of the other
+};
+Kernels pick_kernels(const attn_cache_problem_t* p) {
+  const int group = p->heads_q / p->heads_kv, rows = step_rows(p);
+  const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
+  const int64_t average = static_cast<int64_t>(p->tokens) * group / p->num_seqs;
+  const Kernels few = {true, false, 0x7fffffff, cache_fwd_rows(rows)};
+  if (rows <= (e4m3 ? 32 : 16) || group > kCacheTcTile) return few;
+  if (e4m3 && rows <= 128 && average <= 32) return few;
+  if (e4m3 && p->num_seqs >= 24 && group <= 16 &&
+      p->tokens < static_cast<int64_t>(p->num_seqs) * p->max_new)
+    return {true, true, 16, cache_fwd_rows(group)};
+  return {false, true, 0, 0};
+}
+
 struct Workspace {
   size_t o, stash, ml, meta, bytes;
 };
-// The tcgen05 kernel takes steps with more than 16 query rows per KV head in their
-// longest sequence (its tiles hold 128; the other kernel would read the keys
-// again for every 16), where a whole group fits a tile.
-bool use_tc(const attn_cache_problem_t* p) {
-  return step_rows(p) > 16 && p->heads_q / p->heads_kv <= kCacheTcTile;
-}
-
-Workspace fwd_workspace(const attn_cache_problem_t* p) {
-  const bool tc = use_tc(p);
-  const size_t item = tc ? kCacheTcRows : cache_fwd_rows(step_rows(p));
-  const size_t rows = 2 * static_cast<size_t>(kCacheCtas) * item;
+// The workspace of one kernel, from `at` on.
+Workspace kernel_workspace(size_t at, int item_rows, int head_dim, bool tc) {
+  const size_t rows = 2 * static_cast<size_t>(kCacheCtas) * item_rows;
   Workspace w;
-  w.o = 0;
-  w.stash = rows * p->head_dim * sizeof(float);
-  w.ml = w.stash + (tc ? 0 : kCacheCtas * kCacheWarps * item * p->head_dim * sizeof(float));
+  w.o = at;
+  w.stash = w.o + rows * head_dim * sizeof(float);
+  w.ml = w.stash + (tc ? 0 : static_cast<size_t>(kCacheCtas) * kCacheWarps * item_rows * head_dim * sizeof(float));
   w.meta = w.ml + rows * sizeof(float2);
   w.bytes = w.meta + 2 * kCacheCtas * sizeof(int4);
   return w;
+}
+size_t fwd_workspace(const attn_cache_problem_t* p, const Kernels& k) {
+  size_t n = 0;
+  if (k.few) n = kernel_workspace(n, k.few_rows, p->head_dim, false).bytes;
+  if (k.tc) n = kernel_workspace(n, kCacheTcRows, p->head_dim, true).bytes;
+  return n;
 }
 
 attn_status_t status_of(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
@@ -172,7 +200,7 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
 
 size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p) {
   if (check_step(p) != ATTN_OK) return 0;
-  return fwd_workspace(p).bytes;
+  return fwd_workspace(p, pick_kernels(p));
 }
 
 attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const void* k_cache,
@@ -184,60 +212,69 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
   if (!q || !k_cache || !v_cache || !o || !lse || (e4m3 && (!k_scale || !v_scale)))
     return ATTN_ERR_INVALID_ARG;
-  CacheFwdArgs a;
-  if (!good_stride(p->q_stride, p->heads_q, p->head_dim, &a.q_stride)) return ATTN_ERR_INVALID_ARG;
+  CacheFwdArgs both[2];   // of the kernel for few rows, of the tcgen05 kernel
+  CacheFwdArgs& base = both[0];
+  if (!good_stride(p->q_stride, p->heads_q, p->head_dim, &base.q_stride)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
       !aligned(lse, 16) || !aligned(workspace, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
     return ATTN_ERR_ALIGNMENT;
   if (p->tokens == 0) return ATTN_OK;
-  const Workspace w = fwd_workspace(p);
-  if (!workspace || workspace_bytes < w.bytes) return ATTN_ERR_WORKSPACE;
+  const Kernels kern = pick_kernels(p);
+  if (!workspace || workspace_bytes < fwd_workspace(p, kern)) return ATTN_ERR_WORKSPACE;
 
-  a.s = to_step(p);
-  a.causal = p->causal ? 1 : 0;
-  a.scale_log2 = p->scale * kLog2e;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
-  a.stash = reinterpret_cast<float*>(ws + w.stash);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
-  const int rows = step_rows(p);
-  const bool tc = use_tc(p);
-  const int chunk = tc ? cache_tc_chunk(p->head_dim, e4m3) : kChunk;
+  base.s = to_step(p);
+  base.causal = p->causal ? 1 : 0;
+  base.scale_log2 = p->scale * kLog2e;
+  base.q = static_cast<const __nv_bfloat16*>(q);
+  base.k_cache = k_cache;
+  base.v_cache = v_cache;
+  base.k_scale = k_scale;
+  base.v_scale = v_scale;
+  base.o = static_cast<__nv_bfloat16*>(o);
+  base.lse = lse;
   const int64_t pool_rows = static_cast<int64_t>(p->num_pages) * p->heads_kv * p->page_size;
-  const int box = p->page_size < chunk ? p->page_size : chunk;
-  if (!make_cache_rows_map(&a.tm_k, k_cache, pool_rows, p->head_dim, e4m3, box) ||
-      !make_cache_rows_map(&a.tm_v, v_cache, pool_rows, p->head_dim, e4m3, box))
-    return ATTN_ERR_CUDA;
-  if (tc) {
-    a.tiles = kCacheTcRows / kCacheTcTile;
-    a.tile_tokens = kCacheTcTile / a.s.group;
-    a.tile_rows = a.tile_tokens * a.s.group;
-    if (!make_bf16_heads_map(&a.tm_q, q, p->tokens, p->heads_q, p->head_dim, a.q_stride, a.s.group,
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  size_t used = 0;
+  int grids[2];
+  both[1] = base;
+  for (int tc = 0; tc < 2; ++tc) {
+    if (!(tc ? kern.tc : kern.few)) continue;
+    CacheFwdArgs& a = both[tc];
+    a.rows_lo = tc && kern.few ? kern.split : 0;
+    a.rows_hi = tc ? 0x7fffffff : kern.split;
+    a.pad = tc ? !kern.few : 1;
+    const int chunk = tc ? cache_tc_chunk(p->head_dim, e4m3) : kChunk;
+    const int box = p->page_size < chunk ? p->page_size : chunk;
+    if (!(tc && e4m3) &&
+        (!make_cache_rows_map(&a.tm_k, k_cache, pool_rows, p->head_dim, e4m3, box) ||
+         !make_cache_rows_map(&a.tm_v, v_cache, pool_rows, p->head_dim, e4m3, box)))
+      return ATTN_ERR_CUDA;
+    a.tiles = tc ? kCacheTcRows / kCacheTcTile : 1;
+    a.tile_tokens = tc ? kCacheTcTile / a.s.group : 0;
+    a.tile_rows = tc ? a.tile_tokens * a.s.group : kern.few_rows;
+    if (tc && !e4m3 &&
+        !make_bf16_heads_map(&a.tm_q, q, p->tokens, p->heads_q, p->head_dim, a.q_stride, a.s.group,
                              a.tile_tokens))
       return ATTN_ERR_CUDA;
-  } else {
-    a.tiles = 1;
-    a.tile_rows = cache_fwd_rows(rows);
-    a.tile_tokens = 0;
+    const Workspace w = kernel_workspace(used, a.tiles * (tc ? kCacheTcTile : kern.few_rows), p->head_dim, tc);
+    a.part_o = reinterpret_cast<float*>(ws + w.o);
+    a.stash = reinterpret_cast<float*>(ws + w.stash);
+    a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    a.part_meta = reinterpret_cast<int4*>(ws + w.meta);
+    used = w.bytes;
+    // The most chunks that the step can have.  A CTA takes at least one per warp, of
+    // the tcgen05 kernel one.
+    const double items =
+        (static_cast<double>(p->tokens) * a.s.group / (a.tiles * a.tile_rows) + p->num_seqs) * p->heads_kv;
+    const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size) / chunk + 3);
+    const double ctas = chunks / (tc ? 1 : kCacheWarps) + 1;
+    grids[tc] = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
   }
-  // The most chunks that the step can have.  A CTA takes at least one per warp, of
-  // the tcgen05 kernel one.
-  const double items =
-      (static_cast<double>(p->tokens) * a.s.group / (a.tiles * a.tile_rows) + p->num_seqs) * p->heads_kv;
-  const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size) / chunk + 3);
-  const double ctas = chunks / (tc ? 1 : kCacheWarps) + 1;
-  const int grid = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return status_of(tc ? launch_cache_fwd_tc(a, p->head_dim, e4m3, grid, cs)
-                      : launch_cache_fwd(a, p->head_dim, e4m3, rows, grid, cs));
+  cudaError_t e = cudaSuccess;
+  if (kern.few) e = launch_cache_fwd(both[0], p->head_dim, e4m3, kern.few_rows, grids[0], cs);
+  if (e == cudaSuccess && kern.tc) e = launch_cache_fwd_tc(both[1], p->head_dim, e4m3, grids[1], cs);
+  return status_of(e);
 }
 
 }  // extern "C"

@@ -134,7 +134,7 @@ struct Cfg {
 __device__ __forceinline__ int seq_chunks(const StepSeq& q) { return (q.len + kChunk - 1) / kChunk + 2; }
 template <int ROWS>
 __device__ __forceinline__ int seq_blocks(const CacheFwdArgs& a, const StepSeq& q) {
-  return static_cast<int>((static_cast<int64_t>(q.m) * a.s.group + ROWS - 1) / ROWS);
+  return serves(a, q) ? (q.m * a.s.group + ROWS - 1) / ROWS : 0;
 }
 
 // An item and the walk over the items in the order in which they are dealt:
@@ -844,6 +844,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
   }
 
   // ---- padding rows: at or past cu_seqlens[num_seqs] ----
+  if (!a.pad) return;
   const int end = min(max(__ldg(s.cu + s.num_seqs), 0), s.tokens);
   const int64_t words = static_cast<int64_t>(s.tokens - end) * s.heads_q * (D / 8);
   uint4* o4 = reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(end) * s.heads_q * D);
@@ -990,8 +991,8 @@ cudaError_t launch(const CacheFwdArgs& a, int grid, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_dim(const CacheFwdArgs& a, bool e4m3, int rows, int grid, cudaStream_t st) {
-  if (cache_fwd_rows(rows) == 8)
+cudaError_t launch_dim(const CacheFwdArgs& a, bool e4m3, int item_rows, int grid, cudaStream_t st) {
+  if (item_rows == 8)
     return e4m3 ? launch<D, true, 1>(a, grid, st) : launch<D, false, 1>(a, grid, st);
   return e4m3 ? launch<D, true, 2>(a, grid, st) : launch<D, false, 2>(a, grid, st);
 }
@@ -1008,10 +1009,10 @@ cudaError_t launch_cache_join(const CacheFwdArgs& a, int head_dim, int item_rows
 
 int cache_fwd_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
-cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int rows, int grid,
-                             cudaStream_t st) {
-  return head_dim == 64 ? launch_dim<64>(a, e4m3, rows, grid, st)
-                        : launch_dim<128>(a, e4m3, rows, grid, st);
+cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int head_dim, bool e4m3, int item_rows,
+                             int grid, cudaStream_t st) {
+  return head_dim == 64 ? launch_dim<64>(a, e4m3, item_rows, grid, st)
+                        : launch_dim<128>(a, e4m3, item_rows, grid, st);
 }
 
 }  // namespace attn

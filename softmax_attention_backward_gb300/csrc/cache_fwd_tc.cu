@@ -99,7 +99,7 @@ __device__ __forceinline__ void item_block(const CacheFwdArgs& a, TcItem& it) {
   it.nc = max(it.seen[0], it.seen[1]) + kItemCost<E4M3>;
 }
 __device__ __forceinline__ int seq_blocks(const CacheFwdArgs& a, const StepSeq& q) {
-  return (q.m + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+  return serves(a, q) ? (q.m + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) : 0;
 }
 // The next item; the caller knows that there is one.
 template <int BN, bool E4M3>
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     // Warp w of four has rows 16 w .. 16 w + 15 of every chunk of keys or values; a thread
     // takes vectors of 16 codes.  The scales are left to the softmax.  (code * scale as
     // bf16, four instructions more for two codes, and per-thread copies of the codes took
-    // eight warps and 712 us where this form takes F16US.)
+    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 616.)
     if constexpr (E4M3) {
       if (range > 0) {
         constexpr int VR = D / 16;          // vectors of a row
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   }
 
   // ---- padding rows: at or past cu_seqlens[num_seqs] ----
-  const int end = min(max(__ldg(s.cu + s.num_seqs), 0), s.tokens);
+  const int end = a.pad ? min(max(__ldg(s.cu + s.num_seqs), 0), s.tokens) : s.tokens;
   const int64_t words = static_cast<int64_t>(s.tokens - end) * s.heads_q * (D / 8);
   uint4* o4 = reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(end) * s.heads_q * D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * C::THREADS;

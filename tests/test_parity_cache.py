@@ -131,6 +131,16 @@ def test_chunk_with_bad_pages(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 12, 1)])
+def test_prompts_among_many_decoding_sequences(cache, D, hq, hkv):
+    # e4m3: both kernels in one call; rows on both sides of the border, empty sequences, padding
+    seqs = [((37 * n) % 200 + 1, 1) for n in range(40)]
+    seqs[3], seqs[17], seqs[20], seqs[30], seqs[39] = (300, 200), (0, 0), (90, 8), (100, 9), (70, 60)
+    s = Step(cache, D, hq, hkv, 16, seqs, seed=71)
+    check(s.answer(), *run_fwd(s))
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_many_short_sequences(cache):
     # more sequences than threads of a CTA, empty ones among them, all within few chunks
     seqs = [((7 * n) % 41, 1 if (7 * n) % 41 else 0) for n in range(700)]
