@@ -16,7 +16,6 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -734,6 +733,8 @@ def _cache_problem(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv, c
     n, table = seqlens_kv.numel(), page_table.shape
     if len(table) != 2 or table[0] != n or cu_seqlens.numel() != n + 1:
         raise ValueError("seqlens_kv [n], cu_seqlens [n + 1] and page_table [n, max_pages] disagree")
+    if max_new > 0x7fffffff or table[1] > 0x7fffffff:
+        raise ValueError("max_new and page_table's columns must be below 2^31")
     return _CacheProblem(n, tokens, heads_q, shape[1], shape[3], kind, shape[2], shape[0], table[1],
                          max_new, causal, scale, 0, 0, 0, 0, 0, 0, cu_seqlens.data_ptr(),
                          seqlens_kv.data_ptr(), page_table.data_ptr(), error_word)
@@ -751,18 +752,16 @@ def _rows_stride(t, name, tokens, heads, dim, gpu, device):
 
 def _on(device, stream):
     """The context in which a call on `device` runs and allocates (so that what it
-    allocates belongs to the stream that writes it), and that stream's handle."""
+    allocates belongs to the stream that writes it), None for the present one, and
+    that stream's handle."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream), stream.cuda_stream
     handle = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch._C._cuda_getDevice():
-        return _HERE, handle
+        return None, handle
     return torch.cuda.device(device), handle
-
-
-_HERE = contextlib.nullcontext()
 
 
 def _at(t):
@@ -801,17 +800,23 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
             raise ValueError("cos_sin must be [positions, rot_dim]")
         p.max_position, p.rot_dim = cos_sin.shape
         p.rot_interleaved = 1 if interleaved else 0
+    if q is not None:
+        p.q_stride = _rows_stride(q, "q", T, heads_q, dim, dev.index, dev)
+        if q_out is not None and _need(q_out, "q_out", torch.bfloat16, dev).shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
     ctx, s = _on(dev, stream)
+    if ctx is None:
+        return _append_here(p, q, k, v, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, s)
     with ctx:
-        if q is not None:
-            p.q_stride = _rows_stride(q, "q", T, heads_q, dim, dev.index, dev)
-            if q_out is None:
-                q_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
-            elif _need(q_out, "q_out", torch.bfloat16, dev).shape != q.shape:
-                raise ValueError("q_out must have the shape of q")
-        code = lib().attn_cache_append(ctypes.byref(p), _at(q), k.data_ptr(), v.data_ptr(),
-                                       _at(cos_sin), _at(q_out), k_cache.data_ptr(),
-                                       v_cache.data_ptr(), _at(k_scale), _at(v_scale), s)
+        return _append_here(p, q, k, v, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, s)
+
+
+def _append_here(p, q, k, v, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, s):
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q) if p.q_stride == 0 else q.new_empty(q.shape)
+    code = (_LIB or lib()).attn_cache_append(ctypes.byref(p), _at(q), k.data_ptr(), v.data_ptr(),
+                                             _at(cos_sin), _at(q_out), k_cache.data_ptr(),
+                                             v_cache.data_ptr(), _at(k_scale), _at(v_scale), s)
     if code:
         raise AttnError("attn_cache_append", code)
     return q_out
@@ -846,25 +851,32 @@ def attn_cache_fwd(q, k_cache, v_cache, *, page_table, seqlens_kv, cu_seqlens, m
     dev = k_cache.device
     p = _cache_fwd_problem(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_kv,
                            cu_seqlens, max_new, causal, scale, error_word)
-    shape, ref = q.shape, ctypes.byref(p)
+    if out is not None and _need(out, "out", torch.bfloat16, dev).shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is not None and _need(lse, "lse", torch.float32, dev).shape != (p.heads_q, p.tokens):
+        raise ValueError("lse must be [heads, tokens]")
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
     ctx, s = _on(dev, stream)
+    if ctx is None:
+        return _fwd_here(p, q, k_cache, v_cache, k_scale, v_scale, out, lse, workspace, s)
     with ctx:
-        if out is None:
-            out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
-        elif _need(out, "out", torch.bfloat16, dev).shape != shape:
-            raise ValueError("out must have the shape of q")
-        if lse is None:
-            lse = q.new_empty((shape[1], shape[0]), dtype=torch.float32)
-        elif _need(lse, "lse", torch.float32, dev).shape != (shape[1], shape[0]):
-            raise ValueError("lse must be [heads, tokens]")
-        if workspace is None:
-            n = max(lib().attn_cache_fwd_workspace_size(ref), 16)
-            workspace = q.new_empty(n, dtype=torch.uint8)
-        else:
-            n = _need(workspace, "workspace", torch.uint8, dev).numel()
-        code = lib().attn_cache_fwd(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                    _at(k_scale), _at(v_scale), out.data_ptr(), lse.data_ptr(),
-                                    workspace.data_ptr(), n, s)
+        return _fwd_here(p, q, k_cache, v_cache, k_scale, v_scale, out, lse, workspace, s)
+
+
+def _fwd_here(p, q, k_cache, v_cache, k_scale, v_scale, out, lse, workspace, s):
+    L, ref = _LIB or lib(), ctypes.byref(p)
+    if out is None:
+        out = torch.empty_like(q) if p.q_stride == 0 else q.new_empty(q.shape)
+    if lse is None:
+        lse = q.new_empty((p.heads_q, p.tokens), dtype=torch.float32)
+    if workspace is None:
+        n = L.attn_cache_fwd_workspace_size(ref) or 16
+        workspace = q.new_empty(n, dtype=torch.uint8)
+    else:
+        n = workspace.numel()
+    code = L.attn_cache_fwd(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale),
+                            _at(v_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n, s)
     if code:
         raise AttnError("attn_cache_fwd", code)
     return out, lse

@@ -29,7 +29,8 @@ struct CacheStep {
 // pos0 .. (negative where there are more of them than the length), its keys
 // are 0 .. len - 1.  Rows outside [0, tokens) and keys past the page table are
 // cut off, so that arrays breaking their contract move no access out of its
-// buffer.
+// buffer; so are the last 255 keys below 2^31, so that a length rounded up to
+// whole chunks stays an int.
 struct StepSeq {
   int t0, m, pos0, len;
 };
@@ -40,7 +41,7 @@ __device__ __forceinline__ StepSeq step_seq(const CacheStep& s, int n, int* bad 
   q.t0 = min(max(a, 0), s.tokens);
   q.m = min(max(b, q.t0), s.tokens) - q.t0;
   const int cap = static_cast<int>(
-      min(static_cast<long long>(s.max_pages) << s.ps_shift, static_cast<long long>(0x7fffffff)));
+      min(static_cast<long long>(s.max_pages) << s.ps_shift, static_cast<long long>(0x7fffff00)));
   q.len = min(max(l, 0), cap);
   q.pos0 = max(l, 0) - q.m;
   if (bad && (l > cap || l < 0 || q.m > s.max_new || q.m > l)) *bad |= ATTN_DEVERR_SEQLEN;

@@ -247,16 +247,20 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       __shared__ int sh_unit[2];
       const int item = blockIdx.x / a.head_blocks;
       hw = (blockIdx.x - item * a.head_blocks) * UNITS + group;
-      // block-wide scan over the sequences' touched pages
+      // block-wide scan over the sequences' touched pages; the first block, which looks at all
+      // sequences, flags those that bring nothing because their positions are out of range
       if (threadIdx.x == 0) sh_unit[0] = -1;
       int base = 0;
       for (int n0 = 0; n0 < s.num_seqs; n0 += kThreads) {
         const int nn = n0 + threadIdx.x;
         int cnt = 0;
         if (nn < s.num_seqs) {
-          int lo, hi;
-          append_range(a, step_seq(s, nn), lo, hi);
+          int lo, hi, wrong = 0;
+          const StepSeq q = step_seq(s, nn, &wrong);
+          append_range(a, q, lo, hi);
           if (hi > lo) cnt = ((hi - 1) >> s.ps_shift) - (lo >> s.ps_shift) + 1;
+          else if (q.m > 0) wrong = ATTN_DEVERR_SEQLEN;
+          if (wrong && s.err && blockIdx.x == 0) atomicOr(s.err, wrong);
         }
         int inc = cnt;
 #pragma unroll
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
           sh_unit[1] = item - (end - cnt);
         }
         base = all;
-        if (base > item) break;
+        if (base > item && blockIdx.x > 0) break;
       }
       __syncthreads();
       n = hw < 2 * s.heads_kv ? sh_unit[0] : -1;

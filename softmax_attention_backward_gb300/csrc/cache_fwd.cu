@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
     };
     // A sequence's query rows towards L2 (the first 32 KB), well before their loads
     auto prefetch_q = [&]() {
-      const int words = min(cp.q.m * s.heads_q * (D / 64), 256);   // of 128 bytes
+      const int words = min(min(cp.q.m, 256) * s.heads_q * (D / 64), 256);   // of 128 bytes
       for (int i = lane; i < words; i += 32) {
         const int tok = i / (s.heads_q * (D / 64));
         const __nv_bfloat16* p = a.q + (cp.q.t0 + tok) * a.q_stride + (i - tok * s.heads_q * (D / 64)) * 64;

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       // lane l holds the page of column pg0 + l of sequence pg_n, e4m3: and its scales for
       // KV head pg_h
       int pg0 = -1, pg_n = -1, pg_h = -1, pid = -1;
-      float pks = 1.f, pvs = 0.f;
+      float pks = 1.f, pvs = -INFINITY;
       bool ok = mbar_wait_w(&bar_qempty[0], 1, ac);
       if (ok) issue_q(it, pt, 0);
       while (ok) {
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           if constexpr (E4M3) {
             if (pg_h != it.h) {
               pg_h = it.h;
-              pks = 1.f, pvs = 0.f;
+              pks = 1.f, pvs = -INFINITY;
               if (pid >= 0) {
                 pks = __ldg(a.k_scale + static_cast<int64_t>(pid) * s.heads_kv + it.h);
                 pvs = __log2f(__ldg(a.v_scale + static_cast<int64_t>(pid) * s.heads_kv + it.h));
@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             const float ks = __shfl_sync(0xffffffffu, pks, col - pg0);
             const float vs = __shfl_sync(0xffffffffu, pvs, col - pg0);
             if (lane < 4) sh_scale[gchunk & 31][lane] = make_float2(ks, vs);
+            __syncwarp();
           }
           // bits of the boxes that have a page; the y coordinate of lane l's box
           const uint32_t have = (__ballot_sync(0xffffffffu, pid >= 0) >> (col0 - pg0)) & ((1u << boxes) - 1);
@@ -442,6 +443,11 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         it = nx;
         pt = pn_;
         left = left_nx;
+      }
+      if (!ok) {   // a wait ran out: what is in flight gets a moment to land before the CTA leaves
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000ull) {
+        }
       }
       if constexpr (E4M3) {   // no more chunks
         const int slot = gring % C::RAW;
@@ -730,14 +736,15 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           m_run = m_use;
         } else {
           // four groups of 16 keys with scales of their own: the logits' factor, and log2 of
-          // the values' factor relative to the largest so far, which P takes along and the
-          // row sum takes off again (below 2^-100 nothing of P times it is left in fp16)
+          // the values' factor relative to the largest so far, which P, below 2^9, takes along
+          // and the row sum takes off again (from 2^-40 down nothing of it is left in fp16).
+          // The logits' factor stays above zero, which would make the masks NaN.
           const float2* sc = sh_scale[(gchunk + j) & 31];
           float fg[4], lg[4], mt = -INFINITY, lv_new = lv_ref;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const float2 kv = sc[g];
-            fg[g] = rowf * kv.x;
+            fg[g] = fmaxf(rowf * kv.x, 1e-37f);
             lg[g] = kv.y;
             lv_new = fmaxf(lv_new, kv.y);
             const float* xg = x + 16 * g;
@@ -756,7 +763,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float l = fmaxf(lg[g] - lv_new, -100.f);
+            const float l = fmaxf(lg[g] - lv_new, -40.f);
             const uint64_t nm2 = f2_pack(l - msub, l - msub), f2 = f2_pack(fg[g], fg[g]);
             uint64_t rs2[2] = {0ull, 0ull};
 #pragma unroll
