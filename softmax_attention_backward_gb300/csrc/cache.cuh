@@ -75,7 +75,7 @@ struct AppendArgs {
   int unit_blocks;
   int slots;         // page slots per sequence, 0: found by a scan over the sequences
   int units;         // slots > 0: (page item, KV head, K or V) units
-  int head_blocks;   // slots == 0: blocks of a page item
+  int head_blocks, loop;   // slots == 0: blocks of a page item, units that a thread goes over
   FastDiv fd_slots;
   // the other blocks: row_blocks blocks of tokens for each group of hb heads of q and,
   // bf16, of k and v
@@ -84,8 +84,8 @@ struct AppendArgs {
 
 cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, int page_size,
                                 cudaStream_t st);
-// Blocks that a page item of heads_kv heads takes (pages of page_size rows).
-int append_head_blocks(int head_dim, int page_size, int heads_kv);
+// e4m3 units of pages of page_size rows that a block works on at a time.
+int append_units(int head_dim, int page_size);
 // Tokens of a block of the row path.
 int append_row_tokens(int head_dim);
 

@@ -176,7 +176,11 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
     if (packed < items) items = packed;
   }
   const int64_t units = items * 2 * p->heads_kv;
-  a.head_blocks = append_head_blocks(p->head_dim, p->page_size, p->heads_kv);
+  // slots == 0: as many units (up to 8) go to one thread as leaves a block for every SM
+  const int wide = append_units(p->head_dim, p->page_size);
+  a.loop = 8;
+  while (a.loop > 1 && units / (wide * a.loop) < 152) a.loop /= 2;
+  a.head_blocks = (2 * p->heads_kv + wide * a.loop - 1) / (wide * a.loop);
   const int64_t unit_blocks = !e4m3 ? 0 : small ? (units + 7) / 8 : items * a.head_blocks;
   // Rows: blocks of tokens for groups of heads, as large (up to 8) as leaves two
   // blocks for every SM

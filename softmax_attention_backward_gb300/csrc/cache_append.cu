@@ -215,11 +215,21 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int block) {
   }
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // D: head dim.  G: threads of an e4m3 unit, into which PASSES * (G / (D / 16)) rows
-// fall at most; SCAN: blocks of units of one page item each, found by a scan over
-// the sequences (else slots of a sequence, a warp each).
+// fall at most; SCAN: blocks of a page item each, found by a scan over the sequences,
+// of which a group of G threads takes a.loop units, the next one's rows on their way
+// into shared memory while it works on one (else slots of a sequence, a warp each).
 template <int D, bool E4M3, int G, int PASSES, bool SCAN>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, SCAN ? 2 : 3) cache_append_kernel(const AppendArgs a) {
   if (!E4M3 || static_cast<int>(blockIdx.x) >= a.unit_blocks) {
     append_rows<D>(a, blockIdx.x - a.unit_blocks);
     return;
@@ -227,16 +237,17 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   if constexpr (E4M3) {
     constexpr int CPR = D / 16;              // threads of a row
     constexpr int RP = G / CPR;              // rows of a pass
-    constexpr int UNITS = kThreads / G;      // units of a block
+    constexpr int UNITS = kThreads / G;      // units of a block at a time
     const CacheStep& s = a.s;
     const int group = threadIdx.x / G, tid = threadIdx.x % G;
-    __shared__ float sh_amax[kThreads / 32];
+    __shared__ float sh_amax[4][kThreads / 32];
     int n = -1, j = 0;   // sequence and its page among those that the call touches
-    int hw;              // 2 KV head + (0: K, 1: V)
+    int hw, hw_end;      // 2 KV head + (0: K, 1: V), of the first unit; their end, UNITS apart
     if constexpr (!SCAN) {
       const int unit = blockIdx.x * UNITS + group;
       const int item = unit / (2 * s.heads_kv);
       hw = unit - item * 2 * s.heads_kv;
+      hw_end = hw + 1;
       const int nn = static_cast<int>(fdiv(static_cast<uint32_t>(item), a.fd_slots));
       if (unit < a.units && nn < s.num_seqs) {
         n = nn;
@@ -246,7 +257,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       __shared__ int sh_scan[kThreads / 32];
       __shared__ int sh_unit[2];
       const int item = blockIdx.x / a.head_blocks;
-      hw = (blockIdx.x - item * a.head_blocks) * UNITS + group;
+      hw = (blockIdx.x - item * a.head_blocks) * UNITS * a.loop + group;
+      hw_end = min(hw + UNITS * a.loop, 2 * s.heads_kv);
       // block-wide scan over the sequences' touched pages; the first block, which looks at all
       // sequences, flags those that bring nothing because their positions are out of range
       if (threadIdx.x == 0) sh_unit[0] = -1;
@@ -286,12 +298,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
         if (base > item && blockIdx.x > 0) break;
       }
       __syncthreads();
-      n = hw < 2 * s.heads_kv ? sh_unit[0] : -1;
+      n = sh_unit[0];
       j = sh_unit[1];
     }
 
-    const int h = hw >> 1;
-    const bool is_v = hw & 1;
     bool live = n >= 0;
     int lo = 0, hi = 0, pos0 = 0, t0 = 0, bad = 0;
     if (live) {
@@ -326,85 +336,127 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       if constexpr (G > 32) named_bar_sync(1 + group, G);
       else __syncwarp();
     };
-
-    const Chunks c = chunk_pair(tid % CPR, is_v ? 0 : a.rot_dim, a.interleaved);
-    const __nv_bfloat16* src = (is_v ? a.v + t0 * a.v_stride : a.k + t0 * a.k_stride) + h * D;
-    const int64_t stride = is_v ? a.v_stride : a.k_stride;
-    const int64_t ph = static_cast<int64_t>(page) * s.heads_kv + h;
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (ph << s.ps_shift) * D;
-    float* scale = (is_v ? a.v_scale : a.k_scale) + ph;
-    float old = 0.f;
-    if (first > 0) old = *scale;
-    float v[PASSES][16];
-    {
-      uint4 x[PASSES], y[PASSES];
+    // the largest of a unit's threads; `at`: 0 to 3, another in each of two calls in a row
+    auto largest = [&](float x, int at) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      if constexpr (G > 32) {
+        if (lane_id() == 0) sh_amax[at][warp_id()] = x;
+        sync();
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) x = fmaxf(x, sh_amax[at][group * (G / 32) + w]);
+      }
+      return x;
+    };
+    const int row0 = tid / CPR;   // the thread's first row
+    // The rows of unit hw: into registers, or (SCAN) to the thread's own place in buffer b
+    extern __shared__ uint4 sh_rows[];   // [buffer][PASSES][2][kThreads]
+    auto load = [&](int hw, int b, uint4 (&x)[PASSES], uint4 (&y)[PASSES]) {
+      const Chunks c = chunk_pair(tid % CPR, hw & 1 ? 0 : a.rot_dim, a.interleaved);
+      const int64_t stride = hw & 1 ? a.v_stride : a.k_stride;
+      const __nv_bfloat16* src = (hw & 1 ? a.v : a.k) + t0 * stride + (hw >> 1) * D;
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        const int r = i * RP + tid / CPR;
-        x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < cnt) {
-          x[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.ca * 8);
-          y[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.cb * 8);
+        const int r = i * RP + row0;
+        if constexpr (SCAN) {
+          uint4* at = sh_rows + (b * PASSES + i) * 2 * kThreads + threadIdx.x;
+          if (r < cnt) {
+            cp_async16(at, src + r * stride + c.ca * 8);
+            cp_async16(at + kThreads, src + r * stride + c.cb * 8);
+          }
+        } else {
+          x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < cnt) {
+            x[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.ca * 8);
+            y[i] = *reinterpret_cast<const uint4*>(src + r * stride + c.cb * 8);
+          }
         }
       }
+      if constexpr (SCAN) cp_async_commit();
+    };
+
+    uint4 x[PASSES], y[PASSES];
+    if (hw < hw_end) load(hw, 0, x, y);
+    for (int k = 0; hw < hw_end; ++k, hw += UNITS) {
+      const bool is_v = hw & 1;
+      const Chunks c = chunk_pair(tid % CPR, is_v ? 0 : a.rot_dim, a.interleaved);
+      const int64_t ph = static_cast<int64_t>(page) * s.heads_kv + (hw >> 1);
+      uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (ph << s.ps_shift) * D;
+      float* scale = (is_v ? a.v_scale : a.k_scale) + ph;
+      float old = 0.f;
+      if (first > 0) old = *scale;
+      if constexpr (SCAN) {
+        if (hw + UNITS < hw_end) {
+          load(hw + UNITS, (k + 1) & 1, x, y);
+          cp_async_wait<1>();
+        } else {
+          cp_async_wait<0>();
+        }
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const uint4* at = sh_rows + ((k & 1) * PASSES + i) * 2 * kThreads + threadIdx.x;
+          x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (i * RP + row0 < cnt) x[i] = at[0], y[i] = at[kThreads];
+        }
+      }
+      float v[PASSES][16];
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) unpack16(x[i], y[i], v[i]);
-    }
-    float amax = 0.f;
+      float amax = 0.f;   // (fmaxf leaves NaN out)
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = i * RP + tid / CPR;
-      if (r < cnt && c.rot >= 0) {
-        Angles ang;
-        ang.load(a.cos_sin + static_cast<int64_t>(pos0 + r) * a.rot_dim + c.rot, a.rot_dim >> 1);
-        ang.apply(v[i], a.interleaved);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float m = fabsf(v[i][e]);
-        if (m < INFINITY) amax = fmaxf(amax, m);   // neither infinities nor NaN
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if constexpr (G > 32) {
-      if (lane_id() == 0) sh_amax[warp_id()] = amax;
-      sync();
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) amax = fmaxf(amax, sh_amax[group * (G / 32) + w]);
-    }
-    const int e = scale_exponent(amax);
-    float sc = exp2_int(e);
-    float inv = exp2_int(-e);
-    if (first > 0) {
-      if (old >= sc) {
-        sc = old;
-        inv = 1.f / old;   // exact: a power of two
-      } else {
-        // the page's earlier codes again, under the larger scale
-        const float f = old * inv;
-        uint32_t* w = reinterpret_cast<uint32_t*>(dst);
-        for (int i = tid; i < first * D / 4; i += G) {
-          float x[4];
-          unpack_e4m3(w[i], x);
-          w[i] = pack_e4m3(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = i * RP + row0;
+        if (r < cnt && c.rot >= 0) {
+          Angles ang;
+          ang.load(a.cos_sin + static_cast<int64_t>(pos0 + r) * a.rot_dim + c.rot, a.rot_dim >> 1);
+          ang.apply(v[i], a.interleaved);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[i][e]));
       }
-      sync();   // every thread has read the old scale
-    }
-    if (tid == 0) *scale = sc;
+      amax = largest(amax, k & 1);
+      if (amax == INFINITY) {   // once more, without the infinities
+        amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = i * RP + tid / CPR;
-      if (r < cnt) {
-        uint32_t w[4];
+        for (int i = 0; i < PASSES; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          w[x] = pack_e4m3(v[i][4 * x] * inv, v[i][4 * x + 1] * inv, v[i][4 * x + 2] * inv,
-                           v[i][4 * x + 3] * inv);
-        uint8_t* row = dst + (first + r) * D;
-        *reinterpret_cast<uint2*>(row + c.ca * 8) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(row + c.cb * 8) = make_uint2(w[2], w[3]);
+          for (int e = 0; e < 16; ++e)
+            if (fabsf(v[i][e]) < INFINITY) amax = fmaxf(amax, fabsf(v[i][e]));
+        amax = largest(amax, 2 + (k & 1));
+      }
+      const int e = scale_exponent(amax);
+      float sc = exp2_int(e);
+      float inv = exp2_int(-e);
+      if (first > 0) {
+        if (old >= sc) {
+          sc = old;
+          inv = 1.f / old;   // exact: a power of two
+        } else {
+          // the page's earlier codes again, under the larger scale
+          const float f = old * inv;
+          uint32_t* w = reinterpret_cast<uint32_t*>(dst);
+          for (int i = tid; i < first * D / 4; i += G) {
+            float z[4];
+            unpack_e4m3(w[i], z);
+            w[i] = pack_e4m3(z[0] * f, z[1] * f, z[2] * f, z[3] * f);
+          }
+        }
+        sync();   // every thread has read the old scale
+      }
+      if (tid == 0) *scale = sc;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = i * RP + row0;
+        if (r < cnt) {
+          uint32_t w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            w[z] = pack_e4m3(v[i][4 * z] * inv, v[i][4 * z + 1] * inv, v[i][4 * z + 2] * inv,
+                             v[i][4 * z + 3] * inv);
+          uint8_t* row = dst + (first + r) * D;
+          *reinterpret_cast<uint2*>(row + c.ca * 8) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(row + c.cb * 8) = make_uint2(w[2], w[3]);
+        }
       }
     }
   }
@@ -416,6 +468,17 @@ constexpr int page_threads(int head_dim, int page_size) {
   return page_size * (head_dim / 16) / 4 < 32 ? 32 : page_size * (head_dim / 16) / 4;
 }
 
+template <int D, int PS>
+cudaError_t launch_pages(const AppendArgs& a, int grid, cudaStream_t st) {
+  constexpr int G = page_threads(D, PS), PASSES = PS * (D / 16) / G, SMEM = 2 * PASSES * 2 * kThreads * 16;
+  auto kern = cache_append_kernel<D, true, G, PASSES, true>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kern, SMEM, ready);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, SMEM, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch(const AppendArgs& a, bool e4m3, int page_size, cudaStream_t st) {
   const int grid = a.unit_blocks + a.row_blocks * (a.q_groups + 2 * a.kv_groups);
@@ -425,13 +488,11 @@ cudaError_t launch(const AppendArgs& a, bool e4m3, int page_size, cudaStream_t s
   } else if (a.slots > 0) {   // units of up to kAppendSmall rows, a warp each
     cache_append_kernel<D, true, 32, kAppendSmall * (D / 16) / 32, false><<<grid, kThreads, 0, st>>>(a);
   } else {
-    constexpr int T16 = page_threads(D, 16), T32 = page_threads(D, 32), T64 = page_threads(D, 64),
-                  T128 = page_threads(D, 128);
     switch (page_size) {
-      case 16: cache_append_kernel<D, true, T16, D / T16, true><<<grid, kThreads, 0, st>>>(a); break;
-      case 32: cache_append_kernel<D, true, T32, 2 * D / T32, true><<<grid, kThreads, 0, st>>>(a); break;
-      case 64: cache_append_kernel<D, true, T64, 4 * D / T64, true><<<grid, kThreads, 0, st>>>(a); break;
-      default: cache_append_kernel<D, true, T128, 8 * D / T128, true><<<grid, kThreads, 0, st>>>(a);
+      case 16: return launch_pages<D, 16>(a, grid, st);
+      case 32: return launch_pages<D, 32>(a, grid, st);
+      case 64: return launch_pages<D, 64>(a, grid, st);
+      default: return launch_pages<D, 128>(a, grid, st);
     }
   }
   return cudaGetLastError();
@@ -439,10 +500,7 @@ cudaError_t launch(const AppendArgs& a, bool e4m3, int page_size, cudaStream_t s
 
 }  // namespace
 
-int append_head_blocks(int head_dim, int page_size, int heads_kv) {
-  const int units = kThreads / page_threads(head_dim, page_size);
-  return (2 * heads_kv + units - 1) / units;
-}
+int append_units(int head_dim, int page_size) { return kThreads / page_threads(head_dim, page_size); }
 int append_row_tokens(int head_dim) { return kThreads / (head_dim / 16); }
 
 cudaError_t launch_cache_append(const AppendArgs& a, int head_dim, bool e4m3, int page_size,
