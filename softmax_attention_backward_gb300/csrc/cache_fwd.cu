@@ -860,53 +860,84 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
 // [y ROWS, (y + 1) ROWS) of the item that begins in CTA b and goes on in CTA b + 1
 // (there is at most one): its parts are CTA b's second, then the first of each
 // following CTA until one ends the item.
+//
+// A few KB a block: only latency counts, so that all CTAs' notes are read at once,
+// and then the sequence, the statistics and the first kAhead parts' outputs.
 constexpr int kJoinThreads = 256;   // few enough to wait beside the main kernel's CTA on an SM
+constexpr int kAhead = 4;
+static_assert(kCacheCtas <= kJoinThreads, "a thread reads each CTA's note");
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     cache_join_kernel(const __grid_constant__ CacheFwdArgs a, int grid, int item_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int WARPS = kJoinThreads / 32;
   constexpr int POS = ROWS * (D / 4);                    // float4 positions, rows first
   constexpr int SPLIT = POS >= kJoinThreads ? 1 : kJoinThreads / POS;
+  constexpr int PER = POS * SPLIT / kJoinThreads;        // positions of a thread
   constexpr int LD = D + 8;                              // bf16 row stride of the result
   __shared__ float sh_w[kCacheCtas][ROWS];
   __shared__ float sh_l[ROWS], sh_m[ROWS];
   __shared__ float4 sh_o[SPLIT > 1 ? kJoinThreads : 1];
   __shared__ __align__(16) __nv_bfloat16 sh_out[ROWS * LD];
-  __shared__ int sh_end;
+  __shared__ int sh_end[WARPS];
   const CacheStep& s = a.s;
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, warp = warp_id(), lane = lane_id(), base = blockIdx.y * ROWS;
+  const int c = threadIdx.x;
+  const int kind = c > b && c < grid ? a.part_meta[2 * c].x : 0;
   const int4 meta = a.part_meta[2 * b + 1];
   if (!(meta.x & 1)) return;   // (kind bit 1, "begins", is set in every second part)
-  const StepSeq q = step_seq(s, meta.y);
-  const int rows_all = q.m * s.group;
-  // row rl of the item: row tr of its tile, query row r of the sequence and KV head
-  const int tile_size = item_rows / a.tiles;
-  auto row_of = [&](int rl) {
-    const int tile = rl / tile_size, tr = rl - tile * tile_size;
-    return tr < a.tile_rows ? (meta.w * a.tiles + tile) * a.tile_rows + tr : rows_all;
-  };
-  const int base = blockIdx.y * ROWS;
-  if (threadIdx.x == 0) sh_end = grid;
-  if (!__syncthreads_or(threadIdx.x < ROWS && row_of(base + threadIdx.x) < rows_all)) return;
   // the following CTAs' first parts, until one ends the item
-  for (int c = b + 1 + threadIdx.x; c < grid; c += kJoinThreads)
-    if (a.part_meta[2 * c].x & 4) atomicMin(&sh_end, c);
+  const uint32_t ends = __ballot_sync(0xffffffffu, kind & 4);
+  if (lane == 0) sh_end[warp] = ends ? 32 * warp + __ffs(ends) - 1 : grid - 1;
+  const StepSeq q = step_seq(s, meta.y);
   __syncthreads();
-  const int parts = min(sh_end, grid - 1) - b + 1;
-  const int warp = warp_id(), lane = lane_id();
+  int end = grid - 1;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) end = min(end, sh_end[w]);
+  const int parts = end - b + 1;
   auto slot_of = [&](int p) { return static_cast<int64_t>(p == 0 ? 2 * b + 1 : 2 * (b + p)); };
-  for (int r = warp; r < ROWS; r += kJoinThreads / 32) {
-    if (row_of(base + r) >= rows_all) continue;
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32)
+
+  float4 ahead[PER][kAhead];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = SPLIT > 1 ? threadIdx.x % POS : i * kJoinThreads + threadIdx.x;
+    const int sp = SPLIT > 1 ? threadIdx.x / POS : 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = sp + k * SPLIT;
+      ahead[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < parts)
+        ahead[i][k] = *(reinterpret_cast<const float4*>(a.part_o) +
+                        (slot_of(p) * (D / 4) + e / ROWS) * item_rows + base + e % ROWS);
+    }
+  }
+  // row rl of the item: row tr of its tile, query row r of the sequence and KV head
+  const int rows_all = q.m * s.group;
+  const int tile_size = item_rows / a.tiles, tile = base / tile_size, tr0 = base - tile * tile_size;
+  auto row_of = [&](int rl) {
+    return tr0 + rl < a.tile_rows ? (meta.w * a.tiles + tile) * a.tile_rows + tr0 + rl : rows_all;
+  };
+  float2 ml0[ROWS / WARPS];
+#pragma unroll
+  for (int i = 0; i < ROWS / WARPS; ++i) {
+    ml0[i] = make_float2(-INFINITY, 0.f);
+    if (lane < parts) ml0[i] = a.part_ml[slot_of(lane) * item_rows + base + warp + i * WARPS];
+  }
+  if (row_of(0) >= rows_all) return;   // (a tile's rows that exist come first)
+#pragma unroll
+  for (int i = 0; i < ROWS / WARPS; ++i) {
+    const int r = warp + i * WARPS;
+    if (row_of(r) >= rows_all) continue;
+    float m = ml0[i].x;
+    for (int p = lane + 32; p < parts; p += 32)
       m = fmaxf(m, a.part_ml[slot_of(p) * item_rows + base + r].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ms = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     for (int p = lane; p < parts; p += 32) {
-      const float2 ml = a.part_ml[slot_of(p) * item_rows + base + r];
+      const float2 ml = p < 32 ? ml0[i] : a.part_ml[slot_of(p) * item_rows + base + r];
       const float w = ex2(ml.x - ms);
       sh_w[p][r] = w;
       l += w * ml.y;
@@ -919,16 +950,24 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
   }
   __syncthreads();
-#pragma unroll 2
-  for (int e0 = 0; e0 < POS; e0 += kJoinThreads) {
-    const int e = SPLIT > 1 ? threadIdx.x % POS : e0 + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = SPLIT > 1 ? threadIdx.x % POS : i * kJoinThreads + threadIdx.x;
     const int sp = SPLIT > 1 ? threadIdx.x / POS : 0;
     const int rl = e % ROWS, d4 = e / ROWS;
-    const bool in = row_of(base + rl) < rows_all;
+    const bool in = row_of(rl) < rows_all;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (in) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = sp + k * SPLIT;
+        if (p >= parts) break;
+        const float w = sh_w[p][rl];
+        const float4 x = ahead[i][k];
+        o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+      }
 #pragma unroll 4
-      for (int p = sp; p < parts; p += SPLIT) {
+      for (int p = sp + kAhead * SPLIT; p < parts; p += SPLIT) {
         const float w = sh_w[p][rl];
         const float4 x = *(reinterpret_cast<const float4*>(a.part_o) +
                            (slot_of(p) * (D / 4) + d4) * item_rows + base + rl);
@@ -954,7 +993,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   __syncthreads();
   for (int e = threadIdx.x; e < ROWS * (D / 8); e += kJoinThreads) {
-    const int rl = e / (D / 8), d = (e - rl * (D / 8)) * 8, r = row_of(base + rl);
+    const int rl = e / (D / 8), d = (e - rl * (D / 8)) * 8, r = row_of(rl);
     if (r >= rows_all) continue;
     const int tok = r / s.group, hd = meta.z * s.group + (r - tok * s.group);
     *reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(q.t0 + tok) * s.heads_q + hd) * D + d) =
