@@ -268,9 +268,15 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         if (off < it.nc) break;
         off -= it.nc;
       }
+      int64_t left = f1 - f0;
+      if (off > 0 && off >= max(it.seen[0], it.seen[1])) {   // the CTA before has all of the item
+        left -= it.nc - off;
+        off = 0;
+        if (left > 0) item_next<BN, E4M3>(a, it);
+      }
       sh_item = it;
       sh_c0 = static_cast<int>(off);
-      sh_left = f1 - f0;
+      sh_left = max(left, static_cast<int64_t>(0));
     }
     __syncthreads();
   }
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         PartInfo f;
         f.n_w[0] = pt.n_w[0], f.n_w[1] = pt.n_w[1], f.n_kv = pt.n_kv, f.c0 = pt.c0;
         f.q = it.q, f.n = it.n, f.h = it.h, f.rb = it.rb;
-        f.kind = 1 | (pt.c0 == 0 ? 2 : 0) | (pt.c0 + pt.span == it.nc ? 4 : 0);
+        f.kind = 1 | (pt.c0 == 0 ? 2 : 0) | (pt.c0 + pt.span >= max(it.seen[0], it.seen[1]) ? 4 : 0);
         sh_info[qb] = f;
         if constexpr (E4M3) {   // (the softmax warps bring the rows)
           mbar_arrive(&bar_q[qb]);
@@ -628,42 +634,46 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       float rowf = sl2;            // logit factor of the row
       float lv_ref = -INFINITY;    // e4m3: O is kept in units of 2^lv_ref
       if constexpr (E4M3) {
-        // The row as fp16 times a power of two, its largest element below 512: exact down
-        // to 2^-32 of it and then within 2^-33 of it.  (The tile is free: its last S of the
-        // part before has been read by this warpgroup.)
+        // The rows as fp16 times a power of two each, its largest element below 512: exact down
+        // to 2^-32 of it and then within 2^-33 of it.  D / 8 lanes take a row.  (The tile is
+        // free: its last S of the part before has been read by this warpgroup.)
         if (nt > 0) {
-          const __nv_bfloat16* src = a.q + static_cast<int64_t>(max(row_out, 0)) * a.q_stride + hd * D;
-          uint8_t* row = sQ + t * C::Q_BYTES + tr * 128;
-          uint4 v[D / 8];
+          constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
+          const int64_t at = row_out < 0 ? -1 : static_cast<int64_t>(row_out) * a.q_stride + hd * D;
+          const int sub = lane / LPR, vec = lane % LPR;
+          uint4 v[NI];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
+          for (int i = 0; i < NI; ++i) {
+            const int64_t src = __shfl_sync(0xffffffffu, at, i * RPI + sub);
             v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row_out >= 0) v[i] = *reinterpret_cast<const uint4*>(src + i * 8);
+            if (src >= 0) v[i] = *reinterpret_cast<const uint4*>(a.q + src + vec * 8);
           }
-          float amax = 0.f;
+          int k_row = 0;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int i = 0; i < NI; ++i) {
+            uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float amax = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w4[e] << 16)),
                                        fabsf(__uint_as_float(w4[e] & 0xffff0000u))));
-          }
-          const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
-          rowf *= __uint_as_float(static_cast<uint32_t>(k - 8 + 127) << 23);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
+            const int mine = __shfl_sync(0xffffffffu, k, (lane % RPI) * LPR);
+            if (lane / RPI == i) k_row = mine;   // of the thread's own row
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __half2 hh = __floats2half2_rn(__uint_as_float(w4[e] << 16) * up,
                                                    __uint_as_float(w4[e] & 0xffff0000u) * up);
               w4[e] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            *reinterpret_cast<uint4*>(row + (i >> 3) * C::BM * 128 + (((i & 7) ^ (tr & 7)) << 4)) =
-                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            const int r = (warp & 3) * 32 + i * RPI + sub;
+            *reinterpret_cast<uint4*>(sQ + t * C::Q_BYTES + (vec >> 3) * C::BM * 128 + r * 128 +
+                                      (((vec & 7) ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
+          rowf *= __uint_as_float(static_cast<uint32_t>(k_row - 8 + 127) << 23);
           fence_proxy_async_smem();
           mbar_arrive(&bar_qready[t]);
         }
