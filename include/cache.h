@@ -27,7 +27,8 @@ typedef enum {
  *
  * The cache: k_cache and v_cache are pools [num_pages, heads_kv, page_size,
  * head_dim] of bf16 or e4m3; an e4m3 pool comes with k_scale and v_scale, fp32
- * [num_pages, heads_kv], and a code c stands for c * scale.  Sequence n's key j
+ * [num_pages, heads_kv] (positive, finite and not subnormal; attn_cache_append
+ * writes powers of two), and a code c stands for c * scale.  Sequence n's key j
  * lies in row j % page_size of page page_table[n, j / page_size]; page_table is
  * int32 [num_seqs, max_pages].  Sequences may share pages that no call appends
  * to.  Rows and pages that no sequence's length reaches may hold anything.
@@ -127,6 +128,13 @@ size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p);
  * [heads_q, tokens].  A row without a visible key, and the padding rows, get
  * o = 0 and lse = -inf.  Keys past a sequence's length, in rows of a page that
  * was never written, do not affect any result whatever they hold.
+ * A key that is infinite or NaN reaches the rows that see it; a value that is,
+ * through 0 * NaN, also rows of its sequence in the same call that causality
+ * keeps from it.
+ * P is rounded before the product with V: bf16 caches, to bf16 (within 2^-8 of it)
+ * by the kernel for many query rows per KV head and to a sum of two bf16 (2^-16) by
+ * that for few; e4m3 caches, to fp16 (2^-11).  Which kernel serves a
+ * call follows from the problem alone.
  * Any number of new tokens per sequence, one included; sequences of different
  * kinds may share a call.  The result is bitwise reproducible on one device.
  */

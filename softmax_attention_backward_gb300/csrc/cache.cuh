@@ -90,7 +90,9 @@ int append_units(int head_dim, int page_size);
 int append_row_tokens(int head_dim);
 
 // e4m3 calls with at most this many new tokens per sequence give each (page, KV
-// head, K or V) unit to one warp, the others to as many threads as a page needs.
+// head, K or V) unit to one warp, the others to as many threads as a page needs,
+// found by a scan over the sequences.  256 sequences with 1, 8, 12 new tokens: 6.3,
+// 16.3, 39 us by warps (of 16 rows for the 12), 13, 23, 29 us by the scan.
 constexpr int kAppendSmall = 8;
 
 // Chunks of 32 keys are the unit in which attn_cache_fwd deals work.

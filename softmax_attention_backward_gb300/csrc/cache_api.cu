@@ -176,14 +176,17 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
     if (packed < items) items = packed;
   }
   const int64_t units = items * 2 * p->heads_kv;
-  // slots == 0: as many units (up to 8) go to one thread as leaves a block for every SM
+  // slots == 0: as many units (up to 8) go to one thread as leaves a block for every SM.
+  // One, this rule, always eight: 89, 75, 75 us for four prompts, 46, 29, 29 us for 256
+  // sequences with 12 new tokens, 11, 8.2, 11 us for 64, and 3.3, 3.3, 9.3 us for one.
   const int wide = append_units(p->head_dim, p->page_size);
   a.loop = 8;
   while (a.loop > 1 && units / (wide * a.loop) < 152) a.loop /= 2;
   a.head_blocks = (2 * p->heads_kv + wide * a.loop - 1) / (wide * a.loop);
   const int64_t unit_blocks = !e4m3 ? 0 : small ? (units + 7) / 8 : items * a.head_blocks;
   // Rows: blocks of tokens for groups of heads, as large (up to 8) as leaves two
-  // blocks for every SM
+  // blocks for every SM.  One head, this rule, always eight: 94, 75, 75 us for four
+  // prompts, 2.7, 2.7, 4.3 us for one token, 6.5, 4.7, 6.2 us for 512 sequences' tokens.
   const int per = append_row_tokens(p->head_dim);
   a.row_blocks = (p->tokens + per - 1) / per;
   const int64_t heads = (q ? p->heads_q : 0) + (e4m3 ? 0 : 2 * p->heads_kv);

@@ -16,8 +16,12 @@
 // rotated values in registers, reduce their largest magnitude and write the
 // codes.
 //
-// Everything is one pass over the inputs, bound by HBM for prompts and by
-// latency for single tokens.
+// Everything is one pass over the inputs.  Four prompts of 8192 to 350 tokens, 16 heads
+// of 128, into e4m3 pages: 75 us, 3.9 TB/s over what is read and written, bound by the
+// latency of a unit (rows, angles, the maximum, codes) with the 16 warps that the
+// registers leave an SM.  8 chunks of up to 1000 tokens into bf16 pages, 32 heads of 64:
+// 14 us, 3.9 TB/s.  A token for each of 64 sequences, e4m3: 3.5 us, for one: 2.8 us,
+// both the latency of a chain of dependent loads (lengths, page, rows).
 #include "cache.cuh"
 
 namespace attn {

@@ -20,6 +20,24 @@
 // Rows of a page past the sequence's length may hold anything: their logits are
 // masked, and their values are zeroed in shared memory before the MMA reads them
 // (0 * NaN).  The last chunk of an item alone pays for that.
+//
+// e4m3: all operands are fp16, in which codes are exact.  Warp 8 brings the codes of
+// a chunk by bulk copies into a ring of their own, warps 11..14 convert them into
+// the slots that the MMAs read; the softmax warps bring and scale their rows of q.
+// The scales of 16-key groups enter with the softmax: the key scale as a factor of
+// the logits, log2 of the value scale as a summand in the exponent of P, which the
+// row sum takes off again.
+//
+// Bound by the softmax (bf16: 1.34 PFLOP/s, 460 us, for 2 x 2048 new tokens over
+// 8192 cached ones, 32 query heads of 128, 70% of the measured GEMM rate; the dense
+// forward's own rate is 1.27), and for short items by what an item costs beside its
+// chunks: about 5 us until the first logits, 2 us for the outputs, 10 us for the join of
+// partial results (12 sequences of up to 700 new tokens over up to 4000 keys: 52 us).
+// e4m3: 602 us and 78 us for the same two; the conversion, whose instruction shares
+// its pipe with the exponentials, and 64-key chunks with four scales each make a
+// chunk 1.2 us long instead of 0.95.  Converting on the integer pipe takes three
+// instructions for one, 5 more with the check for NaN, and was slower in the four
+// warps that the registers leave room for (827 us without the check, 1414 with it).
 #include "cache.cuh"
 #include "launch.h"
 
@@ -52,9 +70,9 @@ struct TcCfg {
 
 // Chunks by which an item counts more in the dealing than it has, for its query
 // tiles, its first and last chunk and its outputs: 12 sequences of up to 700 new
-// tokens over 4000 keys took 56, 57, 61 us with 3, 6, 10 (bf16) and 94, 86, 80 us
-// (e4m3, whose queries the softmax warps convert), 2 x 4096 fresh tokens 273, 261,
-// 270 us.
+// tokens over up to 4000 keys took 52.2, 52.5, 54.9 us with 4, 5, 7 (bf16) and 88, 85,
+// 78 us with 5, 7, 10 (e4m3, whose queries the softmax warps convert), 2 x 4096 fresh
+// tokens 257, 253, 258 us with 4, 5, 7.
 template <bool E4M3>
 constexpr int kItemCost = E4M3 ? 10 : 5;
 
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     // Warp w of four has rows 16 w .. 16 w + 15 of every chunk of keys or values; a thread
     // takes vectors of 16 codes.  The scales are left to the softmax.  (code * scale as
     // bf16, four instructions more for two codes, and per-thread copies of the codes took
-    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 616.)
+    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 602.)
     if constexpr (E4M3) {
       if (range > 0) {
         constexpr int VR = D / 16;          // vectors of a row
