@@ -97,7 +97,12 @@ constexpr int kAppendSmall = 8;
 
 // Chunks of 32 keys are the unit in which attn_cache_fwd deals work.
 constexpr int kChunk = 32;
-constexpr int kCacheWarps = 8;
+// Warps of a CTA of the kernel for few rows, by the rows of its items.  e4m3 keys take
+// as many instructions as bf16 ones in half the time: one sequence of 262144 of them,
+// 8 and 12 warps, 103 and 98 us; but 16 rows at 12 warps have too few registers (32
+// sequences of 4096 keys with 20 rows each: 136 and 161 us).  bf16: 65 and 75 us for 64
+// sequences of up to 8192 keys.
+constexpr int cache_warps(bool e4m3, int rows) { return e4m3 && rows == 8 ? 12 : 8; }
 // CTAs of attn_cache_fwd (fewer for small steps): a fixed count, not the
 // device's SM count, so that the result does not depend on the device.
 constexpr int kCacheCtas = 152;

@@ -102,20 +102,21 @@ struct Workspace {
   size_t o, stash, ml, meta, bytes;
 };
 // The workspace of one kernel, from `at` on.
-Workspace kernel_workspace(size_t at, int item_rows, int head_dim, bool tc) {
+Workspace kernel_workspace(size_t at, int item_rows, int head_dim, bool tc, bool e4m3) {
   const size_t rows = 2 * static_cast<size_t>(kCacheCtas) * item_rows;
   Workspace w;
   w.o = at;
   w.stash = w.o + rows * head_dim * sizeof(float);
-  w.ml = w.stash + (tc ? 0 : static_cast<size_t>(kCacheCtas) * kCacheWarps * item_rows * head_dim * sizeof(float));
+  w.ml = w.stash + (tc ? 0 : static_cast<size_t>(kCacheCtas) * cache_warps(e4m3, item_rows) * item_rows * head_dim * sizeof(float));
   w.meta = w.ml + rows * sizeof(float2);
   w.bytes = w.meta + 2 * kCacheCtas * sizeof(int4);
   return w;
 }
 size_t fwd_workspace(const attn_cache_problem_t* p, const Kernels& k) {
+  const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
   size_t n = 0;
-  if (k.few) n = kernel_workspace(n, k.few_rows, p->head_dim, false).bytes;
-  if (k.tc) n = kernel_workspace(n, kCacheTcRows, p->head_dim, true).bytes;
+  if (k.few) n = kernel_workspace(n, k.few_rows, p->head_dim, false, e4m3).bytes;
+  if (k.tc) n = kernel_workspace(n, kCacheTcRows, p->head_dim, true, e4m3).bytes;
   return n;
 }
 
@@ -263,7 +264,7 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
         !make_bf16_heads_map(&a.tm_q, q, p->tokens, p->heads_q, p->head_dim, a.q_stride, a.s.group,
                              a.tile_tokens))
       return ATTN_ERR_CUDA;
-    const Workspace w = kernel_workspace(used, a.tiles * (tc ? kCacheTcTile : kern.few_rows), p->head_dim, tc);
+    const Workspace w = kernel_workspace(used, a.tiles * (tc ? kCacheTcTile : kern.few_rows), p->head_dim, tc, e4m3);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     a.stash = reinterpret_cast<float*>(ws + w.stash);
     a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -274,7 +275,7 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
     const double items =
         (static_cast<double>(p->tokens) * a.s.group / (a.tiles * a.tile_rows) + p->num_seqs) * p->heads_kv;
     const double chunks = items * ((static_cast<double>(p->max_pages) * p->page_size) / chunk + 3);
-    const double ctas = chunks / (tc ? 1 : kCacheWarps) + 1;
+    const double ctas = chunks / (tc ? 1 : cache_warps(e4m3, kern.few_rows)) + 1;
     grids[tc] = ctas < kCacheCtas ? static_cast<int>(ctas) : kCacheCtas;
   }
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -32,9 +32,9 @@
 // around that by latency: about 5 us from the launch to the first keys (the dealing, the
 // page lists, the first copies), 3 us for the join in a CTA and 3 for that of CTAs.
 // 64 sequences of 15 to 8192 keys, 32 query heads on 8 KV heads of 128: 66 us for bf16
-// (5.4 TB/s over all), 46 us for e4m3 (3.7 TB/s: half the bytes, and the conversion
-// instructions keep their pipe 75% busy); one sequence of 262144 e4m3 keys: 104 us
-// (5.2 TB/s); one token over 1000 keys: 12 us, latency alone.
+// (5.4 TB/s over all), 46 us for e4m3 (3.8 TB/s: half the bytes for as many instructions,
+// whose own latency the warps wait for); one sequence of 262144 e4m3 keys: 98 us
+// (5.5 TB/s); one token over 1000 keys: 12 us, latency alone.
 //
 // Softmax statistics, sums and O are fp32.  bf16 caches: S is exact products in
 // fp32; P goes in as hi + lo, two bf16 (2^-17).  e4m3 caches: codes convert to
@@ -115,13 +115,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 template <int D, bool E4M3, int NQ>
 struct Cfg {
   static constexpr int ROWS = 8 * NQ;
-  static constexpr int WARPS = kCacheWarps;
+  static constexpr int WARPS = cache_warps(E4M3, ROWS);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int EL = E4M3 ? 1 : 2;
   static constexpr int RB = D * EL < 128 ? D * EL : 128;   // bytes of a row in a panel
   static constexpr int PANELS = D * EL / RB;
   static constexpr int SLOT = kChunk * D * EL;             // keys or values of a chunk
-  // 16 KB a warp, 128 KB an SM: 24 KB measured 3-7% slower, the copies queueing
+  // 16 KB a warp, 128 KB an SM with 8 warps: 24 KB measured 3-7% slower, the copies queueing
   // longer at HBM in front of what an item's start waits for
   static constexpr int RING_MAX = 16384;
   static constexpr int SLOTS = RING_MAX / SLOT < 8 ? RING_MAX / SLOT : 8;
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
         hi.x += w * y.x, hi.y += w * y.y, hi.z += w * y.z, hi.w += w * y.w;
       }
       // of the chain: whether it begins the item, ends it
-      const int kinds = (meta.kind & 2) | ((ends & valid) >> i0 & ((1u << (i1 - i0)) - 1) ? 4 : 0);
+      const int kinds = (meta.kind & 2) | ((ends & valid) >> i0 << (32 - (i1 - i0)) ? 4 : 0);
       const float2 ml = sh_sum[c][rl];
       if (kinds == 6) {
         const StepSeq q = step_seq(s, meta.n);

@@ -33,11 +33,11 @@
 // forward's own rate is 1.27), and for short items by what an item costs beside its
 // chunks: about 5 us until the first logits, 2 us for the outputs, 10 us for the join of
 // partial results (12 sequences of up to 700 new tokens over up to 4000 keys: 52 us).
-// e4m3: 602 us and 78 us for the same two; the conversion, whose instruction shares
-// its pipe with the exponentials, and 64-key chunks with four scales each make a
-// chunk 1.2 us long instead of 0.95.  Converting on the integer pipe takes three
-// instructions for one, 5 more with the check for NaN, and was slower in the four
-// warps that the registers leave room for (827 us without the check, 1414 with it).
+// e4m3: 602 us and 78 us for the same two; with the conversion, four scales a chunk
+// and 128 registers a thread it issues 1.8 times the instructions, which makes a
+// chunk 1.2 us long instead of 0.95.  Converting by shifts and masks (to bf16 for the
+// keys, so that q needs none) takes three instructions for one and a check for NaN:
+// 827 us without the check, 1414 with it, in the four warps that registers leave for it.
 #include "cache.cuh"
 #include "launch.h"
 
@@ -577,28 +577,29 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       if (range > 0) {
         constexpr int VR = D / 16;          // vectors of a row
         constexpr int NV = 16 * VR / 32;    // vectors of a thread
-        const int w = warp - 11, v = lane % VR;
-        // two 16-byte pieces of a vector: dims 16 v .. + 7 and + 8 .. + 15; the upper half of
-        // a 128-dim row stores the second first, so that eight lanes meet eight banks
-        const int ch = 2 * (v & 3), flip = v >> 2;
-        const uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + (16 * w) * D + lane * 16;
+        // two 16-byte pieces of a vector: dims 16 v .. + 7 and + 8 .. + 15.  The lanes of the upper
+        // half of 128 dims take the row beside (row ^ 1), whose swizzle differs in the lowest
+        // bit, so that the eight lanes of a row's place meet eight banks
+        const int w = warp - 11, v = lane % VR, ch = 2 * (v & 3);
+        const int row0 = 16 * w + ((lane / VR) ^ (v >> 2));   // the thread's first row
+        const uint8_t* raw = sRing + C::NSLOT * C::KV_BYTES + row0 * D + v * 16;
         for (int i = 0;; ++i) {
           const int rs = i % C::RAW, slot = i % C::NSLOT;
           if (!mbar_wait_w(&bar_rfull[rs], (i / C::RAW) & 1, ac)) break;
           if (!sh_more[rs]) break;
-          const uint32_t rows = static_cast<uint32_t>(sh_rows[rs] >> (16 * w)) & 0xffffu;
+          const uint64_t rows = sh_rows[rs];
           if (!mbar_wait_w(&bar_empty[slot], ((i / C::NSLOT) & 1) ^ 1, ac)) break;
           uint4 x[NV];
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
             x[k] = *reinterpret_cast<const uint4*>(raw + rs * C::RAW_BYTES + k * 512);
-            if (rows != 0xffffu && !(rows >> (k * (32 / VR) + lane / VR) & 1)) x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (rows != ~0ull && !(rows >> (row0 + k * (32 / VR)) & 1)) x[k] = make_uint4(0u, 0u, 0u, 0u);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_rempty[rs]);
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
-            const int row = 16 * w + k * (32 / VR) + lane / VR;
+            const int row = row0 + k * (32 / VR);
             const uint32_t xx[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             uint32_t y[8];
 #pragma unroll
@@ -606,10 +607,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
               asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
                   : "=r"(y[e])
                   : "h"(static_cast<uint16_t>(xx[e >> 1] >> (16 * (e & 1)))));
-            const uint4 y0 = make_uint4(y[0], y[1], y[2], y[3]), y1 = make_uint4(y[4], y[5], y[6], y[7]);
             uint8_t* line = sRing + slot * C::KV_BYTES + (v >> 2) * (BN * 128) + row * 128;
-            *reinterpret_cast<uint4*>(line + (((ch + flip) ^ (row & 7)) << 4)) = flip ? y1 : y0;
-            *reinterpret_cast<uint4*>(line + (((ch + 1 - flip) ^ (row & 7)) << 4)) = flip ? y0 : y1;
+            *reinterpret_cast<uint4*>(line + ((ch ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
           fence_proxy_async_smem();
           mbar_arrive(&bar_full[slot]);
