@@ -33,7 +33,7 @@
 // forward's own rate is 1.27), and for short items by what an item costs beside its
 // chunks: about 5 us until the first logits, 2 us for the outputs, 10 us for the join of
 // partial results (12 sequences of up to 700 new tokens over up to 4000 keys: 52 us).
-// e4m3: 602 us and 78 us for the same two; with the conversion, four scales a chunk
+// e4m3: 574 us and 76 us for the same two; with the conversion, four scales a chunk
 // and 128 registers a thread it issues 1.8 times the instructions, which makes a
 // chunk 1.2 us long instead of 0.95.  Converting by shifts and masks (to bf16 for the
 // keys, so that q needs none) takes three instructions for one and a check for NaN:
@@ -72,7 +72,7 @@ struct TcCfg {
 // tiles, its first and last chunk and its outputs: 12 sequences of up to 700 new
 // tokens over up to 4000 keys took 52.2, 52.5, 54.9 us with 4, 5, 7 (bf16) and 88, 85,
 // 78 us with 5, 7, 10 (e4m3, whose queries the softmax warps convert), 2 x 4096 fresh
-// tokens 257, 253, 258 us with 4, 5, 7.
+// tokens 257, 253, 258 us with 4, 5, 7 (76 and 242 us by now, with 10 and 5).
 template <bool E4M3>
 constexpr int kItemCost = E4M3 ? 10 : 5;
 
@@ -135,13 +135,38 @@ __device__ __forceinline__ void item_next(const CacheFwdArgs& a, TcItem& it) {
   }
   item_block<BN, E4M3>(a, it);
 }
-// Chunks of one KV head of a sequence in the dealing.
+// Chunks in the dealing of block rb of a sequence (its last token sees most).
+template <int BN, bool E4M3>
+__device__ __forceinline__ int block_chunks(const CacheFwdArgs& a, const StepSeq& q, int rb) {
+  const int vis = a.causal ? min(q.len, q.pos0 + min(q.m, (rb + 1) * 2 * a.tile_tokens)) : q.len;
+  return (vis > 0 ? (vis + BN - 1) / BN : 0) + kItemCost<E4M3>;
+}
+// Those of one KV head of a sequence, summed by the lanes of a warp (q the same in all).
+template <int BN, bool E4M3>
+__device__ __forceinline__ int64_t head_chunks_warp(const CacheFwdArgs& a, const StepSeq& q) {
+  const int nb = seq_blocks(a, q);
+  int64_t w = 0;
+  for (int rb = lane_id(); rb < nb; rb += 32) w += block_chunks<BN, E4M3>(a, q, rb);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w;
+}
+// The same for a sequence per lane (q.m = 0: none), sequences of many blocks by the warp.
 template <int BN, bool E4M3>
 __device__ __forceinline__ int64_t head_chunks(const CacheFwdArgs& a, const StepSeq& q) {
   const int nb = seq_blocks(a, q);
-  int64_t w = static_cast<int64_t>(nb) * kItemCost<E4M3>;
-  for (int rb = 0; rb < nb; ++rb)
-    w += max(tile_seen<BN>(a, q, 2 * rb), tile_seen<BN>(a, q, 2 * rb + 1));
+  int64_t w = 0;
+  for (int rb = 0; rb < (nb <= 16 ? nb : 0); ++rb) w += block_chunks<BN, E4M3>(a, q, rb);
+  for (uint32_t many = __ballot_sync(0xffffffffu, nb > 16); many; many &= many - 1) {
+    const int src = __ffs(many) - 1;
+    StepSeq x;
+    x.t0 = 0;
+    x.m = __shfl_sync(0xffffffffu, q.m, src);
+    x.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+    x.len = __shfl_sync(0xffffffffu, q.len, src);
+    const int64_t sum = head_chunks_warp<BN, E4M3>(a, x);
+    if (static_cast<int>(lane_id()) == src) w = sum;
+  }
   return w;
 }
 
@@ -238,15 +263,18 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
   if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
   if (warp == 9) tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
 
-  // ---- the dealing: every thread sums a slice of the sequences, the thread whose
-  // slice holds the CTA's first chunk finds its item ----
+  // ---- the dealing: every thread sums a slice of the sequences, the warp whose slices
+  // hold the CTA's first chunk finds its item ----
   {
     const int per = (s.num_seqs + C::THREADS - 1) / C::THREADS;
-    const int n0 = threadIdx.x * per, n1 = min(s.num_seqs, n0 + per);
+    const int n0 = threadIdx.x * per;
     int64_t mine = 0;
     int bad = 0;
-    for (int n = n0; n < n1; ++n)
-      mine += s.heads_kv * head_chunks<BN, E4M3>(a, step_seq(s, n, &bad));
+    for (int n = n0; n < n0 + per; ++n) {
+      StepSeq q = {0, 0, 0, 0};
+      if (n < s.num_seqs) q = step_seq(s, n, &bad);
+      mine += s.heads_kv * head_chunks<BN, E4M3>(a, q);
+    }
     if (bad && s.err && blockIdx.x == 0) atomicOr(s.err, bad);
     int64_t inc = mine;
 #pragma unroll
@@ -267,12 +295,14 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     const int64_t f0 = min(total, quota * static_cast<int64_t>(blockIdx.x));
     const int64_t f1 = min(total, f0 + quota);
     const int64_t end = before + inc;
-    if (f0 < f1 && f0 >= end - mine && f0 < end) {
+    const uint32_t who = __ballot_sync(0xffffffffu, f0 < f1 && f0 >= end - mine && f0 < end);
+    if (who) {
+      const int src = __ffs(who) - 1;
       TcItem it;
-      int64_t off = f0 - (end - mine);
-      for (it.n = n0;; ++it.n) {
+      int64_t off = __shfl_sync(0xffffffffu, f0 - (end - mine), src);
+      for (it.n = __shfl_sync(0xffffffffu, n0, src);; ++it.n) {
         it.q = step_seq(s, it.n);
-        const int64_t w = head_chunks<BN, E4M3>(a, it.q);
+        const int64_t w = head_chunks_warp<BN, E4M3>(a, it.q);
         if (off < s.heads_kv * w) {
           it.h = static_cast<int>(off / w);
           off -= it.h * w;
@@ -281,20 +311,35 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
         off -= s.heads_kv * w;
       }
       it.nb = seq_blocks(a, it.q);
-      for (it.rb = 0;; ++it.rb) {
-        item_block<BN, E4M3>(a, it);
-        if (off < it.nc) break;
-        off -= it.nc;
+      for (int rb = lane;; rb += 32) {
+        const int64_t c = rb < it.nb ? block_chunks<BN, E4M3>(a, it.q, rb) : 0;
+        int64_t sum = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += x;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, off < sum);
+        if (in) {
+          const int l = __ffs(in) - 1;
+          it.rb = __shfl_sync(0xffffffffu, rb, l);
+          off -= __shfl_sync(0xffffffffu, sum - c, l);
+          break;
+        }
+        off -= __shfl_sync(0xffffffffu, sum, 31);
       }
+      item_block<BN, E4M3>(a, it);
       int64_t left = f1 - f0;
       if (off > 0 && off >= max(it.seen[0], it.seen[1])) {   // the CTA before has all of the item
         left -= it.nc - off;
         off = 0;
         if (left > 0) item_next<BN, E4M3>(a, it);
       }
-      sh_item = it;
-      sh_c0 = static_cast<int>(off);
-      sh_left = max(left, static_cast<int64_t>(0));
+      if (lane == 0) {
+        sh_item = it;
+        sh_c0 = static_cast<int>(off);
+        sh_left = max(left, static_cast<int64_t>(0));
+      }
     }
     __syncthreads();
   }
@@ -572,7 +617,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     // Warp w of four has rows 16 w .. 16 w + 15 of every chunk of keys or values; a thread
     // takes vectors of 16 codes.  The scales are left to the softmax.  (code * scale as
     // bf16, four instructions more for two codes, and per-thread copies of the codes took
-    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 602.)
+    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 574.)
     if constexpr (E4M3) {
       if (range > 0) {
         constexpr int VR = D / 16;          // vectors of a row

@@ -91,6 +91,21 @@ def test_groups_with_many_rows(cache, D, hq, hkv):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("causal", [True, False])
+def test_sequences_of_many_row_blocks(cache, causal):
+    # blocks of 16 tokens: 44, 19, 1 and 18 of them
+    s = Step(cache, 64, 16, 1, 32, [(900, 700), (350, 300), (40, 3), (600, 280)], seed=73)
+    check(s.answer(causal), *run_fwd(s, causal))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_more_sequences_than_threads_with_prompts_among_them(cache):
+    seqs = [(400, 300) if n % 100 == 50 else (20 + n % 7, n % 3) for n in range(520)]
+    s = Step(cache, 64, 16, 1, 16, seqs, seed=74)
+    check(s.answer(), *run_fwd(s))
+
+
+@pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("case", [FEW, MANY, MIXED], ids=["few", "many", "mixed"])
 def test_pool_past_32_bit_offsets(cache, case):
     # the same step with its pages at the end of a pool of more than 2^32 bytes: the same bits
