@@ -73,13 +73,13 @@ int step_rows(const attn_cache_problem_t* p) {
 // once for 256, but pays more for an item, above all with e4m3 keys.  Measured, few
 // rows / tcgen05, in us:
 //  - 32 sequences of 4096 keys, 8 KV heads of 128, all with the same rows: bf16
-//    181 / 115 at 20 rows; e4m3 142 / 153 at 20, 138 / 155 at 32, 195 / 154 at 40;
+//    177 / 116 at 20 rows; e4m3 137 / 149 at 20, 133 / 149 at 32, 191 / 149 at 40;
 //  - 64 sequences of up to 8192 keys with 1 to 5 new tokens, 10 rows on average and 20
-//    at most: bf16 84 / 91, e4m3 71 / 155.
+//    at most: bf16 79 / 91, e4m3 68 / 152.
 // A batch of decoding sequences with a prompt's chunk among them: both kernels, each
-// for its own sequences, cost two launches more; 63 + one chunk of 128 tokens took
-// bf16 94 us either way, e4m3 84 us with both and 145 us in the tcgen05 kernel alone;
-// 15 + one, e4m3, 58 us either way.
+// for its own sequences, cost two launches more; 63 + one chunk of 128 or of 512
+// tokens took, with both / in the tcgen05 kernel alone, bf16 89 / 94 and 103 / 101 us,
+// e4m3 77 / 146 and 97 / 160 us; 15 + one, e4m3, 50 / 54 and 72 / 69 us.
 struct Kernels {
   bool few, tc;
   int split;       // rows above which a sequence is the tcgen05 kernel's
@@ -91,7 +91,7 @@ Kernels pick_kernels(const attn_cache_problem_t* p) {
   const int64_t average = static_cast<int64_t>(p->tokens) * group / p->num_seqs;
   const Kernels few = {true, false, 0x7fffffff, cache_fwd_rows(rows)};
   if (rows <= (e4m3 ? 32 : 16) || group > kCacheTcTile) return few;
-  if (e4m3 && rows <= 128 && average <= 32) return few;
+  if (rows <= (e4m3 ? 128 : 32) && average <= (e4m3 ? 32 : 10)) return few;
   if (e4m3 && p->num_seqs >= 24 && group <= 16 &&
       p->tokens < static_cast<int64_t>(p->num_seqs) * p->max_new)
     return {true, true, 16, cache_fwd_rows(group)};
