@@ -225,6 +225,27 @@ def test_step_captured_and_replayed(cache, case):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+def test_two_graphs_that_share_a_workspace_one_after_another(cache):
+    steps = [Step(cache, seed=76, **FEW), Step(cache, seed=77, **MANY)]
+    calls = [x.to(DEV) for x in steps]
+    size = max(A.attn_cache_fwd_workspace_size(*x, **kw) for x, kw in calls)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    outs = [A.attn_cache_fwd(*x, workspace=ws, **kw) for x, kw in calls]
+    graphs = []
+    for (x, kw), (o, lse) in zip(calls, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            A.attn_cache_fwd(*x, out=o, lse=lse, workspace=ws, **kw)
+    for o, lse in outs:
+        o.fill_(float("nan")), lse.fill_(float("nan"))
+    for i in (0, 1, 1, 0, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for s, (o, lse) in zip(steps, outs):
+        check(s.answer(), o, lse)
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_many_rows_two_calls_at_once(cache):
     a, b = Step(cache, seed=69, **MANY), Step(cache, seed=70, **MIXED)
     (xa, ka), (xb, kb) = a.to(DEV), b.to(DEV)
