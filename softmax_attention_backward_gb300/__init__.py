@@ -695,7 +695,11 @@ def _need_rows(t, name, heads, dim, device):
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if t.shape[0] > 1 else 0
+    if t.shape[0] <= 1:
+        return 0
+    if st[0] < heads * dim:   # (0 would mean dense to the library)
+        raise ValueError(f"{name}: the tokens must not overlap (a broadcast tensor: call contiguous())")
+    return st[0]
 
 
 # A step of one token takes the GPU a few microseconds, so the checks below look
