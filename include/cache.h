@@ -40,7 +40,8 @@ typedef enum {
  * has position seqlens_kv[n] - m + i.  cu_seqlens [num_seqs + 1], seqlens_kv
  * [num_seqs] and page_table are device memory and never read by the host, so a
  * captured graph may change them between replays.  max_new bounds the new
- * tokens of every sequence.
+ * tokens of every sequence.  With tokens = 0 both calls do nothing, and the
+ * pointers of rows (q, k, v, q_out, o, lse) and the workspace may be NULL.
  *
  * q_stride, k_stride and v_stride are the elements between two tokens' rows
  * (0: dense, heads * head_dim; else at least that and a multiple of 8), so that

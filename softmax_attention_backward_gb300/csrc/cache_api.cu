@@ -136,9 +136,8 @@ attn_status_t attn_cache_append(const attn_cache_problem_t* p, const void* q, co
   const attn_status_t st = check_step(p);
   if (st != ATTN_OK) return st;
   const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
-  if (!k || !v || !k_cache || !v_cache || (q == nullptr) != (q_out == nullptr) ||
-      (e4m3 && (!k_scale || !v_scale)))
-    return ATTN_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || (e4m3 && (!k_scale || !v_scale))) return ATTN_ERR_INVALID_ARG;
+  if (p->tokens > 0 && (!k || !v || (q == nullptr) != (q_out == nullptr))) return ATTN_ERR_INVALID_ARG;
   if (p->rot_dim < 0 || p->rot_dim > p->head_dim || p->rot_dim % 16 ||
       (p->rot_dim > 0 && (!cos_sin || p->max_position <= 0)))
     return ATTN_ERR_INVALID_ARG;
@@ -218,8 +217,8 @@ attn_status_t attn_cache_fwd(const attn_cache_problem_t* p, const void* q, const
   const attn_status_t st = check_step(p);
   if (st != ATTN_OK) return st;
   const bool e4m3 = p->cache_type == ATTN_CACHE_E4M3;
-  if (!q || !k_cache || !v_cache || !o || !lse || (e4m3 && (!k_scale || !v_scale)))
-    return ATTN_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || (e4m3 && (!k_scale || !v_scale))) return ATTN_ERR_INVALID_ARG;
+  if (p->tokens > 0 && (!q || !o || !lse)) return ATTN_ERR_INVALID_ARG;
   CacheFwdArgs both[2];   // of the kernel for few rows, of the tcgen05 kernel
   CacheFwdArgs& base = both[0];
   if (!good_stride(p->q_stride, p->heads_q, p->head_dim, &base.q_stride)) return ATTN_ERR_INVALID_ARG;
