@@ -129,6 +129,17 @@ struct CacheFwdArgs {
   CUtensorMap tm_q;         // cache_fwd_tc: q in boxes of tile_tokens x group heads x 64 dims
 };
 
+// e4m3 caches, few rows: P enters its product with the codes as fp16, as
+//   p_j scale_j 2^(kPHead - R),   R (log2) at most kPSlack below the largest p_j scale_j
+// of the keys that the row has seen (p over the running maximum, scale of the values'
+// page).  R goes by the product, so that neither a page of a large scale that weighs
+// nothing nor a key of no value but a large weight takes the others' bits; it rises by
+// more than kPSlack at a time, which spares O most rescalings.  Below 2^15 always,
+// it is off by 2^-11 of itself and, where fp16 ends, by 2^-36 of the largest product.
+constexpr float kPHead = 11.f, kPSlack = 4.f;
+// 2^kPHead, and back.
+constexpr float kPUp = 2048.f, kPDown = 1.f / 2048.f;
+
 // Rows of an item of the tcgen05 kernel, and of each of its two tiles.
 constexpr int kCacheTcRows = 256, kCacheTcTile = 128;
 // The number of keys of its chunks.

@@ -40,8 +40,8 @@
 // fp32; P goes in as hi + lo, two bf16 (2^-17).  e4m3 caches: codes convert to
 // fp16 exactly; q, scaled by a power of two per row, is exact in fp16 too, and
 // P is rounded to fp16 (2^-11).  The page scales multiply the logits of a page
-// and its P; O is kept relative to the largest value scale seen so far, so that
-// P times scale stays within fp16.
+// and its P, relative to the largest product of P and scale that the row has seen
+// (kPHead in cache.cuh); O is kept in that unit.
 #include "cache.cuh"
 
 namespace attn {
@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
       }
 
       float acc[NQ][MT][4];
-      float mrun[NQ][2], lrun[NQ][2], vref = 0.f, vinv = 0.f;
+      float mrun[NQ][2], lrun[NQ][2];
+      float rref[NQ][2];   // e4m3: R of kPHead; O is in units of 2^(R - kPHead)
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
@@ -512,6 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
         for (int e = 0; e < 2; ++e) {
           mrun[nq][e] = -INFINITY;
           lrun[nq][e] = 0.f;
+          rref[nq][e] = -INFINITY;
         }
       }
 
@@ -573,22 +575,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
         __syncwarp();
         issue();
 
-        // values' factors relative to the largest value scale so far
-        float vratio = 1.f, vf0 = 1.f, vf1 = 1.f;
-        if constexpr (E4M3) {
-          const float top = fmaxf(sc.y, sc.w);
-          if (top > vref) {
-            vratio = vref / top;
-            vref = top;
-            vinv = 1.f / top;
-          }
-          vf0 = sc.y * vinv;
-          vf1 = sc.w * vinv;
-        }
+        // the values' scales (0 without a page) and their log2
+        const float vs0 = sc.y * kPUp, vs1 = sc.w * kPUp;
+        const float lv0 = __log2f(sc.y), lv1 = __log2f(sc.w);
+        const bool apart = E4M3 && sc.y != sc.w;
         constexpr int LO = E4M3 ? 1 : 2;   // P itself, or its hi and lo parts
         uint32_t pb[2][NQ][LO][2];         // B fragments of P^T: 16 keys each
-        bool grow = vratio != 1.f;
-        float alpha[NQ][2];
+        bool grow = false;
+        float alpha[NQ][2];   // O's factor
         const bool dirty = bad != 0 || key0 + kChunk > q.len;
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
@@ -607,25 +601,53 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
               for (int k = 0; k < 4; ++k)
                 if (k * 8 + krow >= lim || (bad >> (k >> 1) & 1)) y[k >> 1][k & 1] = -INFINITY;
             }
-            float mx = fmaxf(fmax3(y[0][0], y[0][1], y[1][0]), y[1][1]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            auto over_quads = [](float v) {
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            };
+            float mx, top;   // the largest logit; log2 of the largest product with a scale
+            if (apart) {
+              const float m0 = over_quads(fmaxf(y[0][0], y[0][1])), m1 = over_quads(fmaxf(y[1][0], y[1][1]));
+              mx = fmaxf(m0, m1);
+              top = fmaxf(m0 + lv0, m1 + lv1);
+            } else {
+              mx = over_quads(fmaxf(fmax3(y[0][0], y[0][1], y[1][0]), y[1][1]));
+              top = mx + lv0;
+            }
             const float mn = fmaxf(mrun[nq][e], mx);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            alpha[nq][e] = ex2(mrun[nq][e] - ms);   // 0 while nothing has been seen
-            grow |= mn > mrun[nq][e];
+            const float decay = ex2(mrun[nq][e] - ms);   // 0 while nothing has been seen
+            float vf0, vf1;   // factors of P
+            if constexpr (E4M3) {
+              float& ref = rref[nq][e];
+              const bool up = top > ref + kPSlack;
+              alpha[nq][e] = up ? ex2(ref - top) : 1.f;
+              ref = up ? top : ref;
+              grow |= up;
+              // P of a factor past fp32 (a key of no weight under a scale that far above the
+              // others', or no key at all) is 0
+              const float f = ex2(ms - ref);
+              vf0 = fminf(vs0 * f, 3.4e38f);
+              vf1 = fminf(vs1 * f, 3.4e38f);
+            } else {
+              alpha[nq][e] = decay;
+              grow |= mn > mrun[nq][e];
+            }
             mrun[nq][e] = mn;
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[k >> 1][k & 1] = ex2(y[k >> 1][k & 1] - ms);
-            lrun[nq][e] = lrun[nq][e] * alpha[nq][e] + ((y[0][0] + y[0][1]) + (y[1][0] + y[1][1]));
+            lrun[nq][e] = lrun[nq][e] * decay + ((y[0][0] + y[0][1]) + (y[1][0] + y[1][1]));
+            if constexpr (E4M3) {
+              y[0][0] *= vf0, y[0][1] *= vf0;
+              y[1][0] *= vf1, y[1][1] *= vf1;
+            }
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float p0 = p[0][k >> 1][k & 1], p1 = p[1][k >> 1][k & 1];
             if constexpr (E4M3) {
-              const float vf = k < 2 ? vf0 : vf1;
-              pb[k >> 1][nq][0][k & 1] = transpose8x8(pack_f16(p0 * vf, p1 * vf));
+              pb[k >> 1][nq][0][k & 1] = transpose8x8(pack_f16(p0, p1));
             } else {
               const uint32_t hi = pack_bf16(p0, p1);
               const uint32_t lo = pack_bf16(p0 - __uint_as_float(hi << 16),
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq) {
-            const float a0 = alpha[nq][0] * vratio, a1 = alpha[nq][1] * vratio;
+            const float a0 = alpha[nq][0], a1 = alpha[nq][1];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
               acc[nq][i][0] *= a0;
@@ -733,6 +755,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
           const int rl = nq * 8 + 2 * t + e, r = rb * ROWS + rl, tok = r / s.group;
           const int hd = h * s.group + (r - tok * s.group);
           const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          // e4m3: from O's unit to that of the row's maximum
+          const float unit = E4M3 ? ex2(rref[nq][e] - (mrun[nq][e] == -INFINITY ? 0.f : mrun[nq][e])) : 1.f;
           // dims VN (8 j + g) + 2 i (c0, c1 of MMA i of panel j) and + 2 i + 1 (c2, c3)
 #pragma unroll
           for (int j = 0; j < C::PANELS; ++j)
@@ -741,7 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
               float o[8];
 #pragma unroll
               for (int z = 0; z < 8; ++z)
-                o[z] = acc[nq][j * (VN / 2) + (i + z) / 2][(z & 1) * 2 + e] * (E4M3 ? vref : 1.f);
+                o[z] = acc[nq][j * (VN / 2) + (i + z) / 2][(z & 1) * 2 + e] * (E4M3 ? kPDown : 1.f) * unit;
               const int d = (8 * j + g) * VN + i;
               const float4 lo = make_float4(o[0], o[1], o[2], o[3]);
               const float4 hi = make_float4(o[4], o[5], o[6], o[7]);
