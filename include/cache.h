@@ -136,8 +136,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p);
  * by the kernel for many query rows per KV head and to a sum of two bf16 (2^-16) by
  * that for few; e4m3 caches, times the scale of its value's page, to fp16 (within
  * 2^-11 of it, or within 2^-36 of the largest P times scale of the keys that the row
- * sees; by the kernel for many rows, within 2^-25 of the largest scale of the keys
- * that it read).  Which kernel serves a call follows from the problem alone.
+ * sees).  Which kernel serves a call follows from the problem alone.
  * Any number of new tokens per sequence, one included; sequences of different
  * kinds may share a call.  The result is bitwise reproducible on one device.
  */

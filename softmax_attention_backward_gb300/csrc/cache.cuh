@@ -129,7 +129,7 @@ struct CacheFwdArgs {
   CUtensorMap tm_q;         // cache_fwd_tc: q in boxes of tile_tokens x group heads x 64 dims
 };
 
-// e4m3 caches, few rows: P enters its product with the codes as fp16, as
+// e4m3 caches: P enters its product with the codes as fp16, as
 //   p_j scale_j 2^(kPHead - R),   R (log2) at most kPSlack below the largest p_j scale_j
 // of the keys that the row has seen (p over the running maximum, scale of the values'
 // page).  R goes by the product, so that neither a page of a large scale that weighs

@@ -26,7 +26,7 @@
 // the slots that the MMAs read; the softmax warps bring and scale their rows of q.
 // The scales of 16-key groups enter with the softmax: the key scale as a factor of
 // the logits, log2 of the value scale as a summand in the exponent of P, which the
-// row sum takes off again.
+// row sum takes off again (kPHead in cache.cuh says in what unit P and O are held).
 //
 // Bound by the softmax (bf16: 1.34 PFLOP/s, 460 us, for 2 x 2048 new tokens over
 // 8192 cached ones, 32 query heads of 128, 70% of the measured GEMM rate; the dense
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       if (lane == 0) mbar_arrive(&bar_qempty[qb]);   // (the warp has read what it needs of f)
       float m_run = -INFINITY, l_run = 0.f;
       float rowf = sl2;            // logit factor of the row
-      float lv_ref = -INFINITY;    // e4m3: O is kept in units of 2^lv_ref
+      float ref = -INFINITY;       // e4m3: R of kPHead; O is in units of 2^(R - kPHead)
       if constexpr (E4M3) {
         // The rows as fp16 times a power of two each, its largest element below 512: exact down
         // to 2^-32 of it and then within 2^-33 of it.  D / 8 lanes take a row.  (The tile is
@@ -808,35 +808,40 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           l_run = l_run * alpha + (((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7)));
           m_run = m_use;
         } else {
-          // four groups of 16 keys with scales of their own: the logits' factor, and log2 of
-          // the values' factor relative to the largest so far, which P, below 2^9, takes along
-          // and the row sum takes off again (from 2^-40 down nothing of it is left in fp16).
+          // four groups of 16 keys with scales of their own: the logits' factor, and the summand
+          // of P's exponent (log2 of the values' scale, relative to R, and kPHead), which the row
+          // sum takes off again.  From -40 down nothing of it is left in fp16, P being below 2^9.
           // The logits' factor stays above zero, which would make the masks NaN.
           const float2* sc = sh_scale[(gchunk + j) & 31];
-          float fg[4], lg[4], mt = -INFINITY, lv_new = lv_ref;
+          float fg[4], lg[4], mt = -INFINITY, top = -INFINITY;   // top: log2 of the largest product
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const float2 kv = sc[g];
             fg[g] = fmaxf(rowf * kv.x, 1e-37f);
             lg[g] = kv.y;
-            lv_new = fmaxf(lv_new, kv.y);
             const float* xg = x + 16 * g;
             float m0 = fmax3(xg[0], xg[1], xg[2]), m1 = fmax3(xg[3], xg[4], xg[5]);
             m0 = fmax3(m0, xg[6], xg[7]);
             m1 = fmax3(m1, xg[8], xg[9]);
             m0 = fmax3(m0, xg[10], xg[11]);
             m1 = fmax3(m1, xg[12], xg[13]);
-            mt = fmaxf(mt, fmax3(fmax3(m0, xg[14], xg[15]), m1, m1) * fg[g]);
+            const float mg = fmax3(fmax3(m0, xg[14], xg[15]), m1, m1) * fg[g];
+            mt = fmaxf(mt, mg);
+            top = fmaxf(top, mg + lg[g]);
           }
           const float m_new = fmaxf(m_run, mt);
           const bool mgrow = m_new > m_run + 8.0f;
           const float m_use = mgrow ? m_new : m_run;
-          alpha = mgrow ? ex2(m_run - m_use) : 1.0f;
+          const float decay = mgrow ? ex2(m_run - m_use) : 1.0f;
           const float msub = (m_use == -INFINITY) ? 0.f : m_use;
+          grow = top > ref + kPSlack;
+          alpha = grow ? ex2(ref - top) : 1.0f;
+          ref = grow ? top : ref;
+          const float base = kPHead + (ref == -INFINITY ? 0.f : msub - ref);
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float l = fmaxf(lg[g] - lv_new, -40.f);
+            const float l = fmaxf(base + lg[g], -40.f);
             const uint64_t nm2 = f2_pack(l - msub, l - msub), f2 = f2_pack(fg[g], fg[g]);
             uint64_t rs2[2] = {0ull, 0ull};
 #pragma unroll
@@ -852,11 +857,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             f2_unpack(f2_add(rs2[0], rs2[1]), r0, r1);
             sum += (r0 + r1) * ex2(-l);
           }
-          l_run = l_run * alpha + sum;
+          l_run = l_run * decay + sum;
           m_run = m_use;
-          grow = mgrow || lv_new > lv_ref;
-          if (lv_new > lv_ref) alpha *= ex2(lv_ref - lv_new);   // from here on O's factor
-          lv_ref = lv_new;
         }
         const bool warp_rescale = j > 0 && __any_sync(0xffffffffu, grow);
         if (j > 0) {
@@ -888,8 +890,13 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       }
       if (ok) {
         const bool valid = row_out >= 0, whole = kind == 7;
-        const float unit = E4M3 && nt > 0 ? ex2(lv_ref) : 1.f;
-        const float inv = (l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f) * unit;
+        // O's unit, of which 2^-kPHead is left to the second factor
+        const float unit = E4M3 ? ex2(ref - (m_run == -INFINITY ? 0.f : m_run)) : 1.f;
+        const float down = E4M3 ? kPDown : 1.f;
+        const float inv = l_run > 0.f || l_run != l_run ? down / l_run : 0.f;
+        auto scaled = [&](uint32_t u, float f) {
+          return E4M3 ? __uint_as_float(u) * unit * f : __uint_as_float(u) * f;
+        };
         __nv_bfloat16* orow = a.o + (static_cast<int64_t>(row_out) * s.heads_q + hd) * D;
         const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1);
         float4* part = reinterpret_cast<float4*>(a.part_o) + at * (D / 4) * 2 * C::BM + t * C::BM + tr;
@@ -908,18 +915,17 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
                 uint4 v;
-                v.x = pack_bf16(__uint_as_float(r[i + 0]) * inv, __uint_as_float(r[i + 1]) * inv);
-                v.y = pack_bf16(__uint_as_float(r[i + 2]) * inv, __uint_as_float(r[i + 3]) * inv);
-                v.z = pack_bf16(__uint_as_float(r[i + 4]) * inv, __uint_as_float(r[i + 5]) * inv);
-                v.w = pack_bf16(__uint_as_float(r[i + 6]) * inv, __uint_as_float(r[i + 7]) * inv);
+                v.x = pack_bf16(scaled(r[i + 0], inv), scaled(r[i + 1], inv));
+                v.y = pack_bf16(scaled(r[i + 2], inv), scaled(r[i + 3], inv));
+                v.z = pack_bf16(scaled(r[i + 4], inv), scaled(r[i + 5], inv));
+                v.w = pack_bf16(scaled(r[i + 6], inv), scaled(r[i + 7], inv));
                 *reinterpret_cast<uint4*>(orow + cc + i) = v;
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 part[(cc + i) / 4 * 2 * C::BM] =
-                    make_float4(__uint_as_float(r[i]) * unit, __uint_as_float(r[i + 1]) * unit,
-                                __uint_as_float(r[i + 2]) * unit, __uint_as_float(r[i + 3]) * unit);
+                    make_float4(scaled(r[i], down), scaled(r[i + 1], down), scaled(r[i + 2], down), scaled(r[i + 3], down));
             }
           }
         }

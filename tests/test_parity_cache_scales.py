@@ -1,6 +1,6 @@
 """GPU tests of the e4m3 cache's attention where the values' page scales lie far apart and
 where probabilities are small: a row's precision goes by what the row sees and weighs.
-`m` new tokens: few rows per KV head."""
+`m` new tokens: few rows per KV head, or as many as the tcgen05 kernel takes."""
 import pytest
 import torch
 
@@ -10,7 +10,7 @@ from test_parity_cache import run_fwd
 
 pytestmark = pytest.mark.gpu
 
-ROWS = [(64, 1), (128, 1), (64, 5)]
+ROWS = [(64, 1), (128, 1), (64, 5), (64, 40), (128, 40)]
 INF = float("inf")
 
 
@@ -79,7 +79,7 @@ def test_large_scale_page_of_no_weight(D, m, ratio, at):
 
 
 @pytest.mark.parametrize("ps", [16, 32, 128])
-@pytest.mark.parametrize("D,m", [(64, 3), (128, 3)])
+@pytest.mark.parametrize("D,m", [(64, 3), (128, 3), (64, 40), (128, 40)])
 @pytest.mark.parametrize("ratio", [16, 24, 80])
 def test_large_scale_page_behind_the_diagonal(ps, D, m, ratio):
     # the newest page's values are 2^ratio times the others'; rows whose positions lie before it do not see it
@@ -126,7 +126,7 @@ def test_rising_weights(D, m):
         check(answer(s, 11, scale=scale), *run_fwd(s, scale=scale))
 
 
-@pytest.mark.parametrize("m", [1])
+@pytest.mark.parametrize("m", [1, 40])
 @pytest.mark.parametrize("ps", [16, 64])
 def test_missing_pages_beside_far_scales(m, ps):
     # a bad page (flagged, left out) between pages of far scales, rows without keys, a last page half full
