@@ -135,7 +135,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p);
  * P is rounded before the product with V: bf16 caches, to bf16 (within 2^-8 of it)
  * by the kernel for many query rows per KV head and to a sum of two bf16 (2^-16) by
  * that for few; e4m3 caches, times the scale of its value's page, to fp16 (within
- * 2^-11 of it, or within 2^-36 of the largest P times scale of the keys that the row
+ * 2^-11 of it, or within 2^-33 of the largest P times scale of the keys that the row
  * sees).  Which kernel serves a call follows from the problem alone.
  * Any number of new tokens per sequence, one included; sequences of different
  * kinds may share a call.  The result is bitwise reproducible on one device.

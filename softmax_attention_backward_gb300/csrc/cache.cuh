@@ -134,11 +134,14 @@ struct CacheFwdArgs {
 // of the keys that the row has seen (p over the running maximum, scale of the values'
 // page).  R goes by the product, so that neither a page of a large scale that weighs
 // nothing nor a key of no value but a large weight takes the others' bits; it rises by
-// more than kPSlack at a time, which spares O most rescalings.  Below 2^15 always,
-// it is off by 2^-11 of itself and, where fp16 ends, by 2^-36 of the largest product.
-constexpr float kPHead = 11.f, kPSlack = 4.f;
-// 2^kPHead, and back.
-constexpr float kPUp = 2048.f, kPDown = 1.f / 2048.f;
+// more than kPSlack at a time, which spares O most rescalings.  P is off by 2^-11 of
+// itself and, where fp16 ends, by 2^-25 2^-kPHead = 2^-33 of the largest product.  It
+// stays below 2^11: the five powers of two to fp16's end are for logits so large that
+// their rounding is whole powers (R is held relative to the maximum for the same reason).
+// Head and slack of 8 and 3, 7 and 4, 11 and 4: 585, 583, 583 us for the chunk of 2 x 2048
+// tokens over 8192.
+constexpr float kPHead = 8.f, kPSlack = 3.f;
+constexpr float kPUp = 256.f, kPDown = 1.f / 256.f;   // 2^kPHead and back
 
 // Rows of an item of the tcgen05 kernel, and of each of its two tiles.
 constexpr int kCacheTcRows = 256, kCacheTcTile = 128;

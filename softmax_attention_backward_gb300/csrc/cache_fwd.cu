@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
 
       float acc[NQ][MT][4];
       float mrun[NQ][2], lrun[NQ][2];
-      float rref[NQ][2];   // e4m3: R of kPHead; O is in units of 2^(R - kPHead)
+      float off[NQ][2];   // e4m3: R of kPHead, less mrun; O is in units of 2^(R - kPHead)
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
         for (int e = 0; e < 2; ++e) {
           mrun[nq][e] = -INFINITY;
           lrun[nq][e] = 0.f;
-          rref[nq][e] = -INFINITY;
+          off[nq][e] = -INFINITY;
         }
       }
 
@@ -606,28 +606,32 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             };
-            float mx, top;   // the largest logit; log2 of the largest product with a scale
+            float mx, m0, m1;   // the largest logit; e4m3: those of the two halves
             if (apart) {
-              const float m0 = over_quads(fmaxf(y[0][0], y[0][1])), m1 = over_quads(fmaxf(y[1][0], y[1][1]));
+              m0 = over_quads(fmaxf(y[0][0], y[0][1])), m1 = over_quads(fmaxf(y[1][0], y[1][1]));
               mx = fmaxf(m0, m1);
-              top = fmaxf(m0 + lv0, m1 + lv1);
             } else {
               mx = over_quads(fmaxf(fmax3(y[0][0], y[0][1], y[1][0]), y[1][1]));
-              top = mx + lv0;
+              m0 = m1 = mx;
             }
             const float mn = fmaxf(mrun[nq][e], mx);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            const float decay = ex2(mrun[nq][e] - ms);   // 0 while nothing has been seen
+            const float rise = mrun[nq][e] - ms;
+            const float decay = ex2(rise);   // 0 while nothing has been seen
             float vf0, vf1;   // factors of P
             if constexpr (E4M3) {
-              float& ref = rref[nq][e];
+              // log2 of the largest product, over the maximum (far below which their sum would drown)
+              float top = m0 - ms + lv0;
+              if (apart) top = fmaxf(top, m1 - ms + lv1);
+              float& ref = off[nq][e];
+              ref += rise;
               const bool up = top > ref + kPSlack;
               alpha[nq][e] = up ? ex2(ref - top) : 1.f;
               ref = up ? top : ref;
               grow |= up;
               // P of a factor past fp32 (a key of no weight under a scale that far above the
               // others', or no key at all) is 0
-              const float f = ex2(ms - ref);
+              const float f = ex2(-ref);
               vf0 = fminf(vs0 * f, 3.4e38f);
               vf1 = fminf(vs1 * f, 3.4e38f);
             } else {
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
           const int hd = h * s.group + (r - tok * s.group);
           const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
           // e4m3: from O's unit to that of the row's maximum
-          const float unit = E4M3 ? ex2(rref[nq][e] - (mrun[nq][e] == -INFINITY ? 0.f : mrun[nq][e])) : 1.f;
+          const float unit = E4M3 ? ex2(off[nq][e]) : 1.f;
           // dims VN (8 j + g) + 2 i (c0, c1 of MMA i of panel j) and + 2 i + 1 (c2, c3)
 #pragma unroll
           for (int j = 0; j < C::PANELS; ++j)

@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       if (lane == 0) mbar_arrive(&bar_qempty[qb]);   // (the warp has read what it needs of f)
       float m_run = -INFINITY, l_run = 0.f;
       float rowf = sl2;            // logit factor of the row
-      float ref = -INFINITY;       // e4m3: R of kPHead; O is in units of 2^(R - kPHead)
+      float off = -3.4e38f;        // e4m3: R of kPHead, less m_run; O is in units of 2^(R - kPHead)
       if constexpr (E4M3) {
         // The rows as fp16 times a power of two each, its largest element below 512: exact down
         // to 2^-32 of it and then within 2^-33 of it.  D / 8 lanes take a row.  (The tile is
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           // sum takes off again.  From -40 down nothing of it is left in fp16, P being below 2^9.
           // The logits' factor stays above zero, which would make the masks NaN.
           const float2* sc = sh_scale[(gchunk + j) & 31];
-          float fg[4], lg[4], mt = -INFINITY, top = -INFINITY;   // top: log2 of the largest product
+          float fg[4], lg[4], mg[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const float2 kv = sc[g];
@@ -825,19 +825,22 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             m1 = fmax3(m1, xg[8], xg[9]);
             m0 = fmax3(m0, xg[10], xg[11]);
             m1 = fmax3(m1, xg[12], xg[13]);
-            const float mg = fmax3(fmax3(m0, xg[14], xg[15]), m1, m1) * fg[g];
-            mt = fmaxf(mt, mg);
-            top = fmaxf(top, mg + lg[g]);
+            mg[g] = fmax3(m0, m1, fmaxf(xg[14], xg[15])) * fg[g];
           }
+          const float mt = fmaxf(fmaxf(mg[0], mg[1]), fmaxf(mg[2], mg[3]));
           const float m_new = fmaxf(m_run, mt);
           const bool mgrow = m_new > m_run + 8.0f;
           const float m_use = mgrow ? m_new : m_run;
           const float decay = mgrow ? ex2(m_run - m_use) : 1.0f;
           const float msub = (m_use == -INFINITY) ? 0.f : m_use;
-          grow = top > ref + kPSlack;
-          alpha = grow ? ex2(ref - top) : 1.0f;
-          ref = grow ? top : ref;
-          const float base = kPHead + (ref == -INFINITY ? 0.f : msub - ref);
+          off = mgrow ? off - (m_use - m_run) : off;
+          // log2 of the largest product, over the maximum (far below which their sum would drown)
+          const float top = fmaxf(fmaxf(mg[0] - msub + lg[0], mg[1] - msub + lg[1]),
+                                  fmaxf(mg[2] - msub + lg[2], mg[3] - msub + lg[3]));
+          grow = __any_sync(0xffffffffu, top > off + kPSlack) && top > off;
+          alpha = grow ? off - top : 0.0f;   // (log2)
+          off = grow ? top : off;
+          const float base = kPHead - off;
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -867,13 +870,14 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
           tc_fence_after();
         }
         if (warp_rescale) {
+          const float a_o = E4M3 ? ex2(alpha) : alpha;
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             uint32_t r[32];
             tmem_ld32_nowait(tO + cc, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * a_o);
             tmem_st32(tO + cc, r);
           }
         }
@@ -890,13 +894,10 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       }
       if (ok) {
         const bool valid = row_out >= 0, whole = kind == 7;
-        // O's unit, of which 2^-kPHead is left to the second factor
-        const float unit = E4M3 ? ex2(ref - (m_run == -INFINITY ? 0.f : m_run)) : 1.f;
-        const float down = E4M3 ? kPDown : 1.f;
-        const float inv = l_run > 0.f || l_run != l_run ? down / l_run : 0.f;
-        auto scaled = [&](uint32_t u, float f) {
-          return E4M3 ? __uint_as_float(u) * unit * f : __uint_as_float(u) * f;
-        };
+        // e4m3: O's unit over the row's maximum, in two halves: it may be subnormal
+        const float half = E4M3 ? ex2(0.5f * (off - kPHead)) : 1.f;
+        const float unit = half * half;
+        const float inv = (l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f) * unit;
         __nv_bfloat16* orow = a.o + (static_cast<int64_t>(row_out) * s.heads_q + hd) * D;
         const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + (kind >> 1 & 1);
         float4* part = reinterpret_cast<float4*>(a.part_o) + at * (D / 4) * 2 * C::BM + t * C::BM + tr;
@@ -915,17 +916,18 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
                 uint4 v;
-                v.x = pack_bf16(scaled(r[i + 0], inv), scaled(r[i + 1], inv));
-                v.y = pack_bf16(scaled(r[i + 2], inv), scaled(r[i + 3], inv));
-                v.z = pack_bf16(scaled(r[i + 4], inv), scaled(r[i + 5], inv));
-                v.w = pack_bf16(scaled(r[i + 6], inv), scaled(r[i + 7], inv));
+                v.x = pack_bf16(__uint_as_float(r[i + 0]) * inv, __uint_as_float(r[i + 1]) * inv);
+                v.y = pack_bf16(__uint_as_float(r[i + 2]) * inv, __uint_as_float(r[i + 3]) * inv);
+                v.z = pack_bf16(__uint_as_float(r[i + 4]) * inv, __uint_as_float(r[i + 5]) * inv);
+                v.w = pack_bf16(__uint_as_float(r[i + 6]) * inv, __uint_as_float(r[i + 7]) * inv);
                 *reinterpret_cast<uint4*>(orow + cc + i) = v;
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 part[(cc + i) / 4 * 2 * C::BM] =
-                    make_float4(scaled(r[i], down), scaled(r[i + 1], down), scaled(r[i + 2], down), scaled(r[i + 3], down));
+                    make_float4(__uint_as_float(r[i]) * unit, __uint_as_float(r[i + 1]) * unit,
+                                __uint_as_float(r[i + 2]) * unit, __uint_as_float(r[i + 3]) * unit);
             }
           }
         }

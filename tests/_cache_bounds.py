@@ -33,9 +33,9 @@ def answer(s, p_bits, causal=True, scale=None):
 
     A logit's error es is as in _cache_util.bounds; a probability's relative to itself is
     twice that.  P is then rounded to 2^-p_bits of itself.  An e4m3 cache's P (p_bits 11)
-    is multiplied by its page's scale and by a power 2^(11 - R) first, R (log2) at most the
+    is multiplied by its page's scale and by a power 2^(8 - R) first, R (log2) at most the
     largest p_j scale_j (over the largest p) of the keys that the row sees, and is off by
-    half of fp16's least subnormal, 2^-25, at the small end: 2^-36 of that largest product
+    half of fp16's least subnormal, 2^-25, at the small end: 2^-33 of that largest product
     for each unit of code that the row sees.  The powers are fp32 exponentials (2^-22
     each, a few dozen of them where R rises) of differences of at most 2^7 (2^-17 each):
     2^-14 together.  Then one rounding to bf16, 2^-8."""
@@ -67,7 +67,7 @@ def answer(s, p_bits, causal=True, scale=None):
             if e4m3:
                 sc = vs[:, h // g]
                 codes = seen.double() @ (vh.abs() / sc[:, None])
-                err += 2.0 ** -36 * (p * sc).amax(-1, keepdim=True) * codes
+                err += 2.0 ** -33 * (p * sc).amax(-1, keepdim=True) * codes
             o[t0:t0 + m, h] = want
             o_tol[t0:t0 + m, h] += err * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
             lse[h, t0:t0 + m] = x.logsumexp(-1)

@@ -143,3 +143,32 @@ def test_missing_pages_beside_far_scales(m, ps):
     t.q, t.table, t.cols = s.q[:m].clone(), s.table[:1, [c for c in range(s.table.shape[1]) if c != 4]], s.cols - 1
     t.pools, t.scales, t.true = s.pools, s.scales, s.true
     check(answer(t, 11, causal=False), o[:m], lse[:, :m])
+
+
+@pytest.mark.parametrize("D,m", ROWS)
+@pytest.mark.parametrize("bits", [16, 22, 24, 25, 30, 40])
+@pytest.mark.parametrize("e", [-40, -7, 9, 30])
+def test_logits_whose_rounding_is_whole_powers(D, m, bits, e):
+    # logits up to 2^bits (log2 units), each a single product, so far apart that one key has all the weight: o is its
+    # value, whatever scale its page has; the other pages' scales lie on both sides of it.  The tcgen05 kernel takes
+    # the maximum off the unrounded product: from 2^26 on that alone is several powers of two
+    if m == 40 and bits > 25:
+        bits = 25
+    L, top = 130, 2.0 ** bits
+    s, _ = one_sink(L, D, m, 1.0, 0.0, seqs=[(L, m)])
+    x = torch.zeros(L, s.hkv, D)
+    x[..., 0] = (torch.arange(L) % 13).float()[:, None]
+    for win in (5, 70, L - m):
+        y = x.clone()
+        y[win, :, 0] = 14.0
+        s.set_rows(0, 0, range(L), y)
+        for c in range(-(-L // 16)):
+            s.set_scales(1, {(0, c): e - 12 if c % 2 else e + 12})
+        s.set_scales(1, {(0, win // 16): e})
+        scale = top / 1.4426950408889634 / 14.0
+        o, lse = run_fwd(s, scale=scale)
+        v = s.keys(0)[1][win].repeat_interleave(s.hq // s.hkv, 0)
+        # P of the key is 1 within 2^-11 and a few exponentials' 2^-22, the row sum too, then bf16
+        assert ((o[:m].double().cpu() - v).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) * v.abs()).all()
+        want = scale * 14.0
+        assert ((lse[:, :m].double().cpu() - want).abs() <= 2.0 ** -21 * want).all()
