@@ -71,15 +71,26 @@ int step_rows(const attn_cache_problem_t* p) {
 // Which kernels serve a step.  The one for few rows goes over the keys once for
 // every 16 rows of a KV head (8 where no sequence has more), the tcgen05 kernel
 // once for 256, but pays more for an item, above all with e4m3 keys.  Measured, few
-// rows / tcgen05, in us:
-//  - 32 sequences of 4096 keys, 8 KV heads of 128, all with the same rows: bf16
-//    177 / 116 at 20 rows; e4m3 137 / 149 at 20, 133 / 149 at 32, 191 / 149 at 40;
-//  - 64 sequences of up to 8192 keys with 1 to 5 new tokens, 10 rows on average and 20
-//    at most: bf16 79 / 91, e4m3 68 / 152.
+// rows / tcgen05, in us, with 8 KV heads of 128 where nothing else is said:
+//  - 32 sequences of 4096 keys, all with the same rows: bf16 101 / 115 at 16 rows, 179 / 116
+//    at 20 (heads of 64: 58 / 75 and 103 / 75); e4m3 81 / 148 at 16, 143 / 150 at 32,
+//    203 / 150 at 40;
+//  - bf16, drafts of 1 to 5 tokens, group 4 (20 rows at most), by the rows on average: 64
+//    sequences of up to 8192 keys 80 / 89 at 10, 81 / 90 at 11, 93 / 90 at 12, 91 / 90 at
+//    14; 16 of up to 16000 56 / 57 at 8, 63 / 57 at 10; heads of 64, the first batch 48 / 72
+//    at 10, 57 / 72 at 16, 68 / 73 at 18, 74 / 73 at 20, the second 37 / 43, 44 / 43, 45 / 43
+//    and 49 / 43.  One sequence of 64 rows among them: 85 / 91 and 68 / 57 at 8;
+//  - e4m3, 64 of up to 8192 keys with 64 rows at most: 109 / 156 at 24, 135 / 153 at 32,
+//    137 / 161 at 36; with 128 at most 93 / 149 at 10 and 143 / 156 at 32; with 160 at most
+//    101 / 148 and 152 / 155, but for 16 of up to 16000 115 / 82 at 32 with 128 at most.
 // A batch of decoding sequences with a prompt's chunk among them: both kernels, each
-// for its own sequences, cost two launches more; 63 + one chunk of 128 or of 512
-// tokens took, with both / in the tcgen05 kernel alone, bf16 89 / 94 and 103 / 101 us,
-// e4m3 77 / 146 and 97 / 160 us; 15 + one, e4m3, 50 / 54 and 72 / 69 us.
+// for its own sequences, cost two launches more.  Both / tcgen05 alone, e4m3, sequences
+// of up to 2000 and of up to 8192 keys with a chunk of 128 | 512 tokens: 8 sequences 38 / 27
+// and 45 / 42 | 48 / 37 and 59 / 58; 16: 39 / 35 and 50 / 58 | 48 / 48 and 62 / 78; 20: 42 / 42
+// and 61 / 73 | 60 / 56 and 93 / 94; 24, the first where both won everywhere: 40 / 48 and
+// 59 / 71 | 51 / 62 and 76 / 96; 64: 50 / 83 and 81 / 154 | 61 / 107 and 92 / 159.  bf16, 64:
+// 51 / 55 and 88 / 93 | 61 / 61 and 98 / 101: the tcgen05 kernel alone.
+// The averages are over `tokens`, padding included: the lists of lengths are the device's.
 struct Kernels {
   bool few, tc;
   int split;       // rows above which a sequence is the tcgen05 kernel's
@@ -91,7 +102,7 @@ Kernels pick_kernels(const attn_cache_problem_t* p) {
   const int64_t average = static_cast<int64_t>(p->tokens) * group / p->num_seqs;
   const Kernels few = {true, false, 0x7fffffff, cache_fwd_rows(rows)};
   if (rows <= (e4m3 ? 32 : 16) || group > kCacheTcTile) return few;
-  if (rows <= (e4m3 ? 128 : 32) && average <= (e4m3 ? 32 : 10)) return few;
+  if (rows <= (e4m3 ? 128 : 32) && average <= (e4m3 ? 32 : p->head_dim == 64 ? 16 : 10)) return few;
   if (e4m3 && p->num_seqs >= 24 && group <= 16 &&
       p->tokens < static_cast<int64_t>(p->num_seqs) * p->max_new)
     return {true, true, 16, cache_fwd_rows(group)};
