@@ -136,7 +136,12 @@ size_t attn_cache_fwd_workspace_size(const attn_cache_problem_t* p);
  * by the kernel for many query rows per KV head and to a sum of two bf16 (2^-16) by
  * that for few; e4m3 caches, times the scale of its value's page, to fp16 (within
  * 2^-11 of it, or within 2^-33 of the largest P times scale of the keys that the row
- * sees).  Which kernel serves a call follows from the problem alone.
+ * sees).  Which kernel serves a call follows from the problem alone: a row of a bf16
+ * cache is held to 2^-16 in a batch of sequences with few new tokens, and to 2^-8
+ * where a prompt's chunk shares the call.
+ * Over an e4m3 cache q is held in fp16 times a power of two for each row: exact for
+ * elements of at least 2^-31 of the row's largest, off by 2^-39 of that below.  The
+ * kernel for many rows expects logits of such a cache below 2^25 in magnitude.
  * Any number of new tokens per sequence, one included; sequences of different
  * kinds may share a call.  The result is bitwise reproducible on one device.
  */

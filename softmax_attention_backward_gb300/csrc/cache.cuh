@@ -143,6 +143,11 @@ struct CacheFwdArgs {
 constexpr float kPHead = 8.f, kPSlack = 3.f;
 constexpr float kPUp = 256.f, kPDown = 1.f / 256.f;   // 2^kPHead and back
 
+// e4m3 caches: a row of q is held in fp16 times a power of two that takes its largest
+// element to [2^kQUp, 2^(kQUp + 1)): a bf16 element is exact down to 2^-31 of that, and
+// then off by 2^-39 of it at most.
+constexpr int kQUp = 14;
+
 // Rows of an item of the tcgen05 kernel, and of each of its two tiles.
 constexpr int kCacheTcRows = 256, kCacheTcTile = 128;
 // The number of keys of its chunks.

@@ -478,11 +478,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NQ>::THREADS, 1)
                                      fabsf(__uint_as_float(w[j] & 0xffff0000u))));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          // q 2^(8 - k), k the exponent of the row's largest element: below
-          // 512, exact in fp16 down to 2^-32 of it and then within 2^-33 of it
+          // q 2^(kQUp - k), k the exponent of the row's largest element
           const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-          const float f = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
-          const float back = __uint_as_float(static_cast<uint32_t>(k - 8 + 127) << 23);
+          const float f = __uint_as_float(static_cast<uint32_t>(kQUp - k + 127) << 23);
+          const float back = __uint_as_float(static_cast<uint32_t>(k - kQUp + 127) << 23);
           qs[nq][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
           qs[nq][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll

@@ -697,8 +697,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
       float rowf = sl2;            // logit factor of the row
       float off = -3.4e38f;        // e4m3: R of kPHead, less m_run; O is in units of 2^(R - kPHead)
       if constexpr (E4M3) {
-        // The rows as fp16 times a power of two each, its largest element below 512: exact down
-        // to 2^-32 of it and then within 2^-33 of it.  D / 8 lanes take a row.  (The tile is
+        // The rows as fp16 times a power of two each (kQUp).  D / 8 lanes take a row.  (The tile is
         // free: its last S of the part before has been read by this warpgroup.)
         if (nt > 0) {
           constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const int k = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(8 - k + 127) << 23);
+            const float up = __uint_as_float(static_cast<uint32_t>(kQUp - k + 127) << 23);
             const int mine = __shfl_sync(0xffffffffu, k, (lane % RPI) * LPR);
             if (lane / RPI == i) k_row = mine;   // of the thread's own row
 #pragma unroll
@@ -736,7 +735,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
             *reinterpret_cast<uint4*>(sQ + t * C::Q_BYTES + (vec >> 3) * C::BM * 128 + r * 128 +
                                       (((vec & 7) ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
-          rowf *= __uint_as_float(static_cast<uint32_t>(k_row - 8 + 127) << 23);
+          rowf *= __uint_as_float(static_cast<uint32_t>(k_row - kQUp + 127) << 23);
           fence_proxy_async_smem();
           mbar_arrive(&bar_qready[t]);
         }

@@ -172,3 +172,21 @@ def test_logits_whose_rounding_is_whole_powers(D, m, bits, e):
         assert ((o[:m].double().cpu() - v).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) * v.abs()).all()
         want = scale * 14.0
         assert ((lse[:, :m].double().cpu() - want).abs() <= 2.0 ** -21 * want).all()
+
+
+@pytest.mark.parametrize("D,m", ROWS)
+@pytest.mark.parametrize("bits", [20, 28, 31])
+def test_small_elements_beside_a_large_one_in_a_query(D, m, bits):
+    # an element 2^bits times the others, where the keys hold zeros: the others, of three bits each, make the logits.
+    # q is held in fp16 times a power of two, exact for bf16 elements of at least 2^-31 of the row's largest
+    s = ScaledStep("e4m3", D, 4, 2, 16, [(300, m), (70, m)], seed=87)
+    g = torch.Generator().manual_seed(9)
+    sign = 1.0 - 2.0 * torch.randint(0, 2, s.q.shape, generator=g)
+    s.q = (sign * (1.0 + torch.randint(0, 8, s.q.shape, generator=g) / 8.0)).to(torch.bfloat16)
+    s.q[:, :, 9] = 2.0 ** bits
+    live = ~s.pools[0].float().isnan()
+    live[..., :9] = False
+    live[..., 10:] = False
+    s.pools[0].view(torch.uint8)[live] = 0
+    s.refresh(0)
+    check(answer(s, 11), *run_fwd(s))
