@@ -783,7 +783,8 @@ def attn_cache_append(q, k, v, k_cache, v_cache, *, page_table, seqlens_kv, cu_s
     cu_seqlens int32 [n + 1]; max_new bounds the new tokens of a sequence.
     cos_sin fp32 [positions, rot_dim] (cosines, then sines) rotates q and k, None
     leaves them; `interleaved` pairs neighbouring dims.  The tokens of q, k and v
-    may lie apart, as in a fused projection."""
+    may lie apart, as in a fused projection, but not over each other (expand).  A
+    step without a token (T = 0) does nothing."""
     dev = k_cache.device
     if q is None:
         if q_out is not None:

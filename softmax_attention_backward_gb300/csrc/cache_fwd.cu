@@ -32,16 +32,18 @@
 // around that by latency: about 5 us from the launch to the first keys (the dealing, the
 // page lists, the first copies), 3 us for the join in a CTA and 3 for that of CTAs.
 // 64 sequences of 15 to 8192 keys, 32 query heads on 8 KV heads of 128: 66 us for bf16
-// (5.4 TB/s over all), 46 us for e4m3 (3.8 TB/s: half the bytes for as many instructions,
-// whose own latency the warps wait for); one sequence of 262144 e4m3 keys: 98 us
-// (5.5 TB/s); one token over 1000 keys: 12 us, latency alone.
+// (5.4 TB/s over all), 48 us for e4m3 (3.7 TB/s: half the bytes for 1.16 times the
+// instructions, whose own latency the warps wait for); one sequence of 262144 e4m3 keys:
+// 97 us (5.5 TB/s); one token over 1000 keys: 12 us, latency alone.
 //
 // Softmax statistics, sums and O are fp32.  bf16 caches: S is exact products in
-// fp32; P goes in as hi + lo, two bf16 (2^-17).  e4m3 caches: codes convert to
-// fp16 exactly; q, scaled by a power of two per row, is exact in fp16 too, and
-// P is rounded to fp16 (2^-11).  The page scales multiply the logits of a page
-// and its P, relative to the largest product of P and scale that the row has seen
-// (kPHead in cache.cuh); O is kept in that unit.
+// fp32; P goes in as hi + lo, two bf16 (2^-16): one would double the output's own
+// rounding of 2^-8, and the MMAs are far from what bounds this kernel.  e4m3
+// caches: codes convert to fp16 exactly, q nearly always (kQUp in cache.cuh), and
+// P is rounded to fp16 once (2^-11, an eighth of the output's rounding).  The
+// page scales multiply the logits of a page and its P, relative to the largest
+// product of P and scale that the row has seen (kPHead in cache.cuh); O is kept
+// in that unit.
 #include "cache.cuh"
 
 namespace attn {

@@ -28,13 +28,18 @@
 // the logits, log2 of the value scale as a summand in the exponent of P, which the
 // row sum takes off again (kPHead in cache.cuh says in what unit P and O are held).
 //
-// Bound by the softmax (bf16: 1.34 PFLOP/s, 460 us, for 2 x 2048 new tokens over
+// Rounding.  Statistics, sums and O are fp32, and the row sum takes P unrounded.  bf16: P
+// goes in as one bf16 (2^-8), as in attn_fwd: a second one for the rest would make the
+// MMAs half as many again, which at the measured GEMM rate is longer (480 us for the chunk
+// below) than all that the kernel takes now.  e4m3: one fp16 (2^-11).
+//
+// Bound by the softmax (bf16: 1.36 PFLOP/s, 455 us, for 2 x 2048 new tokens over
 // 8192 cached ones, 32 query heads of 128, 70% of the measured GEMM rate; the dense
 // forward's own rate is 1.27), and for short items by what an item costs beside its
 // chunks: about 5 us until the first logits, 2 us for the outputs, 10 us for the join of
 // partial results (12 sequences of up to 700 new tokens over up to 4000 keys: 52 us).
-// e4m3: 574 us and 76 us for the same two; with the conversion, four scales a chunk
-// and 128 registers a thread it issues 1.8 times the instructions, which makes a
+// e4m3: 584 us and 77 us for the same two; with the conversion, four scales a chunk
+// and 128 registers a thread it issues 1.7 times the instructions, which makes a
 // chunk 1.2 us long instead of 0.95.  Converting by shifts and masks (to bf16 for the
 // keys, so that q needs none) takes three instructions for one and a check for NaN:
 // 827 us without the check, 1414 with it, in the four warps that registers leave for it.
@@ -72,7 +77,7 @@ struct TcCfg {
 // tiles, its first and last chunk and its outputs: 12 sequences of up to 700 new
 // tokens over up to 4000 keys took 52.2, 52.5, 54.9 us with 4, 5, 7 (bf16) and 88, 85,
 // 78 us with 5, 7, 10 (e4m3, whose queries the softmax warps convert), 2 x 4096 fresh
-// tokens 257, 253, 258 us with 4, 5, 7 (76 and 242 us by now, with 10 and 5).
+// tokens 257, 253, 258 us with 4, 5, 7 (77 and 243 us by now, with 10 and 5).
 template <bool E4M3>
 constexpr int kItemCost = E4M3 ? 10 : 5;
 
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3>::THREADS, 1)
     // Warp w of four has rows 16 w .. 16 w + 15 of every chunk of keys or values; a thread
     // takes vectors of 16 codes.  The scales are left to the softmax.  (code * scale as
     // bf16, four instructions more for two codes, and per-thread copies of the codes took
-    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 574.)
+    // eight warps and 712 us for 2 x 2048 tokens over 8192 keys, where this form takes 584.)
     if constexpr (E4M3) {
       if (range > 0) {
         constexpr int VR = D / 16;          // vectors of a row
