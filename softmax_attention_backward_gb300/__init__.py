@@ -13,9 +13,13 @@ Entry points (same names as the C ABI):
   dsa_indexer_fwd, dsa_topk, dsa_indexer_bwd_workspace_size, dsa_indexer_bwd, dsa_sparse_kl,
   csa_compressor_fwd, csa_compressor_bwd_workspace_size, csa_compressor_bwd  (include/dsa.h)
   attn_cache_append, attn_cache_fwd_workspace_size, attn_cache_fwd  (include/cache.h)
+  attn_rotary_table, attn_rotary_fwd, attn_rotary_bwd  (include/rotary.h)
+  linear_attn_fwd_workspace_size, linear_attn_fwd, linear_attn_bwd_workspace_size, linear_attn_bwd,
+  linear_attn_step  (include/linear.h)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -33,6 +37,9 @@ __all__ = [
     "csa_compressor_bwd", "dsa_indexer_fwd", "dsa_topk", "dsa_indexer_bwd_workspace_size",
     "dsa_indexer_bwd", "dsa_sparse_kl", "INDEXER_HEAD_DIM", "attn_wait_selftest",
     "attn_cache_append", "attn_cache_fwd_workspace_size", "attn_cache_fwd", "attn_cache_empty",
+    "attn_rotary_table", "attn_rotary_fwd", "attn_rotary_bwd",
+    "linear_attn_fwd_workspace_size", "linear_attn_fwd", "linear_attn_bwd_workspace_size",
+    "linear_attn_bwd", "linear_attn_step",
 ]
 
 ATTN_DQ_ATOMIC = 0
@@ -50,6 +57,9 @@ EXPORTED_SYMBOLS = (
     "dsa_indexer_fwd", "dsa_topk", "dsa_indexer_bwd_workspace_size", "dsa_indexer_bwd",
     "dsa_sparse_kl", "attn_wait_selftest",
     "attn_cache_append", "attn_cache_fwd_workspace_size", "attn_cache_fwd",
+    "attn_rotary_table", "attn_rotary_fwd", "attn_rotary_bwd",
+    "linear_attn_fwd_workspace_size", "linear_attn_fwd", "linear_attn_bwd_workspace_size",
+    "linear_attn_bwd", "linear_attn_step",
 )
 INDEXER_HEAD_DIM = 128
 FIXED_SCRATCH_BYTES = 16 << 20
@@ -110,6 +120,46 @@ class _CacheProblem(ctypes.Structure):
     ]
 
 
+class _RotaryTable(ctypes.Structure):
+    _fields_ = [
+        ("max_position", ctypes.c_int), ("rot_dim", ctypes.c_int), ("base", ctypes.c_double),
+        ("scaling", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_int),
+        ("fast", ctypes.c_double), ("slow", ctypes.c_double), ("magnitude", ctypes.c_float),
+    ]
+
+
+class _RotaryProblem(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int), ("heads_q", ctypes.c_int), ("heads_k", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("rot_offset", ctypes.c_int),
+        ("interleaved", ctypes.c_int), ("max_position", ctypes.c_int), ("seqlen", ctypes.c_int),
+        ("num_seqs", ctypes.c_int), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class _LinearProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("seqlen", ctypes.c_int), ("tokens", ctypes.c_int),
+        ("heads_q", ctypes.c_int), ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("dout_stride", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("log_decay", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class _LinearStep(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("num_slots", ctypes.c_int), ("heads_q", ctypes.c_int),
+        ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("log_decay", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -155,6 +205,18 @@ def lib() -> ctypes.CDLL:
         L.attn_cache_fwd_workspace_size.argtypes = [KP]
         L.attn_cache_fwd_workspace_size.restype = sz
         L.attn_cache_fwd.argtypes = [KP, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        RP = ctypes.POINTER(_RotaryProblem)
+        L.attn_rotary_table.argtypes = [ctypes.POINTER(_RotaryTable), vp, vp]
+        L.attn_rotary_fwd.argtypes = [RP, vp, vp, vp, vp, vp, vp]
+        L.attn_rotary_bwd.argtypes = [RP, vp, vp, vp, vp, vp, vp]
+        LP = ctypes.POINTER(_LinearProblem)
+        L.linear_attn_fwd_workspace_size.argtypes = [LP]
+        L.linear_attn_fwd_workspace_size.restype = sz
+        L.linear_attn_fwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.linear_attn_bwd_workspace_size.argtypes = [LP]
+        L.linear_attn_bwd_workspace_size.restype = sz
+        L.linear_attn_bwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.linear_attn_step.argtypes = [ctypes.POINTER(_LinearStep), vp, vp, vp, vp, vp, vp]
         L.attn_wait_selftest.argtypes = [vp, ctypes.c_uint, vp, vp]
         L.attn_wait_selftest.restype = i32
         L.attn_status_string.argtypes = [i32]
@@ -163,7 +225,9 @@ def lib() -> ctypes.CDLL:
         for name in ("attn_fwd", "attn_bwd_preprocess", "attn_bwd", "attn_bwd_postprocess",
                      "sparse_attn_fwd", "sparse_attn_bwd", "attn_bwd_fixed_scratch",
                      "csa_compressor_fwd", "csa_compressor_bwd", "dsa_indexer_fwd", "dsa_topk",
-                     "dsa_indexer_bwd", "dsa_sparse_kl", "attn_cache_append", "attn_cache_fwd"):
+                     "dsa_indexer_bwd", "dsa_sparse_kl", "attn_cache_append", "attn_cache_fwd",
+                     "attn_rotary_table", "attn_rotary_fwd", "attn_rotary_bwd", "linear_attn_fwd",
+                     "linear_attn_bwd", "linear_attn_step"):
             getattr(L, name).restype = i32
         _LIB = L
     return _LIB
@@ -885,3 +949,303 @@ def _fwd_here(p, q, k_cache, v_cache, k_scale, v_scale, out, lse, workspace, s):
     if code:
         raise AttnError("attn_cache_fwd", code)
     return out, lse
+
+
+# ----------------------------------------------------------------------------
+# rotation by position (include/rotary.h)
+# ----------------------------------------------------------------------------
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def attn_rotary_table(max_position, rot_dim, *, base=10000.0, scaling="none", factor=1.0,
+                      original=0, fast=32.0, slow=1.0, magnitude=1.0, out=None, device=None,
+                      stream=None):
+    """The table of cosines and sines of attn_rotary_fwd and attn_cache_append: fp32
+    [max_position, rot_dim], magnitude times the cosines of position * frequency,
+    then the sines.  scaling "none", "linear" (frequencies divided by factor),
+    "base" (the base grown so that the lowest is) or "parts" (those divided that
+    turn less than `slow` times over `original` positions, those kept that turn
+    more than `fast` times, a ramp between)."""
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_ROTARY_SCALINGS)}, got {scaling!r}")
+    if out is None:
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+    else:
+        dev = _need(out, "out", torch.float32).device
+        if out.shape != (max_position, rot_dim):
+            raise ValueError("out must be [max_position, rot_dim]")
+        if device is not None and torch.device(device) not in (dev, torch.device("cuda")):
+            raise ValueError(f"out is on {dev}, device is {device}")
+    p = _RotaryTable(int(max_position), int(rot_dim), float(base), _ROTARY_SCALINGS[scaling],
+                     float(factor), int(original), float(fast), float(slow), float(magnitude))
+    ctx, s = _on(dev, stream)
+    with ctx or contextlib.nullcontext():
+        if out is None:
+            out = torch.empty(max(0, p.max_position), max(0, p.rot_dim), dtype=torch.float32, device=dev)
+        _check("attn_rotary_table", (_LIB or lib()).attn_rotary_table(ctypes.byref(p), out.data_ptr(), s))
+    return out
+
+
+def _token_rows(t, name, lead, heads, dim, gpu, device):
+    """bf16 [*lead, heads, dim] (lead one or two dims) whose tokens may lie apart,
+    equally far (a slice of a fused projection); returns the elements between two
+    tokens, 0 for dense ones."""
+    if (t.dtype is torch.bfloat16 and t.get_device() == gpu and t.shape == (*lead, heads, dim)
+            and t.is_contiguous()):
+        return 0
+    if t.shape != (*lead, heads, dim):
+        raise ValueError(f"{name} must be {[*lead, heads, dim]}, got {list(t.shape)}")
+    if len(lead) == 1:
+        return _need_rows(t, name, heads, dim, device)
+    if lead[0] > 1 and lead[1] > 1 and t.stride(0) != lead[1] * t.stride(1) and t.numel():
+        raise ValueError(f"{name}: the sequences must follow each other as the tokens of one do")
+    row = t.stride(1) if lead[1] > 1 else t.stride(0)
+    if t.numel() == 0:
+        row = heads * dim
+    return _need_rows(t.as_strided((lead[0] * lead[1], heads, dim), (row, t.stride(2), t.stride(3)),
+                                   t.storage_offset()), name, heads, dim, device)
+
+
+def _gpu_of(t, name):
+    """The device of a tensor that decides a call's, and its index."""
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return gpu, t.device
+
+
+def _lead(q, cu_seqlens, device):
+    """The leading dims of a dense [batch, seqlen, heads, dim] or packed [tokens,
+    heads, dim] tensor, with the sequences, their length and cu_seqlens' address."""
+    if cu_seqlens is None:
+        if q.dim() != 4:
+            raise ValueError("dense q must be [batch, seqlen, heads, head_dim]")
+        n, length = q.shape[:2]
+        return (n, length), n, length, None
+    if q.dim() != 3:
+        raise ValueError("THD q must be [tokens, heads, head_dim]")
+    if _need(cu_seqlens, "cu_seqlens", torch.int32, device).dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [num_seqs + 1]")
+    return (q.shape[0],), cu_seqlens.numel() - 1, 0, cu_seqlens.data_ptr()
+
+
+def _rotary(name, q, k, cos_sin, positions, cu_seqlens, interleaved, rot_offset, q_out,
+            k_out, error_word, stream):
+    gpu, dev = _gpu_of(q, "q")
+    if positions is not None:
+        if cu_seqlens is not None:
+            raise ValueError("positions and cu_seqlens exclude each other")
+        if q.dim() not in (3, 4):
+            raise ValueError("q must be [tokens, heads, head_dim] or [batch, seqlen, heads, head_dim]")
+        lead, n, length, cu = tuple(q.shape[:-2]), 0, 0, None
+        if _need(positions, "positions", torch.int32, dev).shape != lead:
+            raise ValueError(f"positions must be {list(lead)}, got {list(positions.shape)}")
+    else:
+        lead, n, length, cu = _lead(q, cu_seqlens, dev)
+    heads, dim = q.shape[-2:]
+    heads_k = 0
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out is given without k")
+    else:
+        if k.dim() != q.dim():
+            raise ValueError("q and k must have the same leading dims")
+        heads_k = k.shape[-2]
+    if _need(cos_sin, "cos_sin", torch.float32, dev).dim() != 2:
+        raise ValueError("cos_sin must be [positions, rot_dim]")
+    if error_word is not None:
+        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
+    p = _RotaryProblem(math.prod(lead), heads, heads_k, dim, cos_sin.shape[1], int(rot_offset),
+                       1 if interleaved else 0, cos_sin.shape[0], length, n,
+                       _token_rows(q, "q", lead, heads, dim, gpu, dev),
+                       0 if k is None else _token_rows(k, "k", lead, heads_k, dim, gpu, dev), cu,
+                       _at(positions), error_word)
+    for t, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if o is not None and _need(o, what, torch.bfloat16, dev).shape != t.shape:
+            raise ValueError(f"{what} must have the shape of {what[0]}")
+    ctx, s = _on(dev, stream)
+    with ctx or contextlib.nullcontext():
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        if k is not None and k_out is None:
+            k_out = k.new_empty(k.shape)
+        code = getattr(_LIB or lib(), name)(ctypes.byref(p), q.data_ptr(), _at(k), cos_sin.data_ptr(),
+                                            q_out.data_ptr(), _at(k_out), s)
+    if code:
+        raise AttnError(name, code)
+    return q_out, k_out
+
+
+def attn_rotary_fwd(q, k, cos_sin, *, positions=None, cu_seqlens=None, interleaved=False,
+                    rot_offset=0, q_out=None, k_out=None, error_word=None, stream=None):
+    """Rotates q (bf16 [B, S, H, D], or packed [T, H, D]) and k (likewise, or None) by
+    position: dims rot_offset .. rot_offset + rot_dim by the rows of cos_sin (fp32
+    [positions, rot_dim], cosines then sines), the other dims copied.  Positions
+    are a token's place in its sequence, or `positions` (int32 [*leading dims],
+    -1 for padding).  q_out, k_out may be q, k.  Returns (q_out, k_out)."""
+    return _rotary("attn_rotary_fwd", q, k, cos_sin, positions, cu_seqlens, interleaved,
+                   rot_offset, q_out, k_out, error_word, stream)
+
+
+def attn_rotary_bwd(dq, dk, cos_sin, *, positions=None, cu_seqlens=None, interleaved=False,
+                    rot_offset=0, dq_out=None, dk_out=None, error_word=None, stream=None):
+    """Backward of attn_rotary_fwd: the gradients of the rotated rows in, those of
+    the rows out (the transposed rotation).  Returns (dq_out, dk_out)."""
+    return _rotary("attn_rotary_bwd", dq, dk, cos_sin, positions, cu_seqlens, interleaved,
+                   rot_offset, dq_out, dk_out, error_word, stream)
+
+
+# ----------------------------------------------------------------------------
+# linear attention with a decay for each head (include/linear.h)
+# ----------------------------------------------------------------------------
+def _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word, dout=None):
+    gpu, dev = _gpu_of(q, "q")
+    lead, n, length, cu = _lead(q, cu_seqlens, dev)
+    heads, dim = q.shape[-2:]
+    if k.dim() != q.dim():
+        raise ValueError("q, k and v must have the same leading dims")
+    heads_kv = k.shape[-2]
+    if _need(log_decay, "log_decay", torch.float32, dev).shape != (heads_kv,):
+        raise ValueError(f"log_decay must be [{heads_kv}], got {list(log_decay.shape)}")
+    if error_word is not None:
+        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
+    p = _LinearProblem(n, length, math.prod(lead), heads, heads_kv, dim,
+                       float(scale) if scale is not None else 1.0 / math.sqrt(dim),
+                       _token_rows(q, "q", lead, heads, dim, gpu, dev),
+                       _token_rows(k, "k", lead, heads_kv, dim, gpu, dev),
+                       _token_rows(v, "v", lead, heads_kv, dim, gpu, dev),
+                       0 if dout is None else _token_rows(dout, "dout", lead, heads, dim, gpu, dev),
+                       cu, log_decay.data_ptr(), error_word)
+    return p, dev
+
+
+def _linear_state(t, name, p, dev):
+    if t is not None and _need(t, name, torch.float32, dev).shape != (p.num_seqs, p.heads_kv, p.head_dim, p.head_dim):
+        raise ValueError(f"{name} must be {[p.num_seqs, p.heads_kv, p.head_dim, p.head_dim]}, got {list(t.shape)}")
+    return t
+
+
+def _like(t, name, like, dev):
+    if t is not None and _need(t, name, torch.bfloat16, dev).shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+    return t
+
+
+def linear_attn_fwd_workspace_size(q, k, v, log_decay, *, cu_seqlens=None) -> int:
+    p, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
+    with torch.cuda.device(dev):
+        return int(lib().linear_attn_fwd_workspace_size(ctypes.byref(p)))
+
+
+def linear_attn_bwd_workspace_size(q, k, v, log_decay, *, cu_seqlens=None) -> int:
+    p, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
+    with torch.cuda.device(dev):
+        return int(lib().linear_attn_bwd_workspace_size(ctypes.byref(p)))
+
+
+def linear_attn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initial_state=None,
+                    want_final_state=False, final_state=None, out=None, workspace=None,
+                    error_word=None, stream=None):
+    """Linear attention with a decay for each KV head, in chunks: q bf16
+    [B, S, Hq, D], k, v [B, S, Hkv, D], or packed [T, H, D] with cu_seqlens;
+    log_decay fp32 [Hkv], at most 0; initial_state fp32 [n, Hkv, D, D] or None.
+    Returns (o, final_state), the latter None unless wanted or given.  A workspace
+    is allocated here when none is given."""
+    p, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word)
+    _linear_state(initial_state, "initial_state", p, dev)
+    _linear_state(final_state, "final_state", p, dev)
+    _like(out, "out", q, dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+    ctx, s = _on(dev, stream)
+    with ctx or contextlib.nullcontext():
+        L, ref = _LIB or lib(), ctypes.byref(p)
+        if out is None:
+            out = q.new_empty(q.shape)
+        if final_state is None and want_final_state:
+            final_state = q.new_empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32)
+        if workspace is None:
+            n = L.linear_attn_fwd_workspace_size(ref)
+            workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+        else:
+            n = workspace.numel()
+        code = L.linear_attn_fwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(initial_state),
+                                 out.data_ptr(), _at(final_state), _at(workspace), n, s)
+    if code:
+        raise AttnError("linear_attn_fwd", code)
+    return out, final_state
+
+
+def linear_attn_bwd(q, k, v, dout, log_decay, *, scale=None, cu_seqlens=None, initial_state=None,
+                    dfinal_state=None, want_dinitial_state=False, dinitial_state=None, dq=None,
+                    dk=None, dv=None, workspace=None, error_word=None, stream=None):
+    """Backward of linear_attn_fwd from its inputs, dout and dfinal_state (fp32
+    [n, Hkv, D, D], the final state's gradient, or None).  Returns (dq, dk, dv,
+    dinitial_state), the last None unless wanted or given; bitwise reproducible."""
+    p, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word, dout)
+    for t, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state"),
+                    (dinitial_state, "dinitial_state")):
+        _linear_state(t, name, p, dev)
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        _like(t, name, like, dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+    ctx, s = _on(dev, stream)
+    with ctx or contextlib.nullcontext():
+        L, ref = _LIB or lib(), ctypes.byref(p)
+        dq = q.new_empty(q.shape) if dq is None else dq
+        dk = k.new_empty(k.shape) if dk is None else dk
+        dv = v.new_empty(v.shape) if dv is None else dv
+        if dinitial_state is None and want_dinitial_state:
+            dinitial_state = q.new_empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32)
+        if workspace is None:
+            n = L.linear_attn_bwd_workspace_size(ref)
+            workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+        else:
+            n = workspace.numel()
+        code = L.linear_attn_bwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(),
+                                 _at(initial_state), _at(dfinal_state), dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), _at(dinitial_state), _at(workspace), n, s)
+    if code:
+        raise AttnError("linear_attn_bwd", code)
+    return dq, dk, dv, dinitial_state
+
+
+def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale=None, out=None,
+                     error_word=None, stream=None):
+    """One token for each sequence: q bf16 [n, Hq, D], k, v [n, Hkv, D]; state fp32
+    [slots, Hkv, D, D], updated in place; slots int32 [n], the state of each
+    sequence (-1: padding; None: sequence n's is state[n]).  Returns o."""
+    gpu, dev = _gpu_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [num_seqs, heads, head_dim]")
+    n, heads, dim = q.shape
+    heads_kv = k.shape[1]
+    if _need(state, "state", torch.float32, dev).dim() != 4 or state.shape[1:] != (heads_kv, dim, dim):
+        raise ValueError(f"state must be [slots, {heads_kv}, {dim}, {dim}], got {list(state.shape)}")
+    if _need(log_decay, "log_decay", torch.float32, dev).shape != (heads_kv,):
+        raise ValueError(f"log_decay must be [{heads_kv}], got {list(log_decay.shape)}")
+    if slots is not None and _need(slots, "slots", torch.int32, dev).shape != (n,):
+        raise ValueError(f"slots must be [{n}], got {list(slots.shape)}")
+    if error_word is not None:
+        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
+    _like(out, "out", q, dev)
+    p = _LinearStep(n, state.shape[0], heads, heads_kv, dim,
+                    float(scale) if scale is not None else 1.0 / math.sqrt(dim),
+                    _token_rows(q, "q", (n,), heads, dim, gpu, dev),
+                    _token_rows(k, "k", (n,), heads_kv, dim, gpu, dev),
+                    _token_rows(v, "v", (n,), heads_kv, dim, gpu, dev), _at(slots),
+                    log_decay.data_ptr(), error_word)
+    ctx, s = _on(dev, stream)
+    with ctx or contextlib.nullcontext():
+        if out is None:
+            out = q.new_empty(q.shape)
+        code = (_LIB or lib()).linear_attn_step(ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+                                                v.data_ptr(), state.data_ptr(), out.data_ptr(), s)
+    if code:
+        raise AttnError("linear_attn_step", code)
+    return out

@@ -1,0 +1,344 @@
+// Rotation by position (declared and documented in rotary.h): the table of
+// cosines and sines, and the rotation of queries and keys with its transpose.
+//
+// Table.  A frequency f is held as Phi = f / 2 pi modulo 1 in 64-bit fixed point,
+// so that position p has the phase p Phi modulo 2^64, one turn: two integer
+// multiplications give the angle reduced to half a turn either way, where a
+// product in fp64 (two per clock and SM on this chip) took most of the time.  The
+// phase is split into an fp32 leading part and the rest r; sincospi takes the
+// leading part, and sin(x + r) = sin x + r cos x, cos(x + r) = cos x - r sin x
+// bring the rest back (r < 2^-24, its square is below fp32's resolution).
+//
+// Rotation.  Bound by memory: every row is read and written once.  A thread holds
+// the angles of one unit of dims (two 16-byte pieces half the rotated part
+// apart, or one piece of adjacent pairs) and rotates it in up to four heads of a
+// token, all loads first; the angles come from L1 or L2, once for four heads.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "launch.h"
+#include "rotary.h"
+
+namespace attn {
+namespace {
+
+constexpr int kMaxRot = 256;
+constexpr int kHeads = 4;        // heads of a thread
+constexpr int kTableThreads = 256;
+
+struct Frequencies {
+  uint64_t phi[kMaxRot / 2];   // turns per position, modulo 1, times 2^64
+};
+
+__global__ void __launch_bounds__(kTableThreads)
+    rotary_table_kernel(const __grid_constant__ Frequencies fr, float* out, int rows, int rot,
+                        float magnitude) {
+  // a thread writes 4 cosines and their 4 sines of a row
+  const int quads = rot / 8;
+  const int64_t n = static_cast<int64_t>(rows) * quads;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(kTableThreads) + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kTableThreads) {
+    const uint32_t p = static_cast<uint32_t>(i / quads);
+    const int a = static_cast<int>(i - static_cast<int64_t>(p) * quads) * 4;
+    float c[4], s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t phase = static_cast<int64_t>(p * fr.phi[a + j]);
+      const float lead = __ll2float_rn(phase);
+      // lead = 2^63 only where the phase is within 2^38 of it: the difference wraps to the same
+      const uint64_t back = lead >= 9.223372036854775808e18f ? 0x8000000000000000ull
+                                                             : static_cast<uint64_t>(__float2ll_rn(lead));
+      const float rest = __ll2float_rn(static_cast<int64_t>(static_cast<uint64_t>(phase) - back)) *
+                         (3.14159265358979f * 0x1p-63f);
+      float sn, cs;
+      sincospif(lead * 0x1p-63f, &sn, &cs);
+      c[j] = magnitude * fmaf(-rest, sn, cs);
+      s[j] = magnitude * fmaf(rest, cs, sn);
+    }
+    float* row = out + static_cast<int64_t>(p) * rot + a;
+    *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(row + rot / 2) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
+struct RotArgs {
+  const __nv_bfloat16* in[2];
+  __nv_bfloat16* out[2];
+  int64_t in_stride[2];
+  int heads[2], groups[2];   // groups of kHeads heads
+  int tokens, dim, rot, offset, max_position, num_seqs;
+  const float* cos_sin;
+  const int32_t* cu;
+  const int32_t* positions;
+  int32_t* err;
+  FastDiv fd_units, fd_groups, fd_seqlen;
+  int64_t items;
+};
+
+// The position of token t: -1 for rows that are to be zeros.
+__device__ __forceinline__ int position_of(const RotArgs& a, int t) {
+  int pos, flag;
+  if (a.positions) {
+    pos = __ldg(a.positions + t);
+    if (pos == -1) return -1;
+    flag = ATTN_DEVERR_INDEX_RANGE;
+  } else if (a.cu) {
+    if (t >= __ldg(a.cu + a.num_seqs)) return -1;
+    int lo = 0, hi = a.num_seqs;   // the last sequence that begins at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.cu + mid) <= t) lo = mid;
+      else hi = mid;
+    }
+    pos = t - __ldg(a.cu + lo);
+    flag = ATTN_DEVERR_SEQLEN;
+  } else {
+    pos = static_cast<int>(fmod_u(static_cast<uint32_t>(t), a.fd_seqlen));
+    flag = ATTN_DEVERR_SEQLEN;
+  }
+  if (pos >= 0 && pos < a.max_position) return pos;
+  if (a.err) atomicOr(a.err, flag);
+  return -1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+}
+// x c - y s and y c + x s, each product and sum rounded once
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+  x = u;
+}
+
+// Units of a head: the rotated ones (rot / 16 pairs of pieces, or rot / 8 pieces of
+// adjacent pairs), then the pieces of 8 dims that are copied.
+template <bool kInterleaved, bool kInverse>
+__global__ void __launch_bounds__(256) rotary_kernel(const RotArgs a) {
+  const int64_t item = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
+  if (item >= a.items) return;
+  // groups vary slower than units, tokens slowest; a token has fewer than 2^31 items
+  const uint32_t per_token = a.fd_units.d * a.fd_groups.d;
+  int t;
+  uint32_t rem;
+  if (a.items < (int64_t(1) << 32)) {
+    const uint32_t q = fdiv(static_cast<uint32_t>(item), a.fd_units);
+    t = static_cast<int>(fdiv(q, a.fd_groups));
+    rem = static_cast<uint32_t>(item) - t * per_token;
+  } else {
+    t = static_cast<int>(item / per_token);
+    rem = static_cast<uint32_t>(item - static_cast<int64_t>(t) * per_token);
+  }
+  uint32_t g = fdiv(rem, a.fd_units);
+  const int u = static_cast<int>(rem - g * a.fd_units.d);
+  const int which = g >= static_cast<uint32_t>(a.groups[0]);
+  if (which) g -= a.groups[0];
+  const int h0 = g * kHeads;
+  const int n = min(kHeads, a.heads[which] - h0);
+  const int rotated = kInterleaved ? a.rot / 8 : a.rot / 16;
+  int at, second = 0;   // the first dim of the unit's piece, and the distance of the other piece
+  bool turned = u < rotated;
+  if (turned) {
+    at = a.offset + u * 8;
+    second = kInterleaved ? 0 : a.rot / 2;
+  } else {
+    at = (u - rotated) * 8;
+    if (at >= a.offset) at += a.rot;
+  }
+  const __nv_bfloat16* src = a.in[which] + t * a.in_stride[which] + static_cast<int64_t>(h0) * a.dim + at;
+  uint4 x[kHeads], y[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i)
+    if (i < n) {
+      x[i] = *reinterpret_cast<const uint4*>(src + i * a.dim);
+      if (!kInterleaved && turned) y[i] = *reinterpret_cast<const uint4*>(src + i * a.dim + second);
+    }
+  const int pos = position_of(a, t);
+  float c[8], s[8];
+  if (pos >= 0 && turned) {
+    const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
+    if (kInterleaved) {
+      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + u * 4));
+      const float4 sv = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + u * 4));
+      c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+      s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + u * 8) + j);
+        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + u * 8) + j);
+        c[4 * j] = cv.x, c[4 * j + 1] = cv.y, c[4 * j + 2] = cv.z, c[4 * j + 3] = cv.w;
+        s[4 * j] = sv.x, s[4 * j + 1] = sv.y, s[4 * j + 2] = sv.z, s[4 * j + 3] = sv.w;
+      }
+    }
+    if (kInverse)
+#pragma unroll
+      for (int j = 0; j < (kInterleaved ? 4 : 8); ++j) s[j] = -s[j];
+  }
+  __nv_bfloat16* dst = a.out[which] +
+                       (static_cast<int64_t>(t) * a.heads[which] + h0) * a.dim + at;
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (i >= n) break;
+    uint4 xo = x[i], yo = y[i];
+    if (pos < 0) {
+      xo = yo = make_uint4(0, 0, 0, 0);
+    } else if (turned) {
+      float xf[8], yf[8];
+      unpack8(x[i], xf);
+      if (kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turn(xf[2 * j], xf[2 * j + 1], c[j], s[j]);
+      } else {
+        unpack8(y[i], yf);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turn(xf[j], yf[j], c[j], s[j]);
+        yo = pack8(yf);
+      }
+      xo = pack8(xf);
+    }
+    *reinterpret_cast<uint4*>(dst + i * a.dim) = xo;
+    if (!kInterleaved && turned) *reinterpret_cast<uint4*>(dst + i * a.dim + second) = yo;
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status_t rotate(const attn_rotary_problem_t* p, const void* q, const void* k,
+                     const float* cos_sin, void* q_out, void* k_out, bool inverse,
+                     attn_stream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->heads_q <= 0 || p->heads_k < 0 || p->head_dim <= 0 || p->rot_dim <= 0 ||
+      p->rot_offset < 0 || p->max_position <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!p->positions && (p->cu_seqlens ? p->num_seqs <= 0 : p->seqlen <= 0 && p->tokens > 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->head_dim % 8 || p->head_dim > 1024 || p->rot_dim % 16 || p->rot_dim > kMaxRot ||
+      p->rot_offset % 8)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->rot_offset > p->head_dim - p->rot_dim) return ATTN_ERR_INVALID_ARG;
+  const int64_t heads = static_cast<int64_t>(p->heads_q) + p->heads_k;
+  // (a token's work items then stay below 2^31 as well)
+  if (heads * p->head_dim >= (int64_t(1) << 31) ||
+      p->tokens >= (int64_t(1) << 40) / (heads * p->head_dim))
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->tokens == 0) return ATTN_OK;
+  if (!q || !q_out || !cos_sin || (k == nullptr) != (k_out == nullptr) ||
+      (k != nullptr) != (p->heads_k > 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(cos_sin, 16) || !aligned(p->cu_seqlens, 4) || !aligned(p->positions, 4) ||
+      !aligned(p->error_word, 4))
+    return ATTN_ERR_ALIGNMENT;
+  RotArgs a{};
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  const int64_t stride[2] = {p->q_stride, p->k_stride};
+  for (int i = 0; i < 2; ++i) {
+    a.in[i] = static_cast<const __nv_bfloat16*>(in[i]);
+    a.out[i] = static_cast<__nv_bfloat16*>(out[i]);
+    a.heads[i] = i ? p->heads_k : p->heads_q;
+    a.groups[i] = (a.heads[i] + kHeads - 1) / kHeads;
+    const int64_t dense = static_cast<int64_t>(a.heads[i]) * p->head_dim;
+    a.in_stride[i] = stride[i] == 0 ? dense : stride[i];
+    if (a.in_stride[i] < dense) return ATTN_ERR_INVALID_ARG;
+    if (a.in_stride[i] % 8) return ATTN_ERR_ALIGNMENT;
+    if (in[i] && in[i] == out[i] && a.in_stride[i] != dense) return ATTN_ERR_INVALID_ARG;
+  }
+  a.tokens = p->tokens;
+  a.dim = p->head_dim;
+  a.rot = p->rot_dim;
+  a.offset = p->rot_offset;
+  a.max_position = p->max_position;
+  a.num_seqs = p->num_seqs;
+  a.cos_sin = cos_sin;
+  a.cu = p->cu_seqlens;
+  a.positions = p->positions;
+  a.err = p->error_word;
+  const int units = (p->interleaved ? p->rot_dim / 8 : p->rot_dim / 16) + (p->head_dim - p->rot_dim) / 8;
+  const int groups = a.groups[0] + a.groups[1];
+  a.fd_units = make_fastdiv(units);
+  a.fd_groups = make_fastdiv(groups);
+  a.fd_seqlen = make_fastdiv(p->seqlen > 0 ? p->seqlen : 1);
+  a.items = static_cast<int64_t>(p->tokens) * units * groups;
+  const int64_t blocks = (a.items + 255) / 256;
+  if (blocks >= (int64_t(1) << 31)) return ATTN_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (p->interleaved) {
+    if (inverse) rotary_kernel<true, true><<<grid, 256, 0, st>>>(a);
+    else rotary_kernel<true, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (inverse) rotary_kernel<false, true><<<grid, 256, 0, st>>>(a);
+    else rotary_kernel<false, false><<<grid, 256, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" attn_status_t attn_rotary_table(const attn_rotary_table_t* t, float* cos_sin,
+                                           attn_stream_t stream) {
+  if (!t || t->max_position < 0 || t->rot_dim <= 0) return ATTN_ERR_INVALID_ARG;
+  if (t->rot_dim % 16 || t->rot_dim > kMaxRot) return ATTN_ERR_UNSUPPORTED;
+  if (!(t->base > 0.0) || !std::isfinite(t->base) || !std::isfinite(t->magnitude))
+    return ATTN_ERR_INVALID_ARG;
+  if (t->scaling < ATTN_ROTARY_NONE || t->scaling > ATTN_ROTARY_PARTS) return ATTN_ERR_INVALID_ARG;
+  if (t->scaling != ATTN_ROTARY_NONE && (!(t->factor > 0.0) || !std::isfinite(t->factor)))
+    return ATTN_ERR_INVALID_ARG;
+  if (t->scaling == ATTN_ROTARY_PARTS &&
+      (t->original <= 0 || !std::isfinite(t->fast) || !std::isfinite(t->slow) || !(t->fast > t->slow)))
+    return ATTN_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  Frequencies fr{};
+  const double r = t->rot_dim;
+  const double base = t->scaling == ATTN_ROTARY_BASE ? t->base * std::pow(t->factor, r / (r - 2.0)) : t->base;
+  for (int a = 0; a < t->rot_dim / 2; ++a) {
+    double f = std::pow(base, -2.0 * a / r);
+    if (t->scaling == ATTN_ROTARY_LINEAR) f /= t->factor;
+    if (t->scaling == ATTN_ROTARY_PARTS) {
+      double w = (t->original * f / two_pi - t->slow) / (t->fast - t->slow);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      f *= w + (1.0 - w) / t->factor;
+    }
+    if (!std::isfinite(f)) return ATTN_ERR_INVALID_ARG;
+    double turns = f / two_pi;
+    turns -= std::floor(turns);
+    const double scaled = std::ldexp(turns, 64);   // below 2^64, an integer from 2^53 on
+    fr.phi[a] = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled + (scaled < 0x1p52 ? 0.5 : 0.0));
+  }
+  if (t->max_position == 0) return ATTN_OK;
+  if (!cos_sin) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(cos_sin, 16)) return ATTN_ERR_ALIGNMENT;
+  const size_t work = static_cast<size_t>(t->max_position) * (t->rot_dim / 8);
+  const int grid = resident_grid(rotary_table_kernel, work, kTableThreads, 4);
+  rotary_table_kernel<<<grid, kTableThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      fr, cos_sin, t->max_position, t->rot_dim, t->magnitude);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_rotary_fwd(const attn_rotary_problem_t* p, const void* q,
+                                         const void* k, const float* cos_sin, void* q_out,
+                                         void* k_out, attn_stream_t stream) {
+  return rotate(p, q, k, cos_sin, q_out, k_out, false, stream);
+}
+
+extern "C" attn_status_t attn_rotary_bwd(const attn_rotary_problem_t* p, const void* dq,
+                                         const void* dk, const float* cos_sin, void* dq_out,
+                                         void* dk_out, attn_stream_t stream) {
+  return rotate(p, dq, dk, cos_sin, dq_out, dk_out, true, stream);
+}
