@@ -6,10 +6,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "cache.h"
 #include "common.cuh"
+#include "launch.h"
 
 namespace attn {
 
@@ -46,20 +45,6 @@ __device__ __forceinline__ StepSeq step_seq(const CacheStep& s, int n, int* bad 
   q.pos0 = max(l, 0) - q.m;
   if (bad && (l > cap || l < 0 || q.m > s.max_new || q.m > l)) *bad |= ATTN_DEVERR_SEQLEN;
   return q;
-}
-
-// Allows `kern` its dynamic shared memory, once per device (`ready`: a bit each):
-// the call takes 1 to 2 us of the host's time, of some 30 for a step.
-template <typename Kernel>
-inline cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev < 64 && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) ready.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 struct AppendArgs {

@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "attn.h"
 #include "common.cuh"
 
@@ -50,6 +52,20 @@ inline int resident_grid(Kernel kernel, size_t work, int threads, int waves = 1)
   if (g > cap) g = cap;
   if (g < 1) g = 1;
   return static_cast<int>(g);
+}
+
+// Allows `kern` its dynamic shared memory, once per device (`ready`: a bit each):
+// the call takes 1 to 2 us of the host's time, of some 30 for a step.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 struct FwdArgs {

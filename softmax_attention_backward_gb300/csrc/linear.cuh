@@ -9,7 +9,10 @@
 
 namespace attn {
 
-// The three gradients and the output are one recurrence over rows x, y, z:
+constexpr int kLinearChunk = 128;   // tokens of a chunk
+constexpr int kLinearJobs = 3;      // outputs of one launch at most
+
+// The output and the three gradients are one recurrence over rows x, y, z:
 //   forwards   S = l S + y_t z_t^T,  out_t = scale S^T x_t
 //   backwards  S = S + scale y_t z_t^T,  out_t = S^T x_t,  then S = l S
 //              (over t from the last token down; y, z of every query head of x's KV head)
@@ -17,21 +20,28 @@ namespace attn {
 // (v, dout, q) -> dk.  The state of the second and the last is the transposed
 // one of the first and the third.
 struct LinearJob {
-  const __nv_bfloat16* x;
-  const __nv_bfloat16* y;
-  const __nv_bfloat16* z;
-  int64_t x_stride, y_stride, z_stride;   // elements from token to token
-  __nv_bfloat16* out;                     // dense, heads_x heads
-  int heads_x;
+  CUtensorMap mx, my, mz;   // maps over [tokens, heads, head_dim], boxes of a chunk and 64 dims
+  __nv_bfloat16* out;       // dense, heads_x heads; null: states only
+  int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;
-  int inner;              // heads of y and z that meet one head of x
-  FastDiv fd_kv;          // heads of x per KV head
-  const float* first;     // state before the first token of the walk, or null
-  float* last;            // state after its last token, or null
-  int transposed;         // `first` is held transposed
+  int inner;                // heads of y and z that meet one head of x
+  FastDiv fd_heads;         // heads_x
+  FastDiv fd_kv;            // heads of x per KV head
+  const float* first;       // state before the first token of the walk, or null
+  float* last;              // state after its last token, or null
+  int transposed;           // `first` is held transposed
+  int seg_chunks;           // chunks of a segment at most
+  int slots;                // (sequence, segment) places of the job
+  // States that the segments add, fp32 [slots, heads_kv, D/4, D, 4] (columns in fours,
+  // rows within): read by a job with `out`, written by one without, which also
+  // writes them transposed where that is not null.
+  float* parts;
+  float* parts_t;
 };
 
 struct LinearArgs {
+  LinearJob job[kLinearJobs];
+  int jobs;
   int num_seqs, seqlen, tokens, heads_kv;
   float scale;
   const int32_t* cu;
@@ -39,32 +49,8 @@ struct LinearArgs {
   int32_t* err;
 };
 
-// log2 of a head's decay, at most 0.  -inf becomes a number whose products with 0
-// and with token counts stay finite.
-__device__ __forceinline__ double log2_decay(const LinearArgs& a, int h) {
-  float g = __ldg(a.log_decay + h);
-  if (!(g <= 0.f)) {
-    if (a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
-    g = 0.f;
-  }
-  return fmax(g * 1.4426950408889634, -1e6);
-}
-
-// The rows of sequence n, kept within the tensors whatever cu holds.
-__device__ __forceinline__ void linear_sequence(const LinearArgs& a, int n, int& row0, int& len) {
-  if (!a.cu) {
-    row0 = n * a.seqlen;
-    len = a.seqlen;
-    return;
-  }
-  const int b = __ldg(a.cu + n), e = __ldg(a.cu + n + 1);
-  row0 = min(max(b, 0), a.tokens);
-  const int end = min(max(e, row0), a.tokens);
-  len = end - row0;
-  if ((b != row0 || e != end) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
-}
-
-cudaError_t launch_linear_walk(int head_dim, const LinearArgs& a, const LinearJob& j,
-                               cudaStream_t st);
+// `terms` bf16 terms of a decayed key: 1, or 3 where a state is returned
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, int terms, bool states_only,
+                          cudaStream_t st);
 
 }  // namespace attn

@@ -176,9 +176,9 @@ def test_no_tokens():
 
 def test_fused_projection_and_another_stream():
     s = Rows([190, 190], 4, 2, 128, states=True, seed=12)
-    want = s.call()
     fused = torch.cat([t.flatten(1) for t in (s.q, s.k, s.v)], 1).to(DEV)
     for lead in ((380,), (2, 190)):
+        want = s.call(packed=len(lead) == 1)
         q, k, v = (t.unflatten(-1, (-1, 128)) for t in fused.view(*lead, -1).split([512, 256, 256], -1))
         assert not q.is_contiguous()
         side = torch.cuda.Stream(DEV)
@@ -221,7 +221,7 @@ def test_captured_and_replayed_with_other_lengths():
 
 def test_two_calls_at_once():
     a, b = Rows([900], 4, 2, 128, states=True, seed=14), Rows([700, 650], 4, 4, 128, states=True, seed=15)
-    wa, wb = a.call(), b.call()
+    wa, wb = a.call(packed=True), b.call(packed=True)
     streams = [torch.cuda.Stream(DEV) for _ in range(2)]
     for _ in range(3):
         got = []
