@@ -20,7 +20,7 @@ constexpr int kLinearJobs = 3;      // outputs of one launch at most
 // (v, dout, q) -> dk.  The state of the second and the last is the transposed
 // one of the first and the third.
 struct LinearJob {
-  CUtensorMap mx, my, mz;   // maps over [tokens, heads, head_dim], boxes of a chunk and 64 dims
+  CUtensorMap mx, my, mz, mo;   // maps over [tokens, heads, head_dim], boxes of a chunk and 64 dims
   __nv_bfloat16* out;       // dense, heads_x heads; null: states only
   int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;

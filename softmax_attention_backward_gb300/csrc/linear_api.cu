@@ -142,6 +142,11 @@ bool map_rows(CUtensorMap* m, const linear_attn_problem_t* p, const Rows& r) {
   return make_bf16_heads_map(m, r.p, p->tokens, r.heads, p->head_dim, r.stride, 1, kLinearChunk);
 }
 
+bool map_out(LinearJob* j, const linear_attn_problem_t* p, void* out, int heads) {
+  j->out = static_cast<__nv_bfloat16*>(out);
+  return map_rows(&j->mo, p, {out, static_cast<int64_t>(heads) * p->head_dim, heads});
+}
+
 // What a job takes from the problem; `shared`: heads of x per KV head, `way`: 0 forwards, 1 backwards.
 void set_job(LinearJob& j, const linear_attn_problem_t* p, int heads_x, int shared, int inner, const Cut& c, int way) {
   j.heads_x = heads_x;
@@ -214,9 +219,10 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   LinearArgs a = make_args(p);
   a.jobs = 1;
   LinearJob& j = a.job[0];
-  if (!map_rows(&j.mx, p, rq) || !map_rows(&j.my, p, rk) || !map_rows(&j.mz, p, rv)) return ATTN_ERR_CUDA;
+  if (!map_rows(&j.mx, p, rq) || !map_rows(&j.my, p, rk) || !map_rows(&j.mz, p, rv) ||
+      !map_out(&j, p, o, p->heads_q))
+    return ATTN_ERR_CUDA;
   set_job(j, p, p->heads_q, p->heads_q / p->heads_kv, 1, cut, 0);
-  j.out = static_cast<__nv_bfloat16*>(o);
   j.first = initial_state;
   j.last = final_state;
   j.parts = static_cast<float*>(workspace);
@@ -260,16 +266,14 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   a.jobs = 3;
   // dv and dk first: their walks are the longer ones
   LinearJob &jv = a.job[0], &jk = a.job[1], &jq = a.job[2];
-  if (!map_rows(&jv.mx, p, rk) || !map_rows(&jv.my, p, rq) || !map_rows(&jv.mz, p, rd) || !map_rows(&jk.mx, p, rv))
+  if (!map_rows(&jv.mx, p, rk) || !map_rows(&jv.my, p, rq) || !map_rows(&jv.mz, p, rd) || !map_rows(&jk.mx, p, rv) ||
+      !map_out(&jv, p, dv, p->heads_kv) || !map_out(&jk, p, dk, p->heads_kv) || !map_out(&jq, p, dq, p->heads_q))
     return ATTN_ERR_CUDA;
   jk.my = jv.mz, jk.mz = jv.my;
   jq.mx = jv.mz, jq.my = jk.mx, jq.mz = jv.mx;
   set_job(jv, p, p->heads_kv, 1, group, cut, 1);
   set_job(jk, p, p->heads_kv, 1, group, cut, 1);
   set_job(jq, p, p->heads_q, group, 1, cut, 0);
-  jv.out = static_cast<__nv_bfloat16*>(dv);
-  jk.out = static_cast<__nv_bfloat16*>(dk);
-  jq.out = static_cast<__nv_bfloat16*>(dq);
   jv.first = jk.first = dfinal_state;
   jv.last = dinitial_state;
   jq.first = initial_state;

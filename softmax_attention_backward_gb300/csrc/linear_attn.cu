@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
               umma_ss_w(tmem + C::COL_O2, desc_advance(dx, kmajor_step_bytes(128, k)),
                         desc_advance(dH, mnmajor_step_bytes(k)), idO, k > 0);
           }
-          if (last) umma_commit_w(&bar_xempty[bx]);
         }
         if (!mbar_wait_w(&bar_full[sz], uz, ac)) { ok = false; break; }
         if (!kStates) {
@@ -309,36 +308,45 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       for (int g = 0; ok && g < inner; ++g, ++it, tile += 2) {
         if (!mbar_wait(&bar_s, it & 1, ac)) { ok = false; break; }
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           uint32_t p[16];
           if (back ? b < wq : b > wq) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) p[x] = 0;
-          } else {
-            // off the diagonal block: the exponent left once the table's part is taken
-            const float base = a.scale * ex2(l2 * max(back ? 32 * b - i : i - 32 * b - 31, 0));
+          } else if (b == wq || (back && rows < kLinearChunk)) {
+            // the diagonal block, and backwards columns behind the sequence: an exponential and a
+            // comparison for each element
+            uint32_t s[32];
+            tmem_ld32_nowait(lane_base + C::COL_S + 32 * b, s);
+            tmem_wait_ld();
+            const int lead = back ? 32 * b - i : i - 32 * b, sign = back ? 1 : -1;
+            const int end = back ? rows - 32 * b : 32;
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t s[16];
-              tmem_ld16_nowait(lane_base + C::COL_S + 32 * b + e, s);
-              tmem_wait_ld();
+            for (int x = 0; x < 32; x += 2) {
+              float f[2];
 #pragma unroll
-              for (int x = 0; x < 16; x += 4) {
-                const int j0 = 32 * b + e + x;
-                const float4 t = *reinterpret_cast<const float4*>(s_tab + e + x);
-                float f[4] = {base * t.x, base * t.y, base * t.z, base * t.w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const int d = back ? j0 + y - i : i - j0 - y;
-                  if (b == wq) f[y] = a.scale * ex2(l2 * max(d, 0));
-                  f[y] *= __uint_as_float(s[x + y]);
-                  // the other triangle, and backwards columns behind the sequence
-                  if (d < 0 || (back && j0 + y >= rows)) f[y] = 0.f;
-                }
-                p[(e + x) / 2] = pack_bf16(f[0], f[1]);
-                p[(e + x) / 2 + 1] = pack_bf16(f[2], f[3]);
+              for (int y = 0; y < 2; ++y) {
+                const int d = lead + sign * (x + y);
+                f[y] = __uint_as_float(s[x + y]) * (a.scale * ex2(l2 * max(d, 0)));
+                if (d < 0 || x + y >= end) f[y] = 0.f;
               }
+              p[x / 2] = pack_bf16(f[0], f[1]);
+            }
+          } else {
+            // the exponent left once the table's part is taken
+            uint32_t s[32];
+            tmem_ld32_nowait(lane_base + C::COL_S + 32 * b, s);
+            const float base = a.scale * ex2(l2 * (back ? 32 * b - i : i - 32 * b - 31));
+            const uint64_t base2 = f2_pack(base, base);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(s_tab + x);
+              const uint64_t u = f2_pack(__uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+              const uint64_t v = f2_pack(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+              p[x / 2] = f2_to_bf16x2(f2_mul(u, f2_mul(base2, t.x)));
+              p[x / 2 + 1] = f2_to_bf16x2(f2_mul(v, f2_mul(base2, t.y)));
             }
           }
           tmem_st16p(lane_base + C::COL_S + 16 * b, p);
@@ -361,27 +369,53 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if (!ok || !mbar_wait(&bar_o, n & 1, ac)) break;
       tc_fence_after();
       const float u = back ? ex2(l2 * max(rows - 1 - i, 0)) : a.scale * ex2(l2 * (i + 1));
-      __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + row + i) * j.heads_x + h) * D;
+      // out takes the place of X, which the products have read, and leaves by a bulk copy (by
+      // plain stores where rows behind the sequence are another's): rows written from
+      // registers, 16 bytes of 32 rows at a time, took 2000 cycles
+      const int bx = n & (C::XBUF - 1);
+      uint8_t* so = sX + bx * C::TILE;
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t o1[32], o2[32];
         tmem_ld32_nowait(lane_base + C::COL_O1 + cc, o1);
         tmem_ld32_nowait(lane_base + C::COL_O2 + cc, o2);
         tmem_wait_ld();
-        if (i < rows)
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            uint32_t w[4];
+        for (int x = 0; x < 32; x += 8) {
+          uint32_t w[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = pack_bf16(fmaf(u, __uint_as_float(o2[x + 2 * y]), __uint_as_float(o1[x + 2 * y])),
-                               fmaf(u, __uint_as_float(o2[x + 2 * y + 1]), __uint_as_float(o1[x + 2 * y + 1])));
-            *reinterpret_cast<uint4*>(out + cc + x) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack_bf16(fmaf(u, __uint_as_float(o2[x + 2 * y]), __uint_as_float(o1[x + 2 * y])),
+                             fmaf(u, __uint_as_float(o2[x + 2 * y + 1]), __uint_as_float(o1[x + 2 * y + 1])));
+          *reinterpret_cast<uint4*>(so + sw128_offset(i, cc + x, kLinearChunk)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
       tc_fence_before();
       mbar_arrive(&bar_of);
+      if (rows == kLinearChunk) {
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (i == 0) {
+          for (int pn = 0; pn < PANELS; ++pn)
+            tma_store_3d(&j.mo, so + pn * kLinearChunk * 128, pn * 64, h, pl.row0 + row);
+          bulk_commit();
+          bulk_wait_read<0>();
+          mbar_arrive(&bar_xempty[bx]);
+        }
+      } else {
+        named_bar_sync(1, 128);
+        __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + row) * j.heads_x + h) * D;
+        for (int x = i; x < rows * (D / 8); x += 128) {
+          const int ro = x / (D / 8), co = x % (D / 8) * 8;
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ro) * j.heads_x * D + co) =
+              *reinterpret_cast<const uint4*>(so + sw128_offset(ro, co, kLinearChunk));
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (i == 0) mbar_arrive(&bar_xempty[bx]);
+      }
     }
+    if (i == 0) bulk_wait<0>();
   } else if (warp >= 8 && pl.n >= 0) {
     // ---------------- state ----------------
     const int tid = threadIdx.x - 256, half = tid >> 7, wq = warp & 3;
