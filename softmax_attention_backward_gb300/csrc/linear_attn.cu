@@ -10,8 +10,10 @@
 // A CTA walks the chunks of one (sequence, head, segment) and keeps H in the
 // registers of its state warps:
 //   warp 0        TMA producer: X, then Y and Z of each inner head, into a ring of tiles
-//   warp 1        MMA issuer: S = X Y^T, O2 = X H, O1 += P Z, G += (diag(d) Y)^T Z
-//   warps 4..7    scores: S to P = S o W as packed bf16 in TMEM, then out = O1 + u O2
+//   warp 1        MMA issuer: S = X Y^T, G += (diag(d) Y)^T Z, O = X H, O += P Z
+//   warp 3        bulk copies of the output
+//   warps 4..7    scores: S to P = S o W as packed bf16 in TMEM, and O to diag(u) O before P Z is
+//                 added to it
 //   warps 8..15   state: Y to diag(d) Y in place (bf16; the second and third terms in
 //                 tiles of their own), H = l^C H + G, H as bf16 to shared memory
 // S is scaled by products of two table values below and above the diagonal block
@@ -34,11 +36,14 @@ struct Cfg {
   static constexpr int FIT = (227 * 1024 - 2048 - H_BYTES - EXTRA) / TILE;
   // X has buffers of its own: a chunk's X outlives the tiles of its inner heads
   static constexpr int XBUF = kStates ? 0 : FIT >= 6 ? 2 : 1;
+  static constexpr int XMOD = XBUF ? XBUF : 1;
   static constexpr int NSLOT = (FIT > 8 ? 8 : FIT) - XBUF;
   static constexpr int SMEM = (XBUF + NSLOT) * TILE + H_BYTES + EXTRA + 1024;
   static constexpr int THREADS = 512;
   static constexpr int HC = D / 2;                // state columns of a thread
-  static constexpr uint32_t COL_S = 0, COL_O1 = 128, COL_O2 = 256, COL_G = 384;
+  // S of a step is formed while the step before is still at work, where the ring can hold both
+  static constexpr bool AHEAD = XBUF == 2;
+  static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
 };
 
@@ -118,6 +123,32 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
   return p;
 }
 
+// Bounded waits in few instructions: the kernel's roles have to share the instruction
+// caches (at 117 KB of code the walk ran at half its speed).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const AbortCtx& c) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t n = 0; n < (1u << 20); ++n) {
+    if (mbar_try_wait_hint(addr, parity, 20000u)) return true;
+    if (*reinterpret_cast<volatile int*>(c.smem_abort)) return false;
+  }
+  raise_error(c, ATTN_DEVERR_TIMEOUT);
+  return false;
+}
+// The same by polling, for the warp that issues the products, with a warp-uniform result.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const AbortCtx& c) {
+  const uint32_t addr = smem_u32(bar);
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t n = 0; n < (1u << 26) && !ok; ++n) {
+    ok = mbar_test_wait(addr, parity);
+    if (!ok && (n & 1023) == 1023 && *reinterpret_cast<volatile int*>(c.smem_abort)) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) raise_error(c, ATTN_DEVERR_TIMEOUT);
+  return ok;
+}
+
 template <int D, int NS, bool kStates>
 __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ LinearArgs a) {
   using C = Cfg<D, NS, kStates>;
@@ -131,11 +162,12 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
 
   __shared__ uint64_t bar_full[NSLOT], bar_empty[NSLOT];
   __shared__ uint64_t bar_xfull[2], bar_xempty[2];
-  __shared__ uint64_t bar_s, bar_p, bar_o, bar_of, bar_y, bar_g, bar_h;
+  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_qh, bar_o, bar_out, bar_of, bar_g, bar_gf, bar_h;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ Place s_place;
   __shared__ __align__(16) float s_tab[32];   // decays within a block of 32 columns
+  __shared__ float s_diag[64];                // those of its diagonal, scaled: entry 32 + j - i
 
   const int warp = warp_id();
   AbortCtx ac{&abort_flag, a.err};
@@ -161,12 +193,17 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       mbar_init(&bar_xfull[i], 1);
       mbar_init(&bar_xempty[i], 1);
     }
-    mbar_init(&bar_s, 1);
-    mbar_init(&bar_p, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_p[i], 128);
+      mbar_init(&bar_y[i], 256);
+    }
+    mbar_init(&bar_qh, 1);
     mbar_init(&bar_o, 1);
-    mbar_init(&bar_of, 128);
-    mbar_init(&bar_y, 256);
+    mbar_init(&bar_of, 256);
+    mbar_init(&bar_out, 256);
     mbar_init(&bar_g, 1);
+    mbar_init(&bar_gf, 256);
     mbar_init(&bar_h, 256);
     fence_mbar_init();
   }
@@ -176,7 +213,12 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     const Place p = find_place(a, j, slot);
     if (lane_id() == 0) s_place = p;
   }
-  if (warp == 3) s_tab[lane_id()] = ex2(l2 * (j.backwards ? lane_id() : 31 - lane_id()));
+  if (warp == 3) {
+    const int x = lane_id();
+    s_tab[x] = ex2(l2 * (j.backwards ? x : 31 - x));
+    s_diag[x] = j.backwards ? 0.f : a.scale * ex2(l2 * (32 - x));
+    s_diag[32 + x] = j.backwards || x == 0 ? a.scale * ex2(l2 * x) : 0.f;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -195,6 +237,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   auto chunk_len = [&](int n) { return min(kLinearChunk, pl.len - chunk_row(n)); };
   const bool want_last = kStates || (is_end && j.last && h == hkv * static_cast<int>(j.fd_kv.d));
   const int n_grow = want_last ? n_walk : n_walk - 1;   // chunks that the state takes in
+  const int steps = n_walk * inner;                     // a step: one inner head of a chunk
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -205,7 +248,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       int it = 0;
       bool ok = true;
       auto load = [&](const CUtensorMap* m, uint64_t* full, uint64_t* empty, uint8_t* dst, int use, int head, int row) {
-        if (use > 0 && !mbar_wait_spin(empty, (use & 1) ^ 1, ac)) {
+        if (use > 0 && !wait(empty, (use & 1) ^ 1, ac)) {
           ok = false;
           return;
         }
@@ -221,7 +264,12 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
         for (int t = 0; ok && t < 2 * inner; ++t, ++it) {
           const int s = it % NSLOT;
+
           load(t & 1 ? &j.mz : &j.my, &bar_full[s], &bar_empty[s], ring + s * C::TILE, it / NSLOT, hy + (t >> 1), row);
+          // the next chunk's last Z comes to L2 before its tile, which this chunk's output holds longest
+          if (!kStates && t == 2 * inner - 1 && n + 1 < n_walk)
+            for (int pn = 0; pn < PANELS; ++pn)
+              tma_prefetch_3d(&j.mz, pn * 64, hy + (t >> 1), pl.row0 + chunk_row(n + 1));
         }
       }
     }
@@ -235,108 +283,138 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     const uint64_t dm0 = desc_mnmajor_base(smem_u32(ring), kLinearChunk);
     const uint64_t dH = desc_mnmajor_base(smem_u32(sH), D);
     const uint64_t dE = desc_mnmajor_base(smem_u32(sExtra), kLinearChunk);
-    int tile = 0, it = 0;
-    bool ok = true;
-    for (int n = 0; ok && n < n_walk; ++n) {
-      int bx = 0;
-      if constexpr (!kStates) {
-        bx = n % C::XBUF;
-        if (!mbar_wait_w(&bar_xfull[bx], (n / C::XBUF) & 1, ac)) break;
-      }
-      for (int g = 0; ok && g < inner; ++g, ++it) {
-        const int sy = tile % NSLOT, uy = (tile / NSLOT) & 1;
-        const int sz = (tile + 1) % NSLOT, uz = ((tile + 1) / NSLOT) & 1;
-        tile += 2;
-        const bool last = g == inner - 1;
-        const uint64_t dz = desc_advance(dm0, sz * C::TILE);
-        if (!mbar_wait_w(&bar_full[sy], uy, ac)) { ok = false; break; }
-        if (!kStates) {
-          tc_fence_after();
-          const uint64_t dx = desc_advance(dx0, bx * C::TILE), dy = desc_advance(dk0, sy * C::TILE);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            umma_ss_w(tmem + C::COL_S, desc_advance(dx, kmajor_step_bytes(128, k)),
-                      desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
-          umma_commit_w(&bar_s);
-          if (g == 0) {
-            if (!mbar_wait_w(&bar_h, n & 1, ac) || (n > 0 && !mbar_wait_w(&bar_of, (n - 1) & 1, ac))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              umma_ss_w(tmem + C::COL_O2, desc_advance(dx, kmajor_step_bytes(128, k)),
-                        desc_advance(dH, mnmajor_step_bytes(k)), idO, k > 0);
-          }
-        }
-        if (!mbar_wait_w(&bar_full[sz], uz, ac)) { ok = false; break; }
-        if (!kStates) {
-          if (!mbar_wait_w(&bar_p, it & 1, ac)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
+    auto slot = [](int tile) { return tile % NSLOT; };
+    auto landed = [&](int tile) { return warp_wait(&bar_full[slot(tile)], (tile / NSLOT) & 1, ac); };
+    // S of step t, the g-th of chunk n
+    auto scores = [&](int t, int n, int g) -> bool {
+      const int bx = n % C::XMOD;
+      if (g == 0 && !warp_wait(&bar_xfull[bx], (n / C::XMOD) & 1, ac)) return false;
+      if (!landed(2 * t)) return false;
+      tc_fence_after();
+      const uint64_t dx = desc_advance(dx0, bx * C::TILE), dy = desc_advance(dk0, slot(2 * t) * C::TILE);
+#pragma unroll 2
+      for (int k = 0; k < D / 16; ++k)
+        umma_ss_w(tmem + C::COL_S + 128 * (t & 1), desc_advance(dx, kmajor_step_bytes(128, k)),
+                  desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
+      umma_commit_w(&bar_s[t & 1]);
+      return true;
+    };
+    // what the state takes in
+    auto keys = [&](int t, int n, int g) -> bool {
+      if (!landed(2 * t + 1) || (kStates && !landed(2 * t))) return false;
+      if (n < n_grow) {
+        if (!warp_wait(&bar_y[t & 1], (t >> 1) & 1, ac)) return false;
+        if (g == 0 && n > 0 && !warp_wait(&bar_gf, (n - 1) & 1, ac)) return false;
+        tc_fence_after();
+        const uint64_t dy = desc_advance(dm0, slot(2 * t) * C::TILE), dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
+#pragma unroll 1
+        for (int e = 0; e < NS; ++e)
+#pragma unroll 2
           for (int k = 0; k < 8; ++k)
-            umma_ts_w(tmem + C::COL_O1, tmem + C::COL_S + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)), idO,
-                      (g > 0 || k > 0) ? 1u : 0u);
-          if (last) umma_commit_w(&bar_o);
-        }
-        if (n < n_grow) {
-          if (!mbar_wait_w(&bar_y, it & 1, ac)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dy = desc_advance(dm0, sy * C::TILE);
-#pragma unroll
-          for (int t = 0; t < NS; ++t)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ss_w(tmem + C::COL_G,
-                        desc_advance(t == 0 ? dy : desc_advance(dE, (t - 1) * C::TILE), mnmajor_step_bytes(k)),
-                        desc_advance(dz, mnmajor_step_bytes(k)), idG, (g > 0 || t > 0 || k > 0) ? 1u : 0u);
-        }
-        umma_commit_w(&bar_empty[sy]);
-        umma_commit_w(&bar_empty[sz]);
-        if (n < n_grow && last) umma_commit_w(&bar_g);
+            umma_ss_w(tmem + C::COL_G,
+                      desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
+                      desc_advance(dz, mnmajor_step_bytes(k)), idG, (g > 0 || e > 0 || k > 0) ? 1u : 0u);
       }
+      umma_commit_w(&bar_empty[slot(2 * t)]);
+      if (n < n_grow && g == inner - 1) umma_commit_w(&bar_g);
+      return true;
+    };
+    // X H, at a chunk's first step; behind the S of its last step, X is free
+    auto carried = [&](int n, int g) -> bool {
+      const int bx = n % C::XMOD;
+      if (g == 0) {
+        if (!warp_wait(&bar_h, n & 1, ac) || (n > 0 && !warp_wait(&bar_of, (n - 1) & 1, ac))) return false;
+        tc_fence_after();
+        const uint64_t dx = desc_advance(dx0, bx * C::TILE);
+#pragma unroll 2
+        for (int k = 0; k < D / 16; ++k)
+          umma_ss_w(tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k)),
+                    desc_advance(dH, mnmajor_step_bytes(k)), idO, k > 0);
+        umma_commit_w(&bar_qh);
+      }
+      if (g == inner - 1) umma_commit_w(&bar_xempty[bx]);
+      return true;
+    };
+    auto values = [&](int t, int g) -> bool {
+      if (!warp_wait(&bar_p[t & 1], (t >> 1) & 1, ac)) return false;
+      tc_fence_after();
+      const uint64_t dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
+#pragma unroll 2
+      for (int k = 0; k < 8; ++k)
+        umma_ts_w(tmem + C::COL_O, tmem + C::COL_S + 128 * (t & 1) + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)),
+                  idO, 1u);
+      if (g == inner - 1) umma_commit_w(&bar_o);
+      return true;
+    };
+    // AHEAD, S(t + 1) runs while the score warps scale X H of t, and they form P(t + 1) while the
+    // others' products run
+    int n = 0, g = 0;
+    if (C::AHEAD && (steps == 0 || !scores(0, 0, 0))) n = n_walk;
+    for (int t = 0; n < n_walk; ++t) {
+      const bool last = g == inner - 1;
+      if constexpr (kStates) {
+        if (!keys(t, n, g)) break;
+      } else if constexpr (C::AHEAD) {
+        if (!keys(t, n, g) || !carried(n, g)) break;
+        if (t + 1 < steps && !scores(t + 1, n + last, last ? 0 : g + 1)) break;
+        if (!values(t, g)) break;
+      } else {
+        if (!scores(t, n, g) || !carried(n, g) || !keys(t, n, g) || !values(t, g)) break;
+      }
+      // a chunk's last Z makes room for its output
+      if (kStates || !last) umma_commit_w(&bar_empty[slot(2 * t + 1)]);
+      n += last;
+      g = last ? 0 : g + 1;
+    }
+  } else if (!kStates && warp == 3) {
+    // ---------------- stores ----------------
+    // whole chunks leave by a bulk copy; behind it, or the state warps' own stores, the tile of the
+    // chunk's last Z, in which they lay, is free
+    if (lane_id() == 0) {
+      for (int n = 0; n < n_walk; ++n) {
+        const int b = (2 * (n + 1) * inner - 1) % NSLOT;
+        if (!wait(&bar_out, n & 1, ac)) break;
+        if (chunk_len(n) == kLinearChunk) {
+          for (int pn = 0; pn < PANELS; ++pn)
+            tma_store_3d(&j.mo, ring + b * C::TILE + pn * kLinearChunk * 128, pn * 64, h, pl.row0 + chunk_row(n));
+          bulk_commit();
+          bulk_wait_read<0>();
+        }
+        mbar_arrive(&bar_empty[b]);
+      }
+      bulk_wait<0>();
     }
   } else if (!kStates && warp >= 4 && warp < 8) {
-    // ---------------- scores and output ----------------
+    // ---------------- scores ----------------
     const int wq = warp & 3, i = threadIdx.x & 127;   // row of the chunk, TMEM lane
+    const int lane = lane_id();
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    int tile = 0, it = 0;
-    bool ok = true;
-    for (int n = 0; ok && n < n_walk; ++n) {
-      const int rows = chunk_len(n), row = chunk_row(n);
-      for (int g = 0; ok && g < inner; ++g, ++it, tile += 2) {
-        if (!mbar_wait(&bar_s, it & 1, ac)) { ok = false; break; }
-        tc_fence_after();
+    // step t's scores, of a chunk with `rows` rows, to P
+    auto convert = [&](int t, int rows) -> bool {
+      if (!wait(&bar_s[t & 1], (t >> 1) & 1, ac)) return false;
+      tc_fence_after();
+      const uint32_t tS = lane_base + C::COL_S + 128 * (t & 1);
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          uint32_t p[16];
-          if (back ? b < wq : b > wq) {
+      for (int b = 0; b < 4; ++b) {
+        uint32_t p[16];
+        if (back ? b < wq : b > wq) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) p[x] = 0;
-          } else if (b == wq || (back && rows < kLinearChunk)) {
-            // the diagonal block, and backwards columns behind the sequence: an exponential and a
-            // comparison for each element
-            uint32_t s[32];
-            tmem_ld32_nowait(lane_base + C::COL_S + 32 * b, s);
+          for (int x = 0; x < 16; ++x) p[x] = 0;
+        } else {
+          uint32_t s[32];
+          tmem_ld32_nowait(tS + 32 * b, s);
+          if (b == wq) {
+            const float* diag = s_diag + 32 - lane;
             tmem_wait_ld();
-            const int lead = back ? 32 * b - i : i - 32 * b, sign = back ? 1 : -1;
-            const int end = back ? rows - 32 * b : 32;
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              float f[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int d = lead + sign * (x + y);
-                f[y] = __uint_as_float(s[x + y]) * (a.scale * ex2(l2 * max(d, 0)));
-                if (d < 0 || x + y >= end) f[y] = 0.f;
-              }
-              p[x / 2] = pack_bf16(f[0], f[1]);
+              // (selects: a masked score may be infinite or NaN)
+              const float f0 = diag[x], f1 = diag[x + 1];
+              const float u = __uint_as_float(s[x]) * f0, v = __uint_as_float(s[x + 1]) * f1;
+              p[x / 2] = pack_bf16(f0 != 0.f ? u : 0.f, f1 != 0.f ? v : 0.f);
             }
           } else {
             // the exponent left once the table's part is taken
-            uint32_t s[32];
-            tmem_ld32_nowait(lane_base + C::COL_S + 32 * b, s);
             const float base = a.scale * ex2(l2 * (back ? 32 * b - i : i - 32 * b - 31));
             const uint64_t base2 = f2_pack(base, base);
             tmem_wait_ld();
@@ -349,12 +427,28 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
               p[x / 2 + 1] = f2_to_bf16x2(f2_mul(v, f2_mul(base2, t.y)));
             }
           }
-          tmem_st16p(lane_base + C::COL_S + 16 * b, p);
+          if (back && rows < 32 * b + 32) {   // columns behind the sequence
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              p[x] &= 32 * b + 2 * x + 1 < rows ? 0xffffffffu : 32 * b + 2 * x < rows ? 0xffffu : 0u;
+          }
         }
-        if (rows < kLinearChunk) {
-          // rows of Z behind the sequence may hold anything: zeros, for 0 * NaN
-          const int sz = (tile + 1) % NSLOT;
-          if (!mbar_wait(&bar_full[sz], ((tile + 1) / NSLOT) & 1, ac)) { ok = false; break; }
+        tmem_st16p(tS + 16 * b, p);
+      }
+      return true;
+    };
+    int n = 0, g = 0;
+    bool last = false;
+    for (int t = C::AHEAD ? -1 : 0; t < steps; ++t) {   // step -1: the first scores alone
+      const int rows = chunk_len(n);
+      if (!C::AHEAD && !convert(t, rows)) break;
+      if (t >= 0) {
+        last = g == inner - 1;
+        if (rows < kLinearChunk && n >= n_grow) {
+          // rows of Z behind the sequence may hold anything: zeros, for 0 * NaN (the state warps
+          // see to it where the state takes them in)
+          const int sz = (2 * t + 1) % NSLOT;
+          if (!wait(&bar_full[sz], ((2 * t + 1) / NSLOT) & 1, ac)) break;
           if (i >= rows) {
             uint4* z = reinterpret_cast<uint4*>(ring + sz * C::TILE + i * 128);
 #pragma unroll
@@ -362,62 +456,39 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
           }
           fence_proxy_async_smem();
         }
+        if (g == 0) {
+          // X H of the chunk, times u: what P Z adds to
+          if (!wait(&bar_qh, n & 1, ac)) break;
+          tc_fence_after();
+          const float u = back ? ex2(l2 * max(rows - 1 - i, 0)) : a.scale * ex2(l2 * (i + 1));
+          const uint64_t u2 = f2_pack(u, u);
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32_nowait(lane_base + C::COL_O + cc, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float lo, hi;
+              f2_unpack(f2_mul(u2, f2_pack(__uint_as_float(o[x]), __uint_as_float(o[x + 1]))), lo, hi);
+              o[x] = __float_as_uint(lo);
+              o[x + 1] = __float_as_uint(hi);
+            }
+            tmem_st32(lane_base + C::COL_O + cc, o);
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar_p);
+        mbar_arrive(&bar_p[t & 1]);
       }
-      if (!ok || !mbar_wait(&bar_o, n & 1, ac)) break;
-      tc_fence_after();
-      const float u = back ? ex2(l2 * max(rows - 1 - i, 0)) : a.scale * ex2(l2 * (i + 1));
-      // out takes the place of X, which the products have read, and leaves by a bulk copy (by
-      // plain stores where rows behind the sequence are another's): rows written from
-      // registers, 16 bytes of 32 rows at a time, took 2000 cycles
-      const int bx = n & (C::XBUF - 1);
-      uint8_t* so = sX + bx * C::TILE;
-#pragma unroll
-      for (int cc = 0; cc < D; cc += 32) {
-        uint32_t o1[32], o2[32];
-        tmem_ld32_nowait(lane_base + C::COL_O1 + cc, o1);
-        tmem_ld32_nowait(lane_base + C::COL_O2 + cc, o2);
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            w[y] = pack_bf16(fmaf(u, __uint_as_float(o2[x + 2 * y]), __uint_as_float(o1[x + 2 * y])),
-                             fmaf(u, __uint_as_float(o2[x + 2 * y + 1]), __uint_as_float(o1[x + 2 * y + 1])));
-          *reinterpret_cast<uint4*>(so + sw128_offset(i, cc + x, kLinearChunk)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(&bar_of);
-      if (rows == kLinearChunk) {
-        fence_proxy_async_smem();
-        named_bar_sync(1, 128);
-        if (i == 0) {
-          for (int pn = 0; pn < PANELS; ++pn)
-            tma_store_3d(&j.mo, so + pn * kLinearChunk * 128, pn * 64, h, pl.row0 + row);
-          bulk_commit();
-          bulk_wait_read<0>();
-          mbar_arrive(&bar_xempty[bx]);
-        }
-      } else {
-        named_bar_sync(1, 128);
-        __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + row) * j.heads_x + h) * D;
-        for (int x = i; x < rows * (D / 8); x += 128) {
-          const int ro = x / (D / 8), co = x % (D / 8) * 8;
-          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ro) * j.heads_x * D + co) =
-              *reinterpret_cast<const uint4*>(so + sw128_offset(ro, co, kLinearChunk));
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(1, 128);
-        if (i == 0) mbar_arrive(&bar_xempty[bx]);
+      if (C::AHEAD && t + 1 < steps && !convert(t + 1, chunk_len(last ? n + 1 : n))) break;
+      if (t >= 0) {
+        n += last;
+        g = last ? 0 : g + 1;
       }
     }
-    if (i == 0) bulk_wait<0>();
   } else if (warp >= 8 && pl.n >= 0) {
-    // ---------------- state ----------------
+    // ---------------- output and state ----------------
     const int tid = threadIdx.x - 256, half = tid >> 7, wq = warp & 3;
     // M = 64 results lie in the first 16 lanes of each warp's 32
     const bool mine = D == 128 || (lane_id() < 16);
@@ -430,9 +501,10 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     if (!kStates) {
       // the state before the segment: the first one, then what each segment on the way adds
       if (j.first && mine) {
+        const int sr = j.transposed ? 1 : D, sc = j.transposed ? D : 1;
         const float* f = j.first + (static_cast<int64_t>(pl.n) * a.heads_kv + hkv) * D * D;
 #pragma unroll
-        for (int x = 0; x < C::HC; ++x) H[x] = __ldg(j.transposed ? f + (c0 + x) * D + r : f + r * D + c0 + x);
+        for (int x = 0; x < C::HC; ++x) H[x] = __ldg(f + r * sr + (c0 + x) * sc);
       }
       const int before = back ? pl.nseg - 1 - pl.seg : pl.seg;
       for (int t = 0; t < before; ++t) {
@@ -464,26 +536,85 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       mbar_arrive(&bar_h);
     };
     if (!kStates && n_walk > 0) publish();
-    int tile = 0, it = 0;
-    bool ok = true;
-    const int row = tid & 127;
-    for (int n = 0; ok && n < n_grow; ++n) {
+    // what chunk n adds, and then the state as the next chunk's operand
+    auto grow = [&](int n) -> bool {
+      if (!wait(&bar_g, n & 1, ac)) return false;
+      tc_fence_after();
+      const float keep = ex2(l2 * chunk_len(n));
+#pragma unroll
+      for (int x = 0; x < C::HC; x += 32) {
+        uint32_t v[32];
+        tmem_ld32_nowait(tG + x, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) H[x + y] = fmaf(keep, H[x + y], __uint_as_float(v[y]));
+      }
+      tc_fence_before();
+      mbar_arrive(&bar_gf);
+      if (kStates || n + 1 >= n_walk) return true;
+      if (!wait(&bar_qh, n & 1, ac)) return false;   // the product that read the state before
+      publish();
+      return true;
+    };
+    const int row = tid & 127;   // row of the chunk: of Y, and TMEM lane of the outputs
+    // chunk n's rows, in place of its last Z, which the products have read: rows written from
+    // registers, 16 bytes of 32 rows at a time, took 2000 cycles
+    auto output = [&](int n) -> bool {
+      if (!wait(&bar_o, n & 1, ac)) return false;
+      tc_fence_after();
       const int rows = chunk_len(n);
-      const float d = back ? a.scale * ex2(l2 * (row + 1)) : ex2(l2 * max(rows - 1 - row, 0));
-      for (int g = 0; ok && g < inner; ++g, ++it, tile += 2) {
-        const int sy = tile % NSLOT;
-        if (!mbar_wait(&bar_full[sy], (tile / NSLOT) & 1, ac) || (!kStates && !mbar_wait(&bar_s, it & 1, ac))) {
-          ok = false;
-          break;
+      const uint32_t tO = tmem + (static_cast<uint32_t>(wq * 32) << 16) + c0;
+      uint8_t* so = ring + (2 * (n + 1) * inner - 1) % NSLOT * C::TILE;
+#pragma unroll 1
+      for (int cc = 0; cc < C::HC; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(tO + C::COL_O + cc, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack_bf16(__uint_as_float(o[x + 2 * y]), __uint_as_float(o[x + 2 * y + 1]));
+          *reinterpret_cast<uint4*>(so + sw128_offset(row, c0 + cc + x, kLinearChunk)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
-        // the other terms' tiles: read by the products of the step before
-        if (NS > 1 && g > 0 && !mbar_wait(&bar_empty[(tile - 2) % NSLOT], ((tile - 2) / NSLOT) & 1, ac)) {
-          ok = false;
-          break;
+      }
+      tc_fence_before();
+      mbar_arrive(&bar_of);
+      if (rows < kLinearChunk) {   // rows behind the sequence are another's: plain stores
+        named_bar_sync(1, 256);
+        __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + chunk_row(n)) * j.heads_x + h) * D;
+        for (int x = tid; x < rows * (D / 8); x += 256) {
+          const int ro = x / (D / 8), co = x % (D / 8) * 8;
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ro) * j.heads_x * D + co) =
+              *reinterpret_cast<const uint4*>(so + sw128_offset(ro, co, kLinearChunk));
         }
-        if (kStates && rows < kLinearChunk) {
-          const int sz = (tile + 1) % NSLOT;
-          if (!mbar_wait(&bar_full[sz], ((tile + 1) / NSLOT) & 1, ac)) { ok = false; break; }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bar_out);
+      return true;
+    };
+    int n = 0, g = 0;
+    for (int t = 0; t <= steps; ++t) {
+      const bool next = g == 0 && n > 0;   // a chunk is behind these warps
+      if (next && n - 1 < n_grow && !grow(n - 1)) break;
+      if (!kStates && !C::AHEAD && next && !output(n - 1)) break;
+      if (t < steps && n < n_grow) {
+        const int rows = chunk_len(n);
+        const float d = back ? a.scale * ex2(l2 * (row + 1)) : ex2(l2 * max(rows - 1 - row, 0));
+        const int sy = 2 * t % NSLOT;
+        if (!wait(&bar_full[sy], (2 * t / NSLOT) & 1, ac)) break;
+        if (!kStates && !wait(&bar_s[t & 1], (t >> 1) & 1, ac)) break;
+        // the other terms' tiles: read by the products of the step before.  Where no scores hold
+        // these warps back, they stay within what two barriers can tell apart.
+        const int behind = NS > 1 ? t - 1 : t - 2;
+        if ((NS > 1 || kStates) && behind >= 0 &&
+            !wait(&bar_empty[2 * behind % NSLOT], (2 * behind / NSLOT) & 1, ac))
+          break;
+        if (rows < kLinearChunk) {
+          const int sz = (2 * t + 1) % NSLOT;
+          if (!wait(&bar_full[sz], ((2 * t + 1) / NSLOT) & 1, ac)) break;
           if (row >= rows && half < PANELS) {
             uint4* z = reinterpret_cast<uint4*>(ring + sz * C::TILE + half * (kLinearChunk * 128) + row * 128);
 #pragma unroll
@@ -491,45 +622,46 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
           }
         }
         uint8_t* y = ring + sy * C::TILE;
+        constexpr int kBatch = 4;   // pieces of 16 bytes loaded before the first is stored
+#pragma unroll 1
+        for (int x0 = 0; x0 < C::HC; x0 += 8 * kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int x = 0; x < C::HC; x += 8) {
-          const uint32_t at = sw128_offset(row, c0 + x, kLinearChunk);
-          uint4 v = *reinterpret_cast<const uint4*>(y + at);
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t term[NS][4];
+          for (int x = 0; x < kBatch; ++x)
+            v[x] = *reinterpret_cast<const uint4*>(y + sw128_offset(row, c0 + x0 + 8 * x, kLinearChunk));
+          if (rows < kLinearChunk && row >= rows)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float lo = __uint_as_float(w[e] << 16) * d, hi = __uint_as_float(w[e] & 0xffff0000u) * d;
-            if (row >= rows) lo = hi = 0.f;
+            for (int x = 0; x < kBatch; ++x) v[x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int t = 0; t < NS; ++t) {
-              term[t][e] = pack_bf16(lo, hi);
-              lo -= __uint_as_float(term[t][e] << 16);
-              hi -= __uint_as_float(term[t][e] & 0xffff0000u);
+          for (int x = 0; x < kBatch; ++x) {
+            const uint32_t at = sw128_offset(row, c0 + x0 + 8 * x, kLinearChunk);
+            const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+            uint32_t term[NS][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo = __uint_as_float(w[e] << 16) * d, hi = __uint_as_float(w[e] & 0xffff0000u) * d;
+#pragma unroll
+              for (int q = 0; q < NS; ++q) {
+                term[q][e] = pack_bf16(lo, hi);
+                lo -= __uint_as_float(term[q][e] << 16);
+                hi -= __uint_as_float(term[q][e] & 0xffff0000u);
+              }
             }
-          }
-          *reinterpret_cast<uint4*>(y + at) = make_uint4(term[0][0], term[0][1], term[0][2], term[0][3]);
+            *reinterpret_cast<uint4*>(y + at) = make_uint4(term[0][0], term[0][1], term[0][2], term[0][3]);
 #pragma unroll
-          for (int t = 1; t < NS; ++t)
-            *reinterpret_cast<uint4*>(sExtra + (t - 1) * C::TILE + at) =
-                make_uint4(term[t][0], term[t][1], term[t][2], term[t][3]);
+            for (int q = 1; q < NS; ++q)
+              *reinterpret_cast<uint4*>(sExtra + (q - 1) * C::TILE + at) =
+                  make_uint4(term[q][0], term[q][1], term[q][2], term[q][3]);
+          }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bar_y);
+        mbar_arrive(&bar_y[t & 1]);
       }
-      if (!ok || !mbar_wait(&bar_g, n & 1, ac)) break;
-      tc_fence_after();
-      const float keep = ex2(l2 * rows);
-#pragma unroll
-      for (int x = 0; x < C::HC; x += 32) {
-        uint32_t g[32];
-        tmem_ld32_nowait(tG + x, g);
-        tmem_wait_ld();
-#pragma unroll
-        for (int y = 0; y < 32; ++y) H[x + y] = fmaf(keep, H[x + y], __uint_as_float(g[y]));
+      if (!kStates && C::AHEAD && next && !output(n - 1)) break;
+      if (++g == inner) {
+        g = 0;
+        ++n;
       }
-      tc_fence_before();
-      if (!kStates && n + 1 < n_walk) publish();
     }
     if (kStates) {
       const int64_t at = (static_cast<int64_t>(slot) * a.heads_kv + hkv) * D * D;
