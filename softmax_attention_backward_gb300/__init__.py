@@ -19,7 +19,6 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -983,20 +982,25 @@ def attn_rotary_table(max_position, rot_dim, *, base=10000.0, scaling="none", fa
     p = _RotaryTable(int(max_position), int(rot_dim), float(base), _ROTARY_SCALINGS[scaling],
                      float(factor), int(original), float(fast), float(slow), float(magnitude))
     ctx, s = _on(dev, stream)
-    with ctx or contextlib.nullcontext():
-        if out is None:
-            out = torch.empty(max(0, p.max_position), max(0, p.rot_dim), dtype=torch.float32, device=dev)
-        _check("attn_rotary_table", (_LIB or lib()).attn_rotary_table(ctypes.byref(p), out.data_ptr(), s))
+    if ctx is None:
+        return _table_here(p, out, dev, s)
+    with ctx:
+        return _table_here(p, out, dev, s)
+
+
+def _table_here(p, out, dev, s):
+    if out is None:
+        out = torch.empty((max(0, p.max_position), max(0, p.rot_dim)), dtype=torch.float32, device=dev)
+    code = (_LIB or lib()).attn_rotary_table(ctypes.byref(p), out.data_ptr(), s)
+    if code:
+        raise AttnError("attn_rotary_table", code)
     return out
 
 
-def _token_rows(t, name, lead, heads, dim, gpu, device):
+def _token_rows(t, name, lead, heads, dim, device):
     """bf16 [*lead, heads, dim] (lead one or two dims) whose tokens may lie apart,
     equally far (a slice of a fused projection); returns the elements between two
     tokens, 0 for dense ones."""
-    if (t.dtype is torch.bfloat16 and t.get_device() == gpu and t.shape == (*lead, heads, dim)
-            and t.is_contiguous()):
-        return 0
     if t.shape != (*lead, heads, dim):
         raise ValueError(f"{name} must be {[*lead, heads, dim]}, got {list(t.shape)}")
     if len(lead) == 1:
@@ -1010,6 +1014,13 @@ def _token_rows(t, name, lead, heads, dim, gpu, device):
                                    t.storage_offset()), name, heads, dim, device)
 
 
+# As for the cache, a call on few tokens takes the GPU a few microseconds: the
+# checks below look at each tensor once and leave the wording to the functions
+# above.
+def _ok(t, dtype, gpu):
+    return t.dtype is dtype and t.get_device() == gpu and t.is_contiguous()
+
+
 def _gpu_of(t, name):
     """The device of a tensor that decides a call's, and its index."""
     gpu = t.get_device()
@@ -1018,63 +1029,101 @@ def _gpu_of(t, name):
     return gpu, t.device
 
 
-def _lead(q, cu_seqlens, device):
+def _lead(shape, cu_seqlens, gpu, device):
     """The leading dims of a dense [batch, seqlen, heads, dim] or packed [tokens,
-    heads, dim] tensor, with the sequences, their length and cu_seqlens' address."""
+    heads, dim] tensor: tokens, sequences, their length and cu_seqlens' address."""
     if cu_seqlens is None:
-        if q.dim() != 4:
+        if len(shape) != 4:
             raise ValueError("dense q must be [batch, seqlen, heads, head_dim]")
-        n, length = q.shape[:2]
-        return (n, length), n, length, None
-    if q.dim() != 3:
+        n, length = shape[0], shape[1]
+        return n * length, n, length, None
+    if len(shape) != 3:
         raise ValueError("THD q must be [tokens, heads, head_dim]")
-    if _need(cu_seqlens, "cu_seqlens", torch.int32, device).dim() != 1 or cu_seqlens.numel() < 2:
+    if not _ok(cu_seqlens, torch.int32, gpu):
+        _need(cu_seqlens, "cu_seqlens", torch.int32, device)
+    n = cu_seqlens.numel() - 1
+    if cu_seqlens.dim() != 1 or n < 1:
         raise ValueError("cu_seqlens must be [num_seqs + 1]")
-    return (q.shape[0],), cu_seqlens.numel() - 1, 0, cu_seqlens.data_ptr()
+    return shape[0], n, 0, cu_seqlens.data_ptr()
 
 
-def _rotary(name, q, k, cos_sin, positions, cu_seqlens, interleaved, rot_offset, q_out,
-            k_out, error_word, stream):
+def _word(error_word, gpu, device):
+    if error_word is None:
+        return None
+    if not _ok(error_word, torch.int32, gpu):
+        _need(error_word, "error_word", torch.int32, device)
+    return error_word.data_ptr()
+
+
+def _out_like(t, name, like, gpu, device):
+    """A given bf16 output, dense with the shape of `like`."""
+    if not _ok(t, torch.bfloat16, gpu):
+        _need(t, name, torch.bfloat16, device)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+
+
+def _rotary(name, q, k, cos_sin, positions, cu_seqlens, interleaved, rot_offset, q_out, k_out,
+            error_word, stream):
+    bf16 = torch.bfloat16
     gpu, dev = _gpu_of(q, "q")
-    if positions is not None:
+    shape = q.shape
+    lead = shape[:-2]
+    if positions is None:
+        tokens, n, length, cu = _lead(shape, cu_seqlens, gpu, dev)
+        at = None
+    else:
         if cu_seqlens is not None:
             raise ValueError("positions and cu_seqlens exclude each other")
-        if q.dim() not in (3, 4):
+        if len(shape) not in (3, 4):
             raise ValueError("q must be [tokens, heads, head_dim] or [batch, seqlen, heads, head_dim]")
-        lead, n, length, cu = tuple(q.shape[:-2]), 0, 0, None
-        if _need(positions, "positions", torch.int32, dev).shape != lead:
+        if not _ok(positions, torch.int32, gpu):
+            _need(positions, "positions", torch.int32, dev)
+        if positions.shape != lead:
             raise ValueError(f"positions must be {list(lead)}, got {list(positions.shape)}")
-    else:
-        lead, n, length, cu = _lead(q, cu_seqlens, dev)
-    heads, dim = q.shape[-2:]
-    heads_k = 0
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out is given without k")
-    else:
-        if k.dim() != q.dim():
+        tokens, n, length, cu, at = positions.numel(), 0, 0, None, positions.data_ptr()
+    heads, dim = shape[-2], shape[-1]
+    q_stride = 0 if _ok(q, bf16, gpu) else _token_rows(q, "q", lead, heads, dim, dev)
+    heads_k = k_stride = 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != len(shape):
             raise ValueError("q and k must have the same leading dims")
-        heads_k = k.shape[-2]
-    if _need(cos_sin, "cos_sin", torch.float32, dev).dim() != 2:
+        heads_k = kshape[-2]
+        if kshape[:-2] != lead or kshape[-1] != dim or not _ok(k, bf16, gpu):
+            k_stride = _token_rows(k, "k", lead, heads_k, dim, dev)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    if not _ok(cos_sin, torch.float32, gpu):
+        _need(cos_sin, "cos_sin", torch.float32, dev)
+    if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [positions, rot_dim]")
-    if error_word is not None:
-        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
-    p = _RotaryProblem(math.prod(lead), heads, heads_k, dim, cos_sin.shape[1], int(rot_offset),
-                       1 if interleaved else 0, cos_sin.shape[0], length, n,
-                       _token_rows(q, "q", lead, heads, dim, gpu, dev),
-                       0 if k is None else _token_rows(k, "k", lead, heads_k, dim, gpu, dev), cu,
-                       _at(positions), error_word)
-    for t, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if o is not None and _need(o, what, torch.bfloat16, dev).shape != t.shape:
-            raise ValueError(f"{what} must have the shape of {what[0]}")
+    if q_out is not None:
+        _out_like(q_out, "q_out", q, gpu, dev)
+    if k_out is not None:
+        _out_like(k_out, "k_out", k, gpu, dev)
+    rows, rot = cos_sin.shape
+    p = _RotaryProblem(tokens, heads, heads_k, dim, rot, int(rot_offset), 1 if interleaved else 0,
+                       rows, length, n, q_stride, k_stride, cu, at, _word(error_word, gpu, dev))
     ctx, s = _on(dev, stream)
-    with ctx or contextlib.nullcontext():
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        if k is not None and k_out is None:
-            k_out = k.new_empty(k.shape)
-        code = getattr(_LIB or lib(), name)(ctypes.byref(p), q.data_ptr(), _at(k), cos_sin.data_ptr(),
-                                            q_out.data_ptr(), _at(k_out), s)
+    if ctx is None:
+        return _rotary_here(name, p, q, k, cos_sin, q_out, k_out, s)
+    with ctx:
+        return _rotary_here(name, p, q, k, cos_sin, q_out, k_out, s)
+
+
+def _new_like(t, stride):
+    """A dense tensor like t, whose tokens may lie apart."""
+    return torch.empty_like(t) if stride == 0 else t.new_empty(t.shape)
+
+
+def _rotary_here(name, p, q, k, cos_sin, q_out, k_out, s):
+    if q_out is None:
+        q_out = _new_like(q, p.q_stride)
+    if k is not None and k_out is None:
+        k_out = _new_like(k, p.k_stride)
+    code = getattr(_LIB or lib(), name)(ctypes.byref(p), q.data_ptr(), _at(k), cos_sin.data_ptr(),
+                                        q_out.data_ptr(), _at(k_out), s)
     if code:
         raise AttnError(name, code)
     return q_out, k_out
@@ -1102,47 +1151,62 @@ def attn_rotary_bwd(dq, dk, cos_sin, *, positions=None, cu_seqlens=None, interle
 # ----------------------------------------------------------------------------
 # linear attention with a decay for each head (include/linear.h)
 # ----------------------------------------------------------------------------
+def _linear_heads(q, k, v, log_decay, gpu, dev):
+    """Shape and stride checks of a call's rows: heads_kv and the strides."""
+    bf16 = torch.bfloat16
+    shape, kshape = q.shape, k.shape
+    lead, dim = shape[:-2], shape[-1]
+    if len(kshape) != len(shape):
+        raise ValueError("q, k and v must have the same leading dims")
+    heads_kv = kshape[-2]
+    if not _ok(log_decay, torch.float32, gpu):
+        _need(log_decay, "log_decay", torch.float32, dev)
+    if log_decay.dim() != 1 or log_decay.numel() != heads_kv:
+        raise ValueError(f"log_decay must be [{heads_kv}], got {list(log_decay.shape)}")
+    sq = 0 if _ok(q, bf16, gpu) else _token_rows(q, "q", lead, shape[-2], dim, dev)
+    dense = kshape[:-2] == lead and kshape[-1] == dim
+    sk = 0 if dense and _ok(k, bf16, gpu) else _token_rows(k, "k", lead, heads_kv, dim, dev)
+    sv = 0 if dense and v.shape == kshape and _ok(v, bf16, gpu) else _token_rows(v, "v", lead, heads_kv, dim, dev)
+    return heads_kv, sq, sk, sv
+
+
 def _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word, dout=None):
     gpu, dev = _gpu_of(q, "q")
-    lead, n, length, cu = _lead(q, cu_seqlens, dev)
-    heads, dim = q.shape[-2:]
-    if k.dim() != q.dim():
-        raise ValueError("q, k and v must have the same leading dims")
-    heads_kv = k.shape[-2]
-    if _need(log_decay, "log_decay", torch.float32, dev).shape != (heads_kv,):
-        raise ValueError(f"log_decay must be [{heads_kv}], got {list(log_decay.shape)}")
-    if error_word is not None:
-        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
-    p = _LinearProblem(n, length, math.prod(lead), heads, heads_kv, dim,
-                       float(scale) if scale is not None else 1.0 / math.sqrt(dim),
-                       _token_rows(q, "q", lead, heads, dim, gpu, dev),
-                       _token_rows(k, "k", lead, heads_kv, dim, gpu, dev),
-                       _token_rows(v, "v", lead, heads_kv, dim, gpu, dev),
-                       0 if dout is None else _token_rows(dout, "dout", lead, heads, dim, gpu, dev),
-                       cu, log_decay.data_ptr(), error_word)
-    return p, dev
+    shape = q.shape
+    tokens, n, length, cu = _lead(shape, cu_seqlens, gpu, dev)
+    heads_kv, sq, sk, sv = _linear_heads(q, k, v, log_decay, gpu, dev)
+    sd = 0
+    if dout is not None and (dout.shape != shape or not _ok(dout, torch.bfloat16, gpu)):
+        sd = _token_rows(dout, "dout", shape[:-2], shape[-2], shape[-1], dev)
+    dim = shape[-1]
+    return _LinearProblem(n, length, tokens, shape[-2], heads_kv, dim,
+                          float(scale) if scale is not None else 1.0 / math.sqrt(dim), sq, sk, sv, sd,
+                          cu, log_decay.data_ptr(), _word(error_word, gpu, dev)), gpu, dev
 
 
-def _linear_state(t, name, p, dev):
-    if t is not None and _need(t, name, torch.float32, dev).shape != (p.num_seqs, p.heads_kv, p.head_dim, p.head_dim):
+def _linear_state(t, name, p, gpu, dev):
+    if not _ok(t, torch.float32, gpu):
+        _need(t, name, torch.float32, dev)
+    if t.shape != (p.num_seqs, p.heads_kv, p.head_dim, p.head_dim):
         raise ValueError(f"{name} must be {[p.num_seqs, p.heads_kv, p.head_dim, p.head_dim]}, got {list(t.shape)}")
-    return t
 
 
-def _like(t, name, like, dev):
-    if t is not None and _need(t, name, torch.bfloat16, dev).shape != like.shape:
-        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
-    return t
+def _linear_work(size, p, workspace, like):
+    """A call's workspace and its bytes, allocated where none is given."""
+    if workspace is not None:
+        return workspace, workspace.numel()
+    n = size(ctypes.byref(p))
+    return (torch.empty(n, dtype=torch.uint8, device=like.device) if n else None), n
 
 
 def linear_attn_fwd_workspace_size(q, k, v, log_decay, *, cu_seqlens=None) -> int:
-    p, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
+    p, _, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
     with torch.cuda.device(dev):
         return int(lib().linear_attn_fwd_workspace_size(ctypes.byref(p)))
 
 
 def linear_attn_bwd_workspace_size(q, k, v, log_decay, *, cu_seqlens=None) -> int:
-    p, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
+    p, _, dev = _linear_problem(q, k, v, log_decay, None, cu_seqlens, None)
     with torch.cuda.device(dev):
         return int(lib().linear_attn_bwd_workspace_size(ctypes.byref(p)))
 
@@ -1155,26 +1219,32 @@ def linear_attn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initial_
     log_decay fp32 [Hkv], at most 0; initial_state fp32 [n, Hkv, D, D] or None.
     Returns (o, final_state), the latter None unless wanted or given.  A workspace
     is allocated here when none is given."""
-    p, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word)
-    _linear_state(initial_state, "initial_state", p, dev)
-    _linear_state(final_state, "final_state", p, dev)
-    _like(out, "out", q, dev)
+    p, gpu, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word)
+    if initial_state is not None:
+        _linear_state(initial_state, "initial_state", p, gpu, dev)
+    if final_state is not None:
+        _linear_state(final_state, "final_state", p, gpu, dev)
+    if out is not None:
+        _out_like(out, "out", q, gpu, dev)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev)
     ctx, s = _on(dev, stream)
-    with ctx or contextlib.nullcontext():
-        L, ref = _LIB or lib(), ctypes.byref(p)
-        if out is None:
-            out = q.new_empty(q.shape)
-        if final_state is None and want_final_state:
-            final_state = q.new_empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32)
-        if workspace is None:
-            n = L.linear_attn_fwd_workspace_size(ref)
-            workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-        else:
-            n = workspace.numel()
-        code = L.linear_attn_fwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(initial_state),
-                                 out.data_ptr(), _at(final_state), _at(workspace), n, s)
+    if ctx is None:
+        return _linear_fwd_here(p, q, k, v, initial_state, want_final_state, final_state, out, workspace, s)
+    with ctx:
+        return _linear_fwd_here(p, q, k, v, initial_state, want_final_state, final_state, out, workspace, s)
+
+
+def _linear_fwd_here(p, q, k, v, initial_state, want_final_state, final_state, out, workspace, s):
+    L = _LIB or lib()
+    if out is None:
+        out = _new_like(q, p.q_stride)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32,
+                                  device=q.device)
+    workspace, n = _linear_work(L.linear_attn_fwd_workspace_size, p, workspace, q)
+    code = L.linear_attn_fwd(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(initial_state),
+                             out.data_ptr(), _at(final_state), _at(workspace), n, s)
     if code:
         raise AttnError("linear_attn_fwd", code)
     return out, final_state
@@ -1186,30 +1256,37 @@ def linear_attn_bwd(q, k, v, dout, log_decay, *, scale=None, cu_seqlens=None, in
     """Backward of linear_attn_fwd from its inputs, dout and dfinal_state (fp32
     [n, Hkv, D, D], the final state's gradient, or None).  Returns (dq, dk, dv,
     dinitial_state), the last None unless wanted or given; bitwise reproducible."""
-    p, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word, dout)
+    p, gpu, dev = _linear_problem(q, k, v, log_decay, scale, cu_seqlens, error_word, dout)
     for t, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state"),
                     (dinitial_state, "dinitial_state")):
-        _linear_state(t, name, p, dev)
+        if t is not None:
+            _linear_state(t, name, p, gpu, dev)
     for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        _like(t, name, like, dev)
+        if t is not None:
+            _out_like(t, name, like, gpu, dev)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev)
+    args = (p, q, k, v, dout, initial_state, dfinal_state, want_dinitial_state, dinitial_state, dq, dk, dv, workspace)
     ctx, s = _on(dev, stream)
-    with ctx or contextlib.nullcontext():
-        L, ref = _LIB or lib(), ctypes.byref(p)
-        dq = q.new_empty(q.shape) if dq is None else dq
-        dk = k.new_empty(k.shape) if dk is None else dk
-        dv = v.new_empty(v.shape) if dv is None else dv
-        if dinitial_state is None and want_dinitial_state:
-            dinitial_state = q.new_empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32)
-        if workspace is None:
-            n = L.linear_attn_bwd_workspace_size(ref)
-            workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-        else:
-            n = workspace.numel()
-        code = L.linear_attn_bwd(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(),
-                                 _at(initial_state), _at(dfinal_state), dq.data_ptr(), dk.data_ptr(),
-                                 dv.data_ptr(), _at(dinitial_state), _at(workspace), n, s)
+    if ctx is None:
+        return _linear_bwd_here(*args, s)
+    with ctx:
+        return _linear_bwd_here(*args, s)
+
+
+def _linear_bwd_here(p, q, k, v, dout, initial_state, dfinal_state, want_dinitial_state, dinitial_state, dq, dk, dv,
+                     workspace, s):
+    L = _LIB or lib()
+    dq = _new_like(q, p.q_stride) if dq is None else dq
+    dk = _new_like(k, p.k_stride) if dk is None else dk
+    dv = _new_like(v, p.v_stride) if dv is None else dv
+    if dinitial_state is None and want_dinitial_state:
+        dinitial_state = torch.empty((p.num_seqs, p.heads_kv, p.head_dim, p.head_dim), dtype=torch.float32,
+                                     device=q.device)
+    workspace, n = _linear_work(L.linear_attn_bwd_workspace_size, p, workspace, q)
+    code = L.linear_attn_bwd(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(),
+                             _at(initial_state), _at(dfinal_state), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                             _at(dinitial_state), _at(workspace), n, s)
     if code:
         raise AttnError("linear_attn_bwd", code)
     return dq, dk, dv, dinitial_state
@@ -1221,31 +1298,39 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale=None, out=N
     [slots, Hkv, D, D], updated in place; slots int32 [n], the state of each
     sequence (-1: padding; None: sequence n's is state[n]).  Returns o."""
     gpu, dev = _gpu_of(q, "q")
-    if q.dim() != 3 or k.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q, k and v must be [num_seqs, heads, head_dim]")
-    n, heads, dim = q.shape
-    heads_kv = k.shape[1]
-    if _need(state, "state", torch.float32, dev).dim() != 4 or state.shape[1:] != (heads_kv, dim, dim):
-        raise ValueError(f"state must be [slots, {heads_kv}, {dim}, {dim}], got {list(state.shape)}")
-    if _need(log_decay, "log_decay", torch.float32, dev).shape != (heads_kv,):
-        raise ValueError(f"log_decay must be [{heads_kv}], got {list(log_decay.shape)}")
-    if slots is not None and _need(slots, "slots", torch.int32, dev).shape != (n,):
-        raise ValueError(f"slots must be [{n}], got {list(slots.shape)}")
-    if error_word is not None:
-        error_word = _need(error_word, "error_word", torch.int32, dev).data_ptr()
-    _like(out, "out", q, dev)
-    p = _LinearStep(n, state.shape[0], heads, heads_kv, dim,
-                    float(scale) if scale is not None else 1.0 / math.sqrt(dim),
-                    _token_rows(q, "q", (n,), heads, dim, gpu, dev),
-                    _token_rows(k, "k", (n,), heads_kv, dim, gpu, dev),
-                    _token_rows(v, "v", (n,), heads_kv, dim, gpu, dev), _at(slots),
-                    log_decay.data_ptr(), error_word)
+    n, heads, dim = shape
+    heads_kv, sq, sk, sv = _linear_heads(q, k, v, log_decay, gpu, dev)
+    if not _ok(state, torch.float32, gpu):
+        _need(state, "state", torch.float32, dev)
+    st = state.shape
+    if len(st) != 4 or st[1] != heads_kv or st[2] != dim or st[3] != dim:
+        raise ValueError(f"state must be [slots, {heads_kv}, {dim}, {dim}], got {list(st)}")
+    at = None
+    if slots is not None:
+        if not _ok(slots, torch.int32, gpu):
+            _need(slots, "slots", torch.int32, dev)
+        if slots.dim() != 1 or slots.numel() != n:
+            raise ValueError(f"slots must be [{n}], got {list(slots.shape)}")
+        at = slots.data_ptr()
+    if out is not None:
+        _out_like(out, "out", q, gpu, dev)
+    p = _LinearStep(n, st[0], heads, heads_kv, dim, float(scale) if scale is not None else 1.0 / math.sqrt(dim),
+                    sq, sk, sv, at, log_decay.data_ptr(), _word(error_word, gpu, dev))
     ctx, s = _on(dev, stream)
-    with ctx or contextlib.nullcontext():
-        if out is None:
-            out = q.new_empty(q.shape)
-        code = (_LIB or lib()).linear_attn_step(ctypes.byref(p), q.data_ptr(), k.data_ptr(),
-                                                v.data_ptr(), state.data_ptr(), out.data_ptr(), s)
+    if ctx is None:
+        return _linear_step_here(p, q, k, v, state, out, s)
+    with ctx:
+        return _linear_step_here(p, q, k, v, state, out, s)
+
+
+def _linear_step_here(p, q, k, v, state, out, s):
+    if out is None:
+        out = _new_like(q, p.q_stride)
+    code = (_LIB or lib()).linear_attn_step(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                            state.data_ptr(), out.data_ptr(), s)
     if code:
         raise AttnError("linear_attn_step", code)
     return out

@@ -2,6 +2,7 @@
 // argument validation and the launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "linear.cuh"
@@ -41,74 +42,120 @@ struct Cut {
   bool parts[2];   // a sequence may have several segments
 };
 
-// Costs are counted in tiles of 128 x 128 bf16, the units that a walk loads and
-// stores: a chunk of o or dq takes 4, of dk or dv 2 + 2 group, of the states between
-// segments 2 (2 group).  A walk that is cut costs the pass over the states and its
-// own start (about 3 us, 4 tiles' time at an SM's share of the bandwidth).
-struct Kind {
-  int heads, chunk, state_heads, state_chunk, count;
+// What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
+// heads (S, P Z and the state's product), `state` for each inner head of a chunk in the pass over
+// the states alone.  Measured, 64 chunks against 32 of 8192 and 4096 tokens: head_dim 128,
+// 1, 2, 4 and 8 inner heads, 183, 292, 513 and 947 us; head_dim 64, 145, 237, 417 and 781.
+struct Rates {
+  double base, step, state, part;   // part: a segment's state on the way to another's first
 };
-Cut cut_sequences(const linear_attn_problem_t* p, bool backward) {
-  const int sms = sm_count() > 0 ? sm_count() : 152;
+constexpr Rates kRates[2] = {{0.67, 1.43, 0.80, 0.2}, {1.00, 1.70, 0.94, 0.65}};
+constexpr double kStart = 3.0;     // a walk's start and end
+constexpr double kLaunch = 4.0;    // of the pass over the states
+constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
+
+// The time of na walks of ca and then nb of cb on `sms` SMs, each taking the next as it is free.
+double makespan(int sms, double na, double ca, double nb, double cb) {
+  const double k = std::floor(na / sms), r = na - k * sms;
+  const double low = k * ca, high = r > 0 ? low + ca : low;   // of sms - r SMs, and of r
+  if (nb <= 0) return high;
+  auto fits = [&](double t) {
+    double n = t > low ? (sms - r) * std::floor((t - low) / cb + 1e-9) : 0;
+    if (t > high) n += r * std::floor((t - high) / cb + 1e-9);
+    return n >= nb;
+  };
+  double lo = 0, hi = high + (std::floor(nb / sms) + 1) * cb;
+  for (int i = 0; i < 12; ++i) {
+    const double mid = 0.5 * (lo + hi);
+    if (fits(mid)) hi = mid;
+    else lo = mid;
+  }
+  return hi > high ? hi : high;
+}
+
+// Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, o
+// jobs cut into 3 and the others into 4 segments of a sequence 274, uncut 511; forward of 12 packed
+// sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 8 chunks 86, of 4 100, of
+// 16 103; one sequence of 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161,
+// of 16 169.
+Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   const int group = p->heads_q / p->heads_kv;
-  const double unit = p->head_dim / 128.0, start = 4.0;
-  const Kind kinds[2] = {{p->heads_q, 4, p->heads_kv, 2, 1}, {p->heads_kv, 2 + 2 * group, p->heads_kv, 2 * group, 2}};
+  const Rates& rate = kRates[p->head_dim == 128];
+  const double tile = 2.0 * kLinearChunk * p->head_dim;
   const bool packed = p->cu_seqlens != nullptr;
   // packed sequences: any may hold nearly all tokens
-  const int64_t total = packed ? (static_cast<int64_t>(p->tokens) + kLinearChunk - 1) / kLinearChunk + p->num_seqs / 2
-                               : 0;
   const int longest = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;
-  const int n_kinds = backward ? 2 : 1;
   struct Option {
     int chunks;
-    double items, cost, state;   // walks, tiles of one, tiles of all state walks
+    double walks, cost, states, state_cost, bytes;   // of one job
   };
-  Option opt[2][64];
+  Option opt[2][16];
   int n_opt[2] = {0, 0};
-  for (int i = 0; i < n_kinds; ++i) {
-    const Kind& k = kinds[i];
-    for (int nseg = 1; nseg <= 64 && nseg <= (longest > 1 ? longest : 1); ++nseg) {
+  for (int i = 0; i < (backward ? 2 : 1); ++i) {
+    const int inner = i ? group : 1, heads = i ? p->heads_kv : p->heads_q;
+    // (the first: as many as fill the SMs once)
+    const int fill = packed ? 1 : sms / std::max(1, std::min(sms, p->num_seqs * heads));
+    for (const int nseg : {fill, 1, 2, 3, 4, 5, 6, 8, 11, 16, 22, 32, 45, 64, 90}) {
+      if (nseg > 1 && nseg > longest) continue;
       const int per = longest > 0 ? (longest + nseg - 1) / nseg : 1;
-      if (n_opt[i] && opt[i][n_opt[i] - 1].chunks == per) continue;
+      const int segs = longest > 0 ? (longest + per - 1) / per : 1;
       Option o;
       o.chunks = per;
-      const double walks = packed ? static_cast<double>(total) / per + 0.5 * p->num_seqs
-                                  : static_cast<double>(p->num_seqs) * ((longest + per - 1) / per);
-      o.items = walks * k.heads * k.count;
-      o.cost = start + unit * per * k.chunk;
-      const double cut = packed ? static_cast<double>(total) * (nseg - 1) / nseg
-                                : static_cast<double>(p->num_seqs) * (longest - per);
-      o.state = nseg == 1 ? 0.0 : unit * cut * k.state_heads * k.state_chunk;
+      const double full = per * (rate.base + rate.step * inner);
+      // packed: some chunks are partly empty, and a sequence's segments on average 4 / 5 of the size
+      const double chunks = packed ? longest + 0.5 * p->num_seqs : static_cast<double>(longest) * p->num_seqs;
+      o.walks = (packed ? chunks / per * 1.25 : static_cast<double>(p->num_seqs) * segs) * heads;
+      o.cost = kStart + (packed ? 0.8 * full : full) + rate.part * (packed ? 0.3 : 0.75) * (segs - 1);
+      o.states = segs == 1 ? 0 : (packed ? o.walks / heads : static_cast<double>(p->num_seqs) * (segs - 1)) * p->heads_kv;
+      o.state_cost = kStart + rate.state * inner * per;
+      o.bytes = tile * (chunks * heads * (i ? 2 + 2 * inner : 2 + 2.0 / group) +
+                        (segs == 1 ? 0 : chunks * (segs - 1) / segs * p->heads_kv * 2 * inner));
       opt[i][n_opt[i]++] = o;
     }
   }
-  auto time = [&](const Option& x, const Option* y) {
-    const double items = x.items + (y ? y->items : 0), most = y && y->cost > x.cost ? y->cost : x.cost;
-    const double all = packed ? x.items * (start + 0.7 * (x.cost - start)) + (y ? y->items * (start + 0.7 * (y->cost - start)) : 0)
-                              : x.items * x.cost + (y ? y->items * y->cost : 0);
-    double t;
-    if (items <= sms) t = most;
-    else if (!packed && !y) t = static_cast<double>((static_cast<int64_t>(items) + sms - 1) / sms) * most;
-    else t = all / sms + 0.6 * most;
-    const double state = x.state + (y ? y->state : 0);
-    if (state > 0) t += 2 * start + 1.3 * state / sms;
-    return t;
-  };
+  const Option none{};
   int best[2] = {0, 0};
   double least = 0;
   for (int i = 0; i < n_opt[0]; ++i)
     for (int j = 0; j < (backward ? n_opt[1] : 1); ++j) {
-      const double t = time(opt[0][i], backward ? &opt[1][j] : nullptr);
+      const Option &x = opt[0][i], &y = backward ? opt[1][j] : none;
+      double t = makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
+      // the longest segments of packed sequences may come last
+      if (packed) t += 0.3 * (x.cost > y.cost ? x.cost : y.cost);
+      const double bytes = (x.bytes + 2 * y.bytes) / kBytes;
+      if (bytes > t) t = bytes;
+      if (x.states + y.states > 0) t += kLaunch + makespan(sms, y.states, y.state_cost, x.states, x.state_cost);
       if ((i == 0 && j == 0) || t < least) least = t, best[0] = i, best[1] = j;
     }
   Cut c{};
-  for (int i = 0; i < n_kinds; ++i) {
+  for (int i = 0; i < (backward ? 2 : 1); ++i) {
     c.chunks[i] = opt[i][best[i]].chunks;
     c.slots[i] = packed ? p->tokens / (c.chunks[i] * kLinearChunk) + p->num_seqs
                         : p->num_seqs * (longest > 0 ? (longest + c.chunks[i] - 1) / c.chunks[i] : 1);
     c.parts[i] = c.chunks[i] < longest;
   }
   return c;
+}
+
+// The cut depends on the sizes alone; a thread keeps the last ones it asked for (finding one takes
+// some 10 us of the host's time).
+Cut cut_sequences(const linear_attn_problem_t* p, bool backward) {
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  struct Kept {
+    int key[8];
+    Cut cut;
+  };
+  constexpr int kKept = 8;
+  static thread_local Kept kept[kKept] = {};
+  static thread_local int next = 0;
+  const int key[8] = {sms, backward ? 2 : 1, p->cu_seqlens != nullptr, p->num_seqs,
+                      p->tokens, p->heads_q, p->heads_kv, p->head_dim};
+  for (const Kept& k : kept)
+    if (std::equal(key, key + 8, k.key)) return k.cut;
+  Kept& k = kept[next];
+  next = (next + 1) % kKept;
+  std::copy(key, key + 8, k.key);
+  return k.cut = find_cut(p, backward, sms);
 }
 
 size_t state_bytes(const linear_attn_problem_t* p, int slots) {

@@ -44,6 +44,8 @@ struct Cfg {
   // S of a step is formed while the step before is still at work, where the ring can hold both
   static constexpr bool AHEAD = XBUF == 2;
   static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
+  // without S and O there is room for two of G: a chunk's is read while the next one's is formed
+  static constexpr int GBUF = kStates ? 2 : 1;
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
 };
 
@@ -149,6 +151,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return ok;
 }
 
+// One arrival for a warp, behind all its lanes: 256 arrivals of a role's threads at one barrier
+// take their turns.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+}
+
 template <int D, int NS, bool kStates>
 __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ LinearArgs a) {
   using C = Cfg<D, NS, kStates>;
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
 
   __shared__ uint64_t bar_full[NSLOT], bar_empty[NSLOT];
   __shared__ uint64_t bar_xfull[2], bar_xempty[2];
-  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_qh, bar_o, bar_out, bar_of, bar_g, bar_gf, bar_h;
+  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_g[2], bar_gf[2], bar_qh, bar_o, bar_out, bar_of, bar_h;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ Place s_place;
@@ -195,16 +204,16 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_p[i], 128);
-      mbar_init(&bar_y[i], 256);
+      mbar_init(&bar_p[i], 4);
+      mbar_init(&bar_y[i], 8);
+      mbar_init(&bar_g[i], 1);
+      mbar_init(&bar_gf[i], 8);
     }
     mbar_init(&bar_qh, 1);
     mbar_init(&bar_o, 1);
-    mbar_init(&bar_of, 256);
-    mbar_init(&bar_out, 256);
-    mbar_init(&bar_g, 1);
-    mbar_init(&bar_gf, 256);
-    mbar_init(&bar_h, 256);
+    mbar_init(&bar_of, 8);
+    mbar_init(&bar_out, 8);
+    mbar_init(&bar_h, 8);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
@@ -304,19 +313,19 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if (!landed(2 * t + 1) || (kStates && !landed(2 * t))) return false;
       if (n < n_grow) {
         if (!warp_wait(&bar_y[t & 1], (t >> 1) & 1, ac)) return false;
-        if (g == 0 && n > 0 && !warp_wait(&bar_gf, (n - 1) & 1, ac)) return false;
+        if (g == 0 && n >= C::GBUF && !warp_wait(&bar_gf[n % C::GBUF], (n / C::GBUF - 1) & 1, ac)) return false;
         tc_fence_after();
         const uint64_t dy = desc_advance(dm0, slot(2 * t) * C::TILE), dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
 #pragma unroll 1
         for (int e = 0; e < NS; ++e)
 #pragma unroll 2
           for (int k = 0; k < 8; ++k)
-            umma_ss_w(tmem + C::COL_G,
+            umma_ss_w(tmem + C::COL_G - 128 * (n % C::GBUF),
                       desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
                       desc_advance(dz, mnmajor_step_bytes(k)), idG, (g > 0 || e > 0 || k > 0) ? 1u : 0u);
       }
       umma_commit_w(&bar_empty[slot(2 * t)]);
-      if (n < n_grow && g == inner - 1) umma_commit_w(&bar_g);
+      if (n < n_grow && g == inner - 1) umma_commit_w(&bar_g[n % C::GBUF]);
       return true;
     };
     // X H, at a chunk's first step; behind the S of its last step, X is free
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar_p[t & 1]);
+        warp_arrive(&bar_p[t & 1]);
       }
       if (C::AHEAD && t + 1 < steps && !convert(t + 1, chunk_len(last ? n + 1 : n))) break;
       if (t >= 0) {
@@ -533,24 +542,25 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
           *reinterpret_cast<uint4*>(sH + sw128_offset(r, c0 + x, D)) = v;
         }
       fence_proxy_async_smem();
-      mbar_arrive(&bar_h);
+      warp_arrive(&bar_h);
     };
     if (!kStates && n_walk > 0) publish();
     // what chunk n adds, and then the state as the next chunk's operand
     auto grow = [&](int n) -> bool {
-      if (!wait(&bar_g, n & 1, ac)) return false;
+      const int b = n % C::GBUF;
+      if (!wait(&bar_g[b], (n / C::GBUF) & 1, ac)) return false;
       tc_fence_after();
       const float keep = ex2(l2 * chunk_len(n));
 #pragma unroll
       for (int x = 0; x < C::HC; x += 32) {
         uint32_t v[32];
-        tmem_ld32_nowait(tG + x, v);
+        tmem_ld32_nowait(tG - 128 * b + x, v);
         tmem_wait_ld();
 #pragma unroll
         for (int y = 0; y < 32; ++y) H[x + y] = fmaf(keep, H[x + y], __uint_as_float(v[y]));
       }
       tc_fence_before();
-      mbar_arrive(&bar_gf);
+      warp_arrive(&bar_gf[b]);
       if (kStates || n + 1 >= n_walk) return true;
       if (!wait(&bar_qh, n & 1, ac)) return false;   // the product that read the state before
       publish();
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
       }
       tc_fence_before();
-      mbar_arrive(&bar_of);
+      warp_arrive(&bar_of);
       if (rows < kLinearChunk) {   // rows behind the sequence are another's: plain stores
         named_bar_sync(1, 256);
         __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + chunk_row(n)) * j.heads_x + h) * D;
@@ -592,13 +602,13 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bar_out);
+      warp_arrive(&bar_out);
       return true;
     };
     int n = 0, g = 0;
     for (int t = 0; t <= steps; ++t) {
       const bool next = g == 0 && n > 0;   // a chunk is behind these warps
-      if (next && n - 1 < n_grow && !grow(n - 1)) break;
+      if (!kStates && next && n - 1 < n_grow && !grow(n - 1)) break;
       if (!kStates && !C::AHEAD && next && !output(n - 1)) break;
       if (t < steps && n < n_grow) {
         const int rows = chunk_len(n);
@@ -655,8 +665,9 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bar_y[t & 1]);
+        warp_arrive(&bar_y[t & 1]);
       }
+      if (kStates && next && !grow(n - 1)) break;
       if (!kStates && C::AHEAD && next && !output(n - 1)) break;
       if (++g == inner) {
         g = 0;
