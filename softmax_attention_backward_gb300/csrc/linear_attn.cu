@@ -40,6 +40,9 @@ struct Cfg {
   static constexpr int NSLOT = (FIT > 8 ? 8 : FIT) - XBUF;
   static constexpr int SMEM = (XBUF + NSLOT) * TILE + H_BYTES + EXTRA + 1024;
   static constexpr int THREADS = 512;
+  // Products of one operand pair issued from unrolled code: heads of 64 gain (1 x 8192 tokens, 32
+  // heads, 64.6 -> 58.5 us), heads of 128 lose to the larger code (4 x 4096 tokens 104 -> 108).
+  static constexpr int UNROLL = D == 64 ? 8 : 2;
   static constexpr int HC = D / 2;                // state columns of a thread
   // S of a step is formed while the step before is still at work, where the ring can hold both
   static constexpr bool AHEAD = XBUF == 2;
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if (!landed(2 * t)) return false;
       tc_fence_after();
       const uint64_t dx = desc_advance(dx0, bx * C::TILE), dy = desc_advance(dk0, slot(2 * t) * C::TILE);
-#pragma unroll 2
+#pragma unroll C::UNROLL
       for (int k = 0; k < D / 16; ++k)
         umma_ss_w(tmem + C::COL_S + 128 * (t & 1), desc_advance(dx, kmajor_step_bytes(128, k)),
                   desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         const uint64_t dy = desc_advance(dm0, slot(2 * t) * C::TILE), dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
 #pragma unroll 1
         for (int e = 0; e < NS; ++e)
-#pragma unroll 2
+#pragma unroll C::UNROLL
           for (int k = 0; k < 8; ++k)
             umma_ss_w(tmem + C::COL_G - 128 * (n % C::GBUF),
                       desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         if (!warp_wait(&bar_h, n & 1, ac) || (n > 0 && !warp_wait(&bar_of, (n - 1) & 1, ac))) return false;
         tc_fence_after();
         const uint64_t dx = desc_advance(dx0, bx * C::TILE);
-#pragma unroll 2
+#pragma unroll C::UNROLL
         for (int k = 0; k < D / 16; ++k)
           umma_ss_w(tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k)),
                     desc_advance(dH, mnmajor_step_bytes(k)), idO, k > 0);
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if (!warp_wait(&bar_p[t & 1], (t >> 1) & 1, ac)) return false;
       tc_fence_after();
       const uint64_t dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
-#pragma unroll 2
+#pragma unroll C::UNROLL
       for (int k = 0; k < 8; ++k)
         umma_ts_w(tmem + C::COL_O, tmem + C::COL_S + 128 * (t & 1) + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)),
                   idO, 1u);
