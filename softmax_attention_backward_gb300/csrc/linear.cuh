@@ -24,6 +24,7 @@ struct LinearJob {
   __nv_bfloat16* out;       // dense, heads_x heads; null: states only
   int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;
+  int terms;                // bf16 terms of a decayed key: 1, or 3 where `last` is returned
   int inner;                // heads of y and z that meet one head of x
   FastDiv fd_heads;         // heads_x
   FastDiv fd_kv;            // heads of x per KV head
@@ -49,8 +50,6 @@ struct LinearArgs {
   int32_t* err;
 };
 
-// `terms` bf16 terms of a decayed key: 1, or 3 where a state is returned
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, int terms, bool states_only,
-                          cudaStream_t st);
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, cudaStream_t st);
 
 }  // namespace attn

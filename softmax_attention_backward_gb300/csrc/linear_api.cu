@@ -40,16 +40,17 @@ attn_status_t check(const linear_attn_problem_t* p) {
 struct Cut {
   int chunks[2], slots[2];
   bool parts[2];   // a sequence may have several segments
+  bool dq_first;   // backward: the walks of dq are the longer ones
 };
 
 // What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
 // heads (S, P Z and the state's product), `state` for each inner head of a chunk in the pass over
 // the states alone.  Measured, 64 chunks against 32 of 8192 and 4096 tokens: head_dim 128,
-// 1, 2, 4 and 8 inner heads, 183, 292, 513 and 947 us; head_dim 64, 145, 237, 417 and 781.
+// 1, 2, 4 and 8 inner heads, 183, 292, 517 and 957 us; head_dim 64, 132, 220, 402 and 767.
 struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
 };
-constexpr Rates kRates[2] = {{0.67, 1.43, 0.80, 0.2}, {1.00, 1.70, 0.94, 0.65}};
+constexpr Rates kRates[2] = {{0.46, 1.40, 0.80, 0.2}, {1.00, 1.70, 0.94, 0.65}};
 constexpr double kStart = 3.0;     // a walk's start and end
 constexpr double kLaunch = 4.0;    // of the pass over the states
 constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
@@ -83,11 +84,14 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   const Rates& rate = kRates[p->head_dim == 128];
   const double tile = 2.0 * kLinearChunk * p->head_dim;
   const bool packed = p->cu_seqlens != nullptr;
-  // packed sequences: any may hold nearly all tokens
-  const int longest = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;
+  const int most = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;   // of a sequence
+  // packed sequences have lengths that the host does not know: half a chunk is taken to be empty in
+  // each, and the longest to be three times the average
+  const double chunks = packed ? most + 0.5 * p->num_seqs : static_cast<double>(most) * p->num_seqs;
+  const int longest = packed ? std::min(most, std::max(4, static_cast<int>(3 * chunks / p->num_seqs))) : most;
   struct Option {
     int chunks;
-    double walks, cost, states, state_cost, bytes;   // of one job
+    double walks, cost, longest, states, state_cost, bytes;   // of one job
   };
   Option opt[2][16];
   int n_opt[2] = {0, 0};
@@ -101,15 +105,17 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
       const int segs = longest > 0 ? (longest + per - 1) / per : 1;
       Option o;
       o.chunks = per;
-      const double full = per * (rate.base + rate.step * inner);
-      // packed: some chunks are partly empty, and a sequence's segments on average 4 / 5 of the size
-      const double chunks = packed ? longest + 0.5 * p->num_seqs : static_cast<double>(longest) * p->num_seqs;
-      o.walks = (packed ? chunks / per * 1.25 : static_cast<double>(p->num_seqs) * segs) * heads;
-      o.cost = kStart + (packed ? 0.8 * full : full) + rate.part * (packed ? 0.3 : 0.75) * (segs - 1);
-      o.states = segs == 1 ? 0 : (packed ? o.walks / heads : static_cast<double>(p->num_seqs) * (segs - 1)) * p->heads_kv;
+      const double chunk = rate.base + rate.step * inner;
+      const double walks = packed ? std::max<double>(p->num_seqs, chunks / per + 0.5 * p->num_seqs)
+                                  : static_cast<double>(p->num_seqs) * segs;
+      const double before = rate.part * (packed ? 0.3 : 0.75) * (segs - 1);
+      o.walks = walks * heads;
+      o.longest = kStart + before + chunk * per;
+      o.cost = packed ? kStart + before + chunk * std::min<double>(per, chunks / walks) : o.longest;
+      o.states = (walks - p->num_seqs) * p->heads_kv;
       o.state_cost = kStart + rate.state * inner * per;
       o.bytes = tile * (chunks * heads * (i ? 2 + 2 * inner : 2 + 2.0 / group) +
-                        (segs == 1 ? 0 : chunks * (segs - 1) / segs * p->heads_kv * 2 * inner));
+                        chunks * (walks - p->num_seqs) / walks * p->heads_kv * 2 * inner);
       opt[i][n_opt[i]++] = o;
     }
   }
@@ -119,11 +125,11 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   for (int i = 0; i < n_opt[0]; ++i)
     for (int j = 0; j < (backward ? n_opt[1] : 1); ++j) {
       const Option &x = opt[0][i], &y = backward ? opt[1][j] : none;
-      double t = makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
-      // the longest segments of packed sequences may come last
-      if (packed) t += 0.3 * (x.cost > y.cost ? x.cost : y.cost);
-      const double bytes = (x.bytes + 2 * y.bytes) / kBytes;
-      if (bytes > t) t = bytes;
+      double t = x.longest > y.longest ? makespan(sms, x.walks, x.cost, 2 * y.walks, y.cost)
+                                       : makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
+      // the longest of packed sequences may come last
+      t += 0.5 * std::max(x.longest - x.cost, y.longest - y.cost);
+      t = std::max(t, (x.bytes + 2 * y.bytes) / kBytes);
       if (x.states + y.states > 0) t += kLaunch + makespan(sms, y.states, y.state_cost, x.states, x.state_cost);
       if ((i == 0 && j == 0) || t < least) least = t, best[0] = i, best[1] = j;
     }
@@ -131,9 +137,10 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   for (int i = 0; i < (backward ? 2 : 1); ++i) {
     c.chunks[i] = opt[i][best[i]].chunks;
     c.slots[i] = packed ? p->tokens / (c.chunks[i] * kLinearChunk) + p->num_seqs
-                        : p->num_seqs * (longest > 0 ? (longest + c.chunks[i] - 1) / c.chunks[i] : 1);
-    c.parts[i] = c.chunks[i] < longest;
+                        : p->num_seqs * (most > 0 ? (most + c.chunks[i] - 1) / c.chunks[i] : 1);
+    c.parts[i] = c.chunks[i] < most;
   }
+  c.dq_first = backward && opt[0][best[0]].longest > opt[1][best[1]].longest;
   return c;
 }
 
@@ -198,6 +205,7 @@ bool map_out(LinearJob* j, const linear_attn_problem_t* p, void* out, int heads)
 void set_job(LinearJob& j, const linear_attn_problem_t* p, int heads_x, int shared, int inner, const Cut& c, int way) {
   j.heads_x = heads_x;
   j.backwards = way;
+  j.terms = 1;
   j.inner = inner;
   j.fd_heads = make_fastdiv(heads_x);
   j.fd_kv = make_fastdiv(shared);
@@ -272,13 +280,14 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   set_job(j, p, p->heads_q, p->heads_q / p->heads_kv, 1, cut, 0);
   j.first = initial_state;
   j.last = final_state;
+  j.terms = final_state ? 3 : 1;
   j.parts = static_cast<float*>(workspace);
   if (cut.parts[0]) {
     LinearArgs s = make_args(p);
     s.job[s.jobs++] = state_job(j, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, final_state ? 3 : 1, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return launch_linear(a, p->head_dim, final_state ? 3 : 1, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_linear(a, p->head_dim, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const void* q,
@@ -311,8 +320,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   const int group = p->heads_q / p->heads_kv;
   LinearArgs a = make_args(p);
   a.jobs = 3;
-  // dv and dk first: their walks are the longer ones
-  LinearJob &jv = a.job[0], &jk = a.job[1], &jq = a.job[2];
+  // the longest walks first
+  LinearJob &jv = a.job[cut.dq_first], &jk = a.job[cut.dq_first + 1], &jq = a.job[cut.dq_first ? 0 : 2];
   if (!map_rows(&jv.mx, p, rk) || !map_rows(&jv.my, p, rq) || !map_rows(&jv.mz, p, rd) || !map_rows(&jk.mx, p, rv) ||
       !map_out(&jv, p, dv, p->heads_kv) || !map_out(&jk, p, dk, p->heads_kv) || !map_out(&jq, p, dq, p->heads_q))
     return ATTN_ERR_CUDA;
@@ -332,12 +341,12 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
     ws = jk.parts + state_bytes(p, cut.slots[1]) / sizeof(float);
   }
   jq.parts = ws;
-  const int terms = dinitial_state ? 3 : 1;
+  jv.terms = dinitial_state ? 3 : 1;
   if (cut.parts[0] || cut.parts[1]) {
     LinearArgs s = make_args(p);
     if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);
     if (cut.parts[0]) s.job[s.jobs++] = state_job(jq, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, terms, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return launch_linear(a, p->head_dim, terms, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_linear(a, p->head_dim, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   auto chunk_row = [&](int n) { return (back ? c_hi - 1 - n : c_lo + n) * kLinearChunk; };
   auto chunk_len = [&](int n) { return min(kLinearChunk, pl.len - chunk_row(n)); };
   const bool want_last = kStates || (is_end && j.last && h == hkv * static_cast<int>(j.fd_kv.d));
+  const int terms = NS == 1 || !want_last ? 1 : j.terms;   // bf16 terms of the decayed keys
   const int n_grow = want_last ? n_walk : n_walk - 1;   // chunks that the state takes in
   const int steps = n_walk * inner;                     // a step: one inner head of a chunk
 
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         tc_fence_after();
         const uint64_t dy = desc_advance(dm0, slot(2 * t) * C::TILE), dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
 #pragma unroll 1
-        for (int e = 0; e < NS; ++e)
+        for (int e = 0; e < terms; ++e)
 #pragma unroll C::UNROLL
           for (int k = 0; k < 8; ++k)
             umma_ss_w(tmem + C::COL_G - 128 * (n % C::GBUF),
@@ -621,8 +622,8 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         if (!kStates && !wait(&bar_s[t & 1], (t >> 1) & 1, ac)) break;
         // the other terms' tiles: read by the products of the step before.  Where no scores hold
         // these warps back, they stay within what two barriers can tell apart.
-        const int behind = NS > 1 ? t - 1 : t - 2;
-        if ((NS > 1 || kStates) && behind >= 0 &&
+        const int behind = terms > 1 ? t - 1 : t - 2;
+        if ((terms > 1 || kStates) && behind >= 0 &&
             !wait(&bar_empty[2 * behind % NSLOT], (2 * behind / NSLOT) & 1, ac))
           break;
         if (rows < kLinearChunk) {
@@ -661,10 +662,11 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
               }
             }
             *reinterpret_cast<uint4*>(y + at) = make_uint4(term[0][0], term[0][1], term[0][2], term[0][3]);
+            if (NS > 1 && terms > 1)
 #pragma unroll
-            for (int q = 1; q < NS; ++q)
-              *reinterpret_cast<uint4*>(sExtra + (q - 1) * C::TILE + at) =
-                  make_uint4(term[q][0], term[q][1], term[q][2], term[q][3]);
+              for (int q = 1; q < NS; ++q)
+                *reinterpret_cast<uint4*>(sExtra + (q - 1) * C::TILE + at) =
+                    make_uint4(term[q][0], term[q][1], term[q][2], term[q][3]);
           }
         }
         fence_proxy_async_smem();
@@ -731,8 +733,9 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, int terms, bool states_only,
-                          cudaStream_t st) {
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, cudaStream_t st) {
+  int terms = 1;   // the most that a job has
+  for (int i = 0; i < a.jobs; ++i) terms = a.job[i].terms > terms ? a.job[i].terms : terms;
   if (head_dim == 64) {
     if (states_only) return terms == 1 ? launch<64, 1, true>(a, st) : launch<64, 3, true>(a, st);
     return terms == 1 ? launch<64, 1, false>(a, st) : launch<64, 3, false>(a, st);
