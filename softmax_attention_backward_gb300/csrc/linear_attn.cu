@@ -514,10 +514,17 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     if (!kStates) {
       // the state before the segment: the first one, then what each segment on the way adds
       if (j.first && mine) {
-        const int sr = j.transposed ? 1 : D, sc = j.transposed ? D : 1;
         const float* f = j.first + (static_cast<int64_t>(pl.n) * a.heads_kv + hkv) * D * D;
+        if (j.transposed) {
 #pragma unroll
-        for (int x = 0; x < C::HC; ++x) H[x] = __ldg(f + r * sr + (c0 + x) * sc);
+          for (int x = 0; x < C::HC; ++x) H[x] = __ldg(f + (c0 + x) * D + r);
+        } else {
+#pragma unroll
+          for (int x = 0; x < C::HC; x += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(f + r * D + c0 + x));
+            H[x] = v.x, H[x + 1] = v.y, H[x + 2] = v.z, H[x + 3] = v.w;
+          }
+        }
       }
       const int before = back ? pl.nseg - 1 - pl.seg : pl.seg;
       for (int t = 0; t < before; ++t) {
