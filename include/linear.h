@@ -35,8 +35,8 @@ extern "C" {
  * the device only, so a captured graph may change it between replays), or, with
  * cu_seqlens NULL, rows [n seqlen, (n + 1) seqlen).  Rows at or past
  * cu_seqlens[num_seqs] are padding: outputs there are exact zeros, inputs there
- * do not affect any result.  A sequence may be empty.  A cu_seqlens that
- * decreases or passes `tokens` is flagged ATTN_DEVERR_SEQLEN; the rows of the
+ * do not affect any result.  A sequence may be empty.  A cu_seqlens that does not
+ * begin with 0, decreases or passes `tokens` is flagged ATTN_DEVERR_SEQLEN; the rows of the
  * sequences concerned are unspecified.
  *
  * q_stride .. dout_stride are the elements between two tokens' rows (0: dense,
@@ -48,8 +48,10 @@ extern "C" {
  * keeps everything, -inf keeps only the present token.  It is a property of the
  * layer, not differentiated.
  *
+ * No output may share memory with an input.
+ *
  * Supported: head_dim in {64, 128}; heads_q a multiple of heads_kv, at most 65535;
- * tokens * heads_q < 2^31.
+ * tokens * heads_q < 2^31, num_seqs * heads_q < 2^29.
  */
 typedef struct {
   int num_seqs;
@@ -76,8 +78,7 @@ size_t linear_attn_fwd_workspace_size(const linear_attn_problem_t* p);
 size_t linear_attn_bwd_workspace_size(const linear_attn_problem_t* p);
 
 /*
- * Forward.  initial_state and final_state may be NULL (zeros; not wanted); they
- * must not be the same buffer.
+ * Forward.  initial_state and final_state may be NULL (zeros; not wanted).
  * The products run on bf16 operands with fp32 sums: within a chunk of 128 tokens
  * the decayed scores, and where they meet a later chunk's rows the state, are
  * rounded to bf16 (2^-9 of each); the state itself is kept in fp32, of keys
@@ -97,7 +98,7 @@ attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const void* q, con
  *   head's query heads),   dk_t = D_t v_t,   dv_t = D_t^T k_t,
  * D past the last token standing for dL/d(final state), dfinal_state (NULL: zeros),
  * which meets the last token undecayed; dL/d(initial state) = l D_first goes to
- * dinitial_state unless that is NULL.  The two must not be the same buffer.
+ * dinitial_state unless that is NULL.
  * Rounding as in the forward pass, the three terms where dinitial_state is wanted.
  * Bitwise reproducible.
  */

@@ -20,7 +20,7 @@ bool good_stride(int64_t stride, int heads, int dim, int64_t* out) {
 
 attn_status_t check(const linear_attn_problem_t* p) {
   if (!p) return ATTN_ERR_INVALID_ARG;
-  if (p->num_seqs <= 0 || p->tokens < 0 || p->heads_q <= 0 || p->heads_kv <= 0 || p->head_dim <= 0 ||
+  if (p->num_seqs < 0 || p->tokens < 0 || (p->num_seqs == 0 && p->tokens > 0) || p->heads_q <= 0 || p->heads_kv <= 0 || p->head_dim <= 0 ||
       p->heads_q % p->heads_kv || !std::isfinite(p->scale))
     return ATTN_ERR_INVALID_ARG;
   if (!p->cu_seqlens &&
@@ -28,7 +28,8 @@ attn_status_t check(const linear_attn_problem_t* p) {
     return ATTN_ERR_INVALID_ARG;
   if (!p->log_decay) return ATTN_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return ATTN_ERR_UNSUPPORTED;
-  if (p->heads_q > 65535 || static_cast<int64_t>(p->tokens) * p->heads_q >= (int64_t(1) << 31))
+  if (p->heads_q > 65535 || static_cast<int64_t>(p->tokens) * p->heads_q >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(p->num_seqs) * p->heads_q >= (int64_t(1) << 29))
     return ATTN_ERR_UNSUPPORTED;
   if (!aligned(p->cu_seqlens, 4) || !aligned(p->log_decay, 4) || !aligned(p->error_word, 4))
     return ATTN_ERR_ALIGNMENT;
@@ -224,10 +225,17 @@ LinearJob state_job(const LinearJob& j, const linear_attn_problem_t* p, int inne
   return s;
 }
 
+// Whether a state that is read and one that is written share memory.
+bool overlap(const linear_attn_problem_t* p, const float* a, const float* b) {
+  const size_t n = state_bytes(p, p->num_seqs);
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + n && y < x + n;
+}
+
 // A problem without a token: the last state is the first one.
 attn_status_t pass_state(const linear_attn_problem_t* p, const float* first, float* last,
                          cudaStream_t st) {
-  if (!last) return ATTN_OK;
+  if (!last || p->num_seqs == 0) return ATTN_OK;
   const size_t n = sizeof(float) * p->num_seqs * p->heads_kv * p->head_dim * p->head_dim;
   const cudaError_t e = first ? cudaMemcpyAsync(last, first, n, cudaMemcpyDeviceToDevice, st)
                               : cudaMemsetAsync(last, 0, n, st);
@@ -255,7 +263,7 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
                                          size_t workspace_bytes, attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (initial_state && initial_state == final_state) return ATTN_ERR_INVALID_ARG;
+  if (overlap(p, initial_state, final_state)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return ATTN_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p->tokens == 0) return pass_state(p, initial_state, final_state, st);
@@ -298,7 +306,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
                                          attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (dfinal_state && dfinal_state == dinitial_state) return ATTN_ERR_INVALID_ARG;
+  if (overlap(p, dfinal_state, dinitial_state) || overlap(p, initial_state, dinitial_state))
+    return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(dfinal_state, 16) || !aligned(dinitial_state, 16))
     return ATTN_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -74,7 +74,7 @@ __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& r
   row0 = min(max(b, 0), a.tokens);
   const int end = min(max(e, row0), a.tokens);
   len = end - row0;
-  if ((b != row0 || e != end) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
+  if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
 }
 
 __device__ __forceinline__ int chunks_of(int len) { return (len + kLinearChunk - 1) / kLinearChunk; }
@@ -172,9 +172,11 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   uint8_t* sH = sX + C::XBUF * C::TILE;
   uint8_t* sExtra = sH + C::H_BYTES;
 
-  __shared__ uint64_t bar_full[NSLOT], bar_empty[NSLOT];
+  // bar_out: an output's barrier comes round with its tile at the soonest, so that the warp that
+  // waits is never two phases behind
+  __shared__ uint64_t bar_full[NSLOT], bar_empty[NSLOT], bar_out[NSLOT];
   __shared__ uint64_t bar_xfull[2], bar_xempty[2];
-  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_g[2], bar_gf[2], bar_qh, bar_o, bar_out, bar_of, bar_h;
+  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_g[2], bar_gf[2], bar_qh, bar_o, bar_of, bar_h;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ Place s_place;
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(&bar_full[i], 1);
       mbar_init(&bar_empty[i], 1);
+      mbar_init(&bar_out[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_xfull[i], 1);
@@ -215,7 +218,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     mbar_init(&bar_qh, 1);
     mbar_init(&bar_o, 1);
     mbar_init(&bar_of, 8);
-    mbar_init(&bar_out, 8);
     mbar_init(&bar_h, 8);
     fence_mbar_init();
   }
@@ -381,22 +383,31 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     }
   } else if (!kStates && warp == 3) {
     // ---------------- stores ----------------
-    // whole chunks leave by a bulk copy; behind it, or the state warps' own stores, the tile of the
-    // chunk's last Z, in which they lay, is free
-    if (lane_id() == 0) {
-      for (int n = 0; n < n_walk; ++n) {
-        const int b = (2 * (n + 1) * inner - 1) % NSLOT;
-        if (!wait(&bar_out, n & 1, ac)) break;
-        if (chunk_len(n) == kLinearChunk) {
-          for (int pn = 0; pn < PANELS; ++pn)
-            tma_store_3d(&j.mo, ring + b * C::TILE + pn * kLinearChunk * 128, pn * 64, h, pl.row0 + chunk_row(n));
+    // whole chunks leave by a bulk copy, others (rows behind the sequence are another's) by plain
+    // stores; behind them the tile of the chunk's last Z, in which they lay, is free
+    for (int n = 0; n < n_walk; ++n) {
+      const int b = (2 * (n + 1) * inner - 1) % NSLOT, rows = chunk_len(n), row = pl.row0 + chunk_row(n);
+      uint8_t* so = ring + b * C::TILE;
+      if (!__all_sync(0xffffffffu, wait(&bar_out[n % NSLOT], (n / NSLOT) & 1, ac))) break;
+      if (rows == kLinearChunk) {
+        if (lane_id() == 0) {
+          for (int pn = 0; pn < PANELS; ++pn) tma_store_3d(&j.mo, so + pn * kLinearChunk * 128, pn * 64, h, row);
           bulk_commit();
           bulk_wait_read<0>();
         }
-        mbar_arrive(&bar_empty[b]);
+      } else {
+        __nv_bfloat16* out = j.out + (static_cast<int64_t>(row) * j.heads_x + h) * D;
+#pragma unroll 4
+        for (int x = lane_id(); x < rows * (D / 8); x += 32) {
+          const int ro = x / (D / 8), co = x % (D / 8) * 8;
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ro) * j.heads_x * D + co) =
+              *reinterpret_cast<const uint4*>(so + sw128_offset(ro, co, kLinearChunk));
+        }
+        fence_proxy_async_smem();
       }
-      bulk_wait<0>();
+      warp_arrive(&bar_empty[b]);
     }
+    if (lane_id() == 0) bulk_wait<0>();
   } else if (!kStates && warp >= 4 && warp < 8) {
     // ---------------- scores ----------------
     const int wq = warp & 3, i = threadIdx.x & 127;   // row of the chunk, TMEM lane
@@ -583,7 +594,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     auto output = [&](int n) -> bool {
       if (!wait(&bar_o, n & 1, ac)) return false;
       tc_fence_after();
-      const int rows = chunk_len(n);
       const uint32_t tO = tmem + (static_cast<uint32_t>(wq * 32) << 16) + c0;
       uint8_t* so = ring + (2 * (n + 1) * inner - 1) % NSLOT * C::TILE;
 #pragma unroll 1
@@ -603,17 +613,8 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       }
       tc_fence_before();
       warp_arrive(&bar_of);
-      if (rows < kLinearChunk) {   // rows behind the sequence are another's: plain stores
-        named_bar_sync(1, 256);
-        __nv_bfloat16* out = j.out + (static_cast<int64_t>(pl.row0 + chunk_row(n)) * j.heads_x + h) * D;
-        for (int x = tid; x < rows * (D / 8); x += 256) {
-          const int ro = x / (D / 8), co = x % (D / 8) * 8;
-          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(ro) * j.heads_x * D + co) =
-              *reinterpret_cast<const uint4*>(so + sw128_offset(ro, co, kLinearChunk));
-        }
-      }
       fence_proxy_async_smem();
-      warp_arrive(&bar_out);
+      warp_arrive(&bar_out[n % NSLOT]);
       return true;
     };
     int n = 0, g = 0;

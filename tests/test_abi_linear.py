@@ -26,7 +26,7 @@ def _make(cls, base, kw):
 
 
 def _ptrs(n, at):
-    v = [FAKE + 0x10000 * i for i in range(n)]
+    v = [FAKE + (i << 24) for i in range(n)]
     for i, x in at.items():
         v[i] = x
     return [ctypes.c_void_p(x) for x in v]
@@ -85,7 +85,7 @@ BAD = [(dict(num_seqs=0), 1), (dict(tokens=-1), 1), (dict(tokens=7), 1), (dict(s
        (dict(heads_q=7), 1), (dict(heads_kv=0), 1), (dict(head_dim=0), 1), (dict(head_dim=96), 2), (dict(head_dim=256), 2),
        (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(log_decay=None), 1), (dict(log_decay=FAKE + 2), 3),
        (dict(cu_seqlens=FAKE + 2), 3), (dict(error_word=FAKE + 2), 3), (dict(heads_q=1 << 17), 2),
-       (dict(cu_seqlens=FAKE, tokens=1 << 28), 2)]
+       (dict(cu_seqlens=FAKE, tokens=1 << 28), 2), (dict(cu_seqlens=FAKE, num_seqs=1 << 26), 2)]
 
 
 @pytest.mark.parametrize("kw,code", BAD)
@@ -109,12 +109,15 @@ def test_linear_pointers(L):
         assert _fwd(L, at={i: FAKE + 8}) == 3
     for i in (4, 5, 9):
         assert _bwd(L, at={i: FAKE + 8}) == 3
-    assert _fwd(L, at={5: FAKE + 0x30000}) == 1      # the final state over the initial one
-    assert _bwd(L, at={9: FAKE + 0x50000}) == 1
+    far = {i: (i + 1) << 24 for i in range(11)}      # states of 256 KB, apart
+    for x in (0, 16, 0x3fff0, -0x3fff0):              # the final state over the initial one
+        assert _fwd(L, at={**{i: far[i] for i in range(7)}, 5: far[3] + x}, ws=0) == 1
+        assert _bwd(L, at={**far, 9: far[5] + x}, ws=0) == 1 and _bwd(L, at={**far, 9: far[4] + x}, ws=0) == 1
     for s in ("q_stride", "k_stride", "v_stride"):
         for x in (8, 1028, -1024):
             assert _fwd(L, {s: x}) == 1 and _bwd(L, {s: x}) == 1
     assert _bwd(L, dict(dout_stride=1028)) == 1
+    assert _fwd(L, dict(num_seqs=0, seqlen=0, tokens=0)) == 0 and _bwd(L, dict(num_seqs=0, seqlen=0, tokens=0)) == 0
     # without a token and without a state wanted, nothing is enqueued
     assert _fwd(L, dict(seqlen=0, tokens=0), {i: 0 for i in range(7)}) == 0
     assert _bwd(L, dict(seqlen=0, tokens=0), {i: 0 for i in range(11)}) == 0

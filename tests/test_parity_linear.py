@@ -151,7 +151,7 @@ def test_decay_out_of_range_is_flagged():
 def test_bad_cu_seqlens_is_flagged():
     s = Rows([60, 60], 2, 2, 64, pad=8, seed=11)
     x = [t.nan_to_num().to(DEV) for t in (s.q, s.k, s.v, s.do)]
-    for cu in ([0, 60, 200], [0, 100, 60], [-5, 60, 120], [0, 1 << 30, 120]):
+    for cu in ([0, 60, 200], [0, 100, 60], [-5, 60, 120], [0, 1 << 30, 120], [5, 60, 120]):
         err = torch.zeros(1, **I32)
         kw = dict(cu_seqlens=torch.tensor(cu, **I32), error_word=err)
         A.linear_attn_fwd(*x[:3], s.g.to(DEV), **kw)
@@ -172,6 +172,11 @@ def test_no_tokens():
     assert not A.linear_attn_fwd(q, q, q, g, want_final_state=True)[1].any()
     d = A.linear_attn_bwd(q, q, q, q, g, dfinal_state=init, want_dinitial_state=True)
     assert torch.equal(d[3], init)
+    q = torch.empty(0, 9, 3, 64, dtype=BF, device=DEV)                      # no sequence
+    o, fin = A.linear_attn_fwd(q, q, q, g, want_final_state=True)
+    assert o.shape == q.shape and fin.shape == (0, 3, 64, 64)
+    assert A.linear_attn_step(q[:, 0], q[:, 0], q[:, 0], g, init).shape == (0, 3, 64)
+    assert A.attn_rotary_fwd(q, q, A.attn_rotary_table(9, 64, device=DEV))[0].shape == q.shape
 
 
 def test_fused_projection_and_another_stream():
