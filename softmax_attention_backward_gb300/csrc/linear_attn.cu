@@ -30,7 +30,11 @@ template <int D, int NS, bool kStates>
 struct Cfg {
   static constexpr int C = kLinearChunk;
   static constexpr int TILE = C * D * 2;
-  static constexpr int H_BYTES = kStates ? 0 : D * D * 2;
+  // H meets X in two bf16 terms, or, where there is no room (heads of 128 with terms of the
+  // keys beside them), in one, the keys then in two or three: with P's rounding and the output's,
+  // one of 2^-9 is left on a product's way, as in attn_fwd
+  static constexpr int HTERMS = NS == 1 || D == 64 ? 2 : 1;
+  static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
   static constexpr int EXTRA = (NS - 1) * TILE;   // second and third terms of the decayed keys
   // the tiles that fit: 227 KB of shared memory, 1 KB of it for the alignment
   static constexpr int FIT = (227 * 1024 - 2048 - H_BYTES - EXTRA) / TILE;
@@ -45,22 +49,28 @@ struct Cfg {
   static constexpr int UNROLL = D == 64 ? 8 : 2;
   static constexpr int HC = D / 2;                // state columns of a thread
   // S of a step is formed while the step before is still at work, where the ring can hold both
-  static constexpr bool AHEAD = XBUF == 2;
+  static constexpr bool AHEAD = !kStates && NSLOT >= 4;
   static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
   // without S and O there is room for two of G: a chunk's is read while the next one's is formed
   static constexpr int GBUF = kStates ? 2 : 1;
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
 };
 
-// log2 of a head's decay, at most 0.  -inf becomes a number whose products with 0
+// The logarithm of a head's decay, at most 0.  -inf becomes a number whose products with 0
 // and with token counts stay finite.
-__device__ __forceinline__ float log2_decay(const LinearArgs& a, int h) {
+__device__ __forceinline__ float log_decay_of(const LinearArgs& a, int h) {
   float g = __ldg(a.log_decay + h);
   if (!(g <= 0.f)) {
     if (a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
     g = 0.f;
   }
-  return fmaxf(g * kLog2e, -1e6f);
+  return fmaxf(g, -1e6f);
+}
+
+// exp(g m) for a state that is returned: of the product and, to first order, its rounding.
+__device__ __forceinline__ float decay_exact(float g, float m) {
+  const float p = g * m, e = expf(p);
+  return fmaf(e, fmaf(g, m, -p), e);
 }
 
 // The rows of sequence n, kept within the tensors whatever cu holds.
@@ -181,6 +191,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   __shared__ int abort_flag;
   __shared__ Place s_place;
   __shared__ __align__(16) float s_tab[32];   // decays within a block of 32 columns
+  __shared__ float s_keep[2];                 // a chunk's decay
   __shared__ float s_diag[64];                // those of its diagonal, scaled: entry 32 + j - i
 
   const int warp = warp_id();
@@ -222,13 +233,19 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
-  const float l2 = log2_decay(a, hkv);
+  const float ln = log_decay_of(a, hkv), l2 = ln * kLog2e;
   if (warp == 2) {
     const Place p = find_place(a, j, slot);
     if (lane_id() == 0) s_place = p;
   }
   if (warp == 3) {
     const int x = lane_id();
+    if (NS > 1 && x == 0) {
+      // in two parts: an error of a chunk's decay would grow with every chunk that a state crosses
+      const double keep = exp(static_cast<double>(ln) * kLinearChunk);
+      s_keep[0] = static_cast<float>(keep);
+      s_keep[1] = static_cast<float>(keep - s_keep[0]);
+    }
     s_tab[x] = ex2(l2 * (j.backwards ? x : 31 - x));
     s_diag[x] = j.backwards ? 0.f : a.scale * ex2(l2 * (32 - x));
     s_diag[32 + x] = j.backwards || x == 0 ? a.scale * ex2(l2 * x) : 0.f;
@@ -250,7 +267,13 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   auto chunk_row = [&](int n) { return (back ? c_hi - 1 - n : c_lo + n) * kLinearChunk; };
   auto chunk_len = [&](int n) { return min(kLinearChunk, pl.len - chunk_row(n)); };
   const bool want_last = kStates || (is_end && j.last && h == hkv * static_cast<int>(j.fd_kv.d));
-  const int terms = NS == 1 || !want_last ? 1 : j.terms;   // bf16 terms of the decayed keys
+  // bf16 terms of the decayed keys: three for a state that is returned
+  const int terms = NS > 1 && want_last ? j.terms : C::HTERMS == 2 ? 1 : 2;
+  // The tensor cores cut a sum off rather than round it, at each of the 8 products of a step.  Where
+  // a state is returned the smaller terms are added first, and the steps of a chunk one by
+  // one into H (2 sequences of 4937 tokens, 8 query heads a KV head: 3.6e-6 of the state's
+  // root mean square with the leading terms first and a chunk's steps in one sum).
+  const bool each = NS > 1 && terms > 2;
   const int n_grow = want_last ? n_walk : n_walk - 1;   // chunks that the state takes in
   const int steps = n_walk * inner;                     // a step: one inner head of a chunk
 
@@ -317,21 +340,23 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     // what the state takes in
     auto keys = [&](int t, int n, int g) -> bool {
       if (!landed(2 * t + 1) || (kStates && !landed(2 * t))) return false;
+      const int i = each ? t : n, b = i % C::GBUF;   // G's turn and buffer
       if (n < n_grow) {
         if (!warp_wait(&bar_y[t & 1], (t >> 1) & 1, ac)) return false;
-        if (g == 0 && n >= C::GBUF && !warp_wait(&bar_gf[n % C::GBUF], (n / C::GBUF - 1) & 1, ac)) return false;
+        if ((each || g == 0) && i >= C::GBUF && !warp_wait(&bar_gf[b], (i / C::GBUF - 1) & 1, ac)) return false;
         tc_fence_after();
         const uint64_t dy = desc_advance(dm0, slot(2 * t) * C::TILE), dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
+        uint32_t add = !each && g > 0;
 #pragma unroll 1
-        for (int e = 0; e < terms; ++e)
+        for (int e = terms - 1; e >= 0; --e)
 #pragma unroll C::UNROLL
-          for (int k = 0; k < 8; ++k)
-            umma_ss_w(tmem + C::COL_G - 128 * (n % C::GBUF),
+          for (int k = 0; k < 8; ++k, add = 1)
+            umma_ss_w(tmem + C::COL_G - 128 * b,
                       desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
-                      desc_advance(dz, mnmajor_step_bytes(k)), idG, (g > 0 || e > 0 || k > 0) ? 1u : 0u);
+                      desc_advance(dz, mnmajor_step_bytes(k)), idG, add);
       }
       umma_commit_w(&bar_empty[slot(2 * t)]);
-      if (n < n_grow && g == inner - 1) umma_commit_w(&bar_g[n % C::GBUF]);
+      if (n < n_grow && (each || g == inner - 1)) umma_commit_w(&bar_g[b]);
       return true;
     };
     // X H, at a chunk's first step; behind the S of its last step, X is free
@@ -342,12 +367,12 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         tc_fence_after();
         const uint64_t dx = desc_advance(dx0, bx * C::TILE);
 #pragma unroll C::UNROLL
-        for (int k = 0; k < D / 16; ++k)
-          umma_ss_w(tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k)),
-                    desc_advance(dH, mnmajor_step_bytes(k)), idO, k > 0);
+        for (int k = 0; k < C::HTERMS * D / 16; ++k)   // (the second term lies behind the first)
+          umma_ss_w(tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k % (D / 16))),
+                    desc_advance(dH, (k / (D / 16)) * (D * D * 2) + mnmajor_step_bytes(k % (D / 16))), idO, k > 0);
         umma_commit_w(&bar_qh);
       }
-      if (g == inner - 1) umma_commit_w(&bar_xempty[bx]);
+      if (C::AHEAD ? inner == 1 : g == inner - 1) umma_commit_w(&bar_xempty[bx]);
       return true;
     };
     auto values = [&](int t, int g) -> bool {
@@ -370,9 +395,13 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if constexpr (kStates) {
         if (!keys(t, n, g)) break;
       } else if constexpr (C::AHEAD) {
-        if (!keys(t, n, g) || !carried(n, g)) break;
-        if (t + 1 < steps && !scores(t + 1, n + last, last ? 0 : g + 1)) break;
+        // (with one buffer for X the next chunk's has to wait for X H of this one)
+        const bool late = C::XBUF == 1 && last;
+        if (C::XBUF == 1 ? !carried(n, g) || !keys(t, n, g) : !keys(t, n, g) || !carried(n, g)) break;
+        if (!late && t + 1 < steps && !scores(t + 1, n + last, last ? 0 : g + 1)) break;
+        if (g + 2 == inner) umma_commit_w(&bar_xempty[n % C::XMOD]);
         if (!values(t, g)) break;
+        if (late && t + 1 < steps && !scores(t + 1, n + 1, 0)) break;
       } else {
         if (!scores(t, n, g) || !carried(n, g) || !keys(t, n, g) || !values(t, g)) break;
       }
@@ -541,7 +570,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       for (int t = 0; t < before; ++t) {
         const int sg = back ? pl.nseg - 1 - t : t;
         const int lo = sg * pl.per * kLinearChunk, hi = min(pl.len, lo + pl.per * kLinearChunk);
-        const float keep = ex2(l2 * max(hi - lo, 0));
+        const float keep = NS > 1 ? decay_exact(ln, max(hi - lo, 0)) : ex2(l2 * max(hi - lo, 0));
         const float4* g = reinterpret_cast<const float4*>(
             j.parts + (static_cast<int64_t>(slot + sg - pl.seg) * a.heads_kv + hkv) * D * D);
         if (mine)
@@ -559,31 +588,48 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       if (mine)
 #pragma unroll
         for (int x = 0; x < C::HC; x += 8) {
-          const uint4 v = make_uint4(pack_bf16(H[x], H[x + 1]), pack_bf16(H[x + 2], H[x + 3]),
-                                     pack_bf16(H[x + 4], H[x + 5]), pack_bf16(H[x + 6], H[x + 7]));
-          *reinterpret_cast<uint4*>(sH + sw128_offset(r, c0 + x, D)) = v;
+          uint32_t w[4], rest[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float lo = H[x + 2 * y], hi = H[x + 2 * y + 1];
+            w[y] = pack_bf16(lo, hi);
+            rest[y] = pack_bf16(lo - __uint_as_float(w[y] << 16), hi - __uint_as_float(w[y] & 0xffff0000u));
+          }
+          const uint32_t at = sw128_offset(r, c0 + x, D);
+          *reinterpret_cast<uint4*>(sH + at) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (C::HTERMS == 2)
+            *reinterpret_cast<uint4*>(sH + D * D * 2 + at) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
       fence_proxy_async_smem();
       warp_arrive(&bar_h);
     };
     if (!kStates && n_walk > 0) publish();
-    // what chunk n adds, and then the state as the next chunk's operand
-    auto grow = [&](int n) -> bool {
-      const int b = n % C::GBUF;
-      if (!wait(&bar_g[b], (n / C::GBUF) & 1, ac)) return false;
+    // what G's i-th turn holds, of chunk n, its first or its last; behind the last, the state as the
+    // next chunk's operand
+    auto grow = [&](int i, int n, bool first, bool last) -> bool {
+      const int b = i % C::GBUF;
+      if (!wait(&bar_g[b], (i / C::GBUF) & 1, ac)) return false;
       tc_fence_after();
-      const float keep = ex2(l2 * chunk_len(n));
+      const int rows = chunk_len(n);
+      float keep = ex2(l2 * rows), keep2 = 0.f;
+      if (NS > 1) {
+        keep = !first ? 1.f : rows == kLinearChunk ? s_keep[0] : decay_exact(ln, rows);
+        keep2 = first && rows == kLinearChunk ? s_keep[1] : 0.f;
+      }
 #pragma unroll
       for (int x = 0; x < C::HC; x += 32) {
         uint32_t v[32];
         tmem_ld32_nowait(tG - 128 * b + x, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int y = 0; y < 32; ++y) H[x + y] = fmaf(keep, H[x + y], __uint_as_float(v[y]));
+        for (int y = 0; y < 32; ++y) {
+          const float add = NS > 1 ? fmaf(keep2, H[x + y], __uint_as_float(v[y])) : __uint_as_float(v[y]);
+          H[x + y] = fmaf(keep, H[x + y], add);
+        }
       }
       tc_fence_before();
       warp_arrive(&bar_gf[b]);
-      if (kStates || n + 1 >= n_walk) return true;
+      if (kStates || !last || n + 1 >= n_walk) return true;
       if (!wait(&bar_qh, n & 1, ac)) return false;   // the product that read the state before
       publish();
       return true;
@@ -620,11 +666,15 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     int n = 0, g = 0;
     for (int t = 0; t <= steps; ++t) {
       const bool next = g == 0 && n > 0;   // a chunk is behind these warps
-      if (!kStates && next && n - 1 < n_grow && !grow(n - 1)) break;
-      if (!kStates && !C::AHEAD && next && !output(n - 1)) break;
+      // what is behind of G: a step, or the steps of a chunk
+      const bool grown = each ? t > 0 && t <= n_grow * inner : next && n - 1 < n_grow;
+      const int gi = each ? t - 1 : n - 1, gn = g == 0 ? n - 1 : n;
+      if (!kStates && grown && !grow(gi, gn, !each || inner == 1 || g == 1, g == 0)) break;
+      if (!kStates && C::XBUF == 1 && next && !output(n - 1)) break;
       if (t < steps && n < n_grow) {
         const int rows = chunk_len(n);
-        const float d = back ? a.scale * ex2(l2 * (row + 1)) : ex2(l2 * max(rows - 1 - row, 0));
+        const int far = back ? row + 1 : max(rows - 1 - row, 0);
+        const float d = (back ? a.scale : 1.f) * (NS > 1 ? decay_exact(ln, far) : ex2(l2 * far));
         const int sy = 2 * t % NSLOT;
         if (!wait(&bar_full[sy], (2 * t / NSLOT) & 1, ac)) break;
         if (!kStates && !wait(&bar_s[t & 1], (t >> 1) & 1, ac)) break;
@@ -680,8 +730,8 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         fence_proxy_async_smem();
         warp_arrive(&bar_y[t & 1]);
       }
-      if (kStates && next && !grow(n - 1)) break;
-      if (!kStates && C::AHEAD && next && !output(n - 1)) break;
+      if (kStates && grown && !grow(gi, gn, !each || inner == 1 || g == 1, g == 0)) break;
+      if (!kStates && C::XBUF != 1 && next && !output(n - 1)) break;
       if (++g == inner) {
         g = 0;
         ++n;
