@@ -21,6 +21,8 @@ constexpr int kLinearJobs = 3;      // outputs of one launch at most
 // one of the first and the third.
 struct LinearJob {
   CUtensorMap mx, my, mz, mo;   // maps over [tokens, heads, head_dim], boxes of a chunk and 64 dims
+  const __nv_bfloat16 *x, *y, *z;           // the same rows, for the kernel without maps
+  int64_t x_stride, y_stride, z_stride;     // elements from token to token
   __nv_bfloat16* out;       // dense, heads_x heads; null: states only
   int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;
@@ -50,6 +52,41 @@ struct LinearArgs {
   int32_t* err;
 };
 
+// The logarithm of a head's decay, at most 0.  -inf becomes a number whose products with 0
+// and with token counts stay finite.
+__device__ __forceinline__ float log_decay_of(const LinearArgs& a, int h) {
+  float g = __ldg(a.log_decay + h);
+  if (!(g <= 0.f)) {
+    if (a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
+    g = 0.f;
+  }
+  return fmaxf(g, -1e6f);
+}
+
+// The rows of sequence n, kept within the tensors whatever cu holds.
+__device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& row0, int& len) {
+  if (!a.cu) {
+    row0 = n * a.seqlen;
+    len = a.seqlen;
+    return;
+  }
+  const int b = __ldg(a.cu + n), e = __ldg(a.cu + n + 1);
+  row0 = min(max(b, 0), a.tokens);
+  const int end = min(max(e, row0), a.tokens);
+  len = end - row0;
+  if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
+}
+
 cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, cudaStream_t st);
+
+// Sequences of at most this many tokens (packed: all of them together) go token by token
+// (linear_short.cu).  us with and without, 32 heads of 128, a graph's launch of 5 us included:
+//                              8 tokens       16 tokens      64 x 8      64 x 16
+//   forward                  12.4 / 13.5    15.5 / 13.5    88 / 112    152 / 114
+//   forward, states          12.4 / 21.6    17.5 / 21.6   102 / 206    160 / 207
+//   backward, 8 KV heads     18.6 / 22.7    27.8 / 22.7   177 / 218    321 / 218
+// (of 64 dims 64 x 8: 41 / 93, 64 x 16: 62 / 94).
+constexpr int kLinearShort = 8;
+cudaError_t launch_linear_short(const LinearArgs& a, int head_dim, cudaStream_t st);
 
 }  // namespace attn

@@ -193,13 +193,23 @@ struct Rows {
   int heads;
 };
 
+// Whether no sequence can have more than a few tokens.
+bool all_short(const linear_attn_problem_t* p) {
+  return (p->cu_seqlens ? p->tokens : p->seqlen) <= kLinearShort && p->num_seqs < (1 << 24);
+}
+
+void set_rows(LinearJob* j, const Rows& x, const Rows& y, const Rows& z) {
+  j->x = static_cast<const __nv_bfloat16*>(x.p), j->x_stride = x.stride;
+  j->y = static_cast<const __nv_bfloat16*>(y.p), j->y_stride = y.stride;
+  j->z = static_cast<const __nv_bfloat16*>(z.p), j->z_stride = z.stride;
+}
+
 bool map_rows(CUtensorMap* m, const linear_attn_problem_t* p, const Rows& r) {
   return make_bf16_heads_map(m, r.p, p->tokens, r.heads, p->head_dim, r.stride, 1, kLinearChunk);
 }
 
-bool map_out(LinearJob* j, const linear_attn_problem_t* p, void* out, int heads) {
-  j->out = static_cast<__nv_bfloat16*>(out);
-  return map_rows(&j->mo, p, {out, static_cast<int64_t>(heads) * p->head_dim, heads});
+bool map_out(LinearJob* j, const linear_attn_problem_t* p) {
+  return map_rows(&j->mo, p, {j->out, static_cast<int64_t>(j->heads_x) * p->head_dim, j->heads_x});
 }
 
 // What a job takes from the problem; `shared`: heads of x per KV head, `way`: 0 forwards, 1 backwards.
@@ -282,13 +292,15 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   LinearArgs a = make_args(p);
   a.jobs = 1;
   LinearJob& j = a.job[0];
-  if (!map_rows(&j.mx, p, rq) || !map_rows(&j.my, p, rk) || !map_rows(&j.mz, p, rv) ||
-      !map_out(&j, p, o, p->heads_q))
-    return ATTN_ERR_CUDA;
   set_job(j, p, p->heads_q, p->heads_q / p->heads_kv, 1, cut, 0);
+  set_rows(&j, rq, rk, rv);
+  j.out = static_cast<__nv_bfloat16*>(o);
   j.first = initial_state;
   j.last = final_state;
   j.terms = final_state ? 3 : 1;
+  if (all_short(p)) return launch_linear_short(a, p->head_dim, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (!map_rows(&j.mx, p, rq) || !map_rows(&j.my, p, rk) || !map_rows(&j.mz, p, rv) || !map_out(&j, p))
+    return ATTN_ERR_CUDA;
   j.parts = static_cast<float*>(workspace);
   if (cut.parts[0]) {
     LinearArgs s = make_args(p);
@@ -331,18 +343,25 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   a.jobs = 3;
   // the longest walks first
   LinearJob &jv = a.job[cut.dq_first], &jk = a.job[cut.dq_first + 1], &jq = a.job[cut.dq_first ? 0 : 2];
-  if (!map_rows(&jv.mx, p, rk) || !map_rows(&jv.my, p, rq) || !map_rows(&jv.mz, p, rd) || !map_rows(&jk.mx, p, rv) ||
-      !map_out(&jv, p, dv, p->heads_kv) || !map_out(&jk, p, dk, p->heads_kv) || !map_out(&jq, p, dq, p->heads_q))
-    return ATTN_ERR_CUDA;
-  jk.my = jv.mz, jk.mz = jv.my;
-  jq.mx = jv.mz, jq.my = jk.mx, jq.mz = jv.mx;
   set_job(jv, p, p->heads_kv, 1, group, cut, 1);
   set_job(jk, p, p->heads_kv, 1, group, cut, 1);
   set_job(jq, p, p->heads_q, group, 1, cut, 0);
+  set_rows(&jv, rk, rq, rd);
+  set_rows(&jk, rv, rd, rq);
+  set_rows(&jq, rd, rv, rk);
+  jv.out = static_cast<__nv_bfloat16*>(dv);
+  jk.out = static_cast<__nv_bfloat16*>(dk);
+  jq.out = static_cast<__nv_bfloat16*>(dq);
   jv.first = jk.first = dfinal_state;
   jv.last = dinitial_state;
   jq.first = initial_state;
   jk.transposed = jq.transposed = 1;
+  if (all_short(p)) return launch_linear_short(a, p->head_dim, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (!map_rows(&jv.mx, p, rk) || !map_rows(&jv.my, p, rq) || !map_rows(&jv.mz, p, rd) || !map_rows(&jk.mx, p, rv))
+    return ATTN_ERR_CUDA;
+  jk.my = jv.mz, jk.mz = jv.my;
+  jq.mx = jv.mz, jq.my = jk.mx, jq.mz = jv.mx;
+  if (!map_out(&jv, p) || !map_out(&jk, p) || !map_out(&jq, p)) return ATTN_ERR_CUDA;
   float* ws = static_cast<float*>(workspace);
   if (cut.parts[1]) {
     jv.parts = ws;

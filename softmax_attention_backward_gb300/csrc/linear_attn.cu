@@ -56,35 +56,10 @@ struct Cfg {
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
 };
 
-// The logarithm of a head's decay, at most 0.  -inf becomes a number whose products with 0
-// and with token counts stay finite.
-__device__ __forceinline__ float log_decay_of(const LinearArgs& a, int h) {
-  float g = __ldg(a.log_decay + h);
-  if (!(g <= 0.f)) {
-    if (a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
-    g = 0.f;
-  }
-  return fmaxf(g, -1e6f);
-}
-
 // exp(g m) for a state that is returned: of the product and, to first order, its rounding.
 __device__ __forceinline__ float decay_exact(float g, float m) {
   const float p = g * m, e = expf(p);
   return fmaf(e, fmaf(g, m, -p), e);
-}
-
-// The rows of sequence n, kept within the tensors whatever cu holds.
-__device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& row0, int& len) {
-  if (!a.cu) {
-    row0 = n * a.seqlen;
-    len = a.seqlen;
-    return;
-  }
-  const int b = __ldg(a.cu + n), e = __ldg(a.cu + n + 1);
-  row0 = min(max(b, 0), a.tokens);
-  const int end = min(max(e, row0), a.tokens);
-  len = end - row0;
-  if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
 }
 
 __device__ __forceinline__ int chunks_of(int len) { return (len + kLinearChunk - 1) / kLinearChunk; }

@@ -22,6 +22,28 @@ def test_lengths(D, lens, states):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (6, 2), (12, 1), (40, 2)])
+@pytest.mark.parametrize("lens,pad", [([1], 0), ([2, 2, 2], 0), ([7] * 5, 0), ([8] * 3, 0), ([9] * 3, 0), ([3, 0, 1, 2], 2),
+                                      ([0, 8], 0), ([0], 3), ([5, 1], 3)])
+@pytest.mark.parametrize("decay", [None, -math.inf])
+def test_few_tokens(D, hq, hkv, lens, pad, decay):
+    # Up to 8 tokens (packed: in all) nothing but an output is rounded to bf16: half a step of it, and
+    # fp32 sums and products, of 8 tokens' 40 / 2 heads and 128 dims in chains of 160 and 32 at most, 2^-24 each.
+    for packed in (False, True):
+        for states in (False, True):
+            s = Rows(lens, hq, hkv, D, pad=pad, decay=decay, states=states, seed=31)
+            got = s.call(packed=packed, states=states)
+            check(s, got, states=states)
+            if s.T > 8 if packed or not s.dense else max(lens) > 8:
+                continue
+            for x, w, m in zip(got, *s.answer()):
+                if x is not None:
+                    x = x.to(F64)[s.live] if x.dtype == BF else x.to(F64)
+                    tol = (HALF * 1.01 * w.abs() if x.dim() == 3 else 0) + 2.0 ** -16 * m + 1e-37
+                    assert ((x - w).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 1), (6, 2), (3, 3), (10, 5), (16, 1)])
 @pytest.mark.parametrize("states", [False, True])
 def test_heads(D, hq, hkv, states):
