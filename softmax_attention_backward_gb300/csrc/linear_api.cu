@@ -20,8 +20,9 @@ bool good_stride(int64_t stride, int heads, int dim, int64_t* out) {
 
 attn_status_t check(const linear_attn_problem_t* p) {
   if (!p) return ATTN_ERR_INVALID_ARG;
-  if (p->num_seqs < 0 || p->tokens < 0 || (p->num_seqs == 0 && p->tokens > 0) || p->heads_q <= 0 || p->heads_kv <= 0 || p->head_dim <= 0 ||
-      p->heads_q % p->heads_kv || !std::isfinite(p->scale))
+  if (p->num_seqs < 0 || p->tokens < 0 || (p->num_seqs == 0 && p->tokens > 0) ||
+      p->heads_q <= 0 || p->heads_kv <= 0 || p->head_dim <= 0 || p->heads_q % p->heads_kv ||
+      !std::isfinite(p->scale))
     return ATTN_ERR_INVALID_ARG;
   if (!p->cu_seqlens &&
       (p->seqlen < 0 || static_cast<int64_t>(p->num_seqs) * p->seqlen != p->tokens))
@@ -47,11 +48,11 @@ struct Cut {
 // What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
 // heads (S, P Z and the state's product), `state` for each inner head of a chunk in the pass over
 // the states alone.  Measured, 64 chunks against 32 of 8192 and 4096 tokens: head_dim 128,
-// 1, 2, 4 and 8 inner heads, 183, 292, 517 and 957 us; head_dim 64, 132, 220, 402 and 767.
+// 1, 2, 4 and 8 inner heads, 218, 341, 558 and 987 us; head_dim 64, 140, 229, 412 and 775.
 struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
 };
-constexpr Rates kRates[2] = {{0.46, 1.40, 0.80, 0.2}, {1.00, 1.70, 0.94, 0.65}};
+constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2}, {1.55, 1.72, 0.94, 0.65}};
 constexpr double kStart = 3.0;     // a walk's start and end
 constexpr double kLaunch = 4.0;    // of the pass over the states
 constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
@@ -75,11 +76,11 @@ double makespan(int sms, double na, double ca, double nb, double cb) {
   return hi > high ? hi : high;
 }
 
-// Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, o
-// jobs cut into 3 and the others into 4 segments of a sequence 274, uncut 511; forward of 12 packed
-// sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 8 chunks 86, of 4 100, of
-// 16 103; one sequence of 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161,
-// of 16 169.
+// Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, dq
+// uncut and the others in 8 segments of a sequence 286, in 6 317, in 2 405; forward of 12 packed
+// sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 8 chunks 86, of 6 (taken) 87, of 4
+// 102, of 16 97; their backward, 7 and 20 chunks, 115, taken 124; one sequence of 65536 tokens,
+// 8 heads on 2 of 128, segments of 27 chunks 145, of 32 165, of 16 186.
 Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   const int group = p->heads_q / p->heads_kv;
   const Rates& rate = kRates[p->head_dim == 128];
