@@ -79,12 +79,15 @@ size_t linear_attn_bwd_workspace_size(const linear_attn_problem_t* p);
 
 /*
  * Forward.  initial_state and final_state may be NULL (zeros; not wanted).
- * The products run on bf16 operands with fp32 sums: within a chunk of 128 tokens
- * the decayed scores, and where they meet a later chunk's rows the state, are
- * rounded to bf16 (2^-9 of each); the state itself is kept in fp32, of keys
- * times their decays in bf16 (2^-9 of each) where no state is returned, and in
- * three bf16 terms (2^-25) where one is.  A value that is infinite or NaN reaches
- * the rows that see it and, through 0 * NaN, earlier rows of its chunk.
+ * The products run on bf16 operands with fp32 sums.  Within a chunk of 128 tokens
+ * the decayed scores are rounded to bf16 (2^-9 of each).  The state is kept in
+ * fp32, and for the chunks behind either the keys times their decays or the
+ * state that meets a chunk's rows is rounded so, the other held in two
+ * terms (2^-17).  A state that is returned comes of keys in three terms (2^-25), its
+ * error below that of a sum over the tokens in fp32.  Where no sequence can be longer
+ * than 8 tokens (seqlen, or with cu_seqlens `tokens`) all is fp32 but o.
+ * A value that is infinite or NaN reaches the rows that see it as either and, through
+ * 0 * NaN, earlier rows of its chunk.
  * The result is bitwise reproducible on one device.
  */
 attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const void* q, const void* k,

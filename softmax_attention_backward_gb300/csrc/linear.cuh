@@ -26,7 +26,7 @@ struct LinearJob {
   __nv_bfloat16* out;       // dense, heads_x heads; null: states only
   int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;
-  int terms;                // bf16 terms of a decayed key: 1, or 3 where `last` is returned
+  int terms;                // bf16 terms of a decayed key: 3 where `last` is returned, else 1 (or 2, see Cfg)
   int inner;                // heads of y and z that meet one head of x
   FastDiv fd_heads;         // heads_x
   FastDiv fd_kv;            // heads of x per KV head

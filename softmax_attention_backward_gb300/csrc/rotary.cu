@@ -8,13 +8,14 @@
 // quadrant, the rest is t quarter turns with |t| <= 1/2, and with q = pi / 2
 //   sin(q t) = q t - (q t)^3 / 3! + ... - (q t)^11 / 11!...,  cos(q t) = 1 - (q t)^2 / 2! + ...
 // (Taylor's series, cut behind t^9 and t^10: 2^-29 and 2^-33 of the sum).  Bound by
-// memory: 4 cosines and sines a thread, 16 bytes each.  131072 positions of 128:
-// 52 us with sincospi and 64-bit conversions, see TABLE_US here.
+// memory: 4 cosines and sines a thread, 16 bytes each.  131072 positions of 128 (67 MB):
+// 17.5 us, 5 of them a graph's launch; 52 with the angle in fp64 and sincospi.
 //
 // Rotation.  Bound by memory: every row is read and written once.  A thread holds
 // the angles of one unit of dims (two 16-byte pieces half the rotated part
 // apart, or one piece of adjacent pairs) and rotates it in up to four heads of a
-// token, all loads first; the angles come from L1 or L2, once for four heads.
+// token, all loads first; the angles come from L1 or L2, once for four heads.  4 x 4096
+// tokens of 32 + 8 heads of 128: 58.5 us with the launch, 50 for the bytes alone.
 #include <cuda_runtime.h>
 
 #include <cmath>
