@@ -45,6 +45,7 @@ struct LinearJob {
 struct LinearArgs {
   LinearJob job[kLinearJobs];
   int jobs;
+  int merged;               // 1: one job's items after the other's; `jobs` (all have as many): in turn
   int num_seqs, seqlen, tokens, heads_kv;
   float scale;
   const int32_t* cu;

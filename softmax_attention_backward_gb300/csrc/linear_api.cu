@@ -53,7 +53,7 @@ struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
 };
 constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2}, {1.55, 1.72, 0.94, 0.65}};
-constexpr double kStart = 3.0;     // a walk's start and end
+constexpr double kStart = 4.0;     // a walk's start and end
 constexpr double kLaunch = 4.0;    // of the pass over the states
 constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
 
@@ -79,8 +79,9 @@ double makespan(int sms, double na, double ca, double nb, double cb) {
 // Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, dq
 // uncut and the others in 8 segments of a sequence 286, in 6 317, in 2 405; forward of 12 packed
 // sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 8 chunks 86, of 6 (taken) 87, of 4
-// 102, of 16 97; their backward, 7 and 20 chunks, 115, taken 124; one sequence of 65536 tokens,
-// 8 heads on 2 of 128, segments of 27 chunks 145, of 32 165, of 16 186.
+// 102, of 16 97; backward of
+// 12 of up to 2500, 16 heads of 64, uncut 108, 10 and 20 chunks 118, 10 and 10 120; one sequence of
+// 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161, of 16 180.
 Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   const int group = p->heads_q / p->heads_kv;
   const Rates& rate = kRates[p->head_dim == 128];
@@ -88,9 +89,9 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   const bool packed = p->cu_seqlens != nullptr;
   const int most = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;   // of a sequence
   // packed sequences have lengths that the host does not know: half a chunk is taken to be empty in
-  // each, and the longest to be three times the average
+  // each, and the longest to be four times the average
   const double chunks = packed ? most + 0.5 * p->num_seqs : static_cast<double>(most) * p->num_seqs;
-  const int longest = packed ? std::min(most, std::max(4, static_cast<int>(3 * chunks / p->num_seqs))) : most;
+  const int longest = packed ? std::min(most, std::max(4, static_cast<int>(4 * chunks / p->num_seqs))) : most;
   struct Option {
     int chunks;
     double walks, cost, longest, states, state_cost, bytes;   // of one job
@@ -129,8 +130,10 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
       const Option &x = opt[0][i], &y = backward ? opt[1][j] : none;
       double t = x.longest > y.longest ? makespan(sms, x.walks, x.cost, 2 * y.walks, y.cost)
                                        : makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
-      // the longest of packed sequences may come last
-      t += 0.5 * std::max(x.longest - x.cost, y.longest - y.cost);
+      // the longest of packed sequences come first, of each job or, merged, of all
+      t = std::max(t, std::max(x.longest, y.longest));
+      if (backward && !(group == 1 && x.chunks == y.chunks))
+        t += 0.5 * std::max(x.longest - x.cost, y.longest - y.cost);
       t = std::max(t, (x.bytes + 2 * y.bytes) / kBytes);
       if (x.states + y.states > 0) t += kLaunch + makespan(sms, y.states, y.state_cost, x.states, x.state_cost);
       if ((i == 0 && j == 0) || t < least) least = t, best[0] = i, best[1] = j;
@@ -177,6 +180,7 @@ size_t workspace_bytes_of(const linear_attn_problem_t* p, const Cut& c) {
 
 LinearArgs make_args(const linear_attn_problem_t* p) {
   LinearArgs a{};
+  a.merged = 1;
   a.num_seqs = p->num_seqs;
   a.seqlen = p->seqlen;
   a.tokens = p->tokens;
@@ -371,6 +375,10 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   }
   jq.parts = ws;
   jv.terms = dinitial_state ? 3 : 1;
+  // walks of one length: the jobs' in turn, so that none's longest come late and the rows that
+  // they share are read together (12 packed sequences of up to 2500 tokens, 16 heads of 64, 130 ->
+  // 110 us; 4 x 4096 tokens of 32 heads of 128 339 -> 331)
+  if (group == 1 && cut.chunks[0] == cut.chunks[1]) a.merged = a.jobs;
   if (cut.parts[0] || cut.parts[1]) {
     LinearArgs s = make_args(p);
     if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);

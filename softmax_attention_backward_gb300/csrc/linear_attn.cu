@@ -63,6 +63,8 @@ struct Cfg {
   // S of a step is formed while the step before is still at work, where the ring can hold both: with
   // three tiles the wait for the next Y would hold up the Z that has to leave before it
   static constexpr bool AHEAD = !kStates && NSLOT >= 4;
+  // the warps that write the output
+  static constexpr bool OUT_BY_SCORES = XBUF == 1;
   static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
   // without S and O there is room for two of G: a chunk's is read while the next one's is formed
   static constexpr int GBUF = kStates ? 2 : 1;
@@ -80,18 +82,23 @@ __device__ __forceinline__ int segments_of(int len, int seg_chunks) {
   return max(1, (chunks_of(len) + seg_chunks - 1) / seg_chunks);
 }
 
-// A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most.
+// A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most; `first` is
+// the place of the sequence's first segment among all of them.
 struct Place {
-  int n, row0, len, seg, nseg, per;
+  int n, row0, len, seg, nseg, per, first;
 };
 
-// The place of a slot, by one warp; n = -1 where the slot holds none.
+// The place that the CTAs of a slot take, by one warp; n = -1 where there is none.  The longer
+// walks of each 32 packed sequences come first, so that no SM is left with one at the
+// end (backward of 12 sequences of up to 2500 tokens, 16 heads of 64, the jobs' walks in turn: 110
+// us, 118 with each job's in the sequences' order).
 __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob& j, int slot) {
-  Place p{-1, 0, 0, 0, 1, 1};
+  Place p{-1, 0, 0, 0, 1, 1, 0};
   if (!a.cu) {
     p.nseg = segments_of(a.seqlen, j.seg_chunks);
     p.n = slot / p.nseg;
     p.seg = slot - p.n * p.nseg;
+    p.first = slot - p.seg;
     if (p.n >= a.num_seqs) p.n = -1;
     else sequence_rows(a, p.n, p.row0, p.len);
   } else {
@@ -108,7 +115,15 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
         const int o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
       }
-      const bool here = slot >= before + sum - count && slot < before + sum;
+      // (lanes past the last sequence count none)
+      const int per = count ? (chunks_of(len) + count - 1) / count : 0;
+      int turn = before;   // segments of the block's sequences with longer walks
+#pragma unroll 4
+      for (int d = 0; d < 32; ++d) {
+        const int p2 = __shfl_sync(0xffffffffu, per, d), c2 = __shfl_sync(0xffffffffu, count, d);
+        turn += p2 > per || (p2 == per && d < lane) ? c2 : 0;
+      }
+      const bool here = slot >= turn && slot < turn + count;
       const unsigned who = __ballot_sync(0xffffffffu, here);
       if (who) {
         const int src = __ffs(who) - 1;
@@ -116,7 +131,8 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
         p.row0 = __shfl_sync(0xffffffffu, row0, src);
         p.len = __shfl_sync(0xffffffffu, len, src);
         p.nseg = __shfl_sync(0xffffffffu, count, src);
-        p.seg = slot - before - __shfl_sync(0xffffffffu, sum - count, src);
+        p.seg = slot - __shfl_sync(0xffffffffu, turn, src);
+        p.first = before + __shfl_sync(0xffffffffu, sum - count, src);
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -187,13 +203,19 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
 
   // ---- the walk ----
   int ji = 0, item = blockIdx.x;
-  while (ji + 1 < a.jobs && item >= a.job[ji].slots * a.job[ji].heads_x) {
-    item -= a.job[ji].slots * a.job[ji].heads_x;
-    ++ji;
+  while (ji + a.merged < a.jobs && item >= a.merged * a.job[ji].slots * a.job[ji].heads_x) {
+    item -= a.merged * a.job[ji].slots * a.job[ji].heads_x;
+    ji += a.merged;
+  }
+  int slot = static_cast<int>(fdiv(item, a.job[ji].fd_heads));
+  const int h = item - slot * a.job[ji].heads_x;
+  if (a.merged > 1) {   // the jobs' places in turn
+    const int q = slot / a.merged;
+    ji += slot - q * a.merged;
+    slot = q;
   }
   const LinearJob& j = a.job[ji];
-  const int slot = static_cast<int>(fdiv(item, j.fd_heads));
-  const int h = item - slot * j.heads_x;
+  item = slot * j.heads_x + h;
   const int hkv = static_cast<int>(fdiv(h, j.fd_kv));
 
   if (threadIdx.x == 0) {
@@ -201,7 +223,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(&bar_full[i], 1);
       mbar_init(&bar_empty[i], 1);
-      mbar_init(&bar_out[i], 8);
+      mbar_init(&bar_out[i], C::OUT_BY_SCORES ? 4 : 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_xfull[i], 1);
@@ -216,7 +238,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     }
     mbar_init(&bar_qh, 1);
     mbar_init(&bar_o, 1);
-    mbar_init(&bar_of, 8);
+    mbar_init(&bar_of, C::OUT_BY_SCORES ? 4 : 8);
     mbar_init(&bar_h, 8);
     fence_mbar_init();
   }
@@ -264,6 +286,35 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   const bool each = NS > 1 && terms > 2;
   const int n_grow = want_last ? n_walk : n_walk - 1;   // chunks that the state takes in
   const int steps = n_walk * inner;                     // a step: one inner head of a chunk
+
+  // chunk n's rows, columns [c0, c0 + cols), to the place of its last Z, which the products have
+  // read: rows written from registers, 16 bytes of 32 rows at a time, took 2000 cycles
+  auto output = [&](int n, int c0, int cols) -> bool {
+    if (!wait(&bar_o, n & 1, ac)) return false;
+    tc_fence_after();
+    const int wq = warp & 3, row = threadIdx.x & 127;   // (TMEM lane)
+    const uint32_t tO = tmem + (static_cast<uint32_t>(wq * 32) << 16) + C::COL_O;
+    uint8_t* so = ring + (2 * (n + 1) * inner - 1) % NSLOT * C::TILE;
+#pragma unroll 1
+    for (int cc = c0; cc < c0 + cols; cc += 32) {
+      uint32_t o[32];
+      tmem_ld32_nowait(tO + cc, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int x = 0; x < 32; x += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          w[y] = pack_bf16(__uint_as_float(o[x + 2 * y]), __uint_as_float(o[x + 2 * y + 1]));
+        *reinterpret_cast<uint4*>(so + sw128_offset(row, cc + x, kLinearChunk)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    tc_fence_before();
+    warp_arrive(&bar_of);
+    fence_proxy_async_smem();
+    warp_arrive(&bar_out[n % NSLOT]);
+    return true;
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -520,6 +571,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&bar_p[t & 1]);
+        if (C::OUT_BY_SCORES && last && !output(n, 0, D)) break;
       }
       if (C::AHEAD && t + 1 < steps && !convert(t + 1, chunk_len(last ? n + 1 : n))) break;
       if (t >= 0) {
@@ -559,7 +611,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         const int lo = sg * pl.per * kLinearChunk, hi = min(pl.len, lo + pl.per * kLinearChunk);
         const float keep = NS > 1 ? decay_exact(ln, max(hi - lo, 0)) : ex2(l2 * max(hi - lo, 0));
         const float4* g = reinterpret_cast<const float4*>(
-            j.parts + (static_cast<int64_t>(slot + sg - pl.seg) * a.heads_kv + hkv) * D * D);
+            j.parts + (static_cast<int64_t>(pl.first + sg) * a.heads_kv + hkv) * D * D);
         if (mine)
 #pragma unroll
           for (int x = 0; x < C::HC; x += 4) {
@@ -621,35 +673,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       publish();
       return true;
     };
-    const int row = tid & 127;   // row of the chunk: of Y, and TMEM lane of the outputs
-    // chunk n's rows, in place of its last Z, which the products have read: rows written from
-    // registers, 16 bytes of 32 rows at a time, took 2000 cycles
-    auto output = [&](int n) -> bool {
-      if (!wait(&bar_o, n & 1, ac)) return false;
-      tc_fence_after();
-      const uint32_t tO = tmem + (static_cast<uint32_t>(wq * 32) << 16) + c0;
-      uint8_t* so = ring + (2 * (n + 1) * inner - 1) % NSLOT * C::TILE;
-#pragma unroll 1
-      for (int cc = 0; cc < C::HC; cc += 32) {
-        uint32_t o[32];
-        tmem_ld32_nowait(tO + C::COL_O + cc, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            w[y] = pack_bf16(__uint_as_float(o[x + 2 * y]), __uint_as_float(o[x + 2 * y + 1]));
-          *reinterpret_cast<uint4*>(so + sw128_offset(row, c0 + cc + x, kLinearChunk)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      tc_fence_before();
-      warp_arrive(&bar_of);
-      fence_proxy_async_smem();
-      warp_arrive(&bar_out[n % NSLOT]);
-      return true;
-    };
+    const int row = tid & 127;   // row of the chunk
     int n = 0, g = 0;
     for (int t = 0; t <= steps; ++t) {
       const bool next = g == 0 && n > 0;   // a chunk is behind these warps
@@ -657,7 +681,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       const bool grown = each ? t > 0 && t <= n_grow * inner : next && n - 1 < n_grow;
       const int gi = each ? t - 1 : n - 1, gn = g == 0 ? n - 1 : n;
       if (!kStates && grown && !grow(gi, gn, !each || inner == 1 || g == 1, g == 0)) break;
-      if (!kStates && C::XBUF == 1 && next && !output(n - 1)) break;
       if (t < steps && n < n_grow) {
         const int rows = chunk_len(n);
         const int far = back ? row + 1 : max(rows - 1 - row, 0);
@@ -718,14 +741,14 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         warp_arrive(&bar_y[t & 1]);
       }
       if (kStates && grown && !grow(gi, gn, !each || inner == 1 || g == 1, g == 0)) break;
-      if (!kStates && C::XBUF != 1 && next && !output(n - 1)) break;
+      if (!kStates && !C::OUT_BY_SCORES && next && !output(n - 1, c0, C::HC)) break;
       if (++g == inner) {
         g = 0;
         ++n;
       }
     }
     if (kStates) {
-      const int64_t at = (static_cast<int64_t>(slot) * a.heads_kv + hkv) * D * D;
+      const int64_t at = (static_cast<int64_t>(pl.first + pl.seg) * a.heads_kv + hkv) * D * D;
       if (mine)
 #pragma unroll
         for (int x = 0; x < C::HC; x += 4) {

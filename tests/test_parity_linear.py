@@ -78,6 +78,14 @@ def test_many_long_sequences():
     check(s, s.call())
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (3, 1)])
+def test_more_packed_sequences_than_a_warp_holds(hq, hkv):
+    # 70 sequences of 0 to 900 tokens: the order of the walks by length, and places of the segments
+    lens = [(i * i * 37 + 11 * i) % 901 if i % 7 else 0 for i in range(70)]
+    s = Rows(lens, hq, hkv, 64, pad=21, states=True, seed=6)
+    check(s, s.call())
+
+
 def test_scales():
     for scale in (0.0, -0.25, 3.0):
         s = Rows([200], 2, 1, 64, states=True, scale=scale, seed=6)
