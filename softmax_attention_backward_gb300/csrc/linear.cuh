@@ -78,7 +78,8 @@ __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& r
   if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
 }
 
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, cudaStream_t st);
+// `follows`: the launch before on the stream is the pass over its states.
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool follows, cudaStream_t st);
 
 // Sequences of at most this many tokens (packed: all of them together) go token by token
 // (linear_short.cu).  us with and without, 32 heads of 128, a graph's launch of 5 us included:

@@ -54,7 +54,7 @@ struct Rates {
 };
 constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2}, {1.55, 1.72, 0.94, 0.65}};
 constexpr double kStart = 4.0;     // a walk's start and end
-constexpr double kLaunch = 4.0;    // of the pass over the states
+constexpr double kLaunch = 1.5;    // of the pass over the states, whose end the walks overlap
 constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
 
 // The time of na walks of ca and then nb of cb on `sms` SMs, each taking the next as it is free.
@@ -218,7 +218,8 @@ bool map_out(LinearJob* j, const linear_attn_problem_t* p) {
 }
 
 // What a job takes from the problem; `shared`: heads of x per KV head, `way`: 0 forwards, 1 backwards.
-void set_job(LinearJob& j, const linear_attn_problem_t* p, int heads_x, int shared, int inner, const Cut& c, int way) {
+void set_job(LinearJob& j, const linear_attn_problem_t* p, int heads_x, int shared, int inner,
+             const Cut& c, int way) {
   j.heads_x = heads_x;
   j.backwards = way;
   j.terms = 1;
@@ -310,9 +311,9 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   if (cut.parts[0]) {
     LinearArgs s = make_args(p);
     s.job[s.jobs++] = state_job(j, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return launch_linear(a, p->head_dim, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_linear(a, p->head_dim, false, cut.parts[0], st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const void* q,
@@ -383,7 +384,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
     LinearArgs s = make_args(p);
     if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);
     if (cut.parts[0]) s.job[s.jobs++] = state_job(jq, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, true, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return launch_linear(a, p->head_dim, false, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const bool follows = cut.parts[0] || cut.parts[1];
+  return launch_linear(a, p->head_dim, false, follows, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -198,6 +198,11 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   __shared__ float s_keep[2];                 // a chunk's decay
   __shared__ float s_diag[64];                // those of its diagonal, scaled: entry 32 + j - i
 
+  // The walks of the outputs start on SMs that the pass over the states leaves, once all of its CTAs
+  // have theirs, and wait for its end where they take a state from it (2 to 4 us of each
+  // call with such a pass).
+  if (kStates) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   const int warp = warp_id();
   AbortCtx ac{&abort_flag, a.err};
 
@@ -606,6 +611,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         }
       }
       const int before = back ? pl.nseg - 1 - pl.seg : pl.seg;
+      if (before > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int t = 0; t < before; ++t) {
         const int sg = back ? pl.nseg - 1 - t : t;
         const int lo = sg * pl.per * kLinearChunk, hi = min(pl.len, lo + pl.per * kLinearChunk);
@@ -776,6 +782,8 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       o4[w] = make_uint4(0u, 0u, 0u, 0u);
   }
 
+  // (no grid ends before the one that it follows)
+  if (!kStates) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -786,7 +794,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
 }
 
 template <int D, int NS, bool kStates>
-cudaError_t launch(const LinearArgs& a, cudaStream_t st) {
+cudaError_t launch(const LinearArgs& a, bool follows, cudaStream_t st) {
   using C = Cfg<D, NS, kStates>;
   auto kern = linear_kernel<D, NS, kStates>;
   static std::atomic<uint64_t> ready{0};
@@ -795,21 +803,30 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t st) {
   int64_t grid = 0;
   for (int i = 0; i < a.jobs; ++i) grid += static_cast<int64_t>(a.job[i].slots) * a.job[i].heads_x;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = follows ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, cudaStream_t st) {
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool follows, cudaStream_t st) {
   int terms = 1;   // the most that a job has
   for (int i = 0; i < a.jobs; ++i) terms = a.job[i].terms > terms ? a.job[i].terms : terms;
   if (head_dim == 64) {
-    if (states_only) return terms == 1 ? launch<64, 1, true>(a, st) : launch<64, 3, true>(a, st);
-    return terms == 1 ? launch<64, 1, false>(a, st) : launch<64, 3, false>(a, st);
+    if (states_only) return terms == 1 ? launch<64, 1, true>(a, follows, st) : launch<64, 3, true>(a, follows, st);
+    return terms == 1 ? launch<64, 1, false>(a, follows, st) : launch<64, 3, false>(a, follows, st);
   }
-  if (states_only) return terms == 1 ? launch<128, 1, true>(a, st) : launch<128, 3, true>(a, st);
-  return terms == 1 ? launch<128, 1, false>(a, st) : launch<128, 3, false>(a, st);
+  if (states_only) return terms == 1 ? launch<128, 1, true>(a, follows, st) : launch<128, 3, true>(a, follows, st);
+  return terms == 1 ? launch<128, 1, false>(a, follows, st) : launch<128, 3, false>(a, follows, st);
 }
 
 }  // namespace attn
