@@ -78,16 +78,20 @@ __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& r
   if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
 }
 
-// `follows`: the launch before on the stream is the pass over its states.
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool follows, cudaStream_t st);
+// `pairs` (head_dim 64): two CTAs on an SM.  `follows`: the launch before on the stream is the pass
+// over its states.
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool pairs, bool follows,
+                          cudaStream_t st);
 
 // Sequences of at most this many tokens (packed: all of them together) go token by token
-// (linear_short.cu).  us with and without, 32 heads of 128, a graph's launch of 5 us included:
-//                              8 tokens       16 tokens      64 x 8      64 x 16
-//   forward                  12.4 / 13.5    15.5 / 13.5    88 / 112    152 / 114
-//   forward, states          12.4 / 21.6    17.5 / 21.6   102 / 206    160 / 207
-//   backward, 8 KV heads     18.6 / 22.7    27.8 / 22.7   177 / 218    321 / 218
-// (of 64 dims 64 x 8: 41 / 93, 64 x 16: 62 / 94).
+// (linear_short.cu).  us with and without, 32 heads, a graph's launch of 5 us included:
+//                                   8 tokens       64 x 8
+//   128 dims, forward              12.4 / 13.5     83 / 111
+//     forward, states              12.4 / 19.6     93 / 202
+//     backward, 8 KV heads         18.6 / 23.6    172 / 217
+//   64 dims, forward               11.4 / 13.4     34 / 55
+//     backward, 8 KV heads         16.5 / 18.6     65 / 119
+// 16 tokens of 8 KV heads, backward, would take 27 for 23.
 constexpr int kLinearShort = 8;
 cudaError_t launch_linear_short(const LinearArgs& a, int head_dim, cudaStream_t st);
 

@@ -43,6 +43,8 @@ struct Cut {
   int chunks[2], slots[2];
   bool parts[2];   // a sequence may have several segments
   bool dq_first;   // backward: the walks of dq are the longer ones
+  bool pairs;      // head_dim 64: two CTAs on an SM
+  double us;       // what it is taken to cost
 };
 
 // What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
@@ -51,9 +53,14 @@ struct Cut {
 // 1, 2, 4 and 8 inner heads, 218, 341, 558 and 987 us; head_dim 64, 140, 229, 412 and 775.
 struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
+  double start;                     // a walk's start and end
 };
-constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2}, {1.55, 1.72, 0.94, 0.65}};
-constexpr double kStart = 4.0;     // a walk's start and end
+constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2, 4.0}, {1.55, 1.72, 0.94, 0.65, 4.0}};
+// Two CTAs of head_dim 64 on an SM hide each other's starts, ends and waits, but leave a walk fewer
+// tiles and registers.  us with one and with two, 32 heads: 16 sequences of 100 tokens 34 and 24, 64
+// of 100 97 and 61, 8 of 4096 with 38 heads 153 and 150, 4 of 4096 with 38 81 and 104; packed, 64
+// of 16 to 400, 16 heads 92 and 69, their backward 231 and 174, 12 of up to 8192 83 and 75.
+constexpr Rates kPairs = {1.39, 2.96, 1.4, 0.3, 3.0};
 constexpr double kLaunch = 1.5;    // of the pass over the states, whose end the walks overlap
 constexpr double kBytes = 5.9e6;   // bytes per us that all walks together get
 
@@ -77,14 +84,14 @@ double makespan(int sms, double na, double ca, double nb, double cb) {
 }
 
 // Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, dq
-// uncut and the others in 8 segments of a sequence 286, in 6 317, in 2 405; forward of 12 packed
-// sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 8 chunks 86, of 6 (taken) 87, of 4
-// 102, of 16 97; backward of
-// 12 of up to 2500, 16 heads of 64, uncut 108, 10 and 20 chunks 118, 10 and 10 120; one sequence of
-// 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161, of 16 180.
-Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
+// uncut and the others in 8 segments of a sequence 286, in 6 317, in 2 405; one sequence of 65536
+// tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161, of 16 180; packed, forward of
+// 12 sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 7 chunks (taken) 75, of 12 73, of
+// 4 81; 40 of 16 to 4096, 16 heads of 128, of 13 (taken) 179, of 16 167, uncut 191.
+Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs) {
   const int group = p->heads_q / p->heads_kv;
-  const Rates& rate = kRates[p->head_dim == 128];
+  const Rates& rate = pairs ? kPairs : kRates[p->head_dim == 128];
+  if (pairs) sms *= 2;
   const double tile = 2.0 * kLinearChunk * p->head_dim;
   const bool packed = p->cu_seqlens != nullptr;
   const int most = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;   // of a sequence
@@ -113,10 +120,10 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
                                   : static_cast<double>(p->num_seqs) * segs;
       const double before = rate.part * (packed ? 0.3 : 0.75) * (segs - 1);
       o.walks = walks * heads;
-      o.longest = kStart + before + chunk * per;
-      o.cost = packed ? kStart + before + chunk * std::min<double>(per, chunks / walks) : o.longest;
+      o.longest = rate.start + before + chunk * per;
+      o.cost = packed ? rate.start + before + chunk * std::min<double>(per, chunks / walks) : o.longest;
       o.states = (walks - p->num_seqs) * p->heads_kv;
-      o.state_cost = kStart + rate.state * inner * per;
+      o.state_cost = rate.start + rate.state * inner * per;
       o.bytes = tile * (chunks * heads * (i ? 2 + 2 * inner : 2 + 2.0 / group) +
                         chunks * (walks - p->num_seqs) / walks * p->heads_kv * 2 * inner);
       opt[i][n_opt[i]++] = o;
@@ -128,14 +135,25 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
   for (int i = 0; i < n_opt[0]; ++i)
     for (int j = 0; j < (backward ? n_opt[1] : 1); ++j) {
       const Option &x = opt[0][i], &y = backward ? opt[1][j] : none;
-      double t = x.longest > y.longest ? makespan(sms, x.walks, x.cost, 2 * y.walks, y.cost)
-                                       : makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
-      // the longest of packed sequences come first, of each job or, merged, of all
-      t = std::max(t, std::max(x.longest, y.longest));
-      if (backward && !(group == 1 && x.chunks == y.chunks))
-        t += 0.5 * std::max(x.longest - x.cost, y.longest - y.cost);
+      double t;
+      if (packed) {
+        // walks of many lengths, the longest first (of each job, or merged of all): the SMs fill up,
+        // but for a part of the longest, of two on an SM less, as the last ones run alone
+        const double tail = pairs ? 0.25 : 0.5;
+        t = (x.walks * x.cost + 2 * y.walks * y.cost) / sms + tail * std::max(x.longest, y.longest);
+        if (backward && !(group == 1 && x.chunks == y.chunks))
+          t += 0.5 * std::max(x.longest - x.cost, y.longest - y.cost);
+        t = std::max(t, std::max(x.longest, y.longest));
+        if (x.states + y.states > 0)
+          t += kLaunch + (x.states * x.state_cost + y.states * y.state_cost) / sms +
+               tail * std::max(x.state_cost, y.state_cost);
+      } else {
+        t = x.longest > y.longest ? makespan(sms, x.walks, x.cost, 2 * y.walks, y.cost)
+                                  : makespan(sms, 2 * y.walks, y.cost, x.walks, x.cost);
+        if (x.states + y.states > 0)
+          t += kLaunch + makespan(sms, y.states, y.state_cost, x.states, x.state_cost);
+      }
       t = std::max(t, (x.bytes + 2 * y.bytes) / kBytes);
-      if (x.states + y.states > 0) t += kLaunch + makespan(sms, y.states, y.state_cost, x.states, x.state_cost);
       if ((i == 0 && j == 0) || t < least) least = t, best[0] = i, best[1] = j;
     }
   Cut c{};
@@ -145,6 +163,8 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms) {
                         : p->num_seqs * (most > 0 ? (most + c.chunks[i] - 1) / c.chunks[i] : 1);
     c.parts[i] = c.chunks[i] < most;
   }
+  c.pairs = pairs;
+  c.us = least;
   c.dq_first = backward && opt[0][best[0]].longest > opt[1][best[1]].longest;
   return c;
 }
@@ -167,7 +187,12 @@ Cut cut_sequences(const linear_attn_problem_t* p, bool backward) {
   Kept& k = kept[next];
   next = (next + 1) % kKept;
   std::copy(key, key + 8, k.key);
-  return k.cut = find_cut(p, backward, sms);
+  k.cut = find_cut(p, backward, sms, false);
+  if (p->head_dim == 64) {
+    const Cut two = find_cut(p, backward, sms, true);
+    if (two.us < k.cut.us) k.cut = two;
+  }
+  return k.cut;
 }
 
 size_t state_bytes(const linear_attn_problem_t* p, int slots) {
@@ -311,9 +336,9 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   if (cut.parts[0]) {
     LinearArgs s = make_args(p);
     s.job[s.jobs++] = state_job(j, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, true, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, false, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return launch_linear(a, p->head_dim, false, cut.parts[0], st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_linear(a, p->head_dim, false, cut.pairs, cut.parts[0], st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const void* q,
@@ -384,8 +409,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
     LinearArgs s = make_args(p);
     if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);
     if (cut.parts[0]) s.job[s.jobs++] = state_job(jq, p, 1, nullptr);
-    if (launch_linear(s, p->head_dim, true, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_linear(s, p->head_dim, true, false, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   const bool follows = cut.parts[0] || cut.parts[1];
-  return launch_linear(a, p->head_dim, false, follows, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_linear(a, p->head_dim, false, cut.pairs, follows, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

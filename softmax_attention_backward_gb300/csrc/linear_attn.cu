@@ -29,15 +29,14 @@
 // 4 x 4096 tokens of 32 heads of 128: 124 us with the launch, 79 for the bytes alone.
 // Slower, same sizes: two issuing warps 8 %, one wait for several barriers 5 %, fully unrolled
 // products 4 %, the next chunks' tiles fetched to L2 11 %, a ring of 3 tiles 11 %.
-// At D = 64 two CTAs on an SM (64 registers a thread) give 12 packed sequences 79 for 87 us
-// and take 4 x 4096 tokens of 38 heads from 85 to 105: shared memory, which the
-// products' operands, the tiles and the warps share, is busy either way.
+// At D = 64 there is a second variant with two CTAs on an SM (kCtas, 64 registers a thread, one
+// buffer of S), for many short walks: linear_api.cu has the rule.
 #include "linear.cuh"
 
 namespace attn {
 namespace {
 
-template <int D, int NS, bool kStates>
+template <int D, int NS, bool kStates, int kCtas>
 struct Cfg {
   static constexpr int C = kLinearChunk;
   static constexpr int TILE = C * D * 2;
@@ -45,11 +44,12 @@ struct Cfg {
   // keys beside them), in one, the keys then in two or three.  So two roundings to bf16 are on a
   // product's way besides the output's at most, one of them for most: 1.41 times the error of the
   // output's alone, 1.6 to 1.7 with one term of each (4 x 4096 tokens 104 us for 124)
-  static constexpr int HTERMS = NS == 1 || D == 64 ? 2 : 1;
+  static constexpr int HTERMS = NS == 1 || (D == 64 && kCtas == 1) ? 2 : 1;
   static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
   static constexpr int EXTRA = (NS - 1) * TILE;   // second and third terms of the decayed keys
-  // the tiles that fit: 227 KB of shared memory, 1 KB of it for the alignment
-  static constexpr int FIT = (227 * 1024 - 2048 - H_BYTES - EXTRA) / TILE;
+  // the tiles that fit: 227 KB of shared memory, or 113 for each of two CTAs, 2 KB of it for the
+  // alignment and what is static
+  static constexpr int FIT = ((kCtas == 2 ? 113 : 227) * 1024 - 2048 - H_BYTES - EXTRA) / TILE;
   // X has buffers of its own: a chunk's X outlives the tiles of its inner heads
   static constexpr int XBUF = kStates ? 0 : FIT >= 6 ? 2 : 1;
   static constexpr int XMOD = XBUF ? XBUF : 1;
@@ -62,10 +62,12 @@ struct Cfg {
   static constexpr int HC = D / 2;                // state columns of a thread
   // S of a step is formed while the step before is still at work, where the ring can hold both: with
   // three tiles the wait for the next Y would hold up the Z that has to leave before it
-  static constexpr bool AHEAD = !kStates && NSLOT >= 4;
+  static constexpr bool AHEAD = !kStates && kCtas == 1 && NSLOT >= 4;
   // the warps that write the output
   static constexpr bool OUT_BY_SCORES = XBUF == 1;
-  static constexpr uint32_t COL_S = 0, COL_O = 256, COL_G = 384;   // S: two buffers
+  static constexpr uint32_t COLS = 512 / kCtas;   // of TMEM
+  static constexpr uint32_t COL_S = 0, S_STEP = AHEAD ? 128 : 0;   // AHEAD: two buffers
+  static constexpr uint32_t COL_O = COLS / 2, COL_G = kStates ? 0 : COL_O + D;
   // without S and O there is room for two of G: a chunk's is read while the next one's is formed
   static constexpr int GBUF = kStates ? 2 : 1;
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
@@ -119,7 +121,7 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
       const int per = count ? (chunks_of(len) + count - 1) / count : 0;
       int turn = before;   // segments of the block's sequences with longer walks
 #pragma unroll 4
-      for (int d = 0; d < 32; ++d) {
+      for (int d = 0; d < min(32, a.num_seqs - n0); ++d) {
         const int p2 = __shfl_sync(0xffffffffu, per, d), c2 = __shfl_sync(0xffffffffu, count, d);
         turn += p2 > per || (p2 == per && d < lane) ? c2 : 0;
       }
@@ -175,9 +177,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if (lane_id() == 0) mbar_arrive(bar);
 }
 
-template <int D, int NS, bool kStates>
-__global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ LinearArgs a) {
-  using C = Cfg<D, NS, kStates>;
+template <int D, int NS, bool kStates, int kCtas>
+__global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constant__ LinearArgs a) {
+  using C = Cfg<D, NS, kStates, kCtas>;
   constexpr int PANELS = D / 64;
   constexpr int NSLOT = C::NSLOT;
   extern __shared__ uint8_t smem_raw[];
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   // waits is never two phases behind
   __shared__ uint64_t bar_full[NSLOT], bar_empty[NSLOT], bar_out[NSLOT];
   __shared__ uint64_t bar_xfull[2], bar_xempty[2];
-  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_g[2], bar_gf[2], bar_qh, bar_o, bar_of, bar_h;
+  __shared__ uint64_t bar_s[2], bar_p[2], bar_y[2], bar_g[2], bar_gf[2], bar_qh, bar_o, bar_of, bar_h, bar_keep;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ Place s_place;
@@ -241,13 +243,17 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       mbar_init(&bar_g[i], 1);
       mbar_init(&bar_gf[i], 8);
     }
+    mbar_init(&bar_keep, 1);
     mbar_init(&bar_qh, 1);
     mbar_init(&bar_o, 1);
     mbar_init(&bar_of, C::OUT_BY_SCORES ? 4 : 8);
     mbar_init(&bar_h, 8);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_sh, C::COLS);
+    tmem_relinquish();
+  }
   const float ln = log_decay_of(a, hkv), l2 = ln * kLog2e;
   if (warp == 2) {
     const Place p = find_place(a, j, slot);
@@ -255,12 +261,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   }
   if (warp == 3) {
     const int x = lane_id();
-    if (NS > 1 && x == 0) {
-      // in two parts: an error of a chunk's decay would grow with every chunk that a state crosses
-      const double keep = exp(static_cast<double>(ln) * kLinearChunk);
-      s_keep[0] = static_cast<float>(keep);
-      s_keep[1] = static_cast<float>(keep - s_keep[0]);
-    }
     s_tab[x] = ex2(l2 * (j.backwards ? x : 31 - x));
     s_diag[x] = j.backwards ? 0.f : a.scale * ex2(l2 * (32 - x));
     s_diag[32 + x] = j.backwards || x == 0 ? a.scale * ex2(l2 * x) : 0.f;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       const uint64_t dx = desc_advance(dx0, bx * C::TILE), dy = desc_advance(dk0, slot(2 * t) * C::TILE);
 #pragma unroll C::UNROLL
       for (int k = 0; k < D / 16; ++k)
-        umma_ss_w(tmem + C::COL_S + 128 * (t & 1), desc_advance(dx, kmajor_step_bytes(128, k)),
+        umma_ss_w(tmem + C::COL_S + C::S_STEP * (t & 1), desc_advance(dx, kmajor_step_bytes(128, k)),
                   desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
       umma_commit_w(&bar_s[t & 1]);
       return true;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
         for (int e = terms - 1; e >= 0; --e)
 #pragma unroll C::UNROLL
           for (int k = 0; k < 8; ++k, add = 1)
-            umma_ss_w(tmem + C::COL_G - 128 * b,
+            umma_ss_w(tmem + C::COL_G + 128 * b,
                       desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
                       desc_advance(dz, mnmajor_step_bytes(k)), idG, add);
       }
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       const uint64_t dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
 #pragma unroll C::UNROLL
       for (int k = 0; k < 8; ++k)
-        umma_ts_w(tmem + C::COL_O, tmem + C::COL_S + 128 * (t & 1) + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)),
+        umma_ts_w(tmem + C::COL_O, tmem + C::COL_S + C::S_STEP * (t & 1) + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)),
                   idO, 1u);
       if (g == inner - 1) umma_commit_w(&bar_o);
       return true;
@@ -453,6 +453,15 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       n += last;
       g = last ? 0 : g + 1;
     }
+  } else if (NS > 1 && warp == 2) {
+    // A chunk's decay in two parts: an error of it would grow with every chunk that a state crosses.
+    // Behind the block's barrier, for exp in fp64 is slow here (500 tokens with states 31 -> 30 us).
+    if (lane_id() == 0) {
+      const double keep = exp(static_cast<double>(ln) * kLinearChunk);
+      s_keep[0] = static_cast<float>(keep);
+      s_keep[1] = static_cast<float>(keep - s_keep[0]);
+      mbar_arrive(&bar_keep);
+    }
   } else if (!kStates && warp == 3) {
     // ---------------- stores ----------------
     // whole chunks leave by a bulk copy, others (rows behind the sequence are another's) by plain
@@ -479,7 +488,6 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       }
       warp_arrive(&bar_empty[b]);
     }
-    if (lane_id() == 0) bulk_wait<0>();
   } else if (!kStates && warp >= 4 && warp < 8) {
     // ---------------- scores ----------------
     const int wq = warp & 3, i = threadIdx.x & 127;   // row of the chunk, TMEM lane
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
     auto convert = [&](int t, int rows) -> bool {
       if (!wait(&bar_s[t & 1], (t >> 1) & 1, ac)) return false;
       tc_fence_after();
-      const uint32_t tS = lane_base + C::COL_S + 128 * (t & 1);
+      const uint32_t tS = lane_base + C::COL_S + C::S_STEP * (t & 1);
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t p[16];
@@ -658,13 +666,14 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
       const int rows = chunk_len(n);
       float keep = ex2(l2 * rows), keep2 = 0.f;
       if (NS > 1) {
+        if (!wait(&bar_keep, 0, ac)) return false;
         keep = !first ? 1.f : rows == kLinearChunk ? s_keep[0] : decay_exact(ln, rows);
         keep2 = first && rows == kLinearChunk ? s_keep[1] : 0.f;
       }
 #pragma unroll
       for (int x = 0; x < C::HC; x += 32) {
         uint32_t v[32];
-        tmem_ld32_nowait(tG - 128 * b + x, v);
+        tmem_ld32_nowait(tG + 128 * b + x, v);
         tmem_wait_ld();
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
@@ -788,15 +797,14 @@ __global__ void __launch_bounds__(512, 1) linear_kernel(const __grid_constant__ 
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
-    tmem_relinquish();
+    tmem_dealloc(tmem, C::COLS);
   }
 }
 
-template <int D, int NS, bool kStates>
+template <int D, int NS, bool kStates, int kCtas = 1>
 cudaError_t launch(const LinearArgs& a, bool follows, cudaStream_t st) {
-  using C = Cfg<D, NS, kStates>;
-  auto kern = linear_kernel<D, NS, kStates>;
+  using C = Cfg<D, NS, kStates, kCtas>;
+  auto kern = linear_kernel<D, NS, kStates, kCtas>;
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(kern, C::SMEM, ready);
   if (e != cudaSuccess) return e;
@@ -818,11 +826,14 @@ cudaError_t launch(const LinearArgs& a, bool follows, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool follows, cudaStream_t st) {
+cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, bool pairs, bool follows,
+                          cudaStream_t st) {
   int terms = 1;   // the most that a job has
   for (int i = 0; i < a.jobs; ++i) terms = a.job[i].terms > terms ? a.job[i].terms : terms;
   if (head_dim == 64) {
-    if (states_only) return terms == 1 ? launch<64, 1, true>(a, follows, st) : launch<64, 3, true>(a, follows, st);
+    if (states_only)
+      return terms == 1 ? launch<64, 1, true, 2>(a, follows, st) : launch<64, 3, true, 2>(a, follows, st);
+    if (pairs) return terms == 1 ? launch<64, 1, false, 2>(a, follows, st) : launch<64, 3, false, 2>(a, follows, st);
     return terms == 1 ? launch<64, 1, false>(a, follows, st) : launch<64, 3, false>(a, follows, st);
   }
   if (states_only) return terms == 1 ? launch<128, 1, true>(a, follows, st) : launch<128, 3, true>(a, follows, st);

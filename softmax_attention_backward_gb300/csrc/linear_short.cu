@@ -7,8 +7,8 @@
 // walks its tokens: lanes are columns, each of four warps holds a quarter of the
 // rows in registers, and an output is the sum of the warps' parts in a fixed
 // order.  Bound by latency for one sequence: the loads of a batch of tokens are one
-// trip to memory (4 tokens: 10.4 us of 5 for the launch, 12.4 with a trip for each
-// token), states of 64 sequences of 32 x 128 x 128 move at 3.4 TB/s.
+// trip to memory (4 tokens: 10.4 us, 5 of them for the launch; 12.4 with a trip for
+// each token).
 #include "linear.cuh"
 
 namespace attn {
@@ -19,6 +19,7 @@ constexpr int kSteps = 8;    // (token, inner head) pairs that are fetched toget
 template <int D>
 __global__ void __launch_bounds__(128) linear_short_kernel(const __grid_constant__ LinearArgs a) {
   constexpr int R = D / 4;   // rows of the state in a thread
+  __shared__ float s_decay[2];
   __shared__ __align__(16) float sx[kSteps][D], sy[kSteps][D], sz[kSteps][32], part[kSteps][4][32];
   const LinearJob& j = a.job[blockIdx.z / (D / 32)];
   const int n = blockIdx.x, h = blockIdx.y, c = threadIdx.x & 31, rg = threadIdx.x >> 5;
@@ -27,9 +28,12 @@ __global__ void __launch_bounds__(128) linear_short_kernel(const __grid_constant
   int row0, len;
   sequence_rows(a, n, row0, len);
   const int hkv = static_cast<int>(fdiv(h, j.fd_kv));
-  // the decay in two parts: an error of it would grow with every token
-  const double ld = exp(static_cast<double>(log_decay_of(a, hkv)));
-  const float l = static_cast<float>(ld), l2 = static_cast<float>(ld - l);
+  // the decay in two parts, by one thread: exp in fp64 by all of them takes 20 us of 64 sequences' 50
+  if (threadIdx.x == 0) {
+    const double ld = exp(static_cast<double>(log_decay_of(a, hkv)));
+    s_decay[0] = static_cast<float>(ld);
+    s_decay[1] = static_cast<float>(ld - s_decay[0]);
+  }
   const size_t at = (static_cast<size_t>(n) * a.heads_kv + hkv) * D * D;
   float s[R];
   if (j.first && j.transposed) {
@@ -77,6 +81,7 @@ __global__ void __launch_bounds__(128) linear_short_kernel(const __grid_constant
       }
     }
     __syncthreads();
+    const float l = s_decay[0], l2 = s_decay[1];
     uint32_t ends = 0;   // the steps that are a token's last
     kk = k, gg = g;
 #pragma unroll 1

@@ -86,6 +86,18 @@ def test_more_packed_sequences_than_a_warp_holds(hq, hkv):
     check(s, s.call())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("states", [False, True])
+def test_many_short_walks(D, states):
+    # more walks than SMs, of one to three chunks: two on an SM at a time where head_dim is 64
+    s = Rows([300, 7, 130, 257, 64, 128, 0, 1, 31, 200], 40, 20, D, pad=3, states=states, seed=7)
+    got = s.call(states=states)
+    check(s, got, states=states)
+    again = s.call(states=states)
+    for x, y in zip(got, again):
+        assert x is None and y is None or torch.equal(x, y)
+
+
 def test_scales():
     for scale in (0.0, -0.25, 3.0):
         s = Rows([200], 2, 1, 64, states=True, scale=scale, seed=6)
