@@ -48,7 +48,7 @@ extern "C" {
  * keeps everything, -inf keeps only the present token.  It is a property of the
  * layer, not differentiated.
  *
- * No output may share memory with an input.
+ * No output may share memory with an input or another output (ATTN_ERR_INVALID_ARG).
  *
  * Supported: head_dim in {64, 128}; heads_q a multiple of heads_kv, at most 65535;
  * tokens * heads_q < 2^31, num_seqs * heads_q < 2^29.
@@ -119,7 +119,8 @@ attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const void* q, con
  * o.  A slot of -1 marks a padding row: its o is zeros.  Slots outside
  * [-1, num_slots) and slots that an earlier sequence of the call has are flagged
  * ATTN_DEVERR_INDEX_RANGE; their rows of o are zeros and they touch no state.
- * Other slots are left as they are.
+ * Other slots are left as they are.  o and the states share no memory with another
+ * argument (ATTN_ERR_INVALID_ARG).
  */
 typedef struct {
   int num_seqs;

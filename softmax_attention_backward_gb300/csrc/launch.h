@@ -161,4 +161,24 @@ cudaError_t launch_sparse_bwd(const SparseArgs& a, float* delta, __nv_bfloat16* 
                               cudaStream_t st);
 cudaError_t launch_sparse_bwd_main(const SparseArgs& a, cudaStream_t st);
 
+// The bytes of an argument, from its first to its last.
+struct Span {
+  uintptr_t begin, end;
+};
+
+// `rows` rows of `width` elements of `size` bytes, `stride` elements apart; none of a null pointer.
+inline Span span_of(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t size) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  return {x, p && rows > 0 ? x + static_cast<uintptr_t>(((rows - 1) * stride + width) * size) : x};
+}
+
+// Whether one of the first `outputs` shares memory with another of them or with an input.
+template <int N>
+inline bool overlap(const Span (&s)[N], int outputs) {
+  for (int i = 0; i < outputs; ++i)
+    for (int k = i + 1; k < N; ++k)
+      if (s[i].begin < s[k].end && s[k].begin < s[i].end) return true;
+  return false;
+}
+
 }  // namespace attn

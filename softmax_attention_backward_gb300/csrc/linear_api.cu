@@ -266,11 +266,12 @@ LinearJob state_job(const LinearJob& j, const linear_attn_problem_t* p, int inne
   return s;
 }
 
-// Whether a state that is read and one that is written share memory.
-bool overlap(const linear_attn_problem_t* p, const float* a, const float* b) {
-  const size_t n = state_bytes(p, p->num_seqs);
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + n && y < x + n;
+Span span(const linear_attn_problem_t* p, const Rows& r) {
+  return span_of(r.p, p->tokens, r.stride, static_cast<int64_t>(r.heads) * p->head_dim, sizeof(__nv_bfloat16));
+}
+
+Span span(const linear_attn_problem_t* p, const float* state) {
+  return span_of(state, 1, 0, state_bytes(p, p->num_seqs), 1);
 }
 
 // A problem without a token: the last state is the first one.
@@ -304,7 +305,7 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
                                          size_t workspace_bytes, attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (overlap(p, initial_state, final_state)) return ATTN_ERR_INVALID_ARG;
+  if (overlap({span(p, final_state), span(p, initial_state)}, 1)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return ATTN_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p->tokens == 0) return pass_state(p, initial_state, final_state, st);
@@ -316,6 +317,10 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
     return ATTN_ERR_ALIGNMENT;
+  const int64_t dense = static_cast<int64_t>(p->heads_q) * p->head_dim;
+  if (overlap({span(p, Rows{o, dense, p->heads_q}), span(p, final_state), span(p, rq), span(p, rk), span(p, rv),
+               span(p, initial_state)}, 2))
+    return ATTN_ERR_INVALID_ARG;
   const Cut cut = cut_sequences(p, false);
   const size_t need = workspace_bytes_of(p, cut);
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
@@ -349,7 +354,7 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
                                          attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (overlap(p, dfinal_state, dinitial_state) || overlap(p, initial_state, dinitial_state))
+  if (overlap({span(p, dinitial_state), span(p, initial_state), span(p, dfinal_state)}, 1))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(dfinal_state, 16) || !aligned(dinitial_state, 16))
     return ATTN_ERR_ALIGNMENT;
@@ -365,6 +370,12 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dout, 16) ||
       !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
     return ATTN_ERR_ALIGNMENT;
+  const int64_t dense_q = static_cast<int64_t>(p->heads_q) * p->head_dim;
+  const int64_t dense_kv = static_cast<int64_t>(p->heads_kv) * p->head_dim;
+  if (overlap({span(p, Rows{dq, dense_q, p->heads_q}), span(p, Rows{dk, dense_kv, p->heads_kv}),
+               span(p, Rows{dv, dense_kv, p->heads_kv}), span(p, dinitial_state), span(p, rq), span(p, rk),
+               span(p, rv), span(p, rd), span(p, initial_state), span(p, dfinal_state)}, 4))
+    return ATTN_ERR_INVALID_ARG;
   const Cut cut = cut_sequences(p, true);
   const size_t need = workspace_bytes_of(p, cut);
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;

@@ -284,6 +284,14 @@ attn_status_t rotate(const attn_rotary_problem_t* p, const void* q, const void* 
     if (a.in_stride[i] % 8) return ATTN_ERR_ALIGNMENT;
     if (in[i] && in[i] == out[i] && a.in_stride[i] != dense) return ATTN_ERR_INVALID_ARG;
   }
+  Span from[2], to[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t dense = static_cast<int64_t>(a.heads[i]) * p->head_dim;
+    from[i] = span_of(in[i], p->tokens, a.in_stride[i], dense, 2);
+    to[i] = span_of(out[i], p->tokens, dense, dense, 2);
+    if (in[i] != out[i] && overlap({to[i], from[i]}, 1)) return ATTN_ERR_INVALID_ARG;
+  }
+  if (overlap({to[0], to[1], from[1]}, 1) || overlap({to[1], from[0]}, 1)) return ATTN_ERR_INVALID_ARG;
   a.tokens = p->tokens;
   a.dim = p->head_dim;
   a.rot = p->rot_dim;

@@ -155,3 +155,25 @@ def test_binding_refusals():
         A.attn_rotary_table(8, 64, device="cpu")
     with pytest.raises(ValueError, match="CUDA"):
         A.attn_rotary_table(8, 64, out=torch.zeros(8, 64))
+
+
+def test_outputs_that_share_memory_are_refused(L):
+    # rows of 4 x 1024 and 4 x 256 bf16 (rotation), 6 x 1024 and 6 x 256 bf16 and states of 256 KB (linear)
+    far = [(i + 1) << 24 for i in range(11)]
+    for fn in ("attn_rotary_fwd", "attn_rotary_bwd"):
+        for i, x in ((3, far[0] + 16), (3, far[0] - 16), (3, far[1]), (4, far[0]), (4, far[1] + 2032), (4, far[3] + 8176)):
+            at = {**dict(enumerate(far[:5])), i: x}
+            assert getattr(L, fn)(ctypes.byref(_make(A._RotaryProblem, ROT, {})), *_ptrs(5, at), None) == 1
+    for out, n, call in (((4, 5), 6, _fwd), ((6, 7, 8, 9), 10, _bwd)):
+        for i in out:
+            for k in range(n):
+                if k != i:
+                    assert call(L, at={**dict(enumerate(far[:n + 1])), i: far[k]}, ws=0) == 1
+    at = dict(enumerate(far[:7]))
+    assert _fwd(L, at={**at, 4: far[0] + 16}, ws=0) == 1 and _fwd(L, at={**at, 4: far[1] - 16}, ws=0) == 1
+    assert _fwd(L, dict(k_stride=4096), {**at, 4: far[1] + 5 * 8192 + 496}, ws=0) == 1   # the last row's last bytes
+    for i in (3, 4):
+        for k in range(5):
+            if k != i:
+                at = {**dict(enumerate(far[:5])), i: far[k]}
+                assert L.linear_attn_step(ctypes.byref(_make(A._LinearStep, STEP, {})), *_ptrs(5, at), None) == 1
