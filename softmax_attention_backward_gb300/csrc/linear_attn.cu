@@ -46,7 +46,11 @@ struct Cfg {
   // output's alone, 1.6 to 1.7 with one term of each (4 x 4096 tokens 104 us for 124)
   static constexpr int HTERMS = NS == 1 || (D == 64 && kCtas == 1) ? 2 : 1;
   static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
-  static constexpr int EXTRA = (NS - 1) * TILE;   // second and third terms of the decayed keys
+  // second and third terms of the decayed keys; two of them where a step's are made while the step
+  // before is at work (12 packed sequences of up to 2500 tokens, 16 heads of 64, their backward with
+  // states 106 -> 93 us)
+  static constexpr int EBUF = kStates && D == 64 && kCtas == 1 ? 2 : 1;
+  static constexpr int EXTRA = EBUF * (NS - 1) * TILE;
   // the tiles that fit: 227 KB of shared memory, or 113 for each of two CTAs, 2 KB of it for the
   // alignment and what is static
   static constexpr int FIT = ((kCtas == 2 ? 113 : 227) * 1024 - 2048 - H_BYTES - EXTRA) / TILE;
@@ -71,6 +75,9 @@ struct Cfg {
   // without S and O there is room for two of G: a chunk's is read while the next one's is formed
   static constexpr int GBUF = kStates ? 2 : 1;
   static_assert(NSLOT >= 3, "Y and Z and one on its way");
+  // (the state warps tell the products of two steps before by a slot's barrier: it must not come
+  // round again until they have)
+  static_assert((!kStates && EBUF == 1) || NSLOT >= 4, "a slot's turns");
 };
 
 // exp(g m) for a state that is returned: of the product and, to first order, its rounding.
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
 #pragma unroll C::UNROLL
           for (int k = 0; k < 8; ++k, add = 1)
             umma_ss_w(tmem + C::COL_G + 128 * b,
-                      desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1) * C::TILE), mnmajor_step_bytes(k)),
+                      desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1 + t % C::EBUF * (NS - 1)) * C::TILE), mnmajor_step_bytes(k)),
                       desc_advance(dz, mnmajor_step_bytes(k)), idG, add);
       }
       umma_commit_w(&bar_empty[slot(2 * t)]);
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
         if (!kStates && !wait(&bar_s[t & 1], (t >> 1) & 1, ac)) break;
         // the other terms' tiles: read by the products of the step before.  Where no scores hold
         // these warps back, they stay within what two barriers can tell apart.
-        const int behind = terms > 1 ? t - 1 : t - 2;
+        const int behind = terms > 1 && C::EBUF == 1 ? t - 1 : t - 2;
         if ((terms > 1 || kStates) && behind >= 0 &&
             !wait(&bar_empty[2 * behind % NSLOT], (2 * behind / NSLOT) & 1, ac))
           break;
@@ -748,7 +755,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
             if (NS > 1 && terms > 1)
 #pragma unroll
               for (int q = 1; q < NS; ++q)
-                *reinterpret_cast<uint4*>(sExtra + (q - 1) * C::TILE + at) =
+                *reinterpret_cast<uint4*>(sExtra + (q - 1 + t % C::EBUF * (NS - 1)) * C::TILE + at) =
                     make_uint4(term[q][0], term[q][1], term[q][2], term[q][3]);
           }
         }
@@ -832,7 +839,7 @@ cudaError_t launch_linear(const LinearArgs& a, int head_dim, bool states_only, b
   for (int i = 0; i < a.jobs; ++i) terms = a.job[i].terms > terms ? a.job[i].terms : terms;
   if (head_dim == 64) {
     if (states_only)
-      return terms == 1 ? launch<64, 1, true, 2>(a, follows, st) : launch<64, 3, true, 2>(a, follows, st);
+      return terms == 1 ? launch<64, 1, true, 2>(a, follows, st) : launch<64, 3, true>(a, follows, st);
     if (pairs) return terms == 1 ? launch<64, 1, false, 2>(a, follows, st) : launch<64, 3, false, 2>(a, follows, st);
     return terms == 1 ? launch<64, 1, false>(a, follows, st) : launch<64, 3, false>(a, follows, st);
   }
