@@ -40,7 +40,7 @@ typedef struct {
   int original;    /* ATTN_ROTARY_PARTS: positions of the trained range */
   double fast;
   double slow;
-  float magnitude; /* multiplies every cosine and sine */
+  double magnitude; /* multiplies every cosine and sine; finite in fp32 */
 } attn_rotary_table_t;
 
 /* cos_sin fp32 [max_position, rot_dim]: row p holds magnitude cos(p f_a) for

@@ -123,7 +123,7 @@ class _RotaryTable(ctypes.Structure):
     _fields_ = [
         ("max_position", ctypes.c_int), ("rot_dim", ctypes.c_int), ("base", ctypes.c_double),
         ("scaling", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_int),
-        ("fast", ctypes.c_double), ("slow", ctypes.c_double), ("magnitude", ctypes.c_float),
+        ("fast", ctypes.c_double), ("slow", ctypes.c_double), ("magnitude", ctypes.c_double),
     ]
 
 

@@ -63,7 +63,7 @@ __device__ __forceinline__ void phase_sincos(uint64_t phase, float& sn, float& c
 
 __global__ void __launch_bounds__(kTableThreads)
     rotary_table_kernel(const __grid_constant__ Frequencies fr, float* out, int rows, int rot,
-                        float magnitude) {
+                        float m, float m2) {   // m + m2: the magnitude
   // a thread writes 4 cosines and their 4 sines of every `step`th row
   const int quads = rot / 8, per = kTableThreads / quads;   // rows of a block at a time
   const int lane = static_cast<int>(threadIdx.x) / quads, a = (static_cast<int>(threadIdx.x) - lane * quads) * 4;
@@ -85,9 +85,13 @@ __global__ void __launch_bounds__(kTableThreads)
       phase[j] += add[j];
     }
     float* row = out + p * rot + a;
-    *reinterpret_cast<float4*>(row) = make_float4(magnitude * c[0], magnitude * c[1], magnitude * c[2], magnitude * c[3]);
-    *reinterpret_cast<float4*>(row + rot / 2) =
-        make_float4(magnitude * s[0], magnitude * s[1], magnitude * s[2], magnitude * s[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = fmaf(m, c[j], m2 * c[j]);
+      s[j] = fmaf(m, s[j], m2 * s[j]);
+    }
+    *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(row + rot / 2) = make_float4(s[0], s[1], s[2], s[3]);
   }
 }
 
@@ -331,7 +335,7 @@ extern "C" attn_status_t attn_rotary_table(const attn_rotary_table_t* t, float* 
                                            attn_stream_t stream) {
   if (!t || t->max_position < 0 || t->rot_dim <= 0) return ATTN_ERR_INVALID_ARG;
   if (t->rot_dim % 16 || t->rot_dim > kMaxRot) return ATTN_ERR_UNSUPPORTED;
-  if (!(t->base > 0.0) || !std::isfinite(t->base) || !std::isfinite(t->magnitude))
+  if (!(t->base > 0.0) || !std::isfinite(t->base) || !std::isfinite(static_cast<float>(t->magnitude)))
     return ATTN_ERR_INVALID_ARG;
   if (t->scaling < ATTN_ROTARY_NONE || t->scaling > ATTN_ROTARY_PARTS) return ATTN_ERR_INVALID_ARG;
   if (t->scaling != ATTN_ROTARY_NONE && (!(t->factor > 0.0) || !std::isfinite(t->factor)))
@@ -363,8 +367,9 @@ extern "C" attn_status_t attn_rotary_table(const attn_rotary_table_t* t, float* 
   const int per = kTableThreads / (t->rot_dim / 8);
   const size_t blocks = (static_cast<size_t>(t->max_position) + per - 1) / per;
   const int grid = resident_grid(rotary_table_kernel, blocks * kTableThreads, kTableThreads, 1);
+  const float m = static_cast<float>(t->magnitude);
   rotary_table_kernel<<<grid, kTableThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      fr, cos_sin, t->max_position, t->rot_dim, t->magnitude);
+      fr, cos_sin, t->max_position, t->rot_dim, m, static_cast<float>(t->magnitude - m));
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

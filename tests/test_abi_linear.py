@@ -40,7 +40,7 @@ def _table(L, out=FAKE, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(max_position=-1), 1), (dict(rot_dim=0), 1), (dict(rot_dim=8), 2), (dict(rot_dim=24), 2), (dict(rot_dim=272), 2),
     (dict(base=0.0), 1), (dict(base=-1.0), 1), (dict(base=float("inf")), 1), (dict(base=float("nan")), 1),
-    (dict(magnitude=float("inf")), 1), (dict(scaling=4), 1), (dict(scaling=-1), 1), (dict(scaling=1, factor=0.0), 1),
+    (dict(magnitude=float("inf")), 1), (dict(magnitude=1e300), 1), (dict(scaling=4), 1), (dict(scaling=-1), 1), (dict(scaling=1, factor=0.0), 1),
     (dict(scaling=2, factor=float("nan")), 1), (dict(scaling=3, factor=2.0), 1),
     (dict(scaling=3, factor=2.0, original=64, fast=1.0), 1), (dict(scaling=3, factor=2.0, original=64, fast=float("inf")), 1),
     (dict(out=0), 1), (dict(out=FAKE + 8), 3), (dict(max_position=0), 0)])

@@ -19,9 +19,8 @@ def exact_table(n, f, magnitude=1.0, first=0):
     return torch.cat([angle.cos(), angle.sin()], 1) * magnitude
 
 
-# An entry's phase is exact to fp32's resolution; sincospif is within 1 ulp of its value
-# (the documented bound: 2^-24 of at most 1), the correction adds three roundings and the
-# magnitude one, 2^-24 of at most 1 each: 6 2^-24 with the phase's own.
+# An entry's phase is exact to fp32's resolution; the series' last steps round its value at most four
+# times and the magnitude once, 2^-24 of at most 1 each: 6 2^-24 with the phase's own.
 TABLE_TOL = 6 * 2.0 ** -24
 
 
@@ -224,3 +223,14 @@ def test_binding_refusals():
     with pytest.raises(A.AttnError):
         A.attn_rotary_fwd(q, None, cs, rot_offset=8)
     assert math.isfinite(A.attn_rotary_fwd(q, None, cs)[0].sum().item())
+
+
+def test_magnitude_between_two_fp32_numbers():
+    # Held in fp32 it would be 1: off by 2^-24 everywhere.  Two roundings (sine or cosine, product) and the
+    # series' own error stay below 1.8 times one rounding in the mean square.
+    m = 1.0 + 2.0 ** -24
+    f = [10000.0 ** (-2.0 * a / 64) for a in range(32)]
+    want = exact_table(3000, f, m)
+    got = A.attn_rotary_table(3000, 64, magnitude=m, device=DEV).cpu().double()
+    once = (want.float().double() - want).square().mean().sqrt()
+    assert (got - want).square().mean().sqrt() <= 1.8 * once
