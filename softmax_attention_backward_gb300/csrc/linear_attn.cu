@@ -13,10 +13,10 @@
 //   warp 1        MMA issuer: S = X Y^T, G += (diag(d) Y)^T Z, O = X H, O += P Z
 //   warp 3        bulk copies of the output
 //   warps 4..7    scores: S to P = S o W as packed bf16 in TMEM, and O to diag(u) O before P Z is
-//                 added to it
+//                 added to it; the output to the tile of the chunk's last Z
 //   warps 8..15   state: Y to diag(d) Y in place (bf16; the second and third terms in
-//                 tiles of their own), H = l^C H + G, H as bf16 to shared memory, and the
-//                 output to the tile of the chunk's last Z
+//                 tiles of their own), H = l^C H + G, H as bf16 to shared memory; where X has
+//                 two buffers the output
 // S is scaled by products of two table values below and above the diagonal block
 // of 32 x 32, by a table of the 63 diagonals in it.
 //
@@ -67,7 +67,9 @@ struct Cfg {
   // S of a step is formed while the step before is still at work, where the ring can hold both: with
   // three tiles the wait for the next Y would hold up the Z that has to leave before it
   static constexpr bool AHEAD = !kStates && kCtas == 1 && NSLOT >= 4;
-  // the warps that write the output
+  // the warps that write the output: the score warps where S of the next chunk is formed late and
+  // leaves them waiting (backward of 4 x 4096 tokens of 32 heads of 128 345 -> 341 us; of 64, one CTA
+  // on an SM, 226 -> 252)
   static constexpr bool OUT_BY_SCORES = XBUF == 1;
   static constexpr uint32_t COLS = 512 / kCtas;   // of TMEM
   static constexpr uint32_t COL_S = 0, S_STEP = AHEAD ? 128 : 0;   // AHEAD: two buffers

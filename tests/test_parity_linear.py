@@ -266,6 +266,46 @@ def test_captured_and_replayed_with_other_lengths():
     del side
 
 
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (64, 24, 24), (128, 4, 1)])
+def test_calls_in_a_row_of_one_workspace(D, hq, hkv):
+    # Long sequences, so that each call's walks start while its pass over the states runs: their inputs
+    # come from the kernel before, their outputs go to the one behind, and the next call's pass
+    # writes the same workspace.  Eager and replayed.
+    s = Rows([3000, 1500], hq, hkv, D, states=True, seed=14)
+    x = [t.to(DEV) for t in (s.q, s.k, s.v, s.do)]
+    cu, g, dfin = s.cu.to(DEV), s.g.to(DEV), s.dfin.to(DEV)
+    cs = A.attn_rotary_table(3000, D, device=DEV)
+    ws = torch.empty(max(f(*x[:3], g, cu_seqlens=cu) for f in
+                         (A.linear_attn_fwd_workspace_size, A.linear_attn_bwd_workspace_size)), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 0
+    kw = dict(cu_seqlens=cu, workspace=ws)
+
+    def run(initial):
+        q, k = A.attn_rotary_fwd(x[0], x[1], cs, cu_seqlens=cu)
+        o, state = A.linear_attn_fwd(q, k, x[2], g, initial_state=initial, want_final_state=True, **kw)
+        o2, state2 = A.linear_attn_fwd(q, k, o[:, :hkv].contiguous(), g, initial_state=state, want_final_state=True, **kw)
+        dq, dk, dv, dini = A.linear_attn_bwd(q, k, x[2], o2, g, initial_state=initial, dfinal_state=dfin,
+                                             want_dinitial_state=True, **kw)
+        return o, state, o2, state2, *A.attn_rotary_bwd(dq, dk, cs, cu_seqlens=cu), dv, dini
+
+    initial = s.init.to(DEV)
+    want = []
+    for t in run(initial):
+        torch.cuda.synchronize()
+        want.append(t.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(initial)
+    for i in range(6):
+        for t in out:
+            t.fill_(float("nan"))
+        ws.fill_(0xFF)
+        graph.replay()
+        ws.fill_(0xFF)       # (behind the replay: nothing of it may still want the workspace)
+        for a, b, c in zip(out, want, run(initial)):
+            assert torch.equal(a, b) and torch.equal(c, b)
+
+
 def test_two_calls_at_once():
     a, b = Rows([900], 4, 2, 128, states=True, seed=14), Rows([700, 650], 4, 4, 128, states=True, seed=15)
     wa, wb = a.call(packed=True), b.call(packed=True)
