@@ -50,12 +50,12 @@ struct Cut {
 // What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
 // heads (S, P Z and the state's product), `state` for each inner head of a chunk in the pass over
 // the states alone.  Measured, 64 chunks against 32 of 8192 and 4096 tokens: head_dim 128,
-// 1, 2, 4 and 8 inner heads, 218, 341, 558 and 987 us; head_dim 64, 140, 229, 412 and 775.
+// 1, 2, 4 and 8 inner heads, 195, 315, 530 and 970 us; head_dim 64, 140, 229, 412 and 775.
 struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
   double start;                     // a walk's start and end
 };
-constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2, 4.0}, {1.55, 1.72, 0.94, 0.65, 4.0}};
+constexpr Rates kRates[2] = {{0.58, 1.41, 0.80, 0.2, 4.0}, {1.15, 1.73, 0.94, 0.65, 4.0}};
 // Two CTAs of head_dim 64 on an SM hide each other's starts, ends and waits, but leave a walk fewer
 // tiles and registers.  us with one and with two, 32 heads: 16 sequences of 100 tokens 34 and 24, 64
 // of 100 97 and 61, 8 of 4096 with 38 heads 153 and 150, 4 of 4096 with 38 81 and 104; packed, 64
@@ -84,8 +84,8 @@ double makespan(int sms, double na, double ca, double nb, double cb) {
 }
 
 // Measured against cuts of every size (us): backward of 2 x 8192 tokens, 32 heads on 8 of 128, dq
-// uncut and the others in 8 segments of a sequence 286, in 6 317, in 2 405; one sequence of 65536
-// tokens, 8 heads on 2 of 128, segments of 27 chunks 142, of 32 161, of 16 180; packed, forward of
+// uncut and the others in 8 segments of a sequence 278, in 6 307, in 4 306 with dq in 2; one
+// sequence of 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 133, of 32 149, of 16 165; packed, forward of
 // 12 sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 7 chunks (taken) 75, of 12 73, of
 // 4 81; 40 of 16 to 4096, 16 heads of 128, of 13 (taken) 179, of 16 167, uncut 191.
 Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs) {
@@ -414,7 +414,7 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   jv.terms = dinitial_state ? 3 : 1;
   // walks of one length: the jobs' in turn, so that none's longest come late and the rows that
   // they share are read together (12 packed sequences of up to 2500 tokens, 16 heads of 64, 130 ->
-  // 110 us; 4 x 4096 tokens of 32 heads of 128 339 -> 331)
+  // 110 us; 4 x 4096 tokens of 32 heads of 128 339 -> 331 at the time)
   if (group == 1 && cut.chunks[0] == cut.chunks[1]) a.merged = a.jobs;
   if (cut.parts[0] || cut.parts[1]) {
     LinearArgs s = make_args(p);

@@ -22,13 +22,14 @@
 //
 // Bound by: a chunk's tiles of 4 x 32 KB take 4700 cycles of an SM's share of the
 // bandwidth where 128 SMs read (D = 128, one inner head), its products 2560 of the
-// tensor cores; measured 6100 (3.2 us), as each product waits in turn for the warps that
+// tensor cores; measured 5600 (2.9 us), as each product waits in turn for the warps that
 // prepare its operands, and the warp that issues them passes one barrier after the
 // other (300 to 400 cycles each).  So the order of the products is what matters: S
 // of the next step goes out before P Z of this one where the ring holds both.
-// 4 x 4096 tokens of 32 heads of 128: 124 us with the launch, 79 for the bytes alone.
-// Slower, same sizes: two issuing warps 8 %, one wait for several barriers 5 %, fully unrolled
-// products 4 %, the next chunks' tiles fetched to L2 11 %, a ring of 3 tiles 11 %.
+// 4 x 4096 tokens of 32 heads of 128: 116 us with the launch, 79 for the bytes alone.
+// Slower, same sizes: two issuing warps 8 %, one wait for several barriers 5 %, the next
+// chunks' tiles fetched to L2 11 %, a ring of 3 tiles 11 %.  Products go out in fours, from loops:
+// two at a time 7 % slower, all unrolled 5 % (the roles share the instruction caches).
 // At D = 64 there is a second variant with two CTAs on an SM (kCtas, 64 registers a thread, one
 // buffer of S), for many short walks: linear_api.cu has the rule.
 #include "linear.cuh"
@@ -43,7 +44,7 @@ struct Cfg {
   // H meets X in two bf16 terms, or, where there is no room (heads of 128 with terms of the
   // keys beside them), in one, the keys then in two or three.  So two roundings to bf16 are on a
   // product's way besides the output's at most, one of them for most: 1.41 times the error of the
-  // output's alone, 1.6 to 1.7 with one term of each (4 x 4096 tokens 104 us for 124)
+  // output's alone, 1.6 to 1.7 with one term of each (then 104 us for 124 of 4 x 4096 tokens)
   static constexpr int HTERMS = NS == 1 || (D == 64 && kCtas == 1) ? 2 : 1;
   static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
   // second and third terms of the decayed keys; two of them where a step's are made while the step
@@ -60,9 +61,6 @@ struct Cfg {
   static constexpr int NSLOT = (FIT > 8 ? 8 : FIT) - XBUF;
   static constexpr int SMEM = (XBUF + NSLOT) * TILE + H_BYTES + EXTRA + 1024;
   static constexpr int THREADS = 512;
-  // Products of one operand pair issued from unrolled code: heads of 64 gain (1 x 8192 tokens, 32
-  // heads, 64.6 -> 58.5 us), heads of 128 lose to the larger code (4 x 4096 tokens 104 -> 108).
-  static constexpr int UNROLL = D == 64 ? 8 : 2;
   static constexpr int HC = D / 2;                // state columns of a thread
   // S of a step is formed while the step before is still at work, where the ring can hold both: with
   // three tiles the wait for the next Y would hold up the Z that has to leave before it
@@ -373,6 +371,8 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
     const uint64_t dm0 = desc_mnmajor_base(smem_u32(ring), kLinearChunk);
     const uint64_t dH = desc_mnmajor_base(smem_u32(sH), D);
     const uint64_t dE = desc_mnmajor_base(smem_u32(sExtra), kLinearChunk);
+    // from one K step to the next, in a descriptor's 16 bytes: along a tile's rows, and down its columns
+    constexpr int kRowStep = kmajor_step_bytes(128, 1) / 16, kColumnStep = mnmajor_step_bytes(1) / 16;
     auto slot = [](int tile) { return tile % NSLOT; };
     auto landed = [&](int tile) { return warp_wait(&bar_full[slot(tile)], (tile / NSLOT) & 1, ac); };
     // S of step t, the g-th of chunk n
@@ -382,10 +382,11 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
       if (!landed(2 * t)) return false;
       tc_fence_after();
       const uint64_t dx = desc_advance(dx0, bx * C::TILE), dy = desc_advance(dk0, slot(2 * t) * C::TILE);
-#pragma unroll C::UNROLL
-      for (int k = 0; k < D / 16; ++k)
-        umma_ss_w(tmem + C::COL_S + C::S_STEP * (t & 1), desc_advance(dx, kmajor_step_bytes(128, k)),
-                  desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
+#pragma unroll 1
+      for (int k = 0; k < D / 16; k += 4)
+        umma4_ss_w<kRowStep, kRowStep>(tmem + C::COL_S + C::S_STEP * (t & 1),
+                                       desc_advance(dx, kmajor_step_bytes(128, k)),
+                                       desc_advance(dy, kmajor_step_bytes(128, k)), idS, k > 0);
       umma_commit_w(&bar_s[t & 1]);
       return true;
     };
@@ -401,11 +402,13 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
         uint32_t add = !each && g > 0;
 #pragma unroll 1
         for (int e = terms - 1; e >= 0; --e)
-#pragma unroll C::UNROLL
-          for (int k = 0; k < 8; ++k, add = 1)
-            umma_ss_w(tmem + C::COL_G + 128 * b,
-                      desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1 + t % C::EBUF * (NS - 1)) * C::TILE), mnmajor_step_bytes(k)),
-                      desc_advance(dz, mnmajor_step_bytes(k)), idG, add);
+#pragma unroll 1
+          for (int k = 0; k < 8; k += 4, add = 1)
+            umma4_ss_w<kColumnStep, kColumnStep>(
+                tmem + C::COL_G + 128 * b,
+                desc_advance(e == 0 ? dy : desc_advance(dE, (e - 1 + t % C::EBUF * (NS - 1)) * C::TILE),
+                             mnmajor_step_bytes(k)),
+                desc_advance(dz, mnmajor_step_bytes(k)), idG, add);
       }
       umma_commit_w(&bar_empty[slot(2 * t)]);
       if (n < n_grow && (each || g == inner - 1)) umma_commit_w(&bar_g[b]);
@@ -418,10 +421,11 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
         if (!warp_wait(&bar_h, n & 1, ac) || (n > 0 && !warp_wait(&bar_of, (n - 1) & 1, ac))) return false;
         tc_fence_after();
         const uint64_t dx = desc_advance(dx0, bx * C::TILE);
-#pragma unroll C::UNROLL
-        for (int k = 0; k < C::HTERMS * D / 16; ++k)   // (the second term lies behind the first)
-          umma_ss_w(tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k % (D / 16))),
-                    desc_advance(dH, (k / (D / 16)) * (D * D * 2) + mnmajor_step_bytes(k % (D / 16))), idO, k > 0);
+#pragma unroll 1
+        for (int k = 0; k < C::HTERMS * D / 16; k += 4)   // (the second term lies behind the first)
+          umma4_ss_w<kRowStep, kColumnStep>(
+              tmem + C::COL_O, desc_advance(dx, kmajor_step_bytes(128, k % (D / 16))),
+              desc_advance(dH, (k / (D / 16)) * (D * D * 2) + mnmajor_step_bytes(k % (D / 16))), idO, k > 0);
         umma_commit_w(&bar_qh);
       }
       if (C::AHEAD ? inner == 1 : g == inner - 1) umma_commit_w(&bar_xempty[bx]);
@@ -431,10 +435,10 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
       if (!warp_wait(&bar_p[t & 1], (t >> 1) & 1, ac)) return false;
       tc_fence_after();
       const uint64_t dz = desc_advance(dm0, slot(2 * t + 1) * C::TILE);
-#pragma unroll C::UNROLL
-      for (int k = 0; k < 8; ++k)
-        umma_ts_w(tmem + C::COL_O, tmem + C::COL_S + C::S_STEP * (t & 1) + 8 * k, desc_advance(dz, mnmajor_step_bytes(k)),
-                  idO, 1u);
+#pragma unroll 1
+      for (int k = 0; k < 8; k += 4)
+        umma4_ts_w<8, kColumnStep>(tmem + C::COL_O, tmem + C::COL_S + C::S_STEP * (t & 1) + 8 * k,
+                                   desc_advance(dz, mnmajor_step_bytes(k)), idO, 1u);
       if (g == inner - 1) umma_commit_w(&bar_o);
       return true;
     };

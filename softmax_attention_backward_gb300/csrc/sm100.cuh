@@ -578,6 +578,38 @@ __device__ __forceinline__ void umma_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Four of them, K steps in a row, in one piece: the operands' descriptors (A in tensor memory:
+// its column) advance by SA and SB, and one lane is elected once.
+template <int SA, int SB>
+__device__ __forceinline__ void umma4_ss_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %4, %4;\n"
+      " add.s64 a1, %1, %5;\n add.s64 b1, %2, %8;\n add.s64 a2, %1, %6;\n add.s64 b2, %2, %9;\n"
+      " add.s64 a3, %1, %7;\n add.s64 b3, %2, %10;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB),
+      "n"(2 * SB), "n"(3 * SB)
+      : "memory");
+}
+template <int SA, int SB>
+__device__ __forceinline__ void umma4_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e, t;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, %4, %4;\n add.s32 a1, %1, %5;\n add.s64 b1, %2, %8;\n add.s32 a2, %1, %6;\n add.s64 b2, %2, %9;\n"
+      " add.s32 a3, %1, %7;\n add.s64 b3, %2, %10;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB),
+      "n"(2 * SB), "n"(3 * SB)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit_w(uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
