@@ -37,7 +37,8 @@ extern "C" {
  * cu_seqlens[num_seqs] are padding: outputs there are exact zeros, inputs there
  * do not affect any result.  A sequence may be empty.  A cu_seqlens that does not
  * begin with 0, decreases or passes `tokens` is flagged ATTN_DEVERR_SEQLEN; the rows of the
- * sequences concerned are unspecified.
+ * sequences concerned are unspecified, and no memory beside the outputs and the workspace is
+ * written whatever it holds.
  *
  * q_stride .. dout_stride are the elements between two tokens' rows (0: dense,
  * heads * head_dim; else at least that and a multiple of 8), so that slices of one

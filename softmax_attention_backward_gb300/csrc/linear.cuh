@@ -6,10 +6,10 @@
 #include "common.cuh"
 #include "launch.h"
 #include "linear.h"
+#include "places.h"
 
 namespace attn {
 
-constexpr int kLinearChunk = 128;   // tokens of a chunk
 constexpr int kLinearJobs = 3;      // outputs of one launch at most
 
 // The output and the three gradients are one recurrence over rows x, y, z:
@@ -64,7 +64,8 @@ __device__ __forceinline__ float log_decay_of(const LinearArgs& a, int h) {
   return fmaxf(g, -1e6f);
 }
 
-// The rows of sequence n, kept within the tensors whatever cu holds.
+// The rows of sequence n alone, kept within the tensors whatever cu holds; two of them may overlap
+// where it decreases.
 __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& row0, int& len) {
   if (!a.cu) {
     row0 = n * a.seqlen;
@@ -76,6 +77,27 @@ __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& r
   const int end = min(max(e, row0), a.tokens);
   len = end - row0;
   if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
+}
+
+// The rows of sequences n0 .. n0 + 31, one a lane (no token past the last), disjoint whatever cu holds;
+// `top` is the end of the sequence before (0 at n0 = 0), then that of the last one.
+__device__ __forceinline__ void packed_rows(const LinearArgs& a, int n0, int& top, int& row0, int& len) {
+  const int lane = lane_id();
+  const bool live = n0 + lane < a.num_seqs;
+  const int first = n0 == 0 ? __ldg(a.cu) : top;
+  const int e = live ? __ldg(a.cu + n0 + lane + 1) : 0;
+  top = packed_end(first, top, a.tokens);
+  int end = packed_end(e, top, a.tokens);
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(0xffffffffu, end, d);
+    if (lane >= d) end = max(end, o);
+  }
+  row0 = __shfl_up_sync(0xffffffffu, end, 1);
+  if (lane == 0) row0 = top;
+  len = end - row0;
+  if (((live && e != end) || (n0 == 0 && first != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
+  top = __shfl_sync(0xffffffffu, end, 31);
 }
 
 // `pairs` (head_dim 64): two CTAs on an SM.  `follows`: the launch before on the stream is the pass

@@ -159,7 +159,7 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs)
   Cut c{};
   for (int i = 0; i < (backward ? 2 : 1); ++i) {
     c.chunks[i] = opt[i][best[i]].chunks;
-    c.slots[i] = packed ? p->tokens / (c.chunks[i] * kLinearChunk) + p->num_seqs
+    c.slots[i] = packed ? packed_places(p->tokens, p->num_seqs, c.chunks[i])
                         : p->num_seqs * (most > 0 ? (most + c.chunks[i] - 1) / c.chunks[i] : 1);
     c.parts[i] = c.chunks[i] < most;
   }

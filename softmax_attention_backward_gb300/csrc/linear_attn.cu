@@ -86,11 +86,6 @@ __device__ __forceinline__ float decay_exact(float g, float m) {
   return fmaf(e, fmaf(g, m, -p), e);
 }
 
-__device__ __forceinline__ int chunks_of(int len) { return (len + kLinearChunk - 1) / kLinearChunk; }
-__device__ __forceinline__ int segments_of(int len, int seg_chunks) {
-  return max(1, (chunks_of(len) + seg_chunks - 1) / seg_chunks);
-}
-
 // A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most; `first` is
 // the place of the sequence's first segment among all of them.
 struct Place {
@@ -112,12 +107,10 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
     else sequence_rows(a, p.n, p.row0, p.len);
   } else {
     const int lane = lane_id();
-    for (int n0 = 0, before = 0; n0 < a.num_seqs; n0 += 32) {
-      int row0 = 0, len = 0, count = 0;
-      if (n0 + lane < a.num_seqs) {
-        sequence_rows(a, n0 + lane, row0, len);
-        count = segments_of(len, j.seg_chunks);
-      }
+    for (int n0 = 0, before = 0, top = 0; n0 < a.num_seqs; n0 += 32) {
+      int row0, len;
+      packed_rows(a, n0, top, row0, len);
+      const int count = n0 + lane < a.num_seqs ? segments_of(len, j.seg_chunks) : 0;
       int sum = count;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
