@@ -26,7 +26,8 @@ struct LinearJob {
   __nv_bfloat16* out;       // dense, heads_x heads; null: states only
   int heads_x;              // heads that the job's items go over (states only: KV heads)
   int backwards;
-  int terms;                // bf16 terms of a decayed key: 3 where `last` is returned, else 1 (or 2, see Cfg)
+  int terms;                // bf16 terms of a decayed key: 3 where `last` is returned; 2 of a pass over the
+                            // states whose walks hold them in one (see state_terms); else 1
   int inner;                // heads of y and z that meet one head of x
   FastDiv fd_heads;         // heads_x
   FastDiv fd_kv;            // heads of x per KV head
@@ -41,6 +42,15 @@ struct LinearJob {
   float* parts;
   float* parts_t;
 };
+
+// The bf16 terms in which a state meets its rows, in a walk of a launch whose keys come in up to `terms`:
+// two, or, where there is no room (heads of 128 or two CTAs on an SM, with terms of the keys
+// beside them), one, the keys then in two or three, in the pass over the states as well.  So two roundings to
+// bf16 are on a product's way besides the output's at most, one of them for most: 1.41 times
+// the error of the output's alone, 1.6 to 1.7 with one term of each (then 104 us for 124 of 4 x 4096 tokens).
+constexpr int state_terms(int head_dim, int terms, bool pairs) {
+  return terms == 1 || (head_dim == 64 && !pairs) ? 2 : 1;
+}
 
 struct LinearArgs {
   LinearJob job[kLinearJobs];

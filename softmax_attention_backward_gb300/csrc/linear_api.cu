@@ -419,7 +419,11 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   if (cut.parts[0] || cut.parts[1]) {
     LinearArgs s = make_args(p);
     if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);
-    if (cut.parts[0]) s.job[s.jobs++] = state_job(jq, p, 1, nullptr);
+    if (cut.parts[0]) {
+      LinearJob& sq = s.job[s.jobs++];
+      sq = state_job(jq, p, 1, nullptr);
+      if (state_terms(p->head_dim, jv.terms, cut.pairs) == 1) sq.terms = 2;
+    }
     if (launch_linear(s, p->head_dim, true, false, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   const bool follows = cut.parts[0] || cut.parts[1];

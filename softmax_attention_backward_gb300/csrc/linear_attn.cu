@@ -41,11 +41,7 @@ template <int D, int NS, bool kStates, int kCtas>
 struct Cfg {
   static constexpr int C = kLinearChunk;
   static constexpr int TILE = C * D * 2;
-  // H meets X in two bf16 terms, or, where there is no room (heads of 128 with terms of the
-  // keys beside them), in one, the keys then in two or three.  So two roundings to bf16 are on a
-  // product's way besides the output's at most, one of them for most: 1.41 times the error of the
-  // output's alone, 1.6 to 1.7 with one term of each (then 104 us for 124 of 4 x 4096 tokens)
-  static constexpr int HTERMS = NS == 1 || (D == 64 && kCtas == 1) ? 2 : 1;
+  static constexpr int HTERMS = state_terms(D, NS, kCtas == 2);
   static constexpr int H_BYTES = kStates ? 0 : D * D * 2 * HTERMS;
   // second and third terms of the decayed keys; two of them where a step's are made while the step
   // before is at work (12 packed sequences of up to 2500 tokens, 16 heads of 64, their backward with
