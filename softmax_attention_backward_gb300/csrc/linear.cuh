@@ -35,10 +35,10 @@ struct LinearJob {
   float* last;              // state after its last token, or null
   int transposed;           // `first` is held transposed
   int seg_chunks;           // chunks of a segment at most
-  int slots;                // (sequence, segment) places of the job
-  // States that the segments add, fp32 [slots, heads_kv, D/4, D, 4] (columns in fours,
-  // rows within): read by a job with `out`, written by one without, which also
-  // writes them transposed where that is not null.
+  int slots;                // (sequence, segment) pairs at most, without `out` those that hand a state on
+  // States that the segments add, but for the last of each sequence in the walk's direction, fp32
+  // [places, heads_kv, D/4, D, 4] (columns in fours, rows within): read by a job with `out`, written
+  // by one without, which also writes them transposed where that is not null.
   float* parts;
   float* parts_t;
 };
@@ -89,22 +89,23 @@ __device__ __forceinline__ void sequence_rows(const LinearArgs& a, int n, int& r
   if ((b != row0 || e != end || (n == 0 && b != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
 }
 
-// The rows of sequences n0 .. n0 + 31, one a lane (no token past the last), disjoint whatever cu holds;
+// The rows of sequences n0 .. n0 + 31, one a lane (any past the last one), disjoint whatever cu holds;
 // `top` is the end of the sequence before (0 at n0 = 0), then that of the last one.
 __device__ __forceinline__ void packed_rows(const LinearArgs& a, int n0, int& top, int& row0, int& len) {
   const int lane = lane_id();
   const bool live = n0 + lane < a.num_seqs;
   const int first = n0 == 0 ? __ldg(a.cu) : top;
-  const int e = live ? __ldg(a.cu + n0 + lane + 1) : 0;
+  const int e = live ? __ldg(a.cu + n0 + lane + 1) : a.tokens;
   top = packed_end(first, top, a.tokens);
   int end = packed_end(e, top, a.tokens);
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int o = __shfl_up_sync(0xffffffffu, end, d);
-    if (lane >= d) end = max(end, o);
-  }
   row0 = __shfl_up_sync(0xffffffffu, end, 1);
   if (lane == 0) row0 = top;
+  if (__any_sync(0xffffffffu, end < row0)) {
+#pragma unroll 1
+    for (int d = 1; d < 32; d *= 2) end = max(end, __shfl_up_sync(0xffffffffu, end, d));
+    row0 = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) row0 = top;
+  }
   len = end - row0;
   if (((live && e != end) || (n0 == 0 && first != 0)) && a.err) atomicOr(a.err, ATTN_DEVERR_SEQLEN);
   top = __shfl_sync(0xffffffffu, end, 31);

@@ -38,9 +38,10 @@ attn_status_t check(const linear_attn_problem_t* p) {
 }
 
 // How sequences are cut into segments: chunks of a segment for the jobs that walk
-// forwards (o, dq) and backwards (dk, dv), and the places that this makes.
+// forwards (o, dq) and backwards (dk, dv), the segments that this makes at most, and the states that
+// they hand on.
 struct Cut {
-  int chunks[2], slots[2];
+  int chunks[2], slots[2], places[2];
   bool parts[2];   // a sequence may have several segments
   bool dq_first;   // backward: the walks of dq are the longer ones
   bool pairs;      // head_dim 64: two CTAs on an SM
@@ -159,8 +160,9 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs)
   Cut c{};
   for (int i = 0; i < (backward ? 2 : 1); ++i) {
     c.chunks[i] = opt[i][best[i]].chunks;
-    c.slots[i] = packed ? packed_places(p->tokens, p->num_seqs, c.chunks[i])
-                        : p->num_seqs * (most > 0 ? (most + c.chunks[i] - 1) / c.chunks[i] : 1);
+    const int segs = most > 0 ? (most + c.chunks[i] - 1) / c.chunks[i] : 1;   // of a sequence, dense
+    c.slots[i] = packed ? packed_walks(p->tokens, p->num_seqs, c.chunks[i]) : p->num_seqs * segs;
+    c.places[i] = packed ? packed_places(p->tokens, c.chunks[i]) : p->num_seqs * (segs - 1);
     c.parts[i] = c.chunks[i] < most;
   }
   c.pairs = pairs;
@@ -195,12 +197,12 @@ Cut cut_sequences(const linear_attn_problem_t* p, bool backward) {
   return k.cut;
 }
 
-size_t state_bytes(const linear_attn_problem_t* p, int slots) {
-  return sizeof(float) * static_cast<size_t>(slots) * p->heads_kv * p->head_dim * p->head_dim;
+size_t state_bytes(const linear_attn_problem_t* p, int states) {
+  return sizeof(float) * static_cast<size_t>(states) * p->heads_kv * p->head_dim * p->head_dim;
 }
 // The states of one launch: forwards those of o or dq, backwards those of dv and, transposed, dk.
 size_t workspace_bytes_of(const linear_attn_problem_t* p, const Cut& c) {
-  return (c.parts[0] ? state_bytes(p, c.slots[0]) : 0) + (c.parts[1] ? 2 * state_bytes(p, c.slots[1]) : 0);
+  return (c.parts[0] ? state_bytes(p, c.places[0]) : 0) + (c.parts[1] ? 2 * state_bytes(p, c.places[1]) : 0);
 }
 
 LinearArgs make_args(const linear_attn_problem_t* p) {
@@ -255,9 +257,10 @@ void set_job(LinearJob& j, const linear_attn_problem_t* p, int heads_x, int shar
   j.slots = c.slots[way];
 }
 // The job that fills `j`'s states, and their transposes where those are wanted.
-LinearJob state_job(const LinearJob& j, const linear_attn_problem_t* p, int inner, float* transposes) {
+LinearJob state_job(const LinearJob& j, const linear_attn_problem_t* p, int inner, const Cut& c, float* transposes) {
   LinearJob s = j;
   s.out = nullptr;
+  s.slots = c.places[j.backwards];
   s.heads_x = p->heads_kv;
   s.inner = inner;
   s.fd_heads = make_fastdiv(p->heads_kv);
@@ -340,7 +343,7 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   j.parts = static_cast<float*>(workspace);
   if (cut.parts[0]) {
     LinearArgs s = make_args(p);
-    s.job[s.jobs++] = state_job(j, p, 1, nullptr);
+    s.job[s.jobs++] = state_job(j, p, 1, cut, nullptr);
     if (launch_linear(s, p->head_dim, true, false, false, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   return launch_linear(a, p->head_dim, false, cut.pairs, cut.parts[0], st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -407,8 +410,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   float* ws = static_cast<float*>(workspace);
   if (cut.parts[1]) {
     jv.parts = ws;
-    jk.parts = ws + state_bytes(p, cut.slots[1]) / sizeof(float);
-    ws = jk.parts + state_bytes(p, cut.slots[1]) / sizeof(float);
+    jk.parts = ws + state_bytes(p, cut.places[1]) / sizeof(float);
+    ws = jk.parts + state_bytes(p, cut.places[1]) / sizeof(float);
   }
   jq.parts = ws;
   jv.terms = dinitial_state ? 3 : 1;
@@ -418,10 +421,10 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
   if (group == 1 && cut.chunks[0] == cut.chunks[1]) a.merged = a.jobs;
   if (cut.parts[0] || cut.parts[1]) {
     LinearArgs s = make_args(p);
-    if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, jk.parts);
+    if (cut.parts[1]) s.job[s.jobs++] = state_job(jv, p, group, cut, jk.parts);
     if (cut.parts[0]) {
       LinearJob& sq = s.job[s.jobs++];
-      sq = state_job(jq, p, 1, nullptr);
+      sq = state_job(jq, p, 1, cut, nullptr);
       if (state_terms(p->head_dim, jv.terms, cut.pairs) == 1) sq.terms = 2;
     }
     if (launch_linear(s, p->head_dim, true, false, false, st) != cudaSuccess) return ATTN_ERR_CUDA;

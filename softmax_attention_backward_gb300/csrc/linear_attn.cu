@@ -83,59 +83,63 @@ __device__ __forceinline__ float decay_exact(float g, float m) {
 }
 
 // A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most; `first` is
-// the place of the sequence's first segment among all of them.
+// the place in the workspace of the first state that its segments hand on.
 struct Place {
   int n, row0, len, seg, nseg, per, first;
 };
 
-// The place that the CTAs of a slot take, by one warp; n = -1 where there is none.  The longer
+// The segment that the CTAs of a slot take, by one warp; n = -1 where there is none.  The pass over the
+// states leaves out each sequence's last segment in the walk's direction.  The longer
 // walks of each 32 packed sequences come first, so that no SM is left with one at the
 // end (backward of 12 sequences of up to 2500 tokens, 16 heads of 64, the jobs' walks in turn: 110
-// us, 118 with each job's in the sequences' order).
+// us, 118 with each job's in the sequences' order).  A search over n sequences takes n / 32 steps, in each
+// CTA: packed sequences by the thousand cost more than their rows.
+template <bool kStates>
 __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob& j, int slot) {
+  constexpr int kLeft = kStates ? 1 : 0;   // segments of a sequence that have no slot
   Place p{-1, 0, 0, 0, 1, 1, 0};
   if (!a.cu) {
     p.nseg = segments_of(a.seqlen, j.seg_chunks);
-    p.n = slot / p.nseg;
-    p.seg = slot - p.n * p.nseg;
-    p.first = slot - p.seg;
+    const int count = p.nseg - kLeft;
+    p.n = count > 0 ? slot / count : a.num_seqs;
+    p.seg = slot - p.n * count;
+    p.first = p.n * (p.nseg - 1);
     if (p.n >= a.num_seqs) p.n = -1;
     else sequence_rows(a, p.n, p.row0, p.len);
   } else {
     const int lane = lane_id();
-    for (int n0 = 0, before = 0, top = 0; n0 < a.num_seqs; n0 += 32) {
+    for (int n0 = 0, before = 0, handed = 0, top = 0; n0 < a.num_seqs; n0 += 32) {
       int row0, len;
       packed_rows(a, n0, top, row0, len);
-      const int count = n0 + lane < a.num_seqs ? segments_of(len, j.seg_chunks) : 0;
-      int sum = count;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      // (lanes past the last sequence count none)
-      const int per = count ? (chunks_of(len) + count - 1) / count : 0;
-      int turn = before;   // segments of the block's sequences with longer walks
+      const bool live = n0 + lane < a.num_seqs;   // (lanes past the last sequence count none)
+      const int nseg = live ? segments_of(len, j.seg_chunks) : 0;
+      const int count = live ? nseg - kLeft : 0;
+      const int all = __reduce_add_sync(0xffffffffu, count);
+      const int on = kStates ? all : all - min(32, a.num_seqs - n0);   // states handed on
+      if (slot < before + all) {
+        const int per = live ? (chunks_of(len) + nseg - 1) / nseg : 0;
+        int turn = before;     // segments of the block's sequences with longer walks
+        int prior = handed;    // states that those before hand on
 #pragma unroll 4
-      for (int d = 0; d < min(32, a.num_seqs - n0); ++d) {
-        const int p2 = __shfl_sync(0xffffffffu, per, d), c2 = __shfl_sync(0xffffffffu, count, d);
-        turn += p2 > per || (p2 == per && d < lane) ? c2 : 0;
-      }
-      const bool here = slot >= turn && slot < turn + count;
-      const unsigned who = __ballot_sync(0xffffffffu, here);
-      if (who) {
-        const int src = __ffs(who) - 1;
+        for (int d = 0; d < min(32, a.num_seqs - n0); ++d) {
+          const int p2 = __shfl_sync(0xffffffffu, per, d), c2 = __shfl_sync(0xffffffffu, count, d);
+          turn += p2 > per || (p2 == per && d < lane) ? c2 : 0;
+          prior += d < lane ? c2 - (1 - kLeft) : 0;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, slot >= turn && slot < turn + count)) - 1;
         p.n = n0 + src;
         p.row0 = __shfl_sync(0xffffffffu, row0, src);
         p.len = __shfl_sync(0xffffffffu, len, src);
-        p.nseg = __shfl_sync(0xffffffffu, count, src);
+        p.nseg = __shfl_sync(0xffffffffu, nseg, src);
         p.seg = slot - __shfl_sync(0xffffffffu, turn, src);
-        p.first = before + __shfl_sync(0xffffffffu, sum - count, src);
+        p.first = __shfl_sync(0xffffffffu, prior, src);
         break;
       }
-      before += __shfl_sync(0xffffffffu, sum, 31);
+      before += all;
+      handed += on;
     }
   }
+  if (kStates && j.backwards) ++p.seg;
   p.per = (chunks_of(p.len) + p.nseg - 1) / p.nseg;
   return p;
 }
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
   }
   const float ln = log_decay_of(a, hkv), l2 = ln * kLog2e;
   if (warp == 2) {
-    const Place p = find_place(a, j, slot);
+    const Place p = find_place<kStates>(a, j, slot);
     if (lane_id() == 0) s_place = p;
   }
   if (warp == 3) {
@@ -265,11 +269,10 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  Place pl = s_place;
+  const Place pl = s_place;
   const bool back = j.backwards;
   // the sequence's last segment in the walk's direction, which no state follows
   const bool is_end = pl.n >= 0 && pl.seg == (back ? 0 : pl.nseg - 1);
-  if (kStates && is_end) pl.n = -1;
   const int nch = pl.n < 0 ? 0 : chunks_of(pl.len);
   const int c_lo = min(nch, pl.seg * pl.per), c_hi = min(nch, c_lo + pl.per);
   const int n_walk = c_hi - c_lo;
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
         const int lo = sg * pl.per * kLinearChunk, hi = min(pl.len, lo + pl.per * kLinearChunk);
         const float keep = NS > 1 ? decay_exact(ln, max(hi - lo, 0)) : ex2(l2 * max(hi - lo, 0));
         const float4* g = reinterpret_cast<const float4*>(
-            j.parts + (static_cast<int64_t>(pl.first + sg) * a.heads_kv + hkv) * D * D);
+            j.parts + (static_cast<int64_t>(pl.first + sg - back) * a.heads_kv + hkv) * D * D);
         if (mine)
 #pragma unroll
           for (int x = 0; x < C::HC; x += 4) {
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
       }
     }
     if (kStates) {
-      const int64_t at = (static_cast<int64_t>(pl.first + pl.seg) * a.heads_kv + hkv) * D * D;
+      const int64_t at = (static_cast<int64_t>(pl.first + pl.seg - back) * a.heads_kv + hkv) * D * D;
       if (mine)
 #pragma unroll
         for (int x = 0; x < C::HC; x += 4) {

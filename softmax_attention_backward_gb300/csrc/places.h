@@ -25,9 +25,11 @@ ATTN_HD int packed_end(int e, int before, int tokens) {
   return kept > before ? kept : before;
 }
 
-// Places for the segments of all sequences: each has one more than `len` fills at most.
-ATTN_HD int packed_places(int tokens, int num_seqs, int seg_chunks) {
+// The CTAs that the segments of all sequences take at most: a sequence has one more than `len` fills.
+ATTN_HD int packed_walks(int tokens, int num_seqs, int seg_chunks) {
   return tokens / (seg_chunks * kLinearChunk) + num_seqs;
 }
+// And the states that segments hand on, all but the last of each sequence: the workspace's places.
+ATTN_HD int packed_places(int tokens, int seg_chunks) { return tokens / (seg_chunks * kLinearChunk); }
 
 }  // namespace attn
