@@ -82,8 +82,8 @@ __device__ __forceinline__ float decay_exact(float g, float m) {
   return fmaf(e, fmaf(g, m, -p), e);
 }
 
-// A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most; `first` is
-// the place in the workspace of the first state that its segments hand on.
+// A walk's place: sequence n, its segment `seg` of `nseg`, each of `per` chunks at most; segment
+// i hands its state on at place first + i of the workspace.
 struct Place {
   int n, row0, len, seg, nseg, per, first;
 };
@@ -139,7 +139,10 @@ __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob
       handed += on;
     }
   }
-  if (kStates && j.backwards) ++p.seg;
+  if (j.backwards) {   // segment 0 hands nothing on
+    if (kStates) ++p.seg;
+    --p.first;
+  }
   p.per = (chunks_of(p.len) + p.nseg - 1) / p.nseg;
   return p;
 }
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
         const int lo = sg * pl.per * kLinearChunk, hi = min(pl.len, lo + pl.per * kLinearChunk);
         const float keep = NS > 1 ? decay_exact(ln, max(hi - lo, 0)) : ex2(l2 * max(hi - lo, 0));
         const float4* g = reinterpret_cast<const float4*>(
-            j.parts + (static_cast<int64_t>(pl.first + sg - back) * a.heads_kv + hkv) * D * D);
+            j.parts + (static_cast<int64_t>(pl.first + sg) * a.heads_kv + hkv) * D * D);
         if (mine)
 #pragma unroll
           for (int x = 0; x < C::HC; x += 4) {
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
       }
     }
     if (kStates) {
-      const int64_t at = (static_cast<int64_t>(pl.first + pl.seg - back) * a.heads_kv + hkv) * D * D;
+      const int64_t at = (static_cast<int64_t>(pl.first + pl.seg) * a.heads_kv + hkv) * D * D;
       if (mine)
 #pragma unroll
         for (int x = 0; x < C::HC; x += 4) {

@@ -11,7 +11,7 @@ namespace attn {
 
 constexpr int kLinearChunk = 128;   // tokens of a chunk
 
-ATTN_HD int chunks_of(int len) { return len / kLinearChunk + (len % kLinearChunk != 0); }
+ATTN_HD int chunks_of(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kLinearChunk - 1) / kLinearChunk); }
 ATTN_HD int segments_of(int len, int seg_chunks) {
   const int n = (chunks_of(len) + seg_chunks - 1) / seg_chunks;
   return n > 1 ? n : 1;
