@@ -38,8 +38,9 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const StepArg
   constexpr int RT = kStepThreads / CT;        // threads over the rows
   constexpr int R = D / RT;                    // rows of a thread
   static_assert(R >= 1, "rows");
-  __shared__ float sk[D], sv[C], sq[kStepHeads][D];
-  __shared__ float part[kStepHeads][RT][C];
+  __shared__ float sk[D], sq[kStepHeads][D];
+  __shared__ __align__(16) float sv[C];   // (read and written in 16-byte pieces)
+  __shared__ __align__(16) float part[kStepHeads][RT][C];
   const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * C;
   const int ct = threadIdx.x % CT, rt = threadIdx.x / CT;
   const int slot = a.slots ? __ldg(a.slots + n) : n;
