@@ -117,7 +117,8 @@ attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const void* q, con
  * [num_slots, heads_kv, head_dim, head_dim]: sequence n's in slot slots[n] (device
  * int32 [num_seqs]; NULL: slot n).  The states are updated in place and o (bf16
  * [num_seqs, heads_q, head_dim]) is written, all in fp32 but for the rounding of
- * o.  A slot of -1 marks a padding row: its o is zeros.  Slots outside
+ * o; the decay is held in two fp32 terms, so that its error does not grow with the steps.  An infinite
+ * or NaN element of a state stays one of either.  A slot of -1 marks a padding row: its o is zeros.  Slots outside
  * [-1, num_slots) and slots that an earlier sequence of the call has are flagged
  * ATTN_DEVERR_INDEX_RANGE; their rows of o are zeros and they touch no state.
  * Other slots are left as they are.  o and the states share no memory with another

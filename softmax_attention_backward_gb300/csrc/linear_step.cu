@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const StepArg
   constexpr int RT = kStepThreads / CT;        // threads over the rows
   constexpr int R = D / RT;                    // rows of a thread
   static_assert(R >= 1, "rows");
-  __shared__ float sk[D], sq[kStepHeads][D];
+  __shared__ float sk[D], sq[kStepHeads][D], s_decay[2];
   __shared__ __align__(16) float sv[C];   // (read and written in 16-byte pieces)
   __shared__ __align__(16) float part[kStepHeads][RT][C];
   const int n = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * C;
@@ -57,6 +57,18 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const StepArg
     for (int i = 0; i < R; ++i) s[i] = *reinterpret_cast<const float4*>(base + i * RT * D);
   if (threadIdx.x < D) sk[threadIdx.x] = __bfloat162float(a.k[n * a.k_stride + h * D + threadIdx.x]);
   if (threadIdx.x < C) sv[threadIdx.x] = __bfloat162float(a.v[n * a.v_stride + h * D + c0 + threadIdx.x]);
+  // The decay in two parts: the rounding of one would be the same in every step (log_decay -2^-11: a
+  // steady state off by 2^-14).  By one thread, while the others' loads are under way.
+  if (threadIdx.x == kStepThreads - 1) {
+    float g = __ldg(a.log_decay + h);
+    if (!(g <= 0.f)) {
+      if (live && a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
+      g = 0.f;
+    }
+    const double l = exp(static_cast<double>(g));
+    s_decay[0] = static_cast<float>(l);
+    s_decay[1] = static_cast<float>(l - s_decay[0]);
+  }
   if (__syncthreads_or(twice)) {
     live = false;
     bad = true;
@@ -68,20 +80,15 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const StepArg
           __float2bfloat16_rn(0.f);
     return;
   }
-  float g = __ldg(a.log_decay + h);
-  if (!(g <= 0.f)) {
-    if (threadIdx.x == 0 && a.err) atomicOr(a.err, ATTN_DEVERR_DECAY);
-    g = 0.f;
-  }
-  const float l = expf(g);
+  const float l = s_decay[0], l2 = s_decay[1];
   const float4 v = *reinterpret_cast<const float4*>(sv + ct * 4);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const float k = sk[rt + i * RT];
-    s[i].x = fmaf(l, s[i].x, k * v.x);
-    s[i].y = fmaf(l, s[i].y, k * v.y);
-    s[i].z = fmaf(l, s[i].z, k * v.z);
-    s[i].w = fmaf(l, s[i].w, k * v.w);
+    s[i].x = fmaf(l, s[i].x, fmaf(l2, s[i].x, k * v.x));
+    s[i].y = fmaf(l, s[i].y, fmaf(l2, s[i].y, k * v.y));
+    s[i].z = fmaf(l, s[i].z, fmaf(l2, s[i].z, k * v.z));
+    s[i].w = fmaf(l, s[i].w, fmaf(l2, s[i].w, k * v.w));
     *reinterpret_cast<float4*>(base + i * RT * D) = s[i];
   }
   for (int g0 = 0; g0 < a.group; g0 += kStepHeads) {

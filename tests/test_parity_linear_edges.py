@@ -76,3 +76,28 @@ def test_two_roundings_and_no_more(D, lens, hq, hkv, states):
         once = (w.to(BF).to(F64) - w).square().mean().sqrt()
         ratio[name] = ((x.to(F64) - w).square().mean().sqrt() / once).item()
     assert max(ratio.values()) <= 1.5, ratio
+
+
+def test_thousands_of_steps_keep_the_decay():
+    # Each step rounds a state once to fp32 (2^-24 of it at most, 1 / sqrt 3 of that in the mean square, in directions
+    # that do not follow from each other: 1 - l is at least 800 steps of fp32).  6000 of them add up to 77 of
+    # one; twice that is allowed.  One fp32 number for the decay is off by the same in every step,
+    # 1.4e-4 of the state after all of them.
+    N, D = 6000, 64
+    g = torch.tensor([-2.0 ** -11, -3e-4, -1e-3, -1e-4])
+    l = torch.exp(g.to(F64))
+    once = 2.0 ** -24 / 3 ** 0.5
+    bound = 2 * N ** 0.5 * once
+    assert (N * (l.float().to(F64) / l - 1).abs()).max() > 4 * bound      # (what the test is to tell apart)
+    gen = torch.Generator().manual_seed(50)
+    k, v = (torch.randn(16, 2, 4, D, generator=gen).to(BF) for _ in range(2))
+    k[:, 0] = 0                                           # one sequence keeps its first state alone
+    state = torch.randn(2, 4, D, D, generator=gen)
+    st, gd, kd, vd = state.to(DEV), g.to(DEV), k.to(DEV), v.to(DEV)
+    want = state.to(F64)
+    kv = k.to(F64)[..., :, None] * v.to(F64)[..., None, :]
+    for i in range(N):
+        A.linear_attn_step(kd[i % 16], kd[i % 16], vd[i % 16], gd, st)
+        want = l[:, None, None] * want + kv[i % 16]
+    rms = ((st.cpu().to(F64) - want).square().mean((2, 3)) / want.square().mean((2, 3))).sqrt()
+    assert (rms <= bound).all(), rms
