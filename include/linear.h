@@ -49,7 +49,7 @@ extern "C" {
  * keeps everything, -inf keeps only the present token.  It is a property of the
  * layer, not differentiated.
  *
- * No output may share memory with an input or another output (ATTN_ERR_INVALID_ARG).
+ * No output, nor the workspace, may share memory with another argument (ATTN_ERR_INVALID_ARG).
  *
  * Supported: head_dim in {64, 128}; heads_q a multiple of heads_kv, at most 65535;
  * tokens * heads_q < 2^31, num_seqs * heads_q < 2^29.

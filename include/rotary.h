@@ -56,7 +56,8 @@ attn_status_t attn_rotary_table(const attn_rotary_table_t* t, float* cos_sin, at
  * between two tokens' rows (0: dense; else at least heads * head_dim and a
  * multiple of 8), so that slices of a fused projection can be passed; the heads
  * of a token are dense.  The outputs are dense and may be the inputs where those
- * are dense.
+ * are dense; else they share no memory with another argument or with each other
+ * (ATTN_ERR_INVALID_ARG).
  *
  * A token's position: positions[t] where `positions` is given (device int32
  * [tokens]; -1 marks a padding row); else its place in its sequence of the THD

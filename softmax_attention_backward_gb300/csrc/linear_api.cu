@@ -277,6 +277,16 @@ Span span(const linear_attn_problem_t* p, const float* state) {
   return span_of(state, 1, 0, state_bytes(p, p->num_seqs), 1);
 }
 
+// What else a call reads, or (its error word) adds to.
+struct Small {
+  Span decay, cu, word;
+};
+Small small(const linear_attn_problem_t* p) {
+  return {span_of(p->log_decay, 1, 0, p->heads_kv, sizeof(float)),
+          span_of(p->cu_seqlens, 1, 0, static_cast<int64_t>(p->num_seqs) + 1, sizeof(int32_t)),
+          span_of(p->error_word, 1, 0, 1, sizeof(int32_t))};
+}
+
 // A problem without a token: the last state is the first one.
 attn_status_t pass_state(const linear_attn_problem_t* p, const float* first, float* last,
                          cudaStream_t st) {
@@ -308,7 +318,8 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
                                          size_t workspace_bytes, attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (overlap({span(p, final_state), span(p, initial_state)}, 1)) return ATTN_ERR_INVALID_ARG;
+  const Small in = small(p);
+  if (overlap({span(p, final_state), span(p, initial_state), in.decay, in.cu, in.word}, 1)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return ATTN_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (p->tokens == 0) return pass_state(p, initial_state, final_state, st);
@@ -321,11 +332,11 @@ extern "C" attn_status_t linear_attn_fwd(const linear_attn_problem_t* p, const v
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
     return ATTN_ERR_ALIGNMENT;
   const int64_t dense = static_cast<int64_t>(p->heads_q) * p->head_dim;
-  if (overlap({span(p, Rows{o, dense, p->heads_q}), span(p, final_state), span(p, rq), span(p, rk), span(p, rv),
-               span(p, initial_state)}, 2))
-    return ATTN_ERR_INVALID_ARG;
   const Cut cut = cut_sequences(p, false);
   const size_t need = workspace_bytes_of(p, cut);
+  if (overlap({span(p, Rows{o, dense, p->heads_q}), span(p, final_state), span_of(workspace, 1, 0, need, 1), span(p, rq),
+               span(p, rk), span(p, rv), span(p, initial_state), in.decay, in.cu, in.word}, 3))
+    return ATTN_ERR_INVALID_ARG;
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return ATTN_ERR_ALIGNMENT;
   LinearArgs a = make_args(p);
@@ -357,7 +368,8 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
                                          attn_stream_t stream) {
   const attn_status_t s = check(p);
   if (s != ATTN_OK) return s;
-  if (overlap({span(p, dinitial_state), span(p, initial_state), span(p, dfinal_state)}, 1))
+  const Small in = small(p);
+  if (overlap({span(p, dinitial_state), span(p, initial_state), span(p, dfinal_state), in.decay, in.cu, in.word}, 1))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(initial_state, 16) || !aligned(dfinal_state, 16) || !aligned(dinitial_state, 16))
     return ATTN_ERR_ALIGNMENT;
@@ -375,12 +387,13 @@ extern "C" attn_status_t linear_attn_bwd(const linear_attn_problem_t* p, const v
     return ATTN_ERR_ALIGNMENT;
   const int64_t dense_q = static_cast<int64_t>(p->heads_q) * p->head_dim;
   const int64_t dense_kv = static_cast<int64_t>(p->heads_kv) * p->head_dim;
-  if (overlap({span(p, Rows{dq, dense_q, p->heads_q}), span(p, Rows{dk, dense_kv, p->heads_kv}),
-               span(p, Rows{dv, dense_kv, p->heads_kv}), span(p, dinitial_state), span(p, rq), span(p, rk),
-               span(p, rv), span(p, rd), span(p, initial_state), span(p, dfinal_state)}, 4))
-    return ATTN_ERR_INVALID_ARG;
   const Cut cut = cut_sequences(p, true);
   const size_t need = workspace_bytes_of(p, cut);
+  if (overlap({span(p, Rows{dq, dense_q, p->heads_q}), span(p, Rows{dk, dense_kv, p->heads_kv}),
+               span(p, Rows{dv, dense_kv, p->heads_kv}), span(p, dinitial_state), span_of(workspace, 1, 0, need, 1),
+               span(p, rq), span(p, rk), span(p, rv), span(p, rd), span(p, initial_state), span(p, dfinal_state),
+               in.decay, in.cu, in.word}, 5))
+    return ATTN_ERR_INVALID_ARG;
   if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return ATTN_ERR_ALIGNMENT;
   const int group = p->heads_q / p->heads_kv;

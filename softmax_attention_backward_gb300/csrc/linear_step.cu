@@ -160,7 +160,9 @@ extern "C" attn_status_t linear_attn_step(const linear_attn_step_t* p, const voi
   const int64_t n = p->num_seqs, wq = static_cast<int64_t>(p->heads_q) * p->head_dim;
   const int64_t wk = static_cast<int64_t>(p->heads_kv) * p->head_dim;
   if (overlap({span_of(o, n, wq, wq, 2), span_of(state, p->num_slots, wk * p->head_dim, wk * p->head_dim, 4),
-               span_of(q, n, a.q_stride, wq, 2), span_of(k, n, a.k_stride, wk, 2), span_of(v, n, a.v_stride, wk, 2)},
+               span_of(q, n, a.q_stride, wq, 2), span_of(k, n, a.k_stride, wk, 2), span_of(v, n, a.v_stride, wk, 2),
+               span_of(p->slots, 1, 0, n, 4), span_of(p->log_decay, 1, 0, p->heads_kv, 4),
+               span_of(p->error_word, 1, 0, 1, 4)},
               2))
     return ATTN_ERR_INVALID_ARG;
   a.q = static_cast<const __nv_bfloat16*>(q);

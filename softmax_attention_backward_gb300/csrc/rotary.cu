@@ -296,6 +296,11 @@ attn_status_t rotate(const attn_rotary_problem_t* p, const void* q, const void* 
     if (in[i] != out[i] && overlap({to[i], from[i]}, 1)) return ATTN_ERR_INVALID_ARG;
   }
   if (overlap({to[0], to[1], from[1]}, 1) || overlap({to[1], from[0]}, 1)) return ATTN_ERR_INVALID_ARG;
+  if (overlap({to[0], to[1], span_of(cos_sin, p->max_position, p->rot_dim, p->rot_dim, 4),
+               span_of(p->cu_seqlens, 1, 0, static_cast<int64_t>(p->num_seqs) + 1, 4),
+               span_of(p->positions, 1, 0, p->tokens, 4), span_of(p->error_word, 1, 0, 1, 4)},
+              2))
+    return ATTN_ERR_INVALID_ARG;
   a.tokens = p->tokens;
   a.dim = p->head_dim;
   a.rot = p->rot_dim;
