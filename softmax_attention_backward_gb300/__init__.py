@@ -967,6 +967,7 @@ def attn_rotary_table(max_position, rot_dim, *, base=10000.0, scaling="none", fa
     more than `fast` times, a ramp between)."""
     if scaling not in _ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {', '.join(_ROTARY_SCALINGS)}, got {scaling!r}")
+    max_position, rot_dim = _size(int(max_position), "positions"), _size(int(rot_dim), "rotated dims")
     if out is None:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if dev.type != "cuda":
@@ -979,13 +980,20 @@ def attn_rotary_table(max_position, rot_dim, *, base=10000.0, scaling="none", fa
             raise ValueError("out must be [max_position, rot_dim]")
         if device is not None and torch.device(device) not in (dev, torch.device("cuda")):
             raise ValueError(f"out is on {dev}, device is {device}")
-    p = _RotaryTable(int(max_position), int(rot_dim), float(base), _ROTARY_SCALINGS[scaling],
-                     float(factor), int(original), float(fast), float(slow), float(magnitude))
+    p = _RotaryTable(max_position, rot_dim, float(base), _ROTARY_SCALINGS[scaling],
+                     float(factor), _size(int(original), "original positions"), float(fast), float(slow), float(magnitude))
     ctx, s = _on(dev, stream)
     if ctx is None:
         return _table_here(p, out, dev, s)
     with ctx:
         return _table_here(p, out, dev, s)
+
+
+def _size(n, what):
+    """A size that the library takes in 32 bits (ctypes would cut off what is above)."""
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"{n} {what}: at most {(1 << 31) - 1} are supported")
+    return n
 
 
 def _table_here(p, out, dev, s):
@@ -1036,7 +1044,7 @@ def _lead(shape, cu_seqlens, gpu, device):
         if len(shape) != 4:
             raise ValueError("dense q must be [batch, seqlen, heads, head_dim]")
         n, length = shape[0], shape[1]
-        return n * length, n, length, None
+        return _size(n * length, "tokens"), _size(n, "sequences"), _size(length, "tokens of a sequence"), None
     if len(shape) != 3:
         raise ValueError("THD q must be [tokens, heads, head_dim]")
     if not _ok(cu_seqlens, torch.int32, gpu):
@@ -1044,7 +1052,7 @@ def _lead(shape, cu_seqlens, gpu, device):
     n = cu_seqlens.numel() - 1
     if cu_seqlens.dim() != 1 or n < 1:
         raise ValueError("cu_seqlens must be [num_seqs + 1]")
-    return shape[0], n, 0, cu_seqlens.data_ptr()
+    return _size(shape[0], "tokens"), _size(n, "sequences"), 0, cu_seqlens.data_ptr()
 
 
 def _word(error_word, gpu, device):
@@ -1081,7 +1089,7 @@ def _rotary(name, q, k, cos_sin, positions, cu_seqlens, interleaved, rot_offset,
             _need(positions, "positions", torch.int32, dev)
         if positions.shape != lead:
             raise ValueError(f"positions must be {list(lead)}, got {list(positions.shape)}")
-        tokens, n, length, cu, at = positions.numel(), 0, 0, None, positions.data_ptr()
+        tokens, n, length, cu, at = _size(positions.numel(), "tokens"), 0, 0, None, positions.data_ptr()
     heads, dim = shape[-2], shape[-1]
     q_stride = 0 if _ok(q, bf16, gpu) else _token_rows(q, "q", lead, heads, dim, dev)
     heads_k = k_stride = 0
@@ -1103,8 +1111,9 @@ def _rotary(name, q, k, cos_sin, positions, cu_seqlens, interleaved, rot_offset,
     if k_out is not None:
         _out_like(k_out, "k_out", k, gpu, dev)
     rows, rot = cos_sin.shape
-    p = _RotaryProblem(tokens, heads, heads_k, dim, rot, int(rot_offset), 1 if interleaved else 0,
-                       rows, length, n, q_stride, k_stride, cu, at, _word(error_word, gpu, dev))
+    p = _RotaryProblem(tokens, _size(heads, "heads"), _size(heads_k, "heads"), dim, rot,
+                       _size(int(rot_offset), "dims before the rotated ones"), 1 if interleaved else 0,
+                       _size(rows, "positions"), length, n, q_stride, k_stride, cu, at, _word(error_word, gpu, dev))
     ctx, s = _on(dev, stream)
     if ctx is None:
         return _rotary_here(name, p, q, k, cos_sin, q_out, k_out, s)
@@ -1317,8 +1326,8 @@ def linear_attn_step(q, k, v, log_decay, state, *, slots=None, scale=None, out=N
         at = slots.data_ptr()
     if out is not None:
         _out_like(out, "out", q, gpu, dev)
-    p = _LinearStep(n, st[0], heads, heads_kv, dim, float(scale) if scale is not None else 1.0 / math.sqrt(dim),
-                    sq, sk, sv, at, log_decay.data_ptr(), _word(error_word, gpu, dev))
+    p = _LinearStep(_size(n, "sequences"), _size(st[0], "states"), heads, heads_kv, dim,
+                    float(scale) if scale is not None else 1.0 / math.sqrt(dim), sq, sk, sv, at, log_decay.data_ptr(), _word(error_word, gpu, dev))
     ctx, s = _on(dev, stream)
     if ctx is None:
         return _linear_step_here(p, q, k, v, state, out, s)

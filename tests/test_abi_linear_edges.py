@@ -1,8 +1,9 @@
 """Host-only checks of calls at the edges of the rotation's and linear attention's contracts: outputs
-over the small arrays and the workspace."""
+over the small arrays and the workspace, sizes that 32 bits do not hold."""
 import ctypes
 
 import pytest
+import torch
 
 import softmax_attention_backward_gb300 as A
 from test_abi_linear import LIN, ROT, STEP, L, _bwd, _fwd, _make, _ptrs   # noqa: F401 (L is a fixture)
@@ -56,3 +57,15 @@ def test_a_rotation_over_its_table_or_positions_is_refused(L, fn):
                        (dict(cu_seqlens=FAR[i] - 4, num_seqs=1), {}), (dict(error_word=FAR[i] + 8), {})):
             p = _make(A._RotaryProblem, ROT, kw)
             assert getattr(L, fn)(ctypes.byref(p), *_ptrs(5, {**dict(enumerate(FAR[:5])), **at}), None) == 1
+
+
+def test_sizes_past_32_bits_are_refused():
+    # (cut off to 32 bits they would be other sizes: 2^32 + 8 positions a table of 8)
+    for kw in (dict(max_position=(1 << 32) + 8), dict(max_position=1 << 31), dict(max_position=8 - (1 << 32)), dict(rot_dim=(1 << 32) + 64),
+               dict(scaling="parts", factor=2.0, original=(1 << 32) + 64)):
+        with pytest.raises(ValueError, match="at most"):
+            A.attn_rotary_table(**{**dict(max_position=8, rot_dim=64, device="cuda:0"), **kw})
+    for shape in ((1 << 16, 1 << 16, 1, 16), (1 << 32, 0, 1, 16), (0, 1 << 32, 1, 16)):
+        with pytest.raises(ValueError, match="at most"):
+            A._lead(torch.Size(shape), None, 0, None)
+    assert A._lead(torch.Size((1 << 15, 1 << 15, 1, 16)), None, 0, None)[:3] == (1 << 30, 1 << 15, 1 << 15)
