@@ -805,6 +805,11 @@ __global__ void __launch_bounds__(512, kCtas) linear_kernel(const __grid_constan
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
+    if (*reinterpret_cast<volatile int*>(&abort_flag)) {   // a wait ran out: the copies and products in
+      const uint64_t t0 = globaltimer();                   // flight get a moment to land before the CTA leaves
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
     tmem_dealloc(tmem, C::COLS);
   }
 }
