@@ -81,7 +81,7 @@ size_t linear_attn_bwd_workspace_size(const linear_attn_problem_t* p);
 /*
  * Forward.  initial_state and final_state may be NULL (zeros; not wanted).
  * The products run on bf16 operands with fp32 sums.  Within a chunk of 128 tokens
- * the decayed scores are rounded to bf16 (2^-9 of each).  The state is kept in
+ * the decayed scores are rounded to bf16 (off by up to 2^-8 of each).  The state is kept in
  * fp32, and for the chunks behind either the keys times their decays or the
  * state that meets a chunk's rows is rounded so, the other held in two
  * terms (2^-17).  A state that is returned comes of keys in three terms (2^-25), its

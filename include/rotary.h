@@ -46,8 +46,9 @@ typedef struct {
 /* cos_sin fp32 [max_position, rot_dim]: row p holds magnitude cos(p f_a) for
  * a < rot_dim / 2, then magnitude sin(p f_a).  The table that attn_rotary_fwd and
  * attn_cache_append read.  An angle is a product of integers modulo one turn, so
- * its error is p 2^-65 turns beside the rounding of f_a to 53 bits, at any
- * position. */
+ * its error is p 2^-65 turns beside p times that of f_a / 2 pi in fp64, at any
+ * position.  Its cosine and sine are summed in fp32: an entry is off by up to 6 2^-24
+ * magnitude, in the mean square 1.1 to 1.3 times what one rounding to fp32 is. */
 attn_status_t attn_rotary_table(const attn_rotary_table_t* t, float* cos_sin, attn_stream_t stream);
 
 /*
