@@ -97,9 +97,12 @@ Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs)
   const bool packed = p->cu_seqlens != nullptr;
   const int most = ((packed ? p->tokens : p->seqlen) + kLinearChunk - 1) / kLinearChunk;   // of a sequence
   // packed sequences have lengths that the host does not know: half a chunk is taken to be empty in
-  // each, and the longest to be four times the average
+  // each, and the longest to be six times the average.  Forward and backward of 16 heads on 4 of 64, 32 on 8 and 16
+  // of 128, of 6, 12, 40 and 200 sequences of one length (8192 to 200 tokens), 12 and 40 of 1 to 4096,
+  // one of 16384 beside 30 of 100, two of 6000 beside 60 of 700: with 1, 2, 4, 6 and 10 times, 10,
+  // 6, 4, 2.6 and 3.2 % over the best of them in the mean, 51, 29, 30, 23 and 23 % at most
   const double chunks = packed ? most + 0.5 * p->num_seqs : static_cast<double>(most) * p->num_seqs;
-  const int longest = packed ? std::min(most, std::max(4, static_cast<int>(4 * chunks / p->num_seqs))) : most;
+  const int longest = packed ? std::min(most, std::max(4, static_cast<int>(6 * chunks / p->num_seqs))) : most;
   struct Option {
     int chunks;
     double walks, cost, longest, states, state_cost, bytes;   // of one job
