@@ -51,7 +51,9 @@ struct Cut {
 // What a walk takes, in us on one SM: `base` for a chunk, `step` for each of its inner
 // heads (S, P Z and the state's product), `state` for each inner head of a chunk in the pass over
 // the states alone.  Measured, 64 chunks against 32 of 8192 and 4096 tokens: head_dim 128,
-// 1, 2, 4 and 8 inner heads, 195, 315, 530 and 970 us; head_dim 64, 140, 229, 412 and 775.
+// 1, 2, 4 and 8 inner heads, 195, 315, 530 and 970 us; head_dim 64, 140, 229, 412 and 775.  Where many
+// SMs read, a chunk takes longer (head_dim 128, 1 inner head, 128 walks 3.07 us, 152 walks 3.26, for 2.88 here),
+// and a walk's start and end 12 us: cuts are compared with each other, not with the clock.
 struct Rates {
   double base, step, state, part;   // part: a segment's state on the way to another's first
   double start;                     // a walk's start and end
@@ -88,7 +90,7 @@ double makespan(int sms, double na, double ca, double nb, double cb) {
 // uncut and the others in 8 segments of a sequence 278, in 6 307, in 4 306 with dq in 2; one
 // sequence of 65536 tokens, 8 heads on 2 of 128, segments of 27 chunks 133, of 32 149, of 16 165; packed, forward of
 // 12 sequences of up to 8192 tokens, 16 heads on 4 of 64, segments of 7 chunks (taken) 75, of 12 73, of
-// 4 81; 40 of 16 to 4096, 16 heads of 128, of 13 (taken) 179, of 16 167, uncut 191.
+// 4 81; 40 of 16 to 4096, 16 heads of 128, of 13 179, of 16 167, uncut 191.
 Cut find_cut(const linear_attn_problem_t* p, bool backward, int sms, bool pairs) {
   const int group = p->heads_q / p->heads_kv;
   const Rates& rate = pairs ? kPairs : kRates[p->head_dim == 128];

@@ -22,16 +22,18 @@
 //
 // Bound by: a chunk's tiles of 4 x 32 KB take 4700 cycles of an SM's share of the
 // bandwidth where 128 SMs read (D = 128, one inner head), its products 2560 of the
-// tensor cores; measured 5600 (2.9 us), as each product waits in turn for the warps that
-// prepare its operands, and the warp that issues them passes one barrier after the
+// tensor cores; measured 5800 (3.1 us: 4 x 8192 tokens against 4 x 4096), as each product waits in turn for
+// the warps that prepare its operands, and the warp that issues them passes one barrier after the
 // other (300 to 400 cycles each).  So the order of the products is what matters: S
 // of the next step goes out before P Z of this one where the ring holds both.
-// 4 x 4096 tokens of 32 heads of 128: 116 us with the launch, 79 for the bytes alone.
+// 4 x 4096 tokens of 32 heads of 128: 116 us, 5 of them a graph's launch and 12 the walks' start and end;
+// 79 for the bytes alone.
 // Slower, same sizes: two issuing warps 8 %, one wait for several barriers 5 %, the next
 // chunks' tiles fetched to L2 11 %, a ring of 3 tiles 11 %.  Products go out in fours, from loops:
 // two at a time 7 % slower, all unrolled 5 % (the roles share the instruction caches).
 // At D = 64 there is a second variant with two CTAs on an SM (kCtas, 64 registers a thread, one
-// buffer of S), for many short walks: linear_api.cu has the rule.
+// buffer of S; it spills 160 to 190 bytes a thread, the others none to 20), for many short walks:
+// linear_api.cu has the rule.
 #include "linear.cuh"
 
 namespace attn {
@@ -91,9 +93,9 @@ struct Place {
 // The segment that the CTAs of a slot take, by one warp; n = -1 where there is none.  The pass over the
 // states leaves out each sequence's last segment in the walk's direction.  The longer
 // walks of each 32 packed sequences come first, so that no SM is left with one at the
-// end (backward of 12 sequences of up to 2500 tokens, 16 heads of 64, the jobs' walks in turn: 110
-// us, 118 with each job's in the sequences' order).  A search over n sequences takes n / 32 steps, in each
-// CTA: packed sequences by the thousand cost more than their rows.
+// end (backward of 12 sequences of up to 2500 tokens, 16 heads of 64, the jobs' walks in turn, then 110
+// us: 118 with each job's in the sequences' order).  The search takes n / 32 steps for n sequences, in each CTA:
+// packed by the thousand they cost more than their rows (2000 of up to 16 tokens, 16 heads of 64, 2.3 ms).
 template <bool kStates>
 __device__ __forceinline__ Place find_place(const LinearArgs& a, const LinearJob& j, int slot) {
   constexpr int kLeft = kStates ? 1 : 0;   // segments of a sequence that have no slot

@@ -15,7 +15,7 @@
 // the angles of one unit of dims (two 16-byte pieces half the rotated part
 // apart, or one piece of adjacent pairs) and rotates it in up to four heads of a
 // token, all loads first; the angles come from L1 or L2, once for four heads.  4 x 4096
-// tokens of 32 + 8 heads of 128: 58.5 us with the launch, 50 for the bytes alone.
+// tokens of 32 + 8 heads of 128: 56.5 us with the launch, 50 for the bytes alone.
 #include <cuda_runtime.h>
 
 #include <cmath>
