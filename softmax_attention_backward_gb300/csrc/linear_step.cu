@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const StepArg
     for (int i = 0; i < R; ++i) s[i] = *reinterpret_cast<const float4*>(base + i * RT * D);
   if (threadIdx.x < D) sk[threadIdx.x] = __bfloat162float(a.k[n * a.k_stride + h * D + threadIdx.x]);
   if (threadIdx.x < C) sv[threadIdx.x] = __bfloat162float(a.v[n * a.v_stride + h * D + c0 + threadIdx.x]);
-  // The decay in two parts: the rounding of one would be the same in every step (log_decay -2^-11: a
-  // steady state off by 2^-14).  By one thread, while the others' loads are under way.
+  // The decay in two parts: the rounding of one would be the same in every step (log_decay near -2^-11: a
+  // steady state off by up to 2^-14).  By one thread, while the others' loads are under way.
   if (threadIdx.x == kStepThreads - 1) {
     float g = __ldg(a.log_decay + h);
     if (!(g <= 0.f)) {
